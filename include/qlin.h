@@ -349,6 +349,135 @@ size_t qlin_moe_w4a16_workspace_bytes(int64_t T, int64_t H, int64_t I, int64_t E
 int qlin_moe_w4a16_workspace_layout(int64_t T, int64_t H, int64_t I, int64_t E, int topk,
                                     size_t offsets[2]);
 
+/* ------------------------------------------------------------------------
+ * Attention over a paged key/value cache: the steps of a decoder layer
+ * between its QKV linear and its output linear ([E2B] "Step 3": the builds
+ * are served with prompts of 128, 1,024 and 8,192 tokens; [PR]: what FP8
+ * weights save is spent on KV cache).
+ *
+ * The cache is a pool of pages of page_size tokens. One page of one key/value
+ * head is a contiguous block, so that what one workgroup reads lies together:
+ *   k, v      [pages][kv_heads][page_size][head_dim], bf16 (QLIN_KV_BF16) or
+ *             OCP E4M3 codes (QLIN_KV_E4M3), 16-byte aligned;
+ *   k_scale, v_scale  [pages][kv_heads][page_size] fp32 for QLIN_KV_E4M3
+ *             (the value of a row is code * scale), NULL for QLIN_KV_BF16.
+ * head_dim is 64, 128 or 256, page_size a power of two from 16 to 256.
+ *
+ * A batch holds `batch` sequences of new tokens, one behind the other:
+ *   q_start   [batch + 1] int32, not falling: sequence b's new tokens are rows
+ *             q_start[b] .. q_start[b+1]-1 of q, k, v and of the outputs (no
+ *             row: an idle slot). Rows outside every sequence (padding behind
+ *             the last one) are neither read nor written;
+ *   kv_len    [batch] int32: tokens of sequence b in the cache, its new ones
+ *             included (they are the last ones). A length over
+ *             table_cols * page_size counts as that;
+ *   page_table [batch][table_cols] int32: page of each page_size tokens;
+ *   max_q     at least the longest sequence's count of new tokens (a host
+ *             value, it selects kernels; with fewer the result is the same).
+ * The arrays are device data, read when the kernels run (a captured graph
+ * sees the values of each replay), so their values are no errors: the keys of
+ * a page outside [0, pages) are not written and not seen.
+ * ------------------------------------------------------------------------ */
+enum { QLIN_KV_BF16 = 0, QLIN_KV_E4M3 = 1 };
+
+typedef struct {
+  void* k;
+  void* v;
+  float* k_scale;
+  float* v_scale;
+  int64_t pages, kv_heads, page_size, head_dim;
+  int fmt; /* QLIN_KV_* */
+} qlin_kv_cache;
+
+typedef struct {
+  const int32_t* q_start;
+  const int32_t* kv_len;
+  const int32_t* page_table;
+  int64_t batch, table_cols, max_q;
+} qlin_kv_batch;
+
+/* Rotary positions: pair i of the first `rot` values of a head is turned by
+ * position * turns[i] whole turns and scaled by `magnitude`:
+ *   a' = m (a cos t - b sin t), b' = m (b cos t + a sin t),
+ * the pair being values i and i + rot/2, or 2i and 2i + 1 (`interleaved`).
+ * turns [rot/2] fp64 is device memory; rot % 16 == 0, 16 <= rot <= head_dim. The
+ * angle is reduced to its part of a turn in fp64, so positions up to the whole
+ * int32 range keep fp32 accuracy. */
+typedef struct {
+  const double* turns;
+  int64_t rot;
+  int interleaved;
+  float magnitude;
+} qlin_rope_plan;
+
+/* Frequency rules, written to HOST memory out[rot/2], in turns a position
+ * (f_i = base^(-2i/rot) / 2 pi):
+ *   QLIN_ROPE_PLAIN   f_i;
+ *   QLIN_ROPE_LINEAR  f_i / factor (positions interpolated);
+ *   QLIN_ROPE_BASE    f_i with the base times factor^(rot/(rot-2));
+ *   QLIN_ROPE_RAMP    f_i / factor below `low` turns over trained_len tokens,
+ *                     f_i above `high`, blended linearly in the number of
+ *                     turns between (YaRN: low 1, high 32 and a magnitude of
+ *                     0.1 ln(factor) + 1).
+ * trained_len, low and high are read by the ramp alone. Errors: QLIN_ERR_ARG
+ * for an unknown rule, a NULL out or a parameter that is not finite or not in
+ * range (base > 1, factor > 0, trained_len > 0, 0 <= low < high);
+ * QLIN_ERR_SHAPE for a rot that is no multiple of 16. */
+enum { QLIN_ROPE_PLAIN = 0, QLIN_ROPE_LINEAR = 1, QLIN_ROPE_BASE = 2, QLIN_ROPE_RAMP = 3 };
+int qlin_rope_turns(int64_t rot, double base, int rule, double factor, double trained_len, double low,
+                    double high, double* out);
+
+/* Rotary positions of x [T][ldx] (H heads of D values at the start of each
+ * row) into y [T][ldy], bf16, computed in fp32 and rounded once. positions
+ * [T] int32. inverse != 0 turns the other way (the gradient with respect to x
+ * of the rotation; undoes it where magnitude is 1). D % 16 == 0, D <= 1024;
+ * ldx, ldy >= H * D, multiples of 8. y may be x itself (with ldy == ldx), else
+ * they must not overlap. */
+int qlin_rope(const qlin_bf16* x, int64_t ldx, int64_t T, int64_t H, int64_t D,
+              const int32_t* positions, const qlin_rope_plan* rope, int inverse, qlin_bf16* y,
+              int64_t ldy, qlin_stream_t stream);
+
+/* The new tokens' keys and values into the cache, in one launch with the
+ * rotation of their keys and queries. Row t of k and v [T][ldk], [T][ldv]
+ * (kv_heads heads of head_dim values) goes to its sequence's slot (its
+ * position in the sequence: kv_len - new tokens + its number). Keys are turned by
+ * `rope` at positions[t], or at that position if positions is NULL; with a
+ * NULL rope they are stored as they are. QLIN_KV_E4M3 rows are quantised from
+ * the fp32 rotated values by the rule of qlin_quant_act (scale = absmax / 448,
+ * codes of x / scale, nearest even, zero row: scale 0 and codes 0).
+ * q [T][ldq] (q_heads heads), turned the same way, goes to q_out [T][ldqo] in
+ * bf16; q = q_out = NULL leaves the queries out, q_out may be q itself. A
+ * token whose slot lies before 0 or outside the page table, or in a page
+ * outside [0, pages), is not stored (its query is still turned). No two
+ * sequences may store into one page's same slot. */
+int qlin_kv_append(const qlin_kv_cache* cache, const qlin_kv_batch* batch, int64_t T,
+                   const qlin_bf16* k, int64_t ldk, const qlin_bf16* v, int64_t ldv,
+                   const qlin_rope_plan* rope, const int32_t* positions, const qlin_bf16* q,
+                   int64_t ldq, int64_t q_heads, qlin_bf16* q_out, int64_t ldqo,
+                   qlin_stream_t stream);
+
+/* Attention of the new tokens over the cache, after qlin_kv_append. With g =
+ * q_heads / kv_heads, query head h of new token i (position p = kv_len - new
+ * tokens + i) gives, over the keys j it sees,
+ *   z_j = scale * q . k_j,  out = sum_j exp(z_j) v_j / sum_j exp(z_j),
+ *   lse = ln sum_j exp(z_j)        (keys and values of head h / g).
+ * It sees every key j < kv_len; j <= p with causal != 0; and j > p - window
+ * with a window > 0 (which needs causal). A row that sees no key gets zeros and
+ * lse = -inf. Scores, softmax statistics and sums are fp32, products are bf16
+ * MFMA: the weights exp(z_j - max) (times v's scale) are rounded to bf16
+ * before they multiply the values. Cached values behind a sequence's end and
+ * outside every page that it uses never reach its result, NaN included.
+ *   q, out [T][ldq], [T][ldo] bf16 (ld >= q_heads * head_dim, multiples of 8);
+ *   lse [T][q_heads] fp32 or NULL; scale finite.
+ * Workspace: qlin_attn_workspace_bytes bytes, 256-byte aligned, no zeroing
+ * (0 when the key axis is not split); calls that overlap need one each. */
+size_t qlin_attn_workspace_bytes(const qlin_kv_cache* cache, const qlin_kv_batch* batch, int64_t T,
+                                 int64_t q_heads);
+int qlin_attn_paged(const qlin_kv_cache* cache, const qlin_kv_batch* batch, int64_t T,
+                    const qlin_bf16* q, int64_t ldq, int64_t q_heads, float scale, int causal,
+                    int64_t window, qlin_bf16* out, int64_t ldo, float* lse, void* ws,
+                    size_t ws_bytes, qlin_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -68,6 +68,12 @@ def _load():
                                   C.c_float, C.c_float, C.c_float, P, P, P, P, P, P]),
         "qo_moe_w4a16": (None, [P, I64, I64, I64, I64, C.c_int, P, P, P, P, P, P, P, P, P, P]),
         "qo_embed_q4": (None, [P, I64, P, P, I64, I64, P]),
+        "qo_rope_turns": (None, [I64, C.c_double, C.c_int, C.c_double, C.c_double, C.c_double, C.c_double,
+                                 P]),
+        "qo_rope": (None, [P, I64, I64, I64, I64, P, P, I64, C.c_int, C.c_double, C.c_int, P, P]),
+        "qo_kv_slots": (None, [P, P, P, I64, I64, I64, I64, I64, P, P]),
+        "qo_attn_paged": (None, [P, I64, I64, I64, I64, P, P, P, P, C.c_int, I64, I64, I64, P, P, P, I64,
+                                 I64, C.c_double, C.c_int, I64, P, P, P, P, P]),
         "qo_max_threads": (C.c_int, []),
         "qo_set_threads": (None, [C.c_int]),
     }
@@ -388,6 +394,52 @@ def embed_q4(ids, packed, steps):
     out = np.empty((ids.size, D), np.uint16)
     _load().qo_embed_q4(_p(ids), ids.size, _p(p), _p(s), V, D, _p(out))
     return out
+
+
+# ---------------------------------------------------------------- attention
+def rope_turns(rot, base=10000.0, rule=0, factor=1.0, trained_len=1.0, low=0.0, high=1.0):
+    out = np.empty(rot // 2, np.float64)
+    _load().qo_rope_turns(rot, base, rule, factor, trained_len, low, high, _p(out))
+    return out
+
+
+def rope(x_bf16, positions, turns, rot, interleaved=False, magnitude=1.0, inverse=False):
+    """x [T,H,D] bf16 bits -> (y, mag) f64 [T,H,D]: the turned values and the
+    magnitudes that their sums are made of."""
+    x, pos, turns = _c(x_bf16, np.uint16), _c(positions, np.int32), _c(turns, np.float64)
+    T, H, D = x.shape
+    y, mag = np.empty((T, H, D)), np.empty((T, H, D))
+    _load().qo_rope(_p(x), H * D, T, H, D, _p(pos), _p(turns), rot, int(interleaved), magnitude,
+                    int(inverse), _p(y), _p(mag))
+    return y, mag
+
+
+def kv_slots(q_start, kv_len, table, page_size, pages, T):
+    """(slot [T], -1 where not stored; place [T] in its sequence)."""
+    qs, kl, tb = _c(q_start, np.int32), _c(kv_len, np.int32), _c(table, np.int32)
+    slot, place = np.empty(T, np.int64), np.zeros(T, np.int64)
+    _load().qo_kv_slots(_p(qs), _p(kl), _p(tb), kl.size, tb.shape[1], page_size, pages, T, _p(slot),
+                        _p(place))
+    return slot, place
+
+
+def attn_paged(q_bf16, k, v, ks, vs, q_start, kv_len, table, scale, causal=True, window=0):
+    """q [T,Hq,D] bf16 bits over pools [pages,Hkv,page,D] (bf16 bits, or u8 codes
+    with f32 scales). Returns dict(out, lse, mag, zmag, seen); rows of no
+    sequence hold NaN (seen 0)."""
+    fp8 = ks is not None
+    q = _c(q_bf16, np.uint16)
+    k, v = (_c(a, np.uint8 if fp8 else np.uint16) for a in (k, v))
+    ks, vs = (None, None) if not fp8 else (_c(ks, np.float32), _c(vs, np.float32))
+    qs, kl, tb = _c(q_start, np.int32), _c(kv_len, np.int32), _c(table, np.int32)
+    T, Hq, D = q.shape
+    pages, Hkv, page, _ = k.shape
+    r = dict(out=np.full((T, Hq, D), np.nan), lse=np.full((T, Hq), np.nan), mag=np.zeros((T, Hq, D)),
+             zmag=np.zeros((T, Hq)), seen=np.zeros((T, Hq), np.int64))
+    _load().qo_attn_paged(_p(q), Hq * D, T, Hq, D, _p(k), _p(v), _p(ks), _p(vs), int(fp8), pages, Hkv, page,
+                          _p(qs), _p(kl), _p(tb), kl.size, tb.shape[1], scale, int(causal), window,
+                          _p(r["out"]), _p(r["lse"]), _p(r["mag"]), _p(r["zmag"]), _p(r["seen"]))
+    return r
 
 
 def max_threads() -> int:

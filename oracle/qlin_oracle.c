@@ -829,6 +829,160 @@ void qo_moe_w4a16(const uint16_t* x, int64_t T, int64_t H, int64_t I, int64_t E,
   }
 }
 
+/* ------------------------------------------------------------------------ */
+/* Attention over a paged key/value cache (fp64 throughout)                 */
+/* ------------------------------------------------------------------------ */
+
+/* Turns a position of the rot/2 pairs. rule: 0 base^(-2i/rot) / 2pi; 1 that
+ * over factor; 2 with the base times factor^(rot/(rot-2)); 3 a blend of 1
+ * (below `low` turns over `len` tokens) and 0 (above `high`). */
+void qo_rope_turns(int64_t rot, double base, int rule, double factor, double len, double low, double high,
+                   double* out) {
+  const double two_pi = 2.0 * acos(-1.0);
+  for (int64_t i = 0; i < rot / 2; ++i) {
+    double b = rule == 2 ? base * pow(factor, (double)rot / (double)(rot - 2)) : base;
+    double f = 1.0 / pow(b, 2.0 * (double)i / (double)rot) / two_pi;
+    if (rule == 1) f /= factor;
+    if (rule == 3) {
+      double n = len * f;
+      if (n <= low)
+        f = f / factor;
+      else if (n < high)
+        f = f * ((n - low) / (high - low)) + f / factor * ((high - n) / (high - low));
+    }
+    out[i] = f;
+  }
+}
+
+/* x [T][ldx] bf16 (H heads of D) turned: y [T][H][D] unrounded, and
+ * mag [T][H][D], the magnitudes that each value's sum is made of. */
+void qo_rope(const uint16_t* x, int64_t ldx, int64_t T, int64_t H, int64_t D, const int32_t* pos,
+             const double* turns, int64_t rot, int interleaved, double magnitude, int inverse, double* y,
+             double* mag) {
+  const double two_pi = 2.0 * acos(-1.0);
+  for (int64_t t = 0; t < T; ++t)
+    for (int64_t h = 0; h < H; ++h) {
+      const uint16_t* src = x + t * ldx + h * D;
+      double* dst = y + (t * H + h) * D;
+      double* m = mag + (t * H + h) * D;
+      for (int64_t d = 0; d < D; ++d) {
+        dst[d] = bf16_value(src[d]);
+        m[d] = fabs(dst[d]);
+      }
+      for (int64_t i = 0; i < rot / 2; ++i) {
+        const int64_t ia = interleaved ? 2 * i : i, ib = interleaved ? 2 * i + 1 : i + rot / 2;
+        const double w = (double)pos[t] * turns[i];
+        const double angle = two_pi * (w - floor(w)) * (inverse ? -1.0 : 1.0);
+        const double a = bf16_value(src[ia]), b = bf16_value(src[ib]);
+        dst[ia] = magnitude * (a * cos(angle) - b * sin(angle));
+        dst[ib] = magnitude * (b * cos(angle) + a * sin(angle));
+        m[ia] = m[ib] = magnitude * (fabs(a) + fabs(b));
+      }
+    }
+}
+
+/* For each of T rows its sequence (-1: none) and its place in it. */
+static void row_places(const int32_t* q_start, const int32_t* kv_len, int64_t B, int64_t T, int64_t cap,
+                       int64_t* seq, int64_t* place) {
+  for (int64_t t = 0; t < T; ++t) seq[t] = -1;
+  for (int64_t b = 0; b < B; ++b)
+    for (int64_t t = q_start[b]; t < q_start[b + 1] && t < T; ++t) {
+      int64_t len = kv_len[b] < cap ? kv_len[b] : cap;
+      seq[t] = b;
+      place[t] = len - (q_start[b + 1] - q_start[b]) + (t - q_start[b]);
+    }
+}
+
+/* Where each row of a batch goes in a cache: slot [T] = page * page_size + the
+ * row in the page, -1 where it is not stored; place [T] its place in its
+ * sequence (0 for rows of no sequence). */
+void qo_kv_slots(const int32_t* q_start, const int32_t* kv_len, const int32_t* table, int64_t B, int64_t cols,
+                 int64_t page_size, int64_t pages, int64_t T, int64_t* slot, int64_t* place) {
+  int64_t* seq = malloc(sizeof(int64_t) * (size_t)(T > 0 ? T : 1));
+  row_places(q_start, kv_len, B, T, cols * page_size, seq, place);
+  for (int64_t t = 0; t < T; ++t) {
+    slot[t] = -1;
+    if (seq[t] < 0) {
+      place[t] = 0;
+      continue;
+    }
+    if (place[t] < 0 || place[t] >= cols * page_size) continue;
+    const int64_t page = table[seq[t] * cols + place[t] / page_size];
+    if (page >= 0 && page < pages) slot[t] = page * page_size + place[t] % page_size;
+  }
+  free(seq);
+}
+
+static double pool_value(const void* pool, const float* scale, int fp8, int64_t row, int64_t D, int64_t d) {
+  if (fp8) return qo_fp8_value(((const uint8_t*)pool)[row * D + d], QO_OCP) * (double)scale[row];
+  return bf16_value(((const uint16_t*)pool)[row * D + d]);
+}
+
+/* Attention of T rows of Hq query heads over a paged cache of Hkv heads,
+ * pools [pages][Hkv][page_size][D]. Outputs, where a row belongs to a
+ * sequence: out [T][Hq][D] unrounded, lse [T][Hq], mag [T][Hq][D] (the mean of
+ * |v| under the weights), zmag [T][Hq] (the largest |scale| sum |q_d k_d|
+ * of a seen key), seen [T][Hq] (keys that the row sees). */
+void qo_attn_paged(const uint16_t* q, int64_t ldq, int64_t T, int64_t Hq, int64_t D, const void* k, const void* v,
+                   const float* ks, const float* vs, int fp8, int64_t pages, int64_t Hkv, int64_t page_size,
+                   const int32_t* q_start, const int32_t* kv_len, const int32_t* table, int64_t B, int64_t cols,
+                   double scale, int causal, int64_t window, double* out, double* lse, double* mag, double* zmag,
+                   int64_t* seen) {
+  int64_t* seq = malloc(sizeof(int64_t) * (size_t)(T > 0 ? T : 1));
+  int64_t* place = malloc(sizeof(int64_t) * (size_t)(T > 0 ? T : 1));
+  const int64_t cap = cols * page_size;
+  row_places(q_start, kv_len, B, T, cap, seq, place);
+#pragma omp parallel for schedule(dynamic, 1) collapse(2)
+  for (int64_t t = 0; t < T; ++t)
+    for (int64_t h = 0; h < Hq; ++h) {
+      if (seq[t] < 0) continue;
+      const int64_t b = seq[t], hk = h / (Hq / Hkv);
+      int64_t len = kv_len[b] < cap ? kv_len[b] : cap;
+      if (len < 0) len = 0;
+      double* z = malloc(sizeof(double) * (size_t)(len > 0 ? len : 1));
+      int64_t* row = malloc(sizeof(int64_t) * (size_t)(len > 0 ? len : 1));
+      double top = -INFINITY, zm = 0.0;
+      int64_t n = 0;
+      for (int64_t j = 0; j < len; ++j) {
+        if (causal && j > place[t]) continue;
+        if (window > 0 && j <= place[t] - window) continue;
+        const int64_t page = table[b * cols + j / page_size];
+        if (page < 0 || page >= pages) continue;
+        const int64_t r = (page * Hkv + hk) * page_size + j % page_size;
+        double sum = 0.0, am = 0.0;
+        for (int64_t d = 0; d < D; ++d) {
+          const double x = (double)bf16_value(q[t * ldq + h * D + d]) * pool_value(k, ks, fp8, r, D, d);
+          sum += x;
+          am += fabs(x);
+        }
+        z[n] = sum * scale;
+        row[n] = r;
+        if (z[n] > top) top = z[n];
+        if (am * fabs(scale) > zm) zm = am * fabs(scale);
+        n++;
+      }
+      double total = 0.0;
+      for (int64_t j = 0; j < n; ++j) total += exp(z[j] - top);
+      for (int64_t d = 0; d < D; ++d) {
+        double o = 0.0, m = 0.0;
+        for (int64_t j = 0; j < n; ++j) {
+          const double x = exp(z[j] - top) * pool_value(v, vs, fp8, row[j], D, d);
+          o += x;
+          m += fabs(x);
+        }
+        out[(t * Hq + h) * D + d] = n ? o / total : 0.0;
+        mag[(t * Hq + h) * D + d] = n ? m / total : 0.0;
+      }
+      lse[t * Hq + h] = n ? top + log(total) : -INFINITY;
+      zmag[t * Hq + h] = zm;
+      seen[t * Hq + h] = n;
+      free(z);
+      free(row);
+    }
+  free(seq);
+  free(place);
+}
+
 int qo_max_threads(void) {
 #ifdef _OPENMP
   return omp_get_max_threads();

@@ -32,9 +32,27 @@ _lib = C.CDLL(LIB_PATH)
 OK, ERR_ARG, ERR_SHAPE, ERR_ALIGN, ERR_WORKSPACE, ERR_UNSUPPORTED, ERR_HIP = range(7)
 E4M3, E4M3FNUZ, INT8 = 0, 1, 2
 OUT_BF16, OUT_F32 = 0, 1
+KV_BF16, KV_E4M3 = 0, 1
+ROPE_PLAIN, ROPE_LINEAR, ROPE_BASE, ROPE_RAMP = range(4)
 OP_GEMM_FP8, OP_GEMM_W8A8, OP_GEMM_W4A16, OP_LINEAR_FP8, OP_LINEAR_W8A8 = range(5)
 
-_P, _I64, _INT, _SZ = C.c_void_p, C.c_int64, C.c_int, C.c_size_t
+_P, _I64, _INT, _SZ, _F32, _F64 = C.c_void_p, C.c_int64, C.c_int, C.c_size_t, C.c_float, C.c_double
+
+
+class _KVCache(C.Structure):
+    _fields_ = [("k", _P), ("v", _P), ("k_scale", _P), ("v_scale", _P), ("pages", _I64),
+                ("kv_heads", _I64), ("page_size", _I64), ("head_dim", _I64), ("fmt", _INT)]
+
+
+class _KVBatch(C.Structure):
+    _fields_ = [("q_start", _P), ("kv_len", _P), ("page_table", _P), ("batch", _I64),
+                ("table_cols", _I64), ("max_q", _I64)]
+
+
+class _RopePlan(C.Structure):
+    _fields_ = [("turns", _P), ("rot", _I64), ("interleaved", _INT), ("magnitude", _F32)]
+
+
 _SIGS = {
     "qlin_abi_version": (_INT, []),
     "qlin_status_str": (C.c_char_p, [_INT]),
@@ -67,6 +85,13 @@ _SIGS = {
     "qlin_moe_w4a16_workspace_layout": (_INT, [_I64, _I64, _I64, _I64, _INT, C.POINTER(_SZ)]),
     "qlin_moe_w4a16": (_INT, [_P, _I64, _I64, _I64, _I64, _INT, _P, _P, _P, _P, _P, _P, _P, _P,
                               _SZ, _P]),
+    "qlin_rope_turns": (_INT, [_I64, _F64, _INT, _F64, _F64, _F64, _F64, C.POINTER(_F64)]),
+    "qlin_rope": (_INT, [_P, _I64, _I64, _I64, _I64, _P, C.POINTER(_RopePlan), _INT, _P, _I64, _P]),
+    "qlin_kv_append": (_INT, [C.POINTER(_KVCache), C.POINTER(_KVBatch), _I64, _P, _I64, _P, _I64,
+                              C.POINTER(_RopePlan), _P, _P, _I64, _I64, _P, _I64, _P]),
+    "qlin_attn_workspace_bytes": (_SZ, [C.POINTER(_KVCache), C.POINTER(_KVBatch), _I64, _I64]),
+    "qlin_attn_paged": (_INT, [C.POINTER(_KVCache), C.POINTER(_KVBatch), _I64, _P, _I64, _I64, _F32,
+                               _INT, _I64, _P, _I64, _P, _P, _SZ, _P]),
 }
 for _name, (_res, _args) in _SIGS.items():
     _f = getattr(_lib, _name)
@@ -500,3 +525,221 @@ def moe_w4a16(x, topk_ids, topk_w, codes13, steps13, codes2, steps2, return_stag
     act = ws[offs[0]: offs[0] + R * I * 2].view(torch.bfloat16).view(R, I)
     d = ws[offs[1]: offs[1] + R * H * 4].view(torch.float32).view(R, H)
     return y, dict(act=act, d=d)
+
+
+# ---------------------------------------------------------------- attention
+def _heads_arg(t, name, head_dim=None, heads=None):
+    """A bf16 tensor [T, heads, head_dim] whose heads lie together; its rows may
+    be further apart (a slice of a fused QKV projection)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must have 3 dims, got {tuple(t.shape)}")
+    T, H, D = t.shape
+    if (head_dim is not None and D != head_dim) or (heads is not None and H != heads):
+        raise ValueError(f"{name}: expected {heads or 'any'} heads of {head_dim}, got {H} of {D}")
+    if (D > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != D):
+        raise ValueError(f"{name}: the heads of a row must lie together")
+    # the stride of a single row says nothing
+    return T, H, D, t.stride(0) if T > 1 else max(H * D, t.stride(0)) // 8 * 8 if T else H * D
+
+
+def _same_device(dev, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, expected {dev}")
+
+
+def _call_on(dev: torch.device, name: str, *args):
+    """A library call on `dev`'s current stream, with `dev` the current device."""
+    if dev.index == torch.cuda.current_device():
+        _call(name, *args, _stream(dev))
+    else:
+        with torch.cuda.device(dev):
+            _call(name, *args, _stream(dev))
+
+
+class Rope:
+    """A rotary plan: the frequencies (fp64, on `device`) of `rot_dim` turning
+    values of a head of `head_dim` (default: all), and the pairs' layout: (i, i +
+    rot_dim/2), or (2i, 2i + 1) if `interleaved`. `scaling` is None, ("linear",
+    factor), ("base", factor) or ("ramp", factor, trained_len, low, high): see
+    qlin_rope_turns. `magnitude` scales the rotated values (YaRN: 0.1 ln(factor)
+    + 1 with ("ramp", factor, trained_len, 1, 32))."""
+
+    _RULES = {"linear": (ROPE_LINEAR, 1), "base": (ROPE_BASE, 1), "ramp": (ROPE_RAMP, 4)}
+
+    def __init__(self, head_dim: int, rot_dim: int | None = None, base: float = 10000.0,
+                 interleaved: bool = False, scaling=None, magnitude: float = 1.0, device="cuda"):
+        self.head_dim, self.rot_dim = int(head_dim), int(head_dim if rot_dim is None else rot_dim)
+        self.interleaved, self.magnitude = bool(interleaved), float(magnitude)
+        if self.rot_dim > self.head_dim:
+            raise ValueError("rot_dim must not exceed head_dim")
+        rule, args = ROPE_PLAIN, []
+        if scaling is not None:
+            if scaling[0] not in self._RULES or len(scaling) - 1 != self._RULES[scaling[0]][1]:
+                raise ValueError(f"scaling {scaling!r}: expected one of {sorted(self._RULES)} and its arguments")
+            rule, args = self._RULES[scaling[0]][0], [float(x) for x in scaling[1:]]
+        args += [1.0, 1.0, 0.0, 1.0][len(args):]
+        out = (_F64 * max(self.rot_dim // 2, 1))()
+        _call("qlin_rope_turns", self.rot_dim, float(base), rule, *args, out)
+        self.turns = torch.tensor(list(out), dtype=torch.float64, device=device)
+        if not self.turns.is_cuda:
+            raise ValueError("device must be a GPU")
+        self.device = self.turns.device
+        self._c = _RopePlan(self.turns.data_ptr(), self.rot_dim, int(self.interleaved), self.magnitude)
+
+
+class PagedKV:
+    """A paged key/value cache: k, v [pages, kv_heads, page_size, head_dim], bf16,
+    or uint8 E4M3 codes with k_scale, v_scale f32 [pages, kv_heads, page_size].
+    Wraps existing tensors; `PagedKV.empty` allocates them."""
+
+    def __init__(self, k, v, k_scale=None, v_scale=None):
+        if not isinstance(k, torch.Tensor) or k.dtype not in (torch.bfloat16, torch.uint8):
+            raise TypeError("k must be a bfloat16 or uint8 tensor")
+        _check(k, "k", k.dtype, 4)
+        _check(v, "v", k.dtype, 4)
+        if v.shape != k.shape:
+            raise ValueError("k and v must have one shape")
+        self.fmt = KV_BF16 if k.dtype == torch.bfloat16 else KV_E4M3
+        if self.fmt == KV_E4M3:
+            _check(k_scale, "k_scale", torch.float32, 3)
+            _check(v_scale, "v_scale", torch.float32, 3)
+            if k_scale.shape != k.shape[:3] or v_scale.shape != k.shape[:3]:
+                raise ValueError("scales must be [pages, kv_heads, page_size]")
+        elif k_scale is not None or v_scale is not None:
+            raise ValueError("a bfloat16 cache has no scales")
+        self.device = k.device
+        _same_device(self.device, v=v, k_scale=k_scale, v_scale=v_scale)
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.pages, self.kv_heads, self.page_size, self.head_dim = k.shape
+        if self.head_dim not in (64, 128, 256):
+            raise ValueError("head_dim must be 64, 128 or 256")
+        if self.page_size not in (16, 32, 64, 128, 256):
+            raise ValueError("page_size must be 16, 32, 64, 128 or 256")
+
+        def addr(t):
+            return None if t is None else t.data_ptr()
+
+        self._c = _KVCache(addr(k), addr(v), addr(k_scale), addr(v_scale), self.pages, self.kv_heads,
+                           self.page_size, self.head_dim, self.fmt)
+
+    @classmethod
+    def empty(cls, pages, kv_heads, head_dim, page_size=64, fmt="bf16", device="cuda"):
+        """An uninitialised cache; fmt "bf16" or "e4m3"."""
+        if fmt not in ("bf16", "e4m3"):
+            raise ValueError("fmt must be 'bf16' or 'e4m3'")
+        shape = (pages, kv_heads, page_size, head_dim)
+        dt = torch.bfloat16 if fmt == "bf16" else torch.uint8
+        t = [torch.empty(shape, dtype=dt, device=device) for _ in range(2)]
+        if fmt == "e4m3":
+            t += [torch.empty(shape[:3], dtype=torch.float32, device=device) for _ in range(2)]
+        return cls(*t)
+
+
+class PagedBatch:
+    """New tokens of a batch of sequences: q_start int32 [B+1], kv_len int32 [B],
+    page_table int32 [B, cols] (device tensors, read when a call runs) and
+    max_q, at least the longest sequence's count of new tokens (its kernels are
+    chosen by it). Contents as at qlin_kv_batch."""
+
+    def __init__(self, q_start, kv_len, page_table, max_q: int):
+        _check(q_start, "q_start", torch.int32, 1)
+        _check(kv_len, "kv_len", torch.int32, 1)
+        _check(page_table, "page_table", torch.int32, 2)
+        B = kv_len.numel()
+        if q_start.numel() != B + 1 or page_table.shape[0] != B:
+            raise ValueError("q_start must be [B+1], kv_len [B] and page_table [B, cols]")
+        self.device = q_start.device
+        _same_device(self.device, kv_len=kv_len, page_table=page_table)
+        self.q_start, self.kv_len, self.page_table, self.max_q = q_start, kv_len, page_table, int(max_q)
+        self.batch = B
+        self._c = _KVBatch(q_start.data_ptr(), kv_len.data_ptr(), page_table.data_ptr(), B,
+                           page_table.shape[1], self.max_q)
+
+
+def rope(x, positions, rope: Rope, out=None, inverse=False):
+    """Rotary positions of x [T, H, D] (bf16) at positions int32 [T]; `out` may be
+    x. inverse=True turns the other way (the gradient of the rotation)."""
+    T, H, D, ldx = _heads_arg(x, "x", rope.head_dim)
+    _check(positions, "positions", torch.int32, 1)
+    if positions.numel() != T:
+        raise ValueError("positions must be [T]")
+    if out is None:
+        out = torch.empty((T, H, D), dtype=torch.bfloat16, device=x.device)
+        ldy = H * D
+    else:
+        T2, _, _, ldy = _heads_arg(out, "out", D, H)
+        if T2 != T:
+            raise ValueError("out shape mismatch")
+    _same_device(x.device, positions=positions, rope=rope, out=out)
+    _call_on(x.device, "qlin_rope", _ptr(x), ldx, T, H, D, _ptr(positions), rope._c, int(inverse), _ptr(out), ldy)
+    return out
+
+
+def kv_append(cache: PagedKV, batch: PagedBatch, k, v, rope: Rope | None = None, q=None, q_out=None,
+              positions=None):
+    """The new tokens' keys (turned by `rope`) and values [T, kv_heads, D] into the
+    cache. With q [T, q_heads, D] also turns the queries: returned, or written to
+    q_out (which may be q). positions int32 [T] replaces each token's place in
+    its sequence as what the rotation uses."""
+    T, _, D, ldk = _heads_arg(k, "k", cache.head_dim, cache.kv_heads)
+    T2, _, _, ldv = _heads_arg(v, "v", cache.head_dim, cache.kv_heads)
+    ldq, ldqo, heads = 0, 0, 0
+    if q is not None:
+        T3, heads, _, ldq = _heads_arg(q, "q", D)
+        if q_out is None:
+            q_out = torch.empty((T3, heads, D), dtype=torch.bfloat16, device=q.device)
+            ldqo = heads * D
+        else:
+            T4, _, _, ldqo = _heads_arg(q_out, "q_out", D, heads)
+            T3 = T3 if T4 == T3 else -1
+    else:
+        if q_out is not None:
+            raise ValueError("q_out without q")
+        T3 = T
+    if T2 != T or T3 != T:
+        raise ValueError("k, v, q and q_out must have the same number of rows")
+    if rope is not None and rope.head_dim != D:
+        raise ValueError("rope and cache differ in head_dim")
+    if positions is not None:
+        _check(positions, "positions", torch.int32, 1)
+        if positions.numel() != T:
+            raise ValueError("positions must be [T]")
+    _same_device(cache.device, batch=batch, k=k, v=v, rope=rope, q=q, q_out=q_out, positions=positions)
+    _call_on(cache.device, "qlin_kv_append", cache._c, batch._c, T, _ptr(k), ldk, _ptr(v), ldv,
+             None if rope is None else rope._c, _ptr(positions), _ptr(q), ldq, heads, _ptr(q_out), ldqo)
+    return q_out
+
+
+def attn_paged(cache: PagedKV, batch: PagedBatch, q, scale=None, causal=True, window=0, out=None,
+               return_lse=False):
+    """Attention of the new tokens' queries q [T, q_heads, D] over the cache, which
+    holds their keys already (kv_append): [T, q_heads, D] bf16, and with
+    return_lse the rows' ln of the sum of exponentials, f32 [T, q_heads]. scale
+    defaults to D ** -0.5; window > 0 limits each token to its last `window` keys.
+    Rows of q outside every sequence are left as they are in `out` (undefined
+    in a new one)."""
+    T, heads, D, ldq = _heads_arg(q, "q", cache.head_dim)
+    if out is None:
+        out = torch.empty((T, heads, D), dtype=torch.bfloat16, device=q.device)
+        ldo = heads * D
+    else:
+        T2, _, _, ldo = _heads_arg(out, "out", D, heads)
+        if T2 != T:
+            raise ValueError("out shape mismatch")
+    _same_device(cache.device, batch=batch, q=q, out=out)
+    lse = torch.empty((T, heads), dtype=torch.float32, device=q.device) if return_lse else None
+    nb = _lib.qlin_attn_workspace_bytes(cache._c, batch._c, T, heads)
+    # torch's own allocation orders reuse by stream and keeps a captured
+    # graph's workspace its own
+    ws = torch.empty(nb, dtype=torch.uint8, device=q.device) if nb else None
+    _call_on(cache.device, "qlin_attn_paged", cache._c, batch._c, T, _ptr(q), ldq, heads,
+             D ** -0.5 if scale is None else float(scale), int(causal), int(window), _ptr(out), ldo, _ptr(lse),
+             _ptr(ws), nb)
+    return (out, lse) if return_lse else out

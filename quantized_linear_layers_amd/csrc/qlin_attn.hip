@@ -1,0 +1,794 @@
+// Attention of new tokens over a paged key/value cache.
+//
+// Mathematics. For one sequence and one key/value head, the new tokens and the
+// query heads that share that head are packed into rows (row = token * group +
+// head of the group). Over tiles of 32 keys a wave computes
+//   S^T = K Q^T          (32 keys x 32 rows, v_mfma_f32_32x32x16_bf16)
+//   P^T = exp2(c S^T - m) with the running maximum m and sum l of each row
+//   O^T = O^T 2^(m_old - m) + V^T P^T
+// with the scores transposed: a lane then owns one row (lane & 31) and 16 of
+// the 32 keys, so maximum and sum are taken inside the lane and once across the
+// wave's halves, and P^T leaves the first product in the lanes where the
+// second needs it. Lane half h holds keys 8b + 4h + r (b, r = 0..3) of a block,
+// while the MFMA's B operand wants 8 consecutive keys a half: the products sum
+// over keys in any order, so V^T is simply read in P's order
+// (ds_read_b64_tr_b16 gives 4 keys of one column from 4 rows of V, two of them
+// an operand; E4M3: ds_read_b64_tr_b8, 8 keys).
+//
+// The maximum is kept in the exponent's units (log2). It is raised only when a
+// row's new maximum passes it by more than 8: until then the weights stay
+// below 2^8, where bf16 and fp32 keep the same relative precision, and O
+// needs no rescaling pass.
+//
+// K and V tiles arrive by buffer_load_dwordx4 ... lds (16 bytes a lane, 1 KB an
+// instruction, no registers). A resource covers 16 rows of one page at most, so
+// the memory system itself zeroes rows behind the last visible key and before
+// the first one, and pages that do not exist: stale values there, NaN too,
+// never reach a product. LDS rows are stored with their 16-byte chunks
+// exclusive-or-ed by row bits (k_swz, v_swz), so that both the row reads of K and
+// the transposing reads of V touch every bank once.
+//
+// Two kernels share this: attn_step_kernel (at most 32 rows: one decode step),
+// where each wave takes its own key tiles and the waves merge at the end, and
+// attn_chunk_kernel, where each wave has its own rows and the workgroup shares the
+// tiles. Either splits the key axis over workgroups when the rows alone do not
+// fill the device; attn_join_kernel then joins the parts.
+#include "qlin_internal.h"
+#include "qlin_device.h"
+
+#include <algorithm>
+#include <cmath>
+
+namespace qlin {
+
+namespace {
+
+typedef float v16f __attribute__((ext_vector_type(16)));
+typedef short v4s __attribute__((ext_vector_type(4)));
+typedef short v8s __attribute__((ext_vector_type(8)));
+typedef int v2i __attribute__((ext_vector_type(2)));
+
+#define QLIN_LDS __attribute__((address_space(3)))
+#define QLIN_CONST __attribute__((address_space(4)))
+
+constexpr float kLn2 = 0.69314718055994530942f;
+constexpr float kInf = __builtin_inff();
+
+struct AttnArgs {
+  const uint8_t *k, *v;
+  const float *ks, *vs;
+  const uint16_t* q;
+  uint16_t* out;
+  float* lse;
+  const int32_t *q_start, *kv_len, *table;
+  int64_t ldq, ldo, pages, T, window;
+  int B, cols, page_shift, kv_heads, group, causal, splits;
+  int tiles;   // row tiles over all sequences, at most (chunk)
+  int negate;  // a negative scale: the queries change sign
+  float c;     // |scale| * log2(e)
+  float* po;   // [splits][T][q_heads][D], with splits > 1
+  float* pml;  // [splits][T][q_heads][2]: running maximum (log2), sum
+};
+
+__device__ __forceinline__ v16f mfma32(v8bf a, v8bf b, v16f c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// 8 E4M3 codes to bf16 (exact).
+__device__ __forceinline__ v8bf cvt_fp8x8(uint32_t lo, uint32_t hi) {
+  const v2bf p0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, false);
+  const v2bf p1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, true);
+  const v2bf p2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, false);
+  const v2bf p3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, true);
+  return v8bf{p0[0], p0[1], p1[0], p1[1], p2[0], p2[1], p3[0], p3[1]};
+}
+
+// Geometry of K and V rows in LDS.
+template <int D, bool FP8>
+struct Geo {
+  static constexpr int kRow = FP8 ? D : 2 * D;       // bytes of a row
+  static constexpr int kChunks = kRow / 16;          // 16-byte chunks of a row
+  static constexpr int kRowsPerLoad = 64 / kChunks;  // rows of one 1 KB load
+  // Exclusive-or of a row's chunk index. K is read 16 bytes a lane, one chunk of
+  // 32 rows at a time; V 64 bytes of 4 rows (bf16) or 32 bytes of 8 rows.
+  static __device__ __forceinline__ int k_swz(int row) {
+    return kChunks >= 16 ? row & 15 : kChunks == 8 ? row & 7 : (row >> 1) & 3;
+  }
+  static __device__ __forceinline__ int v_swz(int row) {
+    if (FP8) {
+      if (kChunks >= 16) return ((row & 3) | ((row >> 1) & 4)) << 1;
+      if (kChunks == 8) return (((row >> 1) & 1) | ((row >> 2) & 2)) << 1;
+      return ((row >> 3) & 1) << 1;
+    }
+    return kChunks >= 16 ? (row & 3) << 2 : ((row >> 1) & 1) << 2;
+  }
+};
+
+// (token, head) rows of one sequence and key/value head, and its keys.
+struct Item {
+  int b, h;     // sequence, key/value head
+  int64_t q0;   // its first row in q
+  int n, len;   // new tokens, keys
+  int rows;     // packed rows
+};
+
+// A buffer resource over the visible rows of one 16-row group (first key `key`)
+// of a pool with `bytes` a row, and the bytes of the group before them.
+struct Window16 {
+  uint64_t row;  // first visible row in the pool
+  int rows;      // visible rows, 0 if the page does not exist
+  int skip;      // rows of the group before them
+};
+__device__ __forceinline__ Window16 window_of(const AttnArgs& a, const Item& it, int key, int page, int lo, int hi) {
+  const bool ok = (uint32_t)page < (uint64_t)a.pages;
+  Window16 w;
+  w.skip = min(max(lo - key, 0), 16);
+  w.rows = ok ? max(min(hi - key, 16) - w.skip, 0) : 0;
+  const int in_page = (key & ((1 << a.page_shift) - 1)) + w.skip;
+  w.row = (((uint64_t)(ok ? page : 0) * a.kv_heads + it.h) << a.page_shift) + (w.rows ? in_page : 0);
+  return w;
+}
+__device__ __forceinline__ v4i resource(const void* pool, const Window16& w, int bytes) {
+  const uint64_t p = (uint64_t)(uintptr_t)pool + w.row * bytes;
+  return v4i{__builtin_amdgcn_readfirstlane((int)(uint32_t)p), __builtin_amdgcn_readfirstlane((int)(uint32_t)(p >> 32)),
+             __builtin_amdgcn_readfirstlane(w.rows * bytes), 0x00020000};
+}
+
+// Inline assembly for the same reason as in the prefill GEMMs: the compiler
+// would wait for every load in flight before the next LDS read. The kernels
+// wait themselves (dma_wait) before they read what a load wrote and before
+// they end. What the compiler would see to is written out: the wait state
+// between a write of m0 and the load that uses it, and (settled) the five
+// between a vector instruction's write of a scalar register and a load's use.
+__device__ __forceinline__ void dma16(uint32_t lds, uint32_t off, const v4i& rs) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(off), "s"(rs)
+               : "memory", "m0");
+}
+__device__ __forceinline__ void dma4(uint32_t lds, uint32_t off, const v4i& rs) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(lds), "v"(off), "s"(rs)
+               : "memory", "m0");
+}
+__device__ __forceinline__ void settled(v4i& a, v4i& b) { asm volatile("s_nop 4" : "+s"(a), "+s"(b)); }
+template <int N>
+__device__ __forceinline__ void dma_wait() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void lds_reads_done() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+
+__device__ __forceinline__ uint32_t lds_addr(const void* p) {
+  return (uint32_t)(uintptr_t)(const QLIN_LDS uint8_t*)p;
+}
+
+// A tile of TK keys in LDS: K rows, V rows, then for E4M3 the scales (the
+// first 16 of every 64 floats: a load writes all 64 lanes). One wave loads ROWS
+// of them (8 or 16 rows of one 16-row group) from row r0.
+template <int D, bool FP8, int TK, int ROWS>
+struct Stage {
+  using G = Geo<D, FP8>;
+  static constexpr int kTile = TK * G::kRow;
+  static constexpr int kScale = FP8 ? TK / 16 * 256 : 0;  // bytes of one scale area
+  static constexpr int kBytes = 2 * kTile + 2 * kScale;
+  static constexpr int kLoads = ROWS / G::kRowsPerLoad;
+  static constexpr int kOps = 2 * kLoads + (FP8 ? 2 : 0);  // loads of one call
+  static_assert(kLoads >= 1, "a load must not pass the wave's rows");
+
+  static __device__ __forceinline__ void load(const AttnArgs& a, const Item& it, int key, int r0, int page, int lo,
+                                              int hi, uint32_t lds) {
+    const int lane = threadIdx.x & 63;
+    const int g0 = r0 & ~15;
+    const Window16 w = window_of(a, it, key + g0, page, lo, hi);
+    v4i rk = resource(a.k, w, G::kRow), rv = resource(a.v, w, G::kRow);
+    settled(rk, rv);
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int row = r0 + i * G::kRowsPerLoad + lane / G::kChunks;
+      const int slot = lane % G::kChunks;
+      // rows before the first visible one fall below the resource: as
+      // unsigned offsets they are far beyond it
+      const uint32_t at = (uint32_t)(((row & 15) - w.skip) * G::kRow);
+      const uint32_t dst = lds + (r0 + i * G::kRowsPerLoad) * G::kRow;
+      dma16(dst, at + 16 * (slot ^ G::k_swz(row)), rk);
+      dma16(dst + kTile, at + 16 * (slot ^ G::v_swz(row)), rv);
+    }
+    if (FP8) {
+      v4i sk = resource(a.ks, w, 4), sv = resource(a.vs, w, 4);
+      settled(sk, sv);
+      const uint32_t at = lane < 16 ? (uint32_t)((lane - w.skip) * 4) : 0xFFFFFFFCu;
+      const uint32_t dst = lds + 2 * kTile + (g0 / 16) * 256;
+      dma4(dst, at, sk);
+      dma4(dst + kScale, at, sv);
+    }
+  }
+};
+
+// Running softmax state of a wave's 32 rows and their output.
+template <int D>
+struct State {
+  v16f o[D / 32];
+  float m, l;  // of row (lane & 31); l sums this lane's keys only
+  __device__ __forceinline__ void clear() {
+    m = -kInf;
+    l = 0.0f;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) o[i] = v16f{};
+  }
+};
+
+// KB * 32 keys in LDS against a wave's 32 rows.
+//   vis_lo, vis_hi: keys that this lane's row sees, relative to the first
+//   masked: whether some row sees only part of them; bad: bit g = the 16-row
+//   group g lies in no page
+template <int D, bool FP8, int KB, int SCALE>
+__device__ __forceinline__ void attend_block(const AttnArgs& a, const v8bf (&q)[D / 16], State<D>& st,
+                                             const uint8_t* lds_k, const uint8_t* lds_v, const uint8_t* lds_s,
+                                             bool masked, int vis_lo, int vis_hi, uint32_t bad) {
+  using G = Geo<D, FP8>;
+  const int lane = threadIdx.x & 63;
+  const int r = lane & 31, h = lane >> 5;
+  v16f s[KB];
+#pragma unroll
+  for (int kb = 0; kb < KB; ++kb) {
+    const int row = 32 * kb + r;
+    const uint8_t* base = lds_k + row * G::kRow;
+    const int sw = G::k_swz(row);
+    v16f acc = {};
+    if (FP8) {
+#pragma unroll
+      for (int u = 0; u < D / 32; ++u) {
+        const v4i x = *reinterpret_cast<const v4i*>(base + 16 * ((2 * u + h) ^ sw));
+        acc = mfma32(cvt_fp8x8(x[0], x[1]), q[2 * u], acc);
+        acc = mfma32(cvt_fp8x8(x[2], x[3]), q[2 * u + 1], acc);
+      }
+    } else {
+#pragma unroll
+      for (int u = 0; u < D / 16; ++u)
+        acc = mfma32(*reinterpret_cast<const v8bf*>(base + 16 * ((2 * u + h) ^ sw)), q[u], acc);
+    }
+    s[kb] = acc;
+  }
+  if (FP8) {
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        const v4f k = *reinterpret_cast<const v4f*>(lds_s + (2 * kb + b / 2) * 256 + (8 * (b & 1) + 4 * h) * 4);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[kb][4 * b + i] *= k[i];
+      }
+  }
+  if (masked) {
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int key = 32 * kb + 8 * (i / 4) + 4 * h + i % 4;
+        const bool see = key >= vis_lo && key < vis_hi && !((bad >> (2 * kb + i / 8)) & 1);
+        s[kb][i] = see ? s[kb][i] : -kInf;
+      }
+  }
+  float mx = s[0][0];
+#pragma unroll
+  for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) mx = fmaxf(mx, s[kb][i]);
+  mx = fmaxf(mx, __shfl_xor(mx, 32, kWave)) * a.c;
+  if (__any(mx > st.m + 8.0f)) {
+    const float m = fmaxf(st.m, mx);
+    const float f = m == -kInf ? 0.0f : exp2_hw(st.m - m);
+    st.m = m;
+    st.l *= f;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+      for (int j = 0; j < 16; ++j) st.o[i][j] *= f;
+  }
+  const float m = st.m == -kInf ? 0.0f : st.m;
+#pragma unroll
+  for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      s[kb][i] = exp2_hw(fmaf(s[kb][i], a.c, -m));
+      st.l += s[kb][i];
+    }
+  if (FP8) {
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        const v4f v =
+            *reinterpret_cast<const v4f*>(lds_s + SCALE + (2 * kb + b / 2) * 256 + (8 * (b & 1) + 4 * h) * 4);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[kb][4 * b + i] *= v[i];
+      }
+  }
+#pragma unroll
+  for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      // P rounded to bf16 for the product (at most 2^-8 of a weight; the sum l
+      // keeps the unrounded weights)
+      v4i pk;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) pk[i] = (int)pack_bf16x2(s[kb][8 * t + 2 * i], s[kb][8 * t + 2 * i + 1]);
+      const v8bf p = __builtin_bit_cast(v8bf, pk);
+      const int key0 = 32 * kb + 16 * t + 4 * h;
+#pragma unroll
+      for (int d = 0; d < D / 32; ++d) {
+        v8bf vt;
+        if (FP8) {
+          const int i = (lane & 15) >> 1;
+          const int row = key0 + (i & 3) + 8 * (i >> 2);
+          const int chunk = 2 * d + ((lane >> 4) & 1);
+          const v2i x = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
+              (QLIN_LDS v2i*)(lds_v + row * G::kRow + 16 * (chunk ^ G::v_swz(row)) + 8 * (lane & 1)));
+          vt = cvt_fp8x8(x[0], x[1]);
+        } else {
+          const int row = key0 + ((lane & 15) >> 2);
+          const int chunk = 4 * d + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
+          const v4s x = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+              (QLIN_LDS v4s*)(lds_v + row * G::kRow + 16 * (chunk ^ G::v_swz(row)) + 8 * (lane & 1)));
+          const v4s y = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+              (QLIN_LDS v4s*)(lds_v + (row + 8) * G::kRow + 16 * (chunk ^ G::v_swz(row + 8)) + 8 * (lane & 1)));
+          vt = __builtin_bit_cast(v8bf, (v8s){x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]});
+        }
+        st.o[d] = mfma32(vt, p, st.o[d]);
+      }
+    }
+}
+
+// The wave's query fragments: one row a lane, values in the order of the K
+// fragments (E4M3 K gives 16 consecutive values a lane, two steps).
+template <int D, bool FP8>
+__device__ __forceinline__ void load_q(const AttnArgs& a, const Item& it, int row, v8bf (&q)[D / 16]) {
+  const int h = (threadIdx.x & 63) >> 5;
+  const int rr = min(row, it.rows - 1);  // rows past the end repeat the last: never stored
+  const int i = rr / a.group, g = rr % a.group;
+  const uint16_t* src = a.q + (it.q0 + i) * a.ldq + (int64_t)(it.h * a.group + g) * D;
+#pragma unroll
+  for (int u = 0; u < D / 16; ++u) {
+    const int off = FP8 ? 32 * (u / 2) + 16 * h + 8 * (u % 2) : 16 * u + 8 * h;
+    uint4 x = ldg16(src + off);
+    if (a.negate) {
+      x.x ^= 0x80008000u;
+      x.y ^= 0x80008000u;
+      x.z ^= 0x80008000u;
+      x.w ^= 0x80008000u;
+    }
+    q[u] = __builtin_bit_cast(v8bf, x);
+  }
+}
+
+// Keys [row_lo, row_hi) that a packed row sees (none: row_hi <= row_lo).
+__device__ __forceinline__ int row_hi(const AttnArgs& a, const Item& it, int row) {
+  if (row >= it.rows) return 0;
+  return a.causal ? it.len - it.n + row / a.group + 1 : it.len;
+}
+__device__ __forceinline__ int row_lo(const AttnArgs& a, const Item& it, int row) {
+  if (a.window <= 0) return 0;
+  const int64_t lo = (int64_t)it.len - it.n + row / a.group + 1 - a.window;
+  return lo > 0 ? (int)lo : 0;
+}
+// Of rows [row0, row1): keys [lo, hi) that some row sees, and [all_lo, all_hi)
+// that every row sees.
+struct Range {
+  int lo, hi, all_lo, all_hi;
+};
+__device__ __forceinline__ Range range_of(const AttnArgs& a, const Item& it, int row0, int row1) {
+  Range r;
+  r.lo = row_lo(a, it, row0);
+  r.hi = max(row_hi(a, it, row1 - 1), 0);
+  r.all_lo = row_lo(a, it, row1 - 1);
+  r.all_hi = row_hi(a, it, row0);
+  return r;
+}
+
+// The page of a key, read through the scalar cache (keys outside the table:
+// some entry, whose rows are then outside the visible range).
+__device__ __forceinline__ int32_t page_of(const AttnArgs& a, const Item& it, int key) {
+  const int col = min(max(key, 0) >> a.page_shift, a.cols - 1);
+  return ((const QLIN_CONST int32_t*)(uintptr_t)a.table)[(int64_t)it.b * a.cols + col];
+}
+
+// A sequence's rows and keys from the batch's device data; false: no rows.
+__device__ __forceinline__ bool item_of(const AttnArgs& a, int b, int h, Item& it) {
+  const int64_t s0 = a.q_start[b], s1 = a.q_start[b + 1];
+  if (s0 < 0 || s1 > a.T || s1 <= s0) return false;
+  it.b = b;
+  it.h = h;
+  it.q0 = s0;
+  it.n = (int)(s1 - s0);
+  const int64_t cap = (int64_t)a.cols << a.page_shift;
+  it.len = (int)max((int64_t)0, min((int64_t)a.kv_len[b], cap));
+  it.rows = it.n * a.group;
+  return true;
+}
+
+// One row's result: final, or a part for attn_join_kernel. This lane holds the
+// head's values 32 d + 8 (i / 4) + 4 h + i % 4 in o[d][i].
+template <int D>
+__device__ __forceinline__ void store_row(const AttnArgs& a, const Item& it, int split, int row, const State<D>& st) {
+  const int h = (threadIdx.x & 63) >> 5;
+  const float l = st.l + __shfl_xor(st.l, 32, kWave);
+  if (row >= it.rows) return;
+  const int64_t t = it.q0 + row / a.group;
+  const int qh = it.h * a.group + row % a.group;
+  const int64_t heads = (int64_t)a.kv_heads * a.group;
+  if (a.splits > 1) {
+    const int64_t at = (split * a.T + t) * heads + qh;
+    if (h == 0) {
+      a.pml[2 * at] = st.m;
+      a.pml[2 * at + 1] = l;
+    }
+    if (st.m == -kInf && l == 0.0f) return;  // no key: the join does not read it
+#pragma unroll
+    for (int d = 0; d < D / 32; ++d)
+#pragma unroll
+      for (int b = 0; b < 4; ++b)
+        *reinterpret_cast<v4f*>(a.po + at * D + 32 * d + 8 * b + 4 * h) =
+            v4f{st.o[d][4 * b], st.o[d][4 * b + 1], st.o[d][4 * b + 2], st.o[d][4 * b + 3]};
+    return;
+  }
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  uint16_t* dst = a.out + t * a.ldo + (int64_t)qh * D;
+#pragma unroll
+  for (int d = 0; d < D / 32; ++d)
+#pragma unroll
+    for (int b = 0; b < 4; ++b)
+      *reinterpret_cast<uint2*>(dst + 32 * d + 8 * b + 4 * h) =
+          make_uint2(pack_bf16x2(st.o[d][4 * b] * inv, st.o[d][4 * b + 1] * inv),
+                     pack_bf16x2(st.o[d][4 * b + 2] * inv, st.o[d][4 * b + 3] * inv));
+  if (a.lse && h == 0) a.lse[t * heads + qh] = l == 0.0f ? -kInf : (st.m + log2f(l)) * kLn2;
+}
+
+// ---------------------------------------------------------------- chunk
+// A workgroup of NW waves has NW * 32 rows of one (sequence, key/value head)
+// and walks their keys in tiles of TK, double buffered: while a tile is
+// multiplied, the loads of the next one are in flight; one barrier a tile.
+template <int D, bool FP8, int NW, int TK>
+__global__ __launch_bounds__(NW * 64, 2) void attn_chunk_kernel(const AttnArgs a) {
+  using St = Stage<D, FP8, TK, TK / NW>;
+  constexpr int BM = NW * 32;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * St::kBytes];
+  __shared__ int bad_rows[2][TK / 16];  // 16-row groups of a tile that lie in no page
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+
+  // Work order: consecutive workgroups go to the 8 XCDs in turn; each XCD gets a
+  // contiguous run of (head, tile) items, so the tiles of one head share its L2.
+  const int items = a.tiles * a.kv_heads * a.splits;
+  const int per = (items + 7) / 8;
+  const int item = (int)(blockIdx.x % 8) * per + (int)(blockIdx.x / 8);
+  if ((int)(blockIdx.x / 8) >= per || item >= items) return;
+  const int split = item % a.splits;
+  const int h = item / a.splits / a.tiles;
+  // the last tiles first: with a causal mask they have the most keys
+  int tile = a.tiles - 1 - item / a.splits % a.tiles;
+  // the tile's sequence: 64 sequences a pass, counted by a prefix sum over lanes
+  int b = -1;
+  for (int b0 = 0; b0 < a.B && b < 0; b0 += 64) {
+    int mine = 0;
+    if (b0 + lane < a.B) {
+      const int64_t n = (int64_t)a.q_start[b0 + lane + 1] - a.q_start[b0 + lane];
+      mine = n > 0 && n <= a.T ? (int)((n * a.group + BM - 1) / BM) : 0;
+    }
+    int sum = mine;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int x = __shfl_up(sum, o, kWave);
+      if (lane >= o) sum += x;
+    }
+    const unsigned long long past = __ballot(sum > tile);
+    if (past) {
+      const int j = __ffsll(past) - 1;
+      b = b0 + j;
+      tile -= __shfl(sum, j, kWave) - __shfl(mine, j, kWave);
+    } else {
+      tile -= __shfl(sum, 63, kWave);
+    }
+  }
+  if (b < 0) return;
+  Item it;
+  if (!item_of(a, __builtin_amdgcn_readfirstlane(b), h, it)) return;
+  const int row0 = __builtin_amdgcn_readfirstlane(tile) * BM;
+
+  const int w0 = row0 + 32 * wave;  // the wave's first row
+  const int row = w0 + (lane & 31);
+  v8bf q[D / 16];
+  load_q<D, FP8>(a, it, row, q);
+  State<D> st;
+  st.clear();
+
+  const Range wg = range_of(a, it, row0, min(row0 + BM, it.rows));
+  const Range own = range_of(a, it, w0, min(w0 + 32, it.rows));
+  const int vlo = row_lo(a, it, row), vhi = row_hi(a, it, row);
+  int t0 = wg.lo / TK, t1 = (wg.hi + TK - 1) / TK;
+  if (a.splits > 1) {
+    const int n = max((t1 - t0 + a.splits - 1) / a.splits, 1);
+    t0 = min(t0 + split * n, t1);
+    t1 = min(t0 + n, t1);
+  }
+  const int r0 = wave * (TK / NW);  // the rows of a tile that this wave loads
+  int page = page_of(a, it, t0 * TK + r0);
+  auto issue = [&](int t, int buf, int pg) {
+    if ((r0 & 15) == 0 && lane == 0) bad_rows[buf][r0 / 16] = (uint32_t)pg >= (uint64_t)a.pages;
+    St::load(a, it, t * TK, r0, pg, wg.lo, wg.hi, lds_addr(lds) + buf * St::kBytes);
+  };
+  if (t0 < t1) issue(t0, 0, page);
+  page = page_of(a, it, (t0 + 1) * TK + r0);
+  for (int t = t0; t < t1; ++t) {
+    const int buf = (t - t0) & 1;
+    dma_wait<0>();
+    __syncthreads();
+    if (t + 1 < t1) issue(t + 1, buf ^ 1, page);
+    page = page_of(a, it, (t + 2) * TK + r0);
+    const int key = t * TK;
+    // nothing of this tile is seen by the wave's rows: past their diagonal,
+    // before their windows, or rows past the end
+    if (w0 >= it.rows || key >= own.hi || key + TK <= own.lo) continue;
+    uint32_t bad = 0;
+#pragma unroll
+    for (int g = 0; g < TK / 16; ++g) bad |= (uint32_t)(bad_rows[buf][g] != 0) << g;
+    bad = __builtin_amdgcn_readfirstlane(bad);
+    const bool masked = bad != 0 || key + TK > own.all_hi || key < own.all_lo;
+    const uint8_t* s = lds + buf * St::kBytes;
+    attend_block<D, FP8, TK / 32, St::kScale>(a, q, st, s, s + St::kTile, s + 2 * St::kTile, masked, vlo - key,
+                                              vhi - key, bad);
+  }
+  store_row<D>(a, it, split, row, st);
+}
+
+// ---------------------------------------------------------------- step
+// At most 32 rows of a (sequence, key/value head): NW waves with the same rows,
+// each with its own key tiles of 32 (wave, wave + NW, ...) and its own two LDS
+// stages, so the loop has no barrier; the waves' results are merged in LDS.
+template <int D, bool FP8, int NW>
+__global__ __launch_bounds__(NW * 64, 1) void attn_step_kernel(const AttnArgs a) {
+  using St = Stage<D, FP8, 32, 16>;
+  constexpr int kOut = D + 4;  // floats of a row in the merge
+  constexpr int kMerge = NW * 32 * kOut * 4, kRing = 2 * NW * St::kBytes;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[kRing > kMerge ? kRing : kMerge];
+  __shared__ float wm[NW][32], wl[NW][32];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int split = blockIdx.x;
+  Item it;
+  if (!item_of(a, blockIdx.z, blockIdx.y, it)) return;
+  it.rows = min(it.rows, 32);  // max_q promises it
+  const int row = lane & 31;
+  const Range rg = range_of(a, it, 0, it.rows);
+  const int vlo = row_lo(a, it, row), vhi = row_hi(a, it, row);
+  int t0 = rg.lo / 32, t1 = (rg.hi + 31) / 32;
+  if (a.splits > 1) {
+    const int n = max((t1 - t0 + a.splits - 1) / a.splits, NW);
+    t0 = min(t0 + split * n, t1);
+    t1 = min(t0 + n, t1);
+  }
+  uint8_t* ring = lds + wave * 2 * St::kBytes;
+  auto issue = [&](int t, int buf, int p0, int p1) {
+    const uint32_t dst = lds_addr(ring) + buf * St::kBytes;
+    St::load(a, it, t * 32, 0, p0, rg.lo, rg.hi, dst);
+    St::load(a, it, t * 32, 16, p1, rg.lo, rg.hi, dst);
+  };
+  int t = t0 + wave;
+  int p0 = page_of(a, it, t * 32), p1 = page_of(a, it, t * 32 + 16);
+  if (t < t1) issue(t, 0, p0, p1);
+  v8bf q[D / 16];
+  load_q<D, FP8>(a, it, row, q);
+  State<D> st;
+  st.clear();
+  int n0 = page_of(a, it, (t + NW) * 32), n1 = page_of(a, it, (t + NW) * 32 + 16);
+  int buf = 0;
+  for (; t < t1; t += NW) {
+    lds_reads_done();  // the stage that the next loads overwrite has been read
+    if (t + NW < t1) {
+      issue(t + NW, buf ^ 1, n0, n1);
+      dma_wait<2 * St::kOps>();
+    } else {
+      dma_wait<0>();
+    }
+    const uint32_t bad = ((uint32_t)p0 >= (uint64_t)a.pages ? 1u : 0u) | ((uint32_t)p1 >= (uint64_t)a.pages ? 2u : 0u);
+    p0 = n0;
+    p1 = n1;
+    n0 = page_of(a, it, (t + 2 * NW) * 32);
+    n1 = page_of(a, it, (t + 2 * NW) * 32 + 16);
+    const int key = t * 32;
+    const bool masked = bad != 0 || key + 32 > rg.all_hi || key < rg.all_lo;
+    const uint8_t* s = ring + buf * St::kBytes;
+    attend_block<D, FP8, 1, St::kScale>(a, q, st, s, s + St::kTile, s + 2 * St::kTile, masked, vlo - key, vhi - key,
+                                        bad);
+    buf ^= 1;
+  }
+  // merge: every wave's rows on the common maximum, then summed over the waves
+  const int hh = lane >> 5;
+  const float l = st.l + __shfl_xor(st.l, 32, kWave);
+  if (hh == 0) {
+    wm[wave][row] = st.m;
+    wl[wave][row] = l;
+  }
+  __syncthreads();
+  float m = -kInf;
+#pragma unroll
+  for (int w = 0; w < NW; ++w) m = fmaxf(m, wm[w][row]);
+  const float f = st.m == -kInf ? (l == 0.0f ? 0.0f : 1.0f) : exp2_hw(st.m - m);
+  float* all = reinterpret_cast<float*>(lds);
+  if (row < it.rows) {
+    float* mine = all + (wave * 32 + row) * kOut;
+#pragma unroll
+    for (int d = 0; d < D / 32; ++d)
+#pragma unroll
+      for (int b = 0; b < 4; ++b)
+        *reinterpret_cast<v4f*>(mine + 32 * d + 8 * b + 4 * hh) =
+            v4f{st.o[d][4 * b] * f, st.o[d][4 * b + 1] * f, st.o[d][4 * b + 2] * f, st.o[d][4 * b + 3] * f};
+    if (hh == 0) wl[wave][row] = l * f;
+  }
+  __syncthreads();
+  const int64_t heads = (int64_t)a.kv_heads * a.group;
+  for (int i = threadIdx.x; i < it.rows * (D / 4); i += NW * 64) {
+    const int r = i / (D / 4), c4 = i % (D / 4) * 4;
+    float mm = -kInf, ll = 0.0f;
+    v4f o = {};
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+      mm = fmaxf(mm, wm[w][r]);
+      ll += wl[w][r];
+      const v4f x = *reinterpret_cast<const v4f*>(all + (w * 32 + r) * kOut + c4);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) o[j] += x[j];
+    }
+    const int64_t tok = it.q0 + r / a.group;
+    const int qh = it.h * a.group + r % a.group;
+    if (a.splits > 1) {
+      const int64_t at = ((int64_t)split * a.T + tok) * heads + qh;
+      if (c4 == 0) {
+        a.pml[2 * at] = mm;
+        a.pml[2 * at + 1] = ll;
+      }
+      *reinterpret_cast<v4f*>(a.po + at * D + c4) = o;
+    } else {
+      const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
+      *reinterpret_cast<uint2*>(a.out + tok * a.ldo + (int64_t)qh * D + c4) =
+          make_uint2(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv));
+      if (a.lse && c4 == 0) a.lse[tok * heads + qh] = ll == 0.0f ? -kInf : (mm + log2f(ll)) * kLn2;
+    }
+  }
+}
+
+// ---------------------------------------------------------------- join
+// The parts of the key axis to one result: a wave a (token, query head).
+template <int D>
+__global__ __launch_bounds__(256) void attn_join_kernel(const AttnArgs a) {
+  constexpr int V = D / 64;  // values a lane
+  const int lane = threadIdx.x & 63;
+  const int64_t heads = (int64_t)a.kv_heads * a.group;
+  const int64_t at = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (at >= a.T * heads) return;
+  // rows of no sequence have no parts (and are left as they are)
+  const int64_t t = at / heads;
+  bool in = false;
+  for (int b0 = 0; b0 < a.B && !in; b0 += 64) {
+    const int b = b0 + lane;
+    in = __any(b < a.B && a.q_start[b] >= 0 && a.q_start[b] <= t && t < a.q_start[b + 1] && a.q_start[b + 1] <= a.T);
+  }
+  if (!in) return;
+  float m = -kInf;
+  for (int s = lane; s < a.splits; s += 64) m = fmaxf(m, a.pml[2 * (s * a.T * heads + at)]);
+  m = wave_max(m);
+  float l = 0.0f, o[V] = {};
+  for (int s = 0; s < a.splits; ++s) {
+    const int64_t p = s * a.T * heads + at;
+    const float ms = a.pml[2 * p], ls = a.pml[2 * p + 1];
+    if (ms == -kInf && ls == 0.0f) continue;  // a part without a key
+    const float w = ms == -kInf ? 1.0f : exp2_hw(ms - m);
+    l += w * ls;
+#pragma unroll
+    for (int i = 0; i < V; ++i) o[i] += w * a.po[p * D + V * lane + i];
+  }
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const __bf16 y = (__bf16)(o[i] * inv);
+    a.out[t * a.ldo + at % heads * D + V * lane + i] = __builtin_bit_cast(uint16_t, y);
+  }
+  if (a.lse && lane == 0) a.lse[at] = l == 0.0f ? -kInf : (m + log2f(l)) * kLn2;
+}
+
+// ---------------------------------------------------------------- host
+struct Plan {
+  bool step;
+  int splits;
+  int64_t tiles;
+};
+
+constexpr int kChunkRows = 128;
+constexpr int kCus = 256;
+
+Plan plan_of(const qlin_kv_cache& cache, const qlin_kv_batch& batch, int64_t T, int64_t q_heads, int64_t window) {
+  Plan p;
+  const int64_t group = q_heads / cache.kv_heads;
+  int64_t keys = batch.table_cols * cache.page_size;
+  if (window > 0) keys = std::min(keys, std::min(window, keys) + batch.max_q);
+  p.step = batch.max_q * group <= 32;
+  if (p.step) {
+    p.tiles = batch.batch;
+    const int64_t wgs = batch.batch * cache.kv_heads;
+    p.splits = (int)std::max<int64_t>(1, std::min((2 * kCus + wgs - 1) / wgs, (keys + 127) / 128));
+  } else {
+    p.tiles = T * group / kChunkRows + batch.batch;
+    const int64_t wgs = p.tiles * cache.kv_heads;
+    p.splits = wgs >= kCus ? 1 : (int)std::max<int64_t>(1, std::min(2 * kCus / wgs, (keys + 255) / 256));
+  }
+  return p;
+}
+
+template <int D, bool FP8>
+void launch_parts(const AttnArgs& a, const Plan& p, hipStream_t st) {
+  if (p.step) {
+    constexpr int NW = D == 256 && !FP8 ? 2 : 4;
+    attn_step_kernel<D, FP8, NW><<<dim3(p.splits, a.kv_heads, a.B), NW * 64, 0, st>>>(a);
+  } else {
+    const int64_t items = p.tiles * a.kv_heads * p.splits;
+    attn_chunk_kernel<D, FP8, 4, D == 256 ? 32 : 64><<<(unsigned)((items + 7) / 8 * 8), 256, 0, st>>>(a);
+  }
+  if (p.splits > 1) {
+    const int64_t rows = a.T * a.kv_heads * a.group;
+    attn_join_kernel<D><<<(unsigned)((rows + 3) / 4), 256, 0, st>>>(a);
+  }
+}
+
+}  // namespace
+
+size_t attn_workspace_bytes(const qlin_kv_cache& cache, const qlin_kv_batch& batch, int64_t T, int64_t q_heads) {
+  const Plan p = plan_of(cache, batch, T, q_heads, 0);
+  if (p.splits <= 1) return 0;
+  const size_t rows = (size_t)p.splits * T * q_heads;
+  return round_up(rows * cache.head_dim * 4, 256) + round_up(rows * 8, 256);
+}
+
+int launch_attn(const qlin_kv_cache& cache, const qlin_kv_batch& batch, int64_t T, const uint16_t* q, int64_t ldq,
+                int64_t q_heads, float scale, int causal, int64_t window, uint16_t* out, int64_t ldo, float* lse,
+                void* ws, hipStream_t st) {
+  const Plan p = plan_of(cache, batch, T, q_heads, window);
+  AttnArgs a = {};
+  a.k = (const uint8_t*)cache.k;
+  a.v = (const uint8_t*)cache.v;
+  a.ks = cache.k_scale;
+  a.vs = cache.v_scale;
+  a.q = q;
+  a.out = out;
+  a.lse = lse;
+  a.q_start = batch.q_start;
+  a.kv_len = batch.kv_len;
+  a.table = batch.page_table;
+  a.ldq = ldq;
+  a.ldo = ldo;
+  a.pages = cache.pages;
+  a.T = T;
+  a.window = window;
+  a.B = (int)batch.batch;
+  a.cols = (int)batch.table_cols;
+  a.page_shift = __builtin_ctzll((unsigned long long)cache.page_size);
+  a.kv_heads = (int)cache.kv_heads;
+  a.group = (int)(q_heads / cache.kv_heads);
+  a.causal = causal;
+  a.splits = p.splits;
+  a.tiles = (int)p.tiles;
+  a.negate = scale < 0.0f;
+  // a scale of 0 must keep masked scores at -inf (0 * -inf is NaN): a positive
+  // one so small that every finite score gets the weight 1
+  a.c = std::max(std::fabs(scale) * 1.44269504088896340736f, 1e-37f);
+  if (p.splits > 1) {
+    const size_t rows = (size_t)p.splits * T * q_heads;
+    a.po = (float*)ws;
+    a.pml = (float*)((uint8_t*)ws + round_up(rows * cache.head_dim * 4, 256));
+  }
+  const bool f8 = cache.fmt == QLIN_KV_E4M3;
+  switch (cache.head_dim) {
+    case 64: f8 ? launch_parts<64, true>(a, p, st) : launch_parts<64, false>(a, p, st); break;
+    case 128: f8 ? launch_parts<128, true>(a, p, st) : launch_parts<128, false>(a, p, st); break;
+    default: f8 ? launch_parts<256, true>(a, p, st) : launch_parts<256, false>(a, p, st); break;
+  }
+  return launch_status();
+}
+
+}  // namespace qlin

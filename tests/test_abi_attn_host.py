@@ -1,0 +1,184 @@
+"""Refusals of the attention entry points, on the host (no GPU needed)."""
+
+import ctypes as C
+import math
+
+import pytest
+import torch
+
+
+@pytest.fixture(scope="module")
+def q():
+    import quantized_linear_layers_amd as qlin
+
+    return qlin
+
+
+A = 0x10000  # fake (never dereferenced) addresses: validation fails before use
+
+
+def cache(q, **over):
+    f = dict(k=A, v=A, k_scale=None, v_scale=None, pages=8, kv_heads=2, page_size=16, head_dim=64, fmt=q.KV_BF16)
+    f.update(over)
+    return q._KVCache(**f)
+
+
+def batch(q, **over):
+    f = dict(q_start=A, kv_len=A, page_table=A, batch=2, table_cols=4, max_q=1)
+    f.update(over)
+    return q._KVBatch(**f)
+
+
+def plan(q, **over):
+    f = dict(turns=A, rot=64, interleaved=0, magnitude=1.0)
+    f.update(over)
+    return q._RopePlan(**f)
+
+
+def p(x):
+    return None if x is None else C.c_void_p(x)
+
+
+def test_turns_on_the_host(q, oracle):
+    for rot in (16, 48, 128):
+        for rule, args in ((0, (1, 1, 0, 1)), (1, (4, 1, 0, 1)), (2, (8, 1, 0, 1)), (3, (16, 8192, 1, 32))):
+            out = (C.c_double * (rot // 2))()
+            assert q.lib().qlin_rope_turns(rot, 10000.0, rule, *map(float, args), out) == q.OK
+            want = oracle.rope_turns(rot, 10000.0, rule, *map(float, args))
+            assert all(abs(g - w) <= 1e-13 * w for g, w in zip(out, want))
+
+
+@pytest.mark.parametrize("args,status", [
+    ((16, 1e4, 4, 1, 1, 0, 1), "ERR_ARG"), ((16, 1e4, -1, 1, 1, 0, 1), "ERR_ARG"),
+    ((8, 1e4, 0, 1, 1, 0, 1), "ERR_SHAPE"), ((40, 1e4, 0, 1, 1, 0, 1), "ERR_SHAPE"),
+    ((1040, 1e4, 0, 1, 1, 0, 1), "ERR_SHAPE"), ((16, 1.0, 0, 1, 1, 0, 1), "ERR_ARG"),
+    ((16, math.inf, 0, 1, 1, 0, 1), "ERR_ARG"), ((16, 1e4, 1, 0, 1, 0, 1), "ERR_ARG"),
+    ((16, 1e4, 2, math.nan, 1, 0, 1), "ERR_ARG"), ((16, 1e4, 3, 2, 0, 1, 2), "ERR_ARG"),
+    ((16, 1e4, 3, 2, 8, 2, 2), "ERR_ARG"), ((16, 1e4, 3, 2, 8, -1, 2), "ERR_ARG"),
+    ((16, 1e4, 3, 2, 8, 1, math.inf), "ERR_ARG")])
+def test_turns_refusals(q, args, status):
+    out = (C.c_double * 512)()
+    rot, base, rule, *rest = args
+    assert q.lib().qlin_rope_turns(rot, base, rule, *map(float, rest), out) == getattr(q, status)
+    assert q.lib().qlin_rope_turns(16, 1e4, 0, 1.0, 1.0, 0.0, 1.0, None) == q.ERR_ARG
+
+
+def rope_call(q, x=A, ldx=128, T=4, H=2, D=64, pos=A, pl="", inverse=0, y=2 * A, ldy=128):
+    pl = plan(q) if pl == "" else pl
+    return q.lib().qlin_rope(p(x), ldx, T, H, D, p(pos), pl, inverse, p(y), ldy, None)
+
+
+def test_rope_refusals(q):
+    assert rope_call(q, T=0) == q.OK
+    assert rope_call(q, H=0) == q.OK
+    for bad in (dict(T=-1), dict(H=-1), dict(D=56), dict(D=0), dict(D=1040, ldx=4096, ldy=4096), dict(ldx=120),
+                dict(ldy=120), dict(y=A, ldy=136), dict(T=1 << 31), dict(pl=plan(q, rot=72)),
+                dict(pl=plan(q, rot=80)), dict(pl=plan(q, rot=0)), dict(H=1 << 16, ldx=1 << 23, ldy=1 << 23)):
+        assert rope_call(q, **bad) == q.ERR_SHAPE, bad
+    for bad in (dict(x=None), dict(y=None), dict(pos=None), dict(pl=None), dict(pl=plan(q, turns=None)),
+                dict(pl=plan(q, magnitude=math.nan))):
+        assert rope_call(q, **bad) == q.ERR_ARG, bad
+    for bad in (dict(x=A + 2), dict(y=A + 8), dict(pos=A + 2), dict(ldx=132), dict(ldy=132),
+                dict(pl=plan(q, turns=A + 4))):
+        assert rope_call(q, **bad) == q.ERR_ALIGN, bad
+
+
+def append_call(q, c=None, b=None, T=4, k=A, ldk=128, v=A, ldv=128, pl=None, pos=None, qq=None, ldq=0, heads=0,
+                out=None, ldo=0):
+    return q.lib().qlin_kv_append(cache(q) if c is None else c, batch(q) if b is None else b, T, p(k), ldk, p(v),
+                                  ldv, pl, p(pos), p(qq), ldq, heads, p(out), ldo, None)
+
+
+BAD_CACHE = [(dict(head_dim=96), "ERR_SHAPE"), (dict(head_dim=512), "ERR_SHAPE"), (dict(page_size=8), "ERR_SHAPE"),
+             (dict(page_size=48), "ERR_SHAPE"), (dict(page_size=512), "ERR_SHAPE"), (dict(pages=0), "ERR_SHAPE"),
+             (dict(pages=1 << 31), "ERR_SHAPE"), (dict(kv_heads=0), "ERR_SHAPE"), (dict(fmt=2), "ERR_ARG"),
+             (dict(k=None), "ERR_ARG"), (dict(v=None), "ERR_ARG"), (dict(k_scale=A), "ERR_ARG"),
+             (dict(fmt=1), "ERR_ARG"), (dict(fmt=1, k_scale=A), "ERR_ARG"), (dict(k=A + 8), "ERR_ALIGN"),
+             (dict(fmt=1, k_scale=A, v_scale=A + 2), "ERR_ALIGN")]
+BAD_BATCH = [(dict(batch=-1), "ERR_SHAPE"), (dict(table_cols=0), "ERR_SHAPE"), (dict(max_q=0), "ERR_SHAPE"),
+             (dict(table_cols=1 << 28), "ERR_SHAPE"), (dict(batch=1 << 16), "ERR_SHAPE"), (dict(q_start=None), "ERR_ARG"),
+             (dict(kv_len=None), "ERR_ARG"), (dict(page_table=None), "ERR_ARG"), (dict(kv_len=A + 2), "ERR_ALIGN")]
+
+
+def test_append_refusals(q):
+    assert append_call(q, T=0) == q.OK
+    assert append_call(q, b=batch(q, batch=0)) == q.OK
+    for over, status in BAD_CACHE:
+        assert append_call(q, c=cache(q, **over)) == getattr(q, status), over
+    for over, status in BAD_BATCH:
+        assert append_call(q, b=batch(q, **over)) == getattr(q, status), over
+    ok_q = dict(qq=A, ldq=256, heads=4, out=2 * A, ldo=256)
+    for over, status in [(dict(T=-1), "ERR_SHAPE"), (dict(ldk=120), "ERR_SHAPE"), (dict(ldv=64), "ERR_SHAPE"),
+                         (dict(ldk=132), "ERR_ALIGN"), (dict(k=None), "ERR_ARG"), (dict(v=None), "ERR_ARG"),
+                         (dict(v=A + 4), "ERR_ALIGN"), (dict(pos=A + 1), "ERR_ALIGN"),
+                         (dict(pl=plan(q, rot=128)), "ERR_SHAPE"), (dict(pl=plan(q, turns=None)), "ERR_ARG"),
+                         (dict(qq=A), "ERR_ARG"), (dict(out=A), "ERR_ARG"), ({**ok_q, "heads": 0}, "ERR_SHAPE"),
+                         ({**ok_q, "ldq": 248}, "ERR_SHAPE"), ({**ok_q, "out": A, "ldo": 264}, "ERR_SHAPE"),
+                         ({**ok_q, "ldo": 260}, "ERR_ALIGN"), ({**ok_q, "qq": A + 2}, "ERR_ALIGN")]:
+        assert append_call(q, **over) == getattr(q, status), over
+
+
+def attn_call(q, c=None, b=None, T=4, qq=A, ldq=256, heads=4, scale=0.1, causal=1, window=0, out=2 * A, ldo=256,
+              lse=None, ws=1 << 20, nb=1 << 40):
+    return q.lib().qlin_attn_paged(cache(q) if c is None else c, batch(q) if b is None else b, T, p(qq), ldq, heads,
+                                   scale, causal, window, p(out), ldo, p(lse), p(ws), nb, None)
+
+
+def test_attn_refusals(q):
+    assert attn_call(q, T=0) == q.OK
+    assert attn_call(q, b=batch(q, batch=0)) == q.OK
+    for over, status in BAD_CACHE:
+        assert attn_call(q, c=cache(q, **over)) == getattr(q, status), over
+    for over, status in BAD_BATCH:
+        assert attn_call(q, b=batch(q, **over)) == getattr(q, status), over
+    for over, status in [(dict(heads=0), "ERR_SHAPE"), (dict(heads=3), "ERR_SHAPE"), (dict(ldq=248), "ERR_SHAPE"),
+                         (dict(ldo=192), "ERR_SHAPE"), (dict(scale=math.nan), "ERR_ARG"),
+                         (dict(scale=math.inf), "ERR_ARG"), (dict(window=-1), "ERR_ARG"),
+                         (dict(window=4, causal=0), "ERR_ARG"), (dict(qq=None), "ERR_ARG"), (dict(out=None), "ERR_ARG"),
+                         (dict(qq=A + 4), "ERR_ALIGN"), (dict(lse=A + 2), "ERR_ALIGN"), (dict(ldq=260), "ERR_ALIGN"),
+                         (dict(T=1 << 30), "ERR_SHAPE")]:
+        assert attn_call(q, **over) == getattr(q, status), over
+
+
+def test_attn_workspace(q):
+    # one sequence, long table: the key axis is split, and the call checks it
+    c, b = cache(q), batch(q, batch=1, table_cols=4096)
+    need = q.lib().qlin_attn_workspace_bytes(c, b, 1, 4)
+    assert need > 0 and need % 256 == 0
+    kw = dict(c=c, b=b, T=1)
+    assert attn_call(q, nb=need - 1, **kw) == q.ERR_WORKSPACE
+    assert attn_call(q, ws=None, nb=need, **kw) == q.ERR_WORKSPACE
+    assert attn_call(q, ws=(1 << 20) + 16, nb=need, **kw) == q.ERR_ALIGN
+    # a window never needs more than the call without one
+    for cols in (1, 7, 300, 4096):
+        for B, mq in ((1, 1), (3, 2), (1, 700), (40, 1)):
+            bb = batch(q, batch=B, table_cols=cols, max_q=mq)
+            assert q.lib().qlin_attn_workspace_bytes(c, bb, B * mq, 4) >= 0
+    assert q.lib().qlin_attn_workspace_bytes(c, b, 0, 4) == 0
+    assert q.lib().qlin_attn_workspace_bytes(None, b, 1, 4) == 0
+    assert q.lib().qlin_attn_workspace_bytes(c, b, 1, 3) == 0
+
+
+def test_binding_refuses_host_tensors(q):
+    x = torch.zeros(4, 2, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        q.PagedKV(torch.zeros(4, 2, 16, 64, dtype=torch.bfloat16), torch.zeros(4, 2, 16, 64, dtype=torch.bfloat16))
+    with pytest.raises(ValueError):
+        q.PagedBatch(torch.zeros(2, dtype=torch.int32), torch.zeros(1, dtype=torch.int32),
+                     torch.zeros(1, 1, dtype=torch.int32), 1)
+    with pytest.raises(ValueError):
+        q.Rope(64, device="cpu")
+    with pytest.raises(ValueError):
+        q.Rope(64, rot_dim=128)
+    with pytest.raises(q.QlinError):
+        q.Rope(64, rot_dim=24, device="cpu")
+    with pytest.raises(ValueError):
+        q.Rope(64, scaling=("linear",), device="cpu")
+    with pytest.raises(ValueError):
+        q.Rope(64, scaling=("other", 2.0), device="cpu")
+
+    class P:
+        head_dim = 64
+
+    with pytest.raises(ValueError):
+        q.rope(x, torch.zeros(4, dtype=torch.int32), P)
