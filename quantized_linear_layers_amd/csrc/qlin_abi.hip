@@ -465,7 +465,8 @@ static int kv_args(const qlin_kv_cache* c, const qlin_kv_batch* b, int64_t T) {
   QLIN_CHECK(c->fmt == QLIN_KV_BF16 || c->fmt == QLIN_KV_E4M3, QLIN_ERR_ARG);
   QLIN_CHECK((c->head_dim == 64 || c->head_dim == 128 || c->head_dim == 256) && c->page_size >= 16 &&
                  c->page_size <= 256 && (c->page_size & (c->page_size - 1)) == 0 && c->pages >= 1 &&
-                 c->pages <= 0x7FFFFFFF && c->kv_heads >= 1 && c->kv_heads <= 0xFFFF,
+                 c->pages <= 0x7FFFFFFF && c->kv_heads >= 1 && c->kv_heads <= 0xFFFF &&
+                 c->pages * c->kv_heads <= 0x7FFFFFFF,
              QLIN_ERR_SHAPE);
   QLIN_CHECK(T >= 0 && T <= 0x7FFFFFFF && b->batch >= 0 && b->batch <= 0xFFFF && b->max_q >= 0 &&
                  b->table_cols >= 0 && b->table_cols <= (0x7FFFFFFF - 65536) / c->page_size,

@@ -38,6 +38,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 namespace qlin {
 
@@ -61,8 +62,8 @@ struct AttnArgs {
   uint16_t* out;
   float* lse;
   const int32_t *q_start, *kv_len, *table;
-  int64_t ldq, ldo, pages, T, window;
-  int B, cols, page_shift, kv_heads, group, causal, splits;
+  int64_t ldq, ldo, T, window;
+  int B, cols, pages, page_shift, kv_heads, group, causal, splits;
   int tiles;   // row tiles over all sequences, at most (chunk)
   int negate;  // a negative scale: the queries change sign
   float c;     // |scale| * log2(e)
@@ -113,42 +114,67 @@ struct Item {
   int rows;     // packed rows
 };
 
-// A buffer resource over the visible rows of one 16-row group (first key `key`)
-// of a pool with `bytes` a row, and the bytes of the group before them.
-struct Window16 {
-  uint64_t row;  // first visible row in the pool
-  int rows;      // visible rows, 0 if the page does not exist
-  int skip;      // rows of the group before them
+// One 16-row group (first key `key`) of a page: its first row in the pool and
+// how many of its rows lie before `hi` (0 if the page does not exist).
+struct Rows16 {
+  uint64_t row;
+  int rows;
 };
-__device__ __forceinline__ Window16 window_of(const AttnArgs& a, const Item& it, int key, int page, int lo, int hi) {
-  const bool ok = (uint32_t)page < (uint64_t)a.pages;
-  Window16 w;
-  w.skip = min(max(lo - key, 0), 16);
-  w.rows = ok ? max(min(hi - key, 16) - w.skip, 0) : 0;
-  const int in_page = (key & ((1 << a.page_shift) - 1)) + w.skip;
-  w.row = (((uint64_t)(ok ? page : 0) * a.kv_heads + it.h) << a.page_shift) + (w.rows ? in_page : 0);
+__device__ __forceinline__ bool no_page(const AttnArgs& a, int page) { return (uint32_t)page >= (uint32_t)a.pages; }
+__device__ __forceinline__ Rows16 rows_of(const AttnArgs& a, const Item& it, int key, int page, int hi) {
+  const bool none = no_page(a, page);
+  const uint32_t block = (uint32_t)(none ? 0 : page) * (uint32_t)a.kv_heads + (uint32_t)it.h;
+  Rows16 w;
+  w.row = ((uint64_t)block << a.page_shift) + (uint32_t)(key & ((1 << a.page_shift) - 1));
+  w.rows = none ? 0 : max(min(hi - key, 16), 0);
   return w;
 }
-__device__ __forceinline__ v4i resource(const void* pool, const Window16& w, int bytes) {
-  const uint64_t p = (uint64_t)(uintptr_t)pool + w.row * bytes;
+template <int BYTES>
+__device__ __forceinline__ v4i resource(const void* pool, const Rows16& w) {
+  const uint64_t p = (uint64_t)(uintptr_t)pool + w.row * BYTES;
   return v4i{__builtin_amdgcn_readfirstlane((int)(uint32_t)p), __builtin_amdgcn_readfirstlane((int)(uint32_t)(p >> 32)),
-             __builtin_amdgcn_readfirstlane(w.rows * bytes), 0x00020000};
+             __builtin_amdgcn_readfirstlane(w.rows * BYTES), 0x00020000};
 }
 
-// Inline assembly for the same reason as in the prefill GEMMs: the compiler
-// would wait for every load in flight before the next LDS read. The kernels
-// wait themselves (dma_wait) before they read what a load wrote and before
-// they end. What the compiler would see to is written out: the wait state
-// between a write of m0 and the load that uses it, and (settled) the five
+// Direct-to-LDS loads of N * 1 KB: lane i's 16 bytes at off[n] + 1024 n of the
+// resource go to lds + 1024 n + 16 i (an instruction's offset adds to both
+// sides). Inline assembly for the same reason as in the prefill GEMMs: the
+// compiler would wait for every load in flight before the next LDS read. The
+// kernels wait themselves (dma_wait) before they read what a load wrote and
+// before they end. What the compiler would see to is written out: the wait
+// state between a write of m0 and the load that uses it, and (settled) the five
 // between a vector instruction's write of a scalar register and a load's use.
-__device__ __forceinline__ void dma16(uint32_t lds, uint32_t off, const v4i& rs) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(off), "s"(rs)
-               : "memory", "m0");
+// No "memory" clobber: the phase and stage borders have one.
+template <int N>
+__device__ __forceinline__ void dma16(uint32_t lds, const uint32_t (&off)[N], const v4i& rs) {
+  static_assert(N == 1 || N == 2 || N == 4 || N == 8, "");
+  const int m = __builtin_amdgcn_readfirstlane((int)lds);
+  if constexpr (N == 1)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(m), "v"(off[0]), "s"(rs)
+                 : "m0");
+  if constexpr (N == 2)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %3, 0 offen lds\n\t"
+                 "buffer_load_dwordx4 %2, %3, 0 offen offset:1024 lds" ::"s"(m), "v"(off[0]), "v"(off[1]), "s"(rs)
+                 : "m0");
+  if constexpr (N >= 4)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %5, 0 offen lds\n\t"
+                 "buffer_load_dwordx4 %2, %5, 0 offen offset:1*1024 lds\n\t"
+                 "buffer_load_dwordx4 %3, %5, 0 offen offset:2*1024 lds\n\t"
+                 "buffer_load_dwordx4 %4, %5, 0 offen offset:3*1024 lds" ::"s"(m), "v"(off[0]), "v"(off[1]),
+                 "v"(off[2]), "v"(off[3]), "s"(rs)
+                 : "m0");
+  if constexpr (N == 8) {
+    const uint32_t hi[4] = {off[4] + 4096, off[5] + 4096, off[6] + 4096, off[7] + 4096};
+    dma16<4>(lds + 4096, hi, rs);
+  }
 }
 __device__ __forceinline__ void dma4(uint32_t lds, uint32_t off, const v4i& rs) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(lds), "v"(off), "s"(rs)
-               : "memory", "m0");
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(
+                   __builtin_amdgcn_readfirstlane((int)lds)),
+               "v"(off), "s"(rs)
+               : "m0");
 }
+__device__ __forceinline__ void settled(v4i& a) { asm volatile("s_nop 4" : "+s"(a)); }
 __device__ __forceinline__ void settled(v4i& a, v4i& b) { asm volatile("s_nop 4" : "+s"(a), "+s"(b)); }
 template <int N>
 __device__ __forceinline__ void dma_wait() {
@@ -160,47 +186,46 @@ __device__ __forceinline__ uint32_t lds_addr(const void* p) {
   return (uint32_t)(uintptr_t)(const QLIN_LDS uint8_t*)p;
 }
 
-// A tile of TK keys in LDS: K rows, V rows, then for E4M3 the scales (the
-// first 16 of every 64 floats: a load writes all 64 lanes). One wave loads ROWS
-// of them (8 or 16 rows of one 16-row group) from row r0.
+// Loads of a tile of TK keys into LDS: ROWS of its rows (8 or 16 rows of one
+// 16-row group) from row r0 by one wave. Scales (E4M3): the first 16 of every 64
+// floats of a group, because a load writes all 64 lanes. With EDGE, rows of the
+// group before `skip` read as zero too (an offset far beyond the resource); only
+// the first tile of a window has such rows.
 template <int D, bool FP8, int TK, int ROWS>
 struct Stage {
   using G = Geo<D, FP8>;
   static constexpr int kTile = TK * G::kRow;
   static constexpr int kScale = FP8 ? TK / 16 * 256 : 0;  // bytes of one scale area
-  static constexpr int kBytes = 2 * kTile + 2 * kScale;
   static constexpr int kLoads = ROWS / G::kRowsPerLoad;
-  static constexpr int kOps = 2 * kLoads + (FP8 ? 2 : 0);  // loads of one call
   static_assert(kLoads >= 1, "a load must not pass the wave's rows");
 
-  static __device__ __forceinline__ void load(const AttnArgs& a, const Item& it, int key, int r0, int page, int lo,
-                                              int hi, uint32_t lds) {
+  template <bool V, bool EDGE>
+  static __device__ __forceinline__ void rows(const v4i& rs, int skip, int r0, uint32_t lds) {
     const int lane = threadIdx.x & 63;
-    const int g0 = r0 & ~15;
-    const Window16 w = window_of(a, it, key + g0, page, lo, hi);
-    v4i rk = resource(a.k, w, G::kRow), rv = resource(a.v, w, G::kRow);
-    settled(rk, rv);
+    uint32_t off[kLoads];
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
       const int row = r0 + i * G::kRowsPerLoad + lane / G::kChunks;
       const int slot = lane % G::kChunks;
-      // rows before the first visible one fall below the resource: as
-      // unsigned offsets they are far beyond it
-      const uint32_t at = (uint32_t)(((row & 15) - w.skip) * G::kRow);
-      const uint32_t dst = lds + (r0 + i * G::kRowsPerLoad) * G::kRow;
-      dma16(dst, at + 16 * (slot ^ G::k_swz(row)), rk);
-      dma16(dst + kTile, at + 16 * (slot ^ G::v_swz(row)), rv);
+      off[i] = (uint32_t)(((r0 & 15) + lane / G::kChunks) * G::kRow + 16 * (slot ^ (V ? G::v_swz(row) : G::k_swz(row))));
+      if (EDGE && (row & 15) < skip) off[i] = 0x80000000u;
     }
-    if (FP8) {
-      v4i sk = resource(a.ks, w, 4), sv = resource(a.vs, w, 4);
-      settled(sk, sv);
-      const uint32_t at = lane < 16 ? (uint32_t)((lane - w.skip) * 4) : 0xFFFFFFFCu;
-      const uint32_t dst = lds + 2 * kTile + (g0 / 16) * 256;
-      dma4(dst, at, sk);
-      dma4(dst + kScale, at, sv);
-    }
+    dma16<kLoads>(lds + r0 * G::kRow, off, rs);
+  }
+  template <bool EDGE>
+  static __device__ __forceinline__ void scales(const v4i& sk, const v4i& sv, int skip, int r0, uint32_t lds) {
+    const int lane = threadIdx.x & 63;
+    const uint32_t at = lane >= 16 || (EDGE && lane < skip) ? 0x80000000u : (uint32_t)(lane * 4);
+    dma4(lds + (r0 / 16) * 256, at, sk);
+    dma4(lds + kScale + (r0 / 16) * 256, at, sv);
   }
 };
+
+// The larger of the wave's halves' values, in both.
+__device__ __forceinline__ float halves_max(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
 
 // Running softmax state of a wave's 32 rows and their output.
 template <int D>
@@ -215,38 +240,97 @@ struct State {
   }
 };
 
-// KB * 32 keys in LDS against a wave's 32 rows.
+// Operand fragments from LDS. K: 32 keys of block kb, step u (E4M3: both steps of
+// the 16 bytes); V^T: 16 keys of step t, columns 32 d.
+template <int D, bool FP8>
+__device__ __forceinline__ v4i k_frag(const uint8_t* lds_k, int kb, int u) {
+  using G = Geo<D, FP8>;
+  const int lane = threadIdx.x & 63;
+  const int row = 32 * kb + (lane & 31);
+  return *reinterpret_cast<const v4i*>(lds_k + row * G::kRow + 16 * ((2 * u + (lane >> 5)) ^ G::k_swz(row)));
+}
+template <int D, bool FP8>
+__device__ __forceinline__ v4i v_frag(const uint8_t* lds_v, int t, int d) {
+  using G = Geo<D, FP8>;
+  const int lane = threadIdx.x & 63;
+  const int key0 = 16 * t + 4 * (lane >> 5);
+  if (FP8) {
+    const int i = (lane & 15) >> 1;
+    const int row = key0 + (i & 3) + 8 * (i >> 2);
+    const int chunk = 2 * d + ((lane >> 4) & 1);
+    const v2i x = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
+        (QLIN_LDS v2i*)(lds_v + row * G::kRow + 16 * (chunk ^ G::v_swz(row)) + 8 * (lane & 1)));
+    return v4i{x[0], x[1], 0, 0};
+  }
+  const int row = key0 + ((lane & 15) >> 2);
+  const int chunk = 4 * d + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
+  const v4s x = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+      (QLIN_LDS v4s*)(lds_v + row * G::kRow + 16 * (chunk ^ G::v_swz(row)) + 8 * (lane & 1)));
+  const v4s y = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+      (QLIN_LDS v4s*)(lds_v + (row + 8) * G::kRow + 16 * (chunk ^ G::v_swz(row + 8)) + 8 * (lane & 1)));
+  return __builtin_bit_cast(v4i, (v8s){x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]});
+}
+__device__ __forceinline__ v8bf as_bf16(const v4i& x) { return __builtin_bit_cast(v8bf, x); }
+
+// The products of KB * 32 keys with a wave's 32 rows: with PV, O^T += V^T P^T of
+// the weights p over lds_v; with QK, the scores S^T of lds_k.
+template <int D, bool FP8, int KB, bool PV, bool QK>
+__device__ __forceinline__ void multiply(const v8bf (&q)[D / 16], State<D>& st, v16f (&s)[KB], const v4i (&p)[2 * KB],
+                                         const uint8_t* lds_v, const uint8_t* lds_k) {
+  if (PV) {
+#pragma unroll
+    for (int t = 0; t < 2 * KB; ++t)
+#pragma unroll
+      for (int d = 0; d < D / 32; ++d) {
+        const v4i x = v_frag<D, FP8>(lds_v, t, d);
+        st.o[d] = mfma32(FP8 ? cvt_fp8x8(x[0], x[1]) : as_bf16(x), as_bf16(p[t]), st.o[d]);
+      }
+  }
+  if (QK) {
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb) s[kb] = v16f{};
+#pragma unroll
+    for (int u = 0; u < (FP8 ? D / 32 : D / 16); ++u)
+#pragma unroll
+      for (int kb = 0; kb < KB; ++kb) {
+        const v4i x = k_frag<D, FP8>(lds_k, kb, u);
+        if (FP8) {
+          s[kb] = mfma32(cvt_fp8x8(x[0], x[1]), q[2 * u], s[kb]);
+          s[kb] = mfma32(cvt_fp8x8(x[2], x[3]), q[2 * u + 1], s[kb]);
+        } else {
+          s[kb] = mfma32(as_bf16(x), q[u], s[kb]);
+        }
+      }
+  }
+  if (!FP8) {
+    // Order of the block's LDS reads and products: AHEAD reads first, then each
+    // product followed by the reads that keep AHEAD of them under way (an LDS
+    // read takes about as long as 4 products).
+    constexpr int kAhead = 8;
+    constexpr int nv = PV ? 2 * KB * (D / 32) : 0, nk = QK ? KB * (D / 16) : 0;
+    constexpr int reads = 2 * nv + nk;
+    __builtin_amdgcn_sched_group_barrier(0x100, kAhead, 0);
+    int left = reads - kAhead;
+#pragma unroll
+    for (int i = 0; i < nv + nk; ++i) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      const int n = left <= 0 ? 0 : (i < nv ? (left < 2 ? left : 2) : 1);
+      if (n == 2) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+      if (n == 1) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+      left -= n;
+    }
+  }
+}
+
+// The weights of a score block, rounded to bf16, and the running maximum and
+// sum (and with a raised maximum O) that go with them.
 //   vis_lo, vis_hi: keys that this lane's row sees, relative to the first
 //   masked: whether some row sees only part of them; bad: bit g = the 16-row
 //   group g lies in no page
 template <int D, bool FP8, int KB, int SCALE>
-__device__ __forceinline__ void attend_block(const AttnArgs& a, const v8bf (&q)[D / 16], State<D>& st,
-                                             const uint8_t* lds_k, const uint8_t* lds_v, const uint8_t* lds_s,
-                                             bool masked, int vis_lo, int vis_hi, uint32_t bad) {
-  using G = Geo<D, FP8>;
-  const int lane = threadIdx.x & 63;
-  const int r = lane & 31, h = lane >> 5;
-  v16f s[KB];
-#pragma unroll
-  for (int kb = 0; kb < KB; ++kb) {
-    const int row = 32 * kb + r;
-    const uint8_t* base = lds_k + row * G::kRow;
-    const int sw = G::k_swz(row);
-    v16f acc = {};
-    if (FP8) {
-#pragma unroll
-      for (int u = 0; u < D / 32; ++u) {
-        const v4i x = *reinterpret_cast<const v4i*>(base + 16 * ((2 * u + h) ^ sw));
-        acc = mfma32(cvt_fp8x8(x[0], x[1]), q[2 * u], acc);
-        acc = mfma32(cvt_fp8x8(x[2], x[3]), q[2 * u + 1], acc);
-      }
-    } else {
-#pragma unroll
-      for (int u = 0; u < D / 16; ++u)
-        acc = mfma32(*reinterpret_cast<const v8bf*>(base + 16 * ((2 * u + h) ^ sw)), q[u], acc);
-    }
-    s[kb] = acc;
-  }
+__device__ __forceinline__ void weight_block(const AttnArgs& a, State<D>& st, v16f (&s)[KB], v4i (&p)[2 * KB],
+                                             const uint8_t* lds_s, bool masked, int vis_lo, int vis_hi, uint32_t bad) {
+  const int h = (threadIdx.x & 63) >> 5;
   if (FP8) {
 #pragma unroll
     for (int kb = 0; kb < KB; ++kb)
@@ -258,12 +342,13 @@ __device__ __forceinline__ void attend_block(const AttnArgs& a, const v8bf (&q)[
       }
   }
   if (masked) {
+    const int lo = vis_lo - 4 * h, hi = vis_hi - 4 * h;
 #pragma unroll
     for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        const int key = 32 * kb + 8 * (i / 4) + 4 * h + i % 4;
-        const bool see = key >= vis_lo && key < vis_hi && !((bad >> (2 * kb + i / 8)) & 1);
+        const int key = 32 * kb + 8 * (i / 4) + i % 4;
+        const bool see = lo <= key && hi > key && !((bad >> (2 * kb + i / 8)) & 1);
         s[kb][i] = see ? s[kb][i] : -kInf;
       }
   }
@@ -272,7 +357,7 @@ __device__ __forceinline__ void attend_block(const AttnArgs& a, const v8bf (&q)[
   for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
     for (int i = 0; i < 16; ++i) mx = fmaxf(mx, s[kb][i]);
-  mx = fmaxf(mx, __shfl_xor(mx, 32, kWave)) * a.c;
+  mx = halves_max(mx) * a.c;
   if (__any(mx > st.m + 8.0f)) {
     const float m = fmaxf(st.m, mx);
     const float f = m == -kInf ? 0.0f : exp2_hw(st.m - m);
@@ -302,39 +387,12 @@ __device__ __forceinline__ void attend_block(const AttnArgs& a, const v8bf (&q)[
         for (int i = 0; i < 4; ++i) s[kb][4 * b + i] *= v[i];
       }
   }
+  // P rounded to bf16 for the product (at most 2^-8 of a weight; the sum l
+  // keeps the unrounded weights)
 #pragma unroll
   for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      // P rounded to bf16 for the product (at most 2^-8 of a weight; the sum l
-      // keeps the unrounded weights)
-      v4i pk;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) pk[i] = (int)pack_bf16x2(s[kb][8 * t + 2 * i], s[kb][8 * t + 2 * i + 1]);
-      const v8bf p = __builtin_bit_cast(v8bf, pk);
-      const int key0 = 32 * kb + 16 * t + 4 * h;
-#pragma unroll
-      for (int d = 0; d < D / 32; ++d) {
-        v8bf vt;
-        if (FP8) {
-          const int i = (lane & 15) >> 1;
-          const int row = key0 + (i & 3) + 8 * (i >> 2);
-          const int chunk = 2 * d + ((lane >> 4) & 1);
-          const v2i x = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
-              (QLIN_LDS v2i*)(lds_v + row * G::kRow + 16 * (chunk ^ G::v_swz(row)) + 8 * (lane & 1)));
-          vt = cvt_fp8x8(x[0], x[1]);
-        } else {
-          const int row = key0 + ((lane & 15) >> 2);
-          const int chunk = 4 * d + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
-          const v4s x = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-              (QLIN_LDS v4s*)(lds_v + row * G::kRow + 16 * (chunk ^ G::v_swz(row)) + 8 * (lane & 1)));
-          const v4s y = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-              (QLIN_LDS v4s*)(lds_v + (row + 8) * G::kRow + 16 * (chunk ^ G::v_swz(row + 8)) + 8 * (lane & 1)));
-          vt = __builtin_bit_cast(v8bf, (v8s){x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]});
-        }
-        st.o[d] = mfma32(vt, p, st.o[d]);
-      }
-    }
+    for (int i = 0; i < 8; ++i) p[2 * kb + i / 4][i % 4] = (int)pack_bf16x2(s[kb][2 * i], s[kb][2 * i + 1]);
 }
 
 // The wave's query fragments: one row a lane, values in the order of the K
@@ -380,6 +438,10 @@ __device__ __forceinline__ Range range_of(const AttnArgs& a, const Item& it, int
   r.hi = max(row_hi(a, it, row1 - 1), 0);
   r.all_lo = row_lo(a, it, row1 - 1);
   r.all_hi = row_hi(a, it, row0);
+  r.lo = __builtin_amdgcn_readfirstlane(r.lo);
+  r.hi = __builtin_amdgcn_readfirstlane(r.hi);
+  r.all_lo = __builtin_amdgcn_readfirstlane(r.all_lo);
+  r.all_hi = __builtin_amdgcn_readfirstlane(r.all_hi);
   return r;
 }
 
@@ -442,15 +504,26 @@ __device__ __forceinline__ void store_row(const AttnArgs& a, const Item& it, int
 }
 
 // ---------------------------------------------------------------- chunk
-// A workgroup of NW waves has NW * 32 rows of one (sequence, key/value head)
-// and walks their keys in tiles of TK, double buffered: while a tile is
-// multiplied, the loads of the next one are in flight; one barrier a tile.
-template <int D, bool FP8, int NW, int TK>
-__global__ __launch_bounds__(NW * 64, 2) void attn_chunk_kernel(const AttnArgs a) {
-  using St = Stage<D, FP8, TK, TK / NW>;
-  constexpr int BM = NW * 32;
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * St::kBytes];
-  __shared__ int bad_rows[2][TK / 16];  // 16-row groups of a tile that lie in no page
+// A workgroup of 8 waves has 256 rows of one (sequence, key/value head), 32 a
+// wave, and walks their keys in tiles of TK that all waves share. A tile costs a
+// wave about as many matrix cycles (scores and values) as vector cycles
+// (weights), so the two waves of a SIMD, w and w + 4, work in opposite phases:
+// while one multiplies (values of tile t - 1, scores of tile t), the other takes
+// the weights of its tile; a barrier ends each phase.
+//   phase   waves 0-3                     waves 4-7
+//   2t      PV(t-1), QK(t); loads         weights(t-1)
+//   2t+1    weights(t)                    PV(t-1), QK(t)
+// K(t) and V(t-1) are free after phase 2t+1. K and V have three places each: in
+// phase 2t waves 0-3 issue the loads of K(t+2) and V(t+1) into those of K(t-1)
+// and V(t-2), and by the end of phase 2t+1 have waited for the ones of a tile
+// before. Scales come with K and are read in the weight phases, the last of them
+// 2t+2: four places.
+template <int D, bool FP8, int TK>
+__global__ __launch_bounds__(512, 2) void attn_chunk_kernel(const AttnArgs a) {
+  using St = Stage<D, FP8, TK, TK / 4>;
+  constexpr int BM = 256, KB = TK / 32;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds_k[3][St::kTile], lds_v[3][St::kTile];
+  __shared__ __attribute__((aligned(1024))) uint8_t lds_s[4][FP8 ? 2 * St::kScale : 16];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 
@@ -500,7 +573,7 @@ __global__ __launch_bounds__(NW * 64, 2) void attn_chunk_kernel(const AttnArgs a
   st.clear();
 
   const Range wg = range_of(a, it, row0, min(row0 + BM, it.rows));
-  const Range own = range_of(a, it, w0, min(w0 + 32, it.rows));
+  const Range own = range_of(a, it, w0, max(min(w0 + 32, it.rows), w0 + 1));
   const int vlo = row_lo(a, it, row), vhi = row_hi(a, it, row);
   int t0 = wg.lo / TK, t1 = (wg.hi + TK - 1) / TK;
   if (a.splits > 1) {
@@ -508,33 +581,103 @@ __global__ __launch_bounds__(NW * 64, 2) void attn_chunk_kernel(const AttnArgs a
     t0 = min(t0 + split * n, t1);
     t1 = min(t0 + n, t1);
   }
-  const int r0 = wave * (TK / NW);  // the rows of a tile that this wave loads
-  int page = page_of(a, it, t0 * TK + r0);
-  auto issue = [&](int t, int buf, int pg) {
-    if ((r0 & 15) == 0 && lane == 0) bad_rows[buf][r0 / 16] = (uint32_t)pg >= (uint64_t)a.pages;
-    St::load(a, it, t * TK, r0, pg, wg.lo, wg.hi, lds_addr(lds) + buf * St::kBytes);
+  t0 = __builtin_amdgcn_readfirstlane(t0);
+  t1 = __builtin_amdgcn_readfirstlane(t1);
+  // whether some page of these keys does not exist
+  bool hole = false;
+  const int c1 = t0 < t1 ? (t1 * TK - 1) >> a.page_shift : -1;
+  for (int c = ((t0 * TK) >> a.page_shift) + (int)threadIdx.x; c <= min(c1, a.cols - 1); c += 512)
+    hole |= no_page(a, a.table[(int64_t)it.b * a.cols + c]);
+  const bool holes = __syncthreads_or(hole);
+
+  const bool first = wave < 4;
+  const int r0 = (wave & 3) * (TK / 4);  // the rows of a tile that this wave loads
+  const int g0 = r0 & ~15;
+  auto page_at = [&](int t) { return page_of(a, it, t * TK + g0); };
+  auto load_k = [&](int t, int page, int place, auto edge) {
+    const Rows16 w = rows_of(a, it, t * TK + g0, page, wg.hi);
+    const int skip = wg.lo - t * TK - g0;
+    v4i rk = resource<St::G::kRow>(a.k, w);
+    settled(rk);
+    St::template rows<false, edge>(rk, skip, r0, lds_addr(lds_k[place]));
+    if constexpr (FP8) {
+      v4i sk = resource<4>(a.ks, w), sv = resource<4>(a.vs, w);
+      settled(sk, sv);
+      St::template scales<edge>(sk, sv, skip, g0, lds_addr(lds_s[t & 3]));
+    }
   };
-  if (t0 < t1) issue(t0, 0, page);
-  page = page_of(a, it, (t0 + 1) * TK + r0);
-  for (int t = t0; t < t1; ++t) {
-    const int buf = (t - t0) & 1;
-    dma_wait<0>();
-    __syncthreads();
-    if (t + 1 < t1) issue(t + 1, buf ^ 1, page);
-    page = page_of(a, it, (t + 2) * TK + r0);
-    const int key = t * TK;
-    // nothing of this tile is seen by the wave's rows: past their diagonal,
-    // before their windows, or rows past the end
-    if (w0 >= it.rows || key >= own.hi || key + TK <= own.lo) continue;
-    uint32_t bad = 0;
-#pragma unroll
-    for (int g = 0; g < TK / 16; ++g) bad |= (uint32_t)(bad_rows[buf][g] != 0) << g;
-    bad = __builtin_amdgcn_readfirstlane(bad);
-    const bool masked = bad != 0 || key + TK > own.all_hi || key < own.all_lo;
-    const uint8_t* s = lds + buf * St::kBytes;
-    attend_block<D, FP8, TK / 32, St::kScale>(a, q, st, s, s + St::kTile, s + 2 * St::kTile, masked, vlo - key,
-                                              vhi - key, bad);
+  auto load_v = [&](int t, int page, int place, auto edge) {
+    const Rows16 w = rows_of(a, it, t * TK + g0, page, wg.hi);
+    v4i rv = resource<St::G::kRow>(a.v, w);
+    settled(rv);
+    St::template rows<true, edge>(rv, wg.lo - t * TK - g0, r0, lds_addr(lds_v[place]));
+  };
+  constexpr std::integral_constant<bool, true> kEdge;
+  constexpr std::integral_constant<bool, false> kInner;
+  constexpr int kOps = 2 * St::kLoads + (FP8 ? 2 : 0);  // loads of an iteration
+  // the end of a phase; no instruction moves from one into another
+  auto phase_end = [&] {
+    __builtin_amdgcn_sched_barrier(0);
+    lds_reads_done();
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+  };
+
+  if (first && t0 < t1) {
+    const int p0 = page_at(t0), p1 = page_at(t0 + 1);
+    load_k(t0, p0, 0, kEdge);
+    load_v(t0, p0, 0, kEdge);
+    if (t0 + 1 < t1) load_k(t0 + 1, p1, 1, kInner);
   }
+  int pv = page_at(t0 + 1), pk = page_at(t0 + 2);  // pages of the next V and K loads
+  int at = 0, next = 1, last = 2;                  // places of tiles t, t + 1 and t + 2 (t - 1)
+  dma_wait<0>();
+  phase_end();
+  if (!first) phase_end();
+  v16f s[KB];
+  v4i p[2 * KB];
+#pragma unroll
+  for (int i = 0; i < 2 * KB; ++i) p[i] = v4i{};
+  // Every wave takes every tile, also one that its rows do not see (past their
+  // diagonal, before their windows, rows past the end): the phases keep the
+  // waves in step, so leaving one out would save nothing.
+  for (int t = t0; t < t1; ++t) {
+    // multiply
+    const bool more = t + 2 < t1;
+    if (first) {
+      // K(t+2) takes K(t-1)'s place, V(t+1) V(t-2)'s
+      if (t + 1 < t1) load_v(t + 1, pv, next, kInner);
+      if (more) load_k(t + 2, pk, last, kInner);
+    }
+    pv = pk;
+    pk = page_at(t + 3);
+    __builtin_amdgcn_s_setprio(1);
+    // (the first tile adds zero weights times its own values)
+    multiply<D, FP8, KB, true, true>(q, st, s, p, lds_v[t > t0 ? last : at], lds_k[at]);
+    __builtin_amdgcn_s_setprio(0);
+    phase_end();
+    // weights
+    const int key = t * TK;
+    uint32_t bad = 0;
+    if (holes)
+      for (int g = 0; g < TK / 16; ++g) bad |= (uint32_t)no_page(a, page_of(a, it, key + 16 * g)) << g;
+    const bool masked = holes || key + TK > own.all_hi || key < own.all_lo;
+    weight_block<D, FP8, KB, St::kScale>(a, st, s, p, lds_s[t & 3], masked, vlo - key, vhi - key, bad);
+    if (first) {
+      if (more)
+        dma_wait<kOps>();
+      else
+        dma_wait<0>();
+    }
+    phase_end();
+    const int x = last;
+    last = at;
+    at = next;
+    next = x;
+  }
+  if (t0 < t1) multiply<D, FP8, KB, true, false>(q, st, s, p, lds_v[last], lds_k[at]);
+  if (first) phase_end();
   store_row<D>(a, it, split, row, st);
 }
 
@@ -545,8 +688,10 @@ __global__ __launch_bounds__(NW * 64, 2) void attn_chunk_kernel(const AttnArgs a
 template <int D, bool FP8, int NW>
 __global__ __launch_bounds__(NW * 64, 1) void attn_step_kernel(const AttnArgs a) {
   using St = Stage<D, FP8, 32, 16>;
+  constexpr int kStage = 2 * St::kTile + 2 * St::kScale;  // K, V, scales
+  constexpr int kOps = 2 * (2 * St::kLoads + (FP8 ? 2 : 0));  // loads of a stage
   constexpr int kOut = D + 4;  // floats of a row in the merge
-  constexpr int kMerge = NW * 32 * kOut * 4, kRing = 2 * NW * St::kBytes;
+  constexpr int kMerge = NW * 32 * kOut * 4, kRing = 2 * NW * kStage;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[kRing > kMerge ? kRing : kMerge];
   __shared__ float wm[NW][32], wl[NW][32];
   const int lane = threadIdx.x & 63;
@@ -564,15 +709,29 @@ __global__ __launch_bounds__(NW * 64, 1) void attn_step_kernel(const AttnArgs a)
     t0 = min(t0 + split * n, t1);
     t1 = min(t0 + n, t1);
   }
-  uint8_t* ring = lds + wave * 2 * St::kBytes;
-  auto issue = [&](int t, int buf, int p0, int p1) {
-    const uint32_t dst = lds_addr(ring) + buf * St::kBytes;
-    St::load(a, it, t * 32, 0, p0, rg.lo, rg.hi, dst);
-    St::load(a, it, t * 32, 16, p1, rg.lo, rg.hi, dst);
+  uint8_t* ring = lds + wave * 2 * kStage;
+  auto issue = [&](int t, int buf, int p0, int p1, auto edge) {
+    const uint32_t dst = lds_addr(ring) + buf * kStage;
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+      const Rows16 w = rows_of(a, it, t * 32 + 16 * g, g ? p1 : p0, rg.hi);
+      const int skip = rg.lo - t * 32 - 16 * g;
+      v4i rk = resource<St::G::kRow>(a.k, w), rv = resource<St::G::kRow>(a.v, w);
+      settled(rk, rv);
+      St::template rows<false, edge>(rk, skip, 16 * g, dst);
+      St::template rows<true, edge>(rv, skip, 16 * g, dst + St::kTile);
+      if constexpr (FP8) {
+        v4i sk = resource<4>(a.ks, w), sv = resource<4>(a.vs, w);
+        settled(sk, sv);
+        St::template scales<edge>(sk, sv, skip, 16 * g, dst + 2 * St::kTile);
+      }
+    }
   };
+  constexpr std::integral_constant<bool, true> kEdge;
+  constexpr std::integral_constant<bool, false> kInner;
   int t = t0 + wave;
   int p0 = page_of(a, it, t * 32), p1 = page_of(a, it, t * 32 + 16);
-  if (t < t1) issue(t, 0, p0, p1);
+  if (t < t1) issue(t, 0, p0, p1, kEdge);
   v8bf q[D / 16];
   load_q<D, FP8>(a, it, row, q);
   State<D> st;
@@ -582,21 +741,24 @@ __global__ __launch_bounds__(NW * 64, 1) void attn_step_kernel(const AttnArgs a)
   for (; t < t1; t += NW) {
     lds_reads_done();  // the stage that the next loads overwrite has been read
     if (t + NW < t1) {
-      issue(t + NW, buf ^ 1, n0, n1);
-      dma_wait<2 * St::kOps>();
+      issue(t + NW, buf ^ 1, n0, n1, kInner);
+      dma_wait<kOps>();
     } else {
       dma_wait<0>();
     }
-    const uint32_t bad = ((uint32_t)p0 >= (uint64_t)a.pages ? 1u : 0u) | ((uint32_t)p1 >= (uint64_t)a.pages ? 2u : 0u);
+    const uint32_t bad = (no_page(a, p0) ? 1u : 0u) | (no_page(a, p1) ? 2u : 0u);
     p0 = n0;
     p1 = n1;
     n0 = page_of(a, it, (t + 2 * NW) * 32);
     n1 = page_of(a, it, (t + 2 * NW) * 32 + 16);
     const int key = t * 32;
     const bool masked = bad != 0 || key + 32 > rg.all_hi || key < rg.all_lo;
-    const uint8_t* s = ring + buf * St::kBytes;
-    attend_block<D, FP8, 1, St::kScale>(a, q, st, s, s + St::kTile, s + 2 * St::kTile, masked, vlo - key, vhi - key,
-                                        bad);
+    const uint8_t* s = ring + buf * kStage;
+    v16f sc[1];
+    v4i w[2];
+    multiply<D, FP8, 1, false, true>(q, st, sc, w, s + St::kTile, s);
+    weight_block<D, FP8, 1, St::kScale>(a, st, sc, w, s + 2 * St::kTile, masked, vlo - key, vhi - key, bad);
+    multiply<D, FP8, 1, true, false>(q, st, sc, w, s + St::kTile, s);
     buf ^= 1;
   }
   // merge: every wave's rows on the common maximum, then summed over the waves
@@ -700,7 +862,7 @@ struct Plan {
   int64_t tiles;
 };
 
-constexpr int kChunkRows = 128;
+constexpr int kChunkRows = 256;
 constexpr int kCus = 256;
 
 Plan plan_of(const qlin_kv_cache& cache, const qlin_kv_batch& batch, int64_t T, int64_t q_heads, int64_t window) {
@@ -728,7 +890,7 @@ void launch_parts(const AttnArgs& a, const Plan& p, hipStream_t st) {
     attn_step_kernel<D, FP8, NW><<<dim3(p.splits, a.kv_heads, a.B), NW * 64, 0, st>>>(a);
   } else {
     const int64_t items = p.tiles * a.kv_heads * p.splits;
-    attn_chunk_kernel<D, FP8, 4, D == 256 ? 32 : 64><<<(unsigned)((items + 7) / 8 * 8), 256, 0, st>>>(a);
+    attn_chunk_kernel<D, FP8, D == 256 ? 32 : 64><<<(unsigned)((items + 7) / 8 * 8), 512, 0, st>>>(a);
   }
   if (p.splits > 1) {
     const int64_t rows = a.T * a.kv_heads * a.group;
@@ -762,7 +924,7 @@ int launch_attn(const qlin_kv_cache& cache, const qlin_kv_batch& batch, int64_t 
   a.table = batch.page_table;
   a.ldq = ldq;
   a.ldo = ldo;
-  a.pages = cache.pages;
+  a.pages = (int)cache.pages;
   a.T = T;
   a.window = window;
   a.B = (int)batch.batch;
