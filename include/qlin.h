@@ -469,8 +469,11 @@ int qlin_kv_append(const qlin_kv_cache* cache, const qlin_kv_batch* batch, int64
  * outside every page that it uses never reach its result, NaN included.
  *   q, out [T][ldq], [T][ldo] bf16 (ld >= q_heads * head_dim, multiples of 8);
  *   lse [T][q_heads] fp32 or NULL; scale finite.
- * Workspace: qlin_attn_workspace_bytes bytes, 256-byte aligned, no zeroing
- * (0 when the key axis is not split); calls that overlap need one each. */
+ * Workspace: qlin_attn_workspace_bytes bytes, 256-byte aligned (0 when the key
+ * axis is not split). As the GEMMs', it starts with 64 KiB of arrival counters
+ * that must be zero before the first call that uses it (qlin_workspace_init);
+ * every call leaves them zero, so one workspace serves GEMMs and attention in
+ * turn. Calls that share one must be ordered on one stream. */
 size_t qlin_attn_workspace_bytes(const qlin_kv_cache* cache, const qlin_kv_batch* batch, int64_t T,
                                  int64_t q_heads);
 int qlin_attn_paged(const qlin_kv_cache* cache, const qlin_kv_batch* batch, int64_t T,

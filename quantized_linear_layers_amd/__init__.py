@@ -528,39 +528,70 @@ def moe_w4a16(x, topk_ids, topk_w, codes13, steps13, codes2, steps2, return_stag
 
 
 # ---------------------------------------------------------------- attention
-def _heads_arg(t, name, head_dim=None, heads=None):
-    """A bf16 tensor [T, heads, head_dim] whose heads lie together; its rows may
-    be further apart (a slice of a fused QKV projection)."""
+# torch's own raw-stream query, where it has one: a Stream object costs more
+# host time than a small launch
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _rows_arg(t, name, dev, head_dim, heads=None):
+    """(rows, heads, row stride) of a bf16 tensor [T, heads, head_dim] on `dev` whose
+    heads lie together; its rows may be further apart (a slice of a fused QKV
+    projection)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a device tensor")
-    if t.dtype != torch.bfloat16:
+    if t.device != dev:
+        raise ValueError(f"{name} must be a tensor on {dev}, got {t.device}")
+    if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
     if t.dim() != 3:
         raise ValueError(f"{name} must have 3 dims, got {tuple(t.shape)}")
     T, H, D = t.shape
-    if (head_dim is not None and D != head_dim) or (heads is not None and H != heads):
-        raise ValueError(f"{name}: expected {heads or 'any'} heads of {head_dim}, got {H} of {D}")
-    if (D > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != D):
+    if D != head_dim or (heads is not None and H != heads):
+        raise ValueError(f"{name}: expected {'any' if heads is None else heads} heads of {head_dim}, got {H} of {D}")
+    s0, s1, s2 = t.stride()
+    if s2 != 1 or (s1 != D and H > 1):
         raise ValueError(f"{name}: the heads of a row must lie together")
-    # the stride of a single row says nothing
-    return T, H, D, t.stride(0) if T > 1 else max(H * D, t.stride(0)) // 8 * 8 if T else H * D
+    return T, H, s0 if T > 1 else H * D  # (the stride of a single row says nothing)
 
 
-def _same_device(dev, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, expected {dev}")
+def _positions_arg(t, dev, T):
+    _check(t, "positions", torch.int32, 1)
+    if t.device != dev or t.numel() != T:
+        raise ValueError(f"positions must be [T] on {dev}")
+    return t.data_ptr()
+
+
+def _on(dev, want, name):
+    if dev != want:
+        raise ValueError(f"{name} is on {dev}, expected {want}")
 
 
 def _call_on(dev: torch.device, name: str, *args):
     """A library call on `dev`'s current stream, with `dev` the current device."""
     if dev.index == torch.cuda.current_device():
-        _call(name, *args, _stream(dev))
+        st = getattr(_lib, name)(*args, _raw_stream(dev.index))
     else:
         with torch.cuda.device(dev):
-            _call(name, *args, _stream(dev))
+            st = getattr(_lib, name)(*args, _raw_stream(dev.index))
+    if st != OK:
+        raise QlinError(name, st)
+
+
+# An attention workspace beyond this is not kept between calls.
+_ATTN_WS_KEEP = 64 << 20
+
+
+def _attn_workspace(nbytes: int, dev: torch.device):
+    """A workspace whose counter area is zero: the stream's own (`workspace`), or
+    one of its own for a call that is being captured (two graphs of one stream
+    may be replayed at once) and for a very large one."""
+    if nbytes <= _ATTN_WS_KEEP and not torch.cuda.is_current_stream_capturing():
+        ws = _ws_cache.get((dev.index, _raw_stream(dev.index)))
+        return ws if ws is not None and ws.numel() >= nbytes else workspace(nbytes, dev)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    ws[:65536].zero_()
+    return ws
 
 
 class Rope:
@@ -592,6 +623,7 @@ class Rope:
             raise ValueError("device must be a GPU")
         self.device = self.turns.device
         self._c = _RopePlan(self.turns.data_ptr(), self.rot_dim, int(self.interleaved), self.magnitude)
+        self._ref = C.byref(self._c)
 
 
 class PagedKV:
@@ -615,7 +647,9 @@ class PagedKV:
         elif k_scale is not None or v_scale is not None:
             raise ValueError("a bfloat16 cache has no scales")
         self.device = k.device
-        _same_device(self.device, v=v, k_scale=k_scale, v_scale=v_scale)
+        for name, t in (("v", v), ("k_scale", k_scale), ("v_scale", v_scale)):
+            if t is not None:
+                _on(t.device, self.device, name)
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.pages, self.kv_heads, self.page_size, self.head_dim = k.shape
         if self.head_dim not in (64, 128, 256):
@@ -628,6 +662,7 @@ class PagedKV:
 
         self._c = _KVCache(addr(k), addr(v), addr(k_scale), addr(v_scale), self.pages, self.kv_heads,
                            self.page_size, self.head_dim, self.fmt)
+        self._ref = C.byref(self._c)
 
     @classmethod
     def empty(cls, pages, kv_heads, head_dim, page_size=64, fmt="bf16", device="cuda"):
@@ -656,29 +691,28 @@ class PagedBatch:
         if q_start.numel() != B + 1 or page_table.shape[0] != B:
             raise ValueError("q_start must be [B+1], kv_len [B] and page_table [B, cols]")
         self.device = q_start.device
-        _same_device(self.device, kv_len=kv_len, page_table=page_table)
+        _on(kv_len.device, self.device, "kv_len")
+        _on(page_table.device, self.device, "page_table")
         self.q_start, self.kv_len, self.page_table, self.max_q = q_start, kv_len, page_table, int(max_q)
         self.batch = B
         self._c = _KVBatch(q_start.data_ptr(), kv_len.data_ptr(), page_table.data_ptr(), B,
                            page_table.shape[1], self.max_q)
+        self._ref = C.byref(self._c)
 
 
 def rope(x, positions, rope: Rope, out=None, inverse=False):
     """Rotary positions of x [T, H, D] (bf16) at positions int32 [T]; `out` may be
     x. inverse=True turns the other way (the gradient of the rotation)."""
-    T, H, D, ldx = _heads_arg(x, "x", rope.head_dim)
-    _check(positions, "positions", torch.int32, 1)
-    if positions.numel() != T:
-        raise ValueError("positions must be [T]")
+    D, dev = rope.head_dim, rope.device
+    T, H, ldx = _rows_arg(x, "x", dev, D)
+    pos = _positions_arg(positions, dev, T)
     if out is None:
-        out = torch.empty((T, H, D), dtype=torch.bfloat16, device=x.device)
-        ldy = H * D
+        out, ldy = x.new_empty((T, H, D)), H * D
     else:
-        T2, _, _, ldy = _heads_arg(out, "out", D, H)
+        T2, _, ldy = _rows_arg(out, "out", dev, D, H)
         if T2 != T:
             raise ValueError("out shape mismatch")
-    _same_device(x.device, positions=positions, rope=rope, out=out)
-    _call_on(x.device, "qlin_rope", _ptr(x), ldx, T, H, D, _ptr(positions), rope._c, int(inverse), _ptr(out), ldy)
+    _call_on(dev, "qlin_rope", x.data_ptr(), ldx, T, H, D, pos, rope._ref, 1 if inverse else 0, out.data_ptr(), ldy)
     return out
 
 
@@ -688,16 +722,17 @@ def kv_append(cache: PagedKV, batch: PagedBatch, k, v, rope: Rope | None = None,
     cache. With q [T, q_heads, D] also turns the queries: returned, or written to
     q_out (which may be q). positions int32 [T] replaces each token's place in
     its sequence as what the rotation uses."""
-    T, _, D, ldk = _heads_arg(k, "k", cache.head_dim, cache.kv_heads)
-    T2, _, _, ldv = _heads_arg(v, "v", cache.head_dim, cache.kv_heads)
-    ldq, ldqo, heads = 0, 0, 0
+    D, dev = cache.head_dim, cache.device
+    _on(batch.device, dev, "batch")
+    T, _, ldk = _rows_arg(k, "k", dev, D, cache.kv_heads)
+    T2, _, ldv = _rows_arg(v, "v", dev, D, cache.kv_heads)
+    ldq = ldqo = heads = 0
     if q is not None:
-        T3, heads, _, ldq = _heads_arg(q, "q", D)
+        T3, heads, ldq = _rows_arg(q, "q", dev, D)
         if q_out is None:
-            q_out = torch.empty((T3, heads, D), dtype=torch.bfloat16, device=q.device)
-            ldqo = heads * D
+            q_out, ldqo = q.new_empty((T3, heads, D)), heads * D
         else:
-            T4, _, _, ldqo = _heads_arg(q_out, "q_out", D, heads)
+            T4, _, ldqo = _rows_arg(q_out, "q_out", dev, D, heads)
             T3 = T3 if T4 == T3 else -1
     else:
         if q_out is not None:
@@ -705,15 +740,13 @@ def kv_append(cache: PagedKV, batch: PagedBatch, k, v, rope: Rope | None = None,
         T3 = T
     if T2 != T or T3 != T:
         raise ValueError("k, v, q and q_out must have the same number of rows")
-    if rope is not None and rope.head_dim != D:
-        raise ValueError("rope and cache differ in head_dim")
-    if positions is not None:
-        _check(positions, "positions", torch.int32, 1)
-        if positions.numel() != T:
-            raise ValueError("positions must be [T]")
-    _same_device(cache.device, batch=batch, k=k, v=v, rope=rope, q=q, q_out=q_out, positions=positions)
-    _call_on(cache.device, "qlin_kv_append", cache._c, batch._c, T, _ptr(k), ldk, _ptr(v), ldv,
-             None if rope is None else rope._c, _ptr(positions), _ptr(q), ldq, heads, _ptr(q_out), ldqo)
+    if rope is not None:
+        _on(rope.device, dev, "rope")
+        if rope.head_dim != D:
+            raise ValueError("rope and cache differ in head_dim")
+    _call_on(dev, "qlin_kv_append", cache._ref, batch._ref, T, k.data_ptr(), ldk, v.data_ptr(), ldv,
+             None if rope is None else rope._ref, None if positions is None else _positions_arg(positions, dev, T),
+             None if q is None else q.data_ptr(), ldq, heads, None if q is None else q_out.data_ptr(), ldqo)
     return q_out
 
 
@@ -725,21 +758,19 @@ def attn_paged(cache: PagedKV, batch: PagedBatch, q, scale=None, causal=True, wi
     defaults to D ** -0.5; window > 0 limits each token to its last `window` keys.
     Rows of q outside every sequence are left as they are in `out` (undefined
     in a new one)."""
-    T, heads, D, ldq = _heads_arg(q, "q", cache.head_dim)
+    D, dev = cache.head_dim, cache.device
+    _on(batch.device, dev, "batch")
+    T, heads, ldq = _rows_arg(q, "q", dev, D)
     if out is None:
-        out = torch.empty((T, heads, D), dtype=torch.bfloat16, device=q.device)
-        ldo = heads * D
+        out, ldo = q.new_empty((T, heads, D)), heads * D
     else:
-        T2, _, _, ldo = _heads_arg(out, "out", D, heads)
+        T2, _, ldo = _rows_arg(out, "out", dev, D, heads)
         if T2 != T:
             raise ValueError("out shape mismatch")
-    _same_device(cache.device, batch=batch, q=q, out=out)
-    lse = torch.empty((T, heads), dtype=torch.float32, device=q.device) if return_lse else None
-    nb = _lib.qlin_attn_workspace_bytes(cache._c, batch._c, T, heads)
-    # torch's own allocation orders reuse by stream and keeps a captured
-    # graph's workspace its own
-    ws = torch.empty(nb, dtype=torch.uint8, device=q.device) if nb else None
-    _call_on(cache.device, "qlin_attn_paged", cache._c, batch._c, T, _ptr(q), ldq, heads,
-             D ** -0.5 if scale is None else float(scale), int(causal), int(window), _ptr(out), ldo, _ptr(lse),
-             _ptr(ws), nb)
+    lse = q.new_empty((T, heads), dtype=torch.float32) if return_lse else None
+    nb = _lib.qlin_attn_workspace_bytes(cache._ref, batch._ref, T, heads)
+    ws = _attn_workspace(nb, dev) if nb else None
+    _call_on(dev, "qlin_attn_paged", cache._ref, batch._ref, T, q.data_ptr(), ldq, heads,
+             D ** -0.5 if scale is None else float(scale), 1 if causal else 0, int(window), out.data_ptr(), ldo,
+             None if lse is None else lse.data_ptr(), None if ws is None else ws.data_ptr(), nb)
     return (out, lse) if return_lse else out

@@ -32,7 +32,8 @@
 // where each wave takes its own key tiles and the waves merge at the end, and
 // attn_chunk_kernel, where each wave has its own rows and the workgroup shares the
 // tiles. Either splits the key axis over workgroups when the rows alone do not
-// fill the device; attn_join_kernel then joins the parts.
+// fill the device; the parts are joined by the last workgroup to arrive (step) or
+// by attn_join_kernel (chunk, whose parts are many rows).
 #include "qlin_internal.h"
 #include "qlin_device.h"
 
@@ -67,8 +68,12 @@ struct AttnArgs {
   int tiles;   // row tiles over all sequences, at most (chunk)
   int negate;  // a negative scale: the queries change sign
   float c;     // |scale| * log2(e)
-  float* po;   // [splits][T][q_heads][D], with splits > 1
-  float* pml;  // [splits][T][q_heads][2]: running maximum (log2), sum
+  // with splits > 1, parts of the key axis: unnormalised O rows and their running
+  // maximum (log2) and sum. Chunk: [splits][T][q_heads][D] and [..][2]; step:
+  // [batch * kv_heads][splits][part_rows][D] and [..][2], and arrival counters
+  float *po, *pml;
+  uint32_t* arrived;  // [batch * kv_heads], 0 between calls
+  int part_rows;
 };
 
 __device__ __forceinline__ v16f mfma32(v8bf a, v8bf b, v16f c) {
@@ -685,28 +690,46 @@ __global__ __launch_bounds__(512, 2) void attn_chunk_kernel(const AttnArgs a) {
 // At most 32 rows of a (sequence, key/value head): NW waves with the same rows,
 // each with its own key tiles of 32 (wave, wave + NW, ...) and its own two LDS
 // stages, so the loop has no barrier; the waves' results are merged in LDS.
+// With splits, every workgroup takes the same number of tiles, the longest
+// sequence's share (device data: the batch's longest range over the splits), so a
+// batch of many lengths is cut into equal pieces; the last workgroup of a
+// (sequence, head) to arrive joins its parts, in their order.
 template <int D, bool FP8, int NW>
 __global__ __launch_bounds__(NW * 64, 1) void attn_step_kernel(const AttnArgs a) {
   using St = Stage<D, FP8, 32, 16>;
-  constexpr int kStage = 2 * St::kTile + 2 * St::kScale;  // K, V, scales
+  constexpr int kStage = 2 * St::kTile + 2 * St::kScale;      // K, V, scales
   constexpr int kOps = 2 * (2 * St::kLoads + (FP8 ? 2 : 0));  // loads of a stage
-  constexpr int kOut = D + 4;  // floats of a row in the merge
+  constexpr int kOut = D + 4;                                 // floats of a row in the merge
   constexpr int kMerge = NW * 32 * kOut * 4, kRing = 2 * NW * kStage;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[kRing > kMerge ? kRing : kMerge];
   __shared__ float wm[NW][32], wl[NW][32];
+  __shared__ int last_flag;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int split = blockIdx.x;
   Item it;
   if (!item_of(a, blockIdx.z, blockIdx.y, it)) return;
-  it.rows = min(it.rows, 32);  // max_q promises it
+  it.rows = min(it.rows, a.part_rows);  // max_q promises it
   const int row = lane & 31;
   const Range rg = range_of(a, it, 0, it.rows);
   const int vlo = row_lo(a, it, row), vhi = row_hi(a, it, row);
   int t0 = rg.lo / 32, t1 = (rg.hi + 31) / 32;
+  int parts = 1;
   if (a.splits > 1) {
-    const int n = max((t1 - t0 + a.splits - 1) / a.splits, NW);
-    t0 = min(t0 + split * n, t1);
+    int span = 0;  // the longest range of keys in the batch
+    for (int b = lane; b < a.B; b += 64) {
+      const int n = a.q_start[b + 1] - a.q_start[b];
+      int len = (int)min((int64_t)a.kv_len[b], (int64_t)a.cols << a.page_shift);
+      if (a.window > 0) len = (int)min((int64_t)len, a.window + n);
+      span = max(span, n > 0 ? len : 0);
+    }
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1) span = max(span, __shfl_xor(span, o, kWave));
+    const int tiles = __builtin_amdgcn_readfirstlane(span) / 32 + 2;
+    const int n = (tiles + a.splits * NW - 1) / (a.splits * NW) * NW;
+    parts = max((t1 - t0 + n - 1) / n, 1);
+    if (split >= parts) return;
+    t0 = t0 + split * n;
     t1 = min(t0 + n, t1);
   }
   uint8_t* ring = lds + wave * 2 * kStage;
@@ -786,6 +809,23 @@ __global__ __launch_bounds__(NW * 64, 1) void attn_step_kernel(const AttnArgs a)
   }
   __syncthreads();
   const int64_t heads = (int64_t)a.kv_heads * a.group;
+  auto finish = [&](int r, int c4, const v4f& o, float mm, float ll) {
+    const int64_t tok = it.q0 + r / a.group;
+    const int qh = it.h * a.group + r % a.group;
+    const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
+    *reinterpret_cast<uint2*>(a.out + tok * a.ldo + (int64_t)qh * D + c4) =
+        make_uint2(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv));
+    if (a.lse && c4 == 0) a.lse[tok * heads + qh] = ll == 0.0f ? -kInf : (mm + log2f(ll)) * kLn2;
+  };
+  // Parts and counter move past the XCDs' own L2 caches (sc1, device scope): a
+  // part is visible everywhere once its store has completed, so the wait before
+  // the counter orders them without flushing a cache.
+  constexpr int kSc1 = 16;
+  const int wg = it.b * a.kv_heads + it.h;
+  const __amdgpu_buffer_rsrc_t ro = __builtin_amdgcn_make_buffer_rsrc(
+      a.po + (int64_t)wg * a.splits * a.part_rows * D, (short)0, a.splits * a.part_rows * D * 4, 0x00020000);
+  const __amdgpu_buffer_rsrc_t rm = __builtin_amdgcn_make_buffer_rsrc(
+      a.pml + (int64_t)wg * a.splits * a.part_rows * 2, (short)0, a.splits * a.part_rows * 8, 0x00020000);
   for (int i = threadIdx.x; i < it.rows * (D / 4); i += NW * 64) {
     const int r = i / (D / 4), c4 = i % (D / 4) * 4;
     float mm = -kInf, ll = 0.0f;
@@ -798,22 +838,64 @@ __global__ __launch_bounds__(NW * 64, 1) void attn_step_kernel(const AttnArgs a)
 #pragma unroll
       for (int j = 0; j < 4; ++j) o[j] += x[j];
     }
-    const int64_t tok = it.q0 + r / a.group;
-    const int qh = it.h * a.group + r % a.group;
-    if (a.splits > 1) {
-      const int64_t at = ((int64_t)split * a.T + tok) * heads + qh;
-      if (c4 == 0) {
-        a.pml[2 * at] = mm;
-        a.pml[2 * at + 1] = ll;
-      }
-      *reinterpret_cast<v4f*>(a.po + at * D + c4) = o;
+    if (parts == 1) {
+      finish(r, c4, o, mm, ll);
     } else {
-      const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
-      *reinterpret_cast<uint2*>(a.out + tok * a.ldo + (int64_t)qh * D + c4) =
-          make_uint2(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv));
-      if (a.lse && c4 == 0) a.lse[tok * heads + qh] = ll == 0.0f ? -kInf : (mm + log2f(ll)) * kLn2;
+      const int at = split * a.part_rows + r;
+      if (c4 == 0) {
+        const v2i x = {(int)__float_as_uint(mm), (int)__float_as_uint(ll)};
+        __builtin_amdgcn_raw_buffer_store_b64(x, rm, at * 8, 0, kSc1);
+      }
+      __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4i, o), ro, (at * D + c4) * 4, 0, kSc1);
     }
   }
+  if (parts == 1) return;
+  __builtin_amdgcn_s_waitcnt(0);
+  __syncthreads();
+  if (threadIdx.x == 0)
+    last_flag = __hip_atomic_fetch_add(&a.arrived[wg], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
+                (uint32_t)(parts - 1);
+  __syncthreads();
+  if (!last_flag) return;
+  // join, a pass of the maxima and one of the sums, four parts' loads at a time
+  for (int i = threadIdx.x; i < it.rows * (D / 4); i += NW * 64) {
+    const int r = i / (D / 4), c4 = i % (D / 4) * 4;
+    float mm = -kInf;
+    for (int s0 = 0; s0 < parts; s0 += 4) {
+      float x[4];
+#pragma unroll
+      for (int b = 0; b < 4; ++b)
+        x[b] = __uint_as_float(
+            __builtin_amdgcn_raw_buffer_load_b32(rm, (min(s0 + b, parts - 1) * a.part_rows + r) * 8, 0, kSc1));
+#pragma unroll
+      for (int b = 0; b < 4; ++b) mm = fmaxf(mm, x[b]);
+    }
+    float ll = 0.0f;
+    v4f o = {};
+    for (int s0 = 0; s0 < parts; s0 += 4) {
+      v2i ml[4];
+      v4i x[4];
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        const int at = min(s0 + b, parts - 1) * a.part_rows + r;
+        ml[b] = __builtin_amdgcn_raw_buffer_load_b64(rm, at * 8, 0, kSc1);
+        x[b] = __builtin_amdgcn_raw_buffer_load_b128(ro, (at * D + c4) * 4, 0, kSc1);
+      }
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        const float ms = __uint_as_float((uint32_t)ml[b][0]);
+        const float w = s0 + b >= parts ? 0.0f : ms == -kInf ? 1.0f : exp2_hw(ms - mm);
+        const v4f y = __builtin_bit_cast(v4f, x[b]);
+        if (s0 + b < parts) {
+          ll = fmaf(w, __uint_as_float((uint32_t)ml[b][1]), ll);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) o[j] = fmaf(w, y[j], o[j]);
+        }
+      }
+    }
+    finish(r, c4, o, mm, ll);
+  }
+  if (threadIdx.x == 0) __hip_atomic_store(&a.arrived[wg], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
 // ---------------------------------------------------------------- join
@@ -860,10 +942,15 @@ struct Plan {
   bool step;
   int splits;
   int64_t tiles;
+  int part_rows;
+  size_t parts;  // rows of parts in the workspace
 };
 
+// Arrival counters at the start of the workspace, as the GEMMs' split-K.
+constexpr size_t kAttnCounterBytes = kGemmCounterBytes;
 constexpr int kChunkRows = 256;
 constexpr int kCus = 256;
+constexpr int kStepTarget = 1024;  // workgroups
 
 Plan plan_of(const qlin_kv_cache& cache, const qlin_kv_batch& batch, int64_t T, int64_t q_heads, int64_t window) {
   Plan p;
@@ -874,12 +961,16 @@ Plan plan_of(const qlin_kv_cache& cache, const qlin_kv_batch& batch, int64_t T, 
   if (p.step) {
     p.tiles = batch.batch;
     const int64_t wgs = batch.batch * cache.kv_heads;
-    p.splits = (int)std::max<int64_t>(1, std::min((2 * kCus + wgs - 1) / wgs, (keys + 127) / 128));
+    p.splits = (int)std::max<int64_t>(1, std::min((kStepTarget + wgs - 1) / wgs, (keys + 127) / 128));
+    if (wgs > (int64_t)(kAttnCounterBytes / 4)) p.splits = 1;
   } else {
     p.tiles = T * group / kChunkRows + batch.batch;
     const int64_t wgs = p.tiles * cache.kv_heads;
     p.splits = wgs >= kCus ? 1 : (int)std::max<int64_t>(1, std::min(2 * kCus / wgs, (keys + 255) / 256));
   }
+  p.part_rows = (int)std::min<int64_t>(32, batch.max_q * group);
+  p.parts = p.splits <= 1 ? 0 : p.step ? (size_t)p.splits * batch.batch * cache.kv_heads * p.part_rows
+                                       : (size_t)p.splits * T * q_heads;
   return p;
 }
 
@@ -892,7 +983,7 @@ void launch_parts(const AttnArgs& a, const Plan& p, hipStream_t st) {
     const int64_t items = p.tiles * a.kv_heads * p.splits;
     attn_chunk_kernel<D, FP8, D == 256 ? 32 : 64><<<(unsigned)((items + 7) / 8 * 8), 512, 0, st>>>(a);
   }
-  if (p.splits > 1) {
+  if (p.splits > 1 && !p.step) {
     const int64_t rows = a.T * a.kv_heads * a.group;
     attn_join_kernel<D><<<(unsigned)((rows + 3) / 4), 256, 0, st>>>(a);
   }
@@ -903,8 +994,7 @@ void launch_parts(const AttnArgs& a, const Plan& p, hipStream_t st) {
 size_t attn_workspace_bytes(const qlin_kv_cache& cache, const qlin_kv_batch& batch, int64_t T, int64_t q_heads) {
   const Plan p = plan_of(cache, batch, T, q_heads, 0);
   if (p.splits <= 1) return 0;
-  const size_t rows = (size_t)p.splits * T * q_heads;
-  return round_up(rows * cache.head_dim * 4, 256) + round_up(rows * 8, 256);
+  return kAttnCounterBytes + round_up(p.parts * cache.head_dim * 4, 256) + round_up(p.parts * 8, 256);
 }
 
 int launch_attn(const qlin_kv_cache& cache, const qlin_kv_batch& batch, int64_t T, const uint16_t* q, int64_t ldq,
@@ -934,15 +1024,16 @@ int launch_attn(const qlin_kv_cache& cache, const qlin_kv_batch& batch, int64_t 
   a.group = (int)(q_heads / cache.kv_heads);
   a.causal = causal;
   a.splits = p.splits;
+  a.part_rows = p.part_rows;
   a.tiles = (int)p.tiles;
   a.negate = scale < 0.0f;
   // a scale of 0 must keep masked scores at -inf (0 * -inf is NaN): a positive
   // one so small that every finite score gets the weight 1
   a.c = std::max(std::fabs(scale) * 1.44269504088896340736f, 1e-37f);
   if (p.splits > 1) {
-    const size_t rows = (size_t)p.splits * T * q_heads;
-    a.po = (float*)ws;
-    a.pml = (float*)((uint8_t*)ws + round_up(rows * cache.head_dim * 4, 256));
+    a.arrived = (uint32_t*)ws;
+    a.po = (float*)((uint8_t*)ws + kAttnCounterBytes);
+    a.pml = (float*)((uint8_t*)a.po + round_up(p.parts * cache.head_dim * 4, 256));
   }
   const bool f8 = cache.fmt == QLIN_KV_E4M3;
   switch (cache.head_dim) {

@@ -179,6 +179,7 @@ def test_binding_refuses_host_tensors(q):
 
     class P:
         head_dim = 64
+        device = torch.device("cuda", 0)
 
     with pytest.raises(ValueError):
         q.rope(x, torch.zeros(4, dtype=torch.int32), P)
