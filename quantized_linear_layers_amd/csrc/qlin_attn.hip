@@ -90,22 +90,27 @@ __device__ __forceinline__ v8bf cvt_fp8x8(uint32_t lo, uint32_t hi) {
   return v8bf{p0[0], p0[1], p1[0], p1[1], p2[0], p2[1], p3[0], p3[1]};
 }
 
-// Geometry of K and V rows in LDS.
-template <int D, bool FP8>
+// Geometry of K and V rows in LDS. NARROW: read by the 16-row products of the
+// step kernel, else by the 32-row ones of the chunk kernel (bf16 there).
+template <int D, bool FP8, bool NARROW = false>
 struct Geo {
   static constexpr int kRow = FP8 ? D : 2 * D;       // bytes of a row
   static constexpr int kChunks = kRow / 16;          // 16-byte chunks of a row
   static constexpr int kRowsPerLoad = 64 / kChunks;  // rows of one 1 KB load
   // Exclusive-or of a row's chunk index. K is read 16 bytes a lane, one chunk of
-  // 32 rows at a time; V 64 bytes of 4 rows (bf16) or 32 bytes of 8 rows.
+  // 32 (16) rows at a time; V by half a wave 64 bytes of 4 rows, narrow: 32 bytes
+  // of 8 rows, or 16 of 16 rows in E4M3.
   static __device__ __forceinline__ int k_swz(int row) {
     return kChunks >= 16 ? row & 15 : kChunks == 8 ? row & 7 : (row >> 1) & 3;
   }
   static __device__ __forceinline__ int v_swz(int row) {
-    if (FP8) {
-      if (kChunks >= 16) return ((row & 3) | ((row >> 1) & 4)) << 1;
-      if (kChunks == 8) return (((row >> 1) & 1) | ((row >> 2) & 2)) << 1;
-      return ((row >> 3) & 1) << 1;
+    if (NARROW) {
+      if (FP8) {
+        if (kChunks >= 16) return (row & 7) | ((row >> 1) & 8);
+        if (kChunks == 8) return ((row >> 1) & 3) | ((row >> 2) & 4);
+        return ((row >> 2) & 1) | ((row >> 3) & 2);
+      }
+      return kChunks >= 16 ? (row & 7) << 1 : ((row >> 1) & 3) << 1;
     }
     return kChunks >= 16 ? (row & 3) << 2 : ((row >> 1) & 1) << 2;
   }
@@ -196,9 +201,9 @@ __device__ __forceinline__ uint32_t lds_addr(const void* p) {
 // floats of a group, because a load writes all 64 lanes. With EDGE, rows of the
 // group before `skip` read as zero too (an offset far beyond the resource); only
 // the first tile of a window has such rows.
-template <int D, bool FP8, int TK, int ROWS>
+template <int D, bool FP8, int TK, int ROWS, bool NARROW = false>
 struct Stage {
-  using G = Geo<D, FP8>;
+  using G = Geo<D, FP8, NARROW>;
   static constexpr int kTile = TK * G::kRow;
   static constexpr int kScale = FP8 ? TK / 16 * 256 : 0;  // bytes of one scale area
   static constexpr int kLoads = ROWS / G::kRowsPerLoad;
@@ -218,11 +223,10 @@ struct Stage {
     dma16<kLoads>(lds + r0 * G::kRow, off, rs);
   }
   template <bool EDGE>
-  static __device__ __forceinline__ void scales(const v4i& sk, const v4i& sv, int skip, int r0, uint32_t lds) {
+  static __device__ __forceinline__ void scale_row(const v4i& rs, int skip, int r0, uint32_t lds) {
     const int lane = threadIdx.x & 63;
     const uint32_t at = lane >= 16 || (EDGE && lane < skip) ? 0x80000000u : (uint32_t)(lane * 4);
-    dma4(lds + (r0 / 16) * 256, at, sk);
-    dma4(lds + kScale + (r0 / 16) * 256, at, sv);
+    dma4(lds + (r0 / 16) * 256, at, rs);
   }
 };
 
@@ -245,85 +249,63 @@ struct State {
   }
 };
 
-// Operand fragments from LDS. K: 32 keys of block kb, step u (E4M3: both steps of
-// the 16 bytes); V^T: 16 keys of step t, columns 32 d.
-template <int D, bool FP8>
-__device__ __forceinline__ v4i k_frag(const uint8_t* lds_k, int kb, int u) {
-  using G = Geo<D, FP8>;
+// Operand fragments from LDS (bf16). K: 32 keys of block kb, step u; V^T: 16 keys
+// of step t, columns 32 d.
+template <int D>
+__device__ __forceinline__ v8bf k_frag(const uint8_t* lds_k, int kb, int u) {
+  using G = Geo<D, false>;
   const int lane = threadIdx.x & 63;
   const int row = 32 * kb + (lane & 31);
-  return *reinterpret_cast<const v4i*>(lds_k + row * G::kRow + 16 * ((2 * u + (lane >> 5)) ^ G::k_swz(row)));
+  return *reinterpret_cast<const v8bf*>(lds_k + row * G::kRow + 16 * ((2 * u + (lane >> 5)) ^ G::k_swz(row)));
 }
-template <int D, bool FP8>
-__device__ __forceinline__ v4i v_frag(const uint8_t* lds_v, int t, int d) {
-  using G = Geo<D, FP8>;
+template <int D>
+__device__ __forceinline__ v8bf v_frag(const uint8_t* lds_v, int t, int d) {
+  using G = Geo<D, false>;
   const int lane = threadIdx.x & 63;
-  const int key0 = 16 * t + 4 * (lane >> 5);
-  if (FP8) {
-    const int i = (lane & 15) >> 1;
-    const int row = key0 + (i & 3) + 8 * (i >> 2);
-    const int chunk = 2 * d + ((lane >> 4) & 1);
-    const v2i x = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
-        (QLIN_LDS v2i*)(lds_v + row * G::kRow + 16 * (chunk ^ G::v_swz(row)) + 8 * (lane & 1)));
-    return v4i{x[0], x[1], 0, 0};
-  }
-  const int row = key0 + ((lane & 15) >> 2);
+  const int row = 16 * t + 4 * (lane >> 5) + ((lane & 15) >> 2);
   const int chunk = 4 * d + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
   const v4s x = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
       (QLIN_LDS v4s*)(lds_v + row * G::kRow + 16 * (chunk ^ G::v_swz(row)) + 8 * (lane & 1)));
   const v4s y = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
       (QLIN_LDS v4s*)(lds_v + (row + 8) * G::kRow + 16 * (chunk ^ G::v_swz(row + 8)) + 8 * (lane & 1)));
-  return __builtin_bit_cast(v4i, (v8s){x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]});
+  return __builtin_bit_cast(v8bf, (v8s){x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]});
 }
 __device__ __forceinline__ v8bf as_bf16(const v4i& x) { return __builtin_bit_cast(v8bf, x); }
 
 // The products of KB * 32 keys with a wave's 32 rows: with PV, O^T += V^T P^T of
 // the weights p over lds_v; with QK, the scores S^T of lds_k.
-template <int D, bool FP8, int KB, bool PV, bool QK>
+template <int D, int KB, bool PV, bool QK>
 __device__ __forceinline__ void multiply(const v8bf (&q)[D / 16], State<D>& st, v16f (&s)[KB], const v4i (&p)[2 * KB],
                                          const uint8_t* lds_v, const uint8_t* lds_k) {
   if (PV) {
 #pragma unroll
     for (int t = 0; t < 2 * KB; ++t)
 #pragma unroll
-      for (int d = 0; d < D / 32; ++d) {
-        const v4i x = v_frag<D, FP8>(lds_v, t, d);
-        st.o[d] = mfma32(FP8 ? cvt_fp8x8(x[0], x[1]) : as_bf16(x), as_bf16(p[t]), st.o[d]);
-      }
+      for (int d = 0; d < D / 32; ++d) st.o[d] = mfma32(v_frag<D>(lds_v, t, d), as_bf16(p[t]), st.o[d]);
   }
   if (QK) {
 #pragma unroll
     for (int kb = 0; kb < KB; ++kb) s[kb] = v16f{};
 #pragma unroll
-    for (int u = 0; u < (FP8 ? D / 32 : D / 16); ++u)
+    for (int u = 0; u < D / 16; ++u)
 #pragma unroll
-      for (int kb = 0; kb < KB; ++kb) {
-        const v4i x = k_frag<D, FP8>(lds_k, kb, u);
-        if (FP8) {
-          s[kb] = mfma32(cvt_fp8x8(x[0], x[1]), q[2 * u], s[kb]);
-          s[kb] = mfma32(cvt_fp8x8(x[2], x[3]), q[2 * u + 1], s[kb]);
-        } else {
-          s[kb] = mfma32(as_bf16(x), q[u], s[kb]);
-        }
-      }
+      for (int kb = 0; kb < KB; ++kb) s[kb] = mfma32(k_frag<D>(lds_k, kb, u), q[u], s[kb]);
   }
-  if (!FP8) {
-    // Order of the block's LDS reads and products: AHEAD reads first, then each
-    // product followed by the reads that keep AHEAD of them under way (an LDS
-    // read takes about as long as 4 products).
-    constexpr int kAhead = 8;
-    constexpr int nv = PV ? 2 * KB * (D / 32) : 0, nk = QK ? KB * (D / 16) : 0;
-    constexpr int reads = 2 * nv + nk;
-    __builtin_amdgcn_sched_group_barrier(0x100, kAhead, 0);
-    int left = reads - kAhead;
+  // Order of the block's LDS reads and products: kAhead reads first, then each
+  // product followed by the reads that keep kAhead of them under way (an LDS
+  // read takes about as long as 4 products).
+  constexpr int kAhead = 8;
+  constexpr int nv = PV ? 2 * KB * (D / 32) : 0, nk = QK ? KB * (D / 16) : 0;
+  constexpr int reads = 2 * nv + nk;
+  __builtin_amdgcn_sched_group_barrier(0x100, kAhead, 0);
+  int left = reads - kAhead;
 #pragma unroll
-    for (int i = 0; i < nv + nk; ++i) {
-      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-      const int n = left <= 0 ? 0 : (i < nv ? (left < 2 ? left : 2) : 1);
-      if (n == 2) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
-      if (n == 1) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-      left -= n;
-    }
+  for (int i = 0; i < nv + nk; ++i) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    const int n = left <= 0 ? 0 : (i < nv ? (left < 2 ? left : 2) : 1);
+    if (n == 2) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+    if (n == 1) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+    left -= n;
   }
 }
 
@@ -400,26 +382,28 @@ __device__ __forceinline__ void weight_block(const AttnArgs& a, State<D>& st, v1
     for (int i = 0; i < 8; ++i) p[2 * kb + i / 4][i % 4] = (int)pack_bf16x2(s[kb][2 * i], s[kb][2 * i + 1]);
 }
 
-// The wave's query fragments: one row a lane, values in the order of the K
-// fragments (E4M3 K gives 16 consecutive values a lane, two steps).
-template <int D, bool FP8>
-__device__ __forceinline__ void load_q(const AttnArgs& a, const Item& it, int row, v8bf (&q)[D / 16]) {
-  const int h = (threadIdx.x & 63) >> 5;
-  const int rr = min(row, it.rows - 1);  // rows past the end repeat the last: never stored
-  const int i = rr / a.group, g = rr % a.group;
-  const uint16_t* src = a.q + (it.q0 + i) * a.ldq + (int64_t)(it.h * a.group + g) * D;
-#pragma unroll
-  for (int u = 0; u < D / 16; ++u) {
-    const int off = FP8 ? 32 * (u / 2) + 16 * h + 8 * (u % 2) : 16 * u + 8 * h;
-    uint4 x = ldg16(src + off);
-    if (a.negate) {
-      x.x ^= 0x80008000u;
-      x.y ^= 0x80008000u;
-      x.z ^= 0x80008000u;
-      x.w ^= 0x80008000u;
-    }
-    q[u] = __builtin_bit_cast(v8bf, x);
+// Eight values of a query row (negated for a negative scale).
+__device__ __forceinline__ v8bf load_q8(const AttnArgs& a, const uint16_t* src) {
+  uint4 x = ldg16(src);
+  if (a.negate) {
+    x.x ^= 0x80008000u;
+    x.y ^= 0x80008000u;
+    x.z ^= 0x80008000u;
+    x.w ^= 0x80008000u;
   }
+  return __builtin_bit_cast(v8bf, x);
+}
+// A packed row of queries; rows past the end repeat the last: never stored.
+template <int D>
+__device__ __forceinline__ const uint16_t* q_row(const AttnArgs& a, const Item& it, int row) {
+  const int r = min(row, it.rows - 1);
+  return a.q + (it.q0 + r / a.group) * a.ldq + (int64_t)(it.h * a.group + r % a.group) * D;
+}
+template <int D>
+__device__ __forceinline__ void load_q(const AttnArgs& a, const Item& it, int row, v8bf (&q)[D / 16]) {
+  const uint16_t* src = q_row<D>(a, it, row) + 8 * ((threadIdx.x & 63) >> 5);
+#pragma unroll
+  for (int u = 0; u < D / 16; ++u) q[u] = load_q8(a, src + 16 * u);
 }
 
 // Keys [row_lo, row_hi) that a packed row sees (none: row_hi <= row_lo).
@@ -515,20 +499,28 @@ __device__ __forceinline__ void store_row(const AttnArgs& a, const Item& it, int
 // (weights), so the two waves of a SIMD, w and w + 4, work in opposite phases:
 // while one multiplies (values of tile t - 1, scores of tile t), the other takes
 // the weights of its tile; a barrier ends each phase.
-//   phase   waves 0-3                     waves 4-7
-//   2t      PV(t-1), QK(t); loads         weights(t-1)
-//   2t+1    weights(t)                    PV(t-1), QK(t)
+//   phase   waves 0-3           waves 4-7
+//   2t      PV(t-1), QK(t)      weights(t-1)
+//   2t+1    weights(t)          PV(t-1), QK(t)
 // K(t) and V(t-1) are free after phase 2t+1. K and V have three places each: in
-// phase 2t waves 0-3 issue the loads of K(t+2) and V(t+1) into those of K(t-1)
-// and V(t-2), and by the end of phase 2t+1 have waited for the ones of a tile
-// before. Scales come with K and are read in the weight phases, the last of them
-// 2t+2: four places.
+// their weight phase of tile t (the shorter one: products of 32 keys by 32 rows
+// wait for LDS) waves 0-3 issue the loads of K(t+2) and V(t+1) into those of K(t-1)
+// and V(t-2), and by its end have waited for those of the tile before.
+// E4M3 tiles become bf16 on the way into LDS, once a workgroup (converting
+// fragments would cost every wave 8 instructions a product, in the phase in
+// which its partner needs the vector unit: 763 us against TIME_FP8 us for
+// eight chunks of up to 1024 tokens over 9001). They pass through registers: in
+// its weight phase of tile t each wave writes its piece of K(t+2) and V(t+1),
+// loaded one tile before, and loads K(t+3) and V(t+2). Scales come with K and are
+// read in the weight phases: places for 8 tiles.
 template <int D, bool FP8, int TK>
 __global__ __launch_bounds__(512, 2) void attn_chunk_kernel(const AttnArgs a) {
-  using St = Stage<D, FP8, TK, TK / 4>;
+  using St = Stage<D, false, TK, TK / 4>;
+  using G = Geo<D, false>;
   constexpr int BM = 256, KB = TK / 32;
+  constexpr int kScale = TK / 16 * 256;  // bytes of one scale area
   __shared__ __attribute__((aligned(1024))) uint8_t lds_k[3][St::kTile], lds_v[3][St::kTile];
-  __shared__ __attribute__((aligned(1024))) uint8_t lds_s[4][FP8 ? 2 * St::kScale : 16];
+  __shared__ __attribute__((aligned(1024))) uint8_t lds_s[8][FP8 ? 2 * kScale : 16];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 
@@ -540,29 +532,32 @@ __global__ __launch_bounds__(512, 2) void attn_chunk_kernel(const AttnArgs a) {
   if ((int)(blockIdx.x / 8) >= per || item >= items) return;
   const int split = item % a.splits;
   const int h = item / a.splits / a.tiles;
-  // the last tiles first: with a causal mask they have the most keys
-  int tile = a.tiles - 1 - item / a.splits % a.tiles;
-  // the tile's sequence: 64 sequences a pass, counted by a prefix sum over lanes
+  int tile = item / a.splits % a.tiles;
+  // the tile's sequence: 64 sequences a pass, a lane each, the ones with the most
+  // keys first (of a batch of many lengths the longest work must not come last)
   int b = -1;
   for (int b0 = 0; b0 < a.B && b < 0; b0 += 64) {
-    int mine = 0;
+    int mine = 0, keys = 0;
     if (b0 + lane < a.B) {
       const int64_t n = (int64_t)a.q_start[b0 + lane + 1] - a.q_start[b0 + lane];
       mine = n > 0 && n <= a.T ? (int)((n * a.group + BM - 1) / BM) : 0;
+      keys = a.kv_len[b0 + lane];
     }
-    int sum = mine;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const int x = __shfl_up(sum, o, kWave);
-      if (lane >= o) sum += x;
+    int before = 0, all = 0;  // tiles of the pass that come before this lane's; all
+    for (int j = 0; j < min(a.B - b0, 64); ++j) {
+      const int n = __builtin_amdgcn_readlane(mine, j), k = __builtin_amdgcn_readlane(keys, j);
+      before += k > keys || (k == keys && j > lane) ? n : 0;
+      all += n;
     }
-    const unsigned long long past = __ballot(sum > tile);
-    if (past) {
-      const int j = __ffsll(past) - 1;
+    const unsigned long long here = __ballot(tile >= before && tile < before + mine);
+    if (here) {
+      const int j = __ffsll(here) - 1;
       b = b0 + j;
-      tile -= __shfl(sum, j, kWave) - __shfl(mine, j, kWave);
+      tile -= __builtin_amdgcn_readlane(before, j);
+      // its last tiles first: with a causal mask they have the most keys
+      tile = __builtin_amdgcn_readlane(mine, j) - 1 - tile;
     } else {
-      tile -= __shfl(sum, 63, kWave);
+      tile -= all;
     }
   }
   if (b < 0) return;
@@ -573,7 +568,7 @@ __global__ __launch_bounds__(512, 2) void attn_chunk_kernel(const AttnArgs a) {
   const int w0 = row0 + 32 * wave;  // the wave's first row
   const int row = w0 + (lane & 31);
   v8bf q[D / 16];
-  load_q<D, FP8>(a, it, row, q);
+  load_q<D>(a, it, row, q);
   State<D> st;
   st.clear();
 
@@ -596,30 +591,44 @@ __global__ __launch_bounds__(512, 2) void attn_chunk_kernel(const AttnArgs a) {
   const bool holes = __syncthreads_or(hole);
 
   const bool first = wave < 4;
-  const int r0 = (wave & 3) * (TK / 4);  // the rows of a tile that this wave loads
+  // the rows of a tile that this wave loads, of one 16-row group (bf16: waves 0-3;
+  // E4M3: 16 bytes a lane, with heads of 64 waves 4-7 repeat waves 0-3)
+  const int r0 = FP8 ? wave * (1024 / D) % TK : (wave & 3) * (TK / 4);
   const int g0 = r0 & ~15;
   auto page_at = [&](int t) { return page_of(a, it, t * TK + g0); };
-  auto load_k = [&](int t, int page, int place, auto edge) {
-    const Rows16 w = rows_of(a, it, t * TK + g0, page, wg.hi);
-    const int skip = wg.lo - t * TK - g0;
-    v4i rk = resource<St::G::kRow>(a.k, w);
-    settled(rk);
-    St::template rows<false, edge>(rk, skip, r0, lds_addr(lds_k[place]));
-    if constexpr (FP8) {
-      v4i sk = resource<4>(a.ks, w), sv = resource<4>(a.vs, w);
-      settled(sk, sv);
-      St::template scales<edge>(sk, sv, skip, g0, lds_addr(lds_s[t & 3]));
-    }
-  };
-  auto load_v = [&](int t, int page, int place, auto edge) {
-    const Rows16 w = rows_of(a, it, t * TK + g0, page, wg.hi);
-    v4i rv = resource<St::G::kRow>(a.v, w);
-    settled(rv);
-    St::template rows<true, edge>(rv, wg.lo - t * TK - g0, r0, lds_addr(lds_v[place]));
-  };
   constexpr std::integral_constant<bool, true> kEdge;
   constexpr std::integral_constant<bool, false> kInner;
-  constexpr int kOps = 2 * St::kLoads + (FP8 ? 2 : 0);  // loads of an iteration
+  constexpr int kOps = 2 * St::kLoads;  // loads of an iteration (bf16)
+  // bf16: straight into LDS
+  auto load = [&](int t, int page, uint8_t* to, auto is_v, auto edge) {
+    const Rows16 w = rows_of(a, it, t * TK + g0, page, wg.hi);
+    v4i rs = resource<G::kRow>(is_v ? a.v : a.k, w);
+    settled(rs);
+    St::template rows<is_v, edge>(rs, wg.lo - t * TK - g0, r0, lds_addr(to));
+  };
+  // E4M3: this lane's 16 codes of K or V, and the scales of a group
+  const int my_row = r0 + lane / (D / 16), my_chunk = lane % (D / 16);
+  auto fetch = [&](int t, int page, auto is_v, auto edge) {
+    const Rows16 w = rows_of(a, it, t * TK + g0, page, wg.hi);
+    const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<uint8_t*>(is_v ? a.v : a.k) + w.row * D, (short)0, w.rows * D, 0x00020000);
+    const bool skip = edge && (my_row & 15) < wg.lo - t * TK - g0;
+    return __builtin_amdgcn_raw_buffer_load_b128(rs, skip ? (int)0x80000000 : (my_row & 15) * D + 16 * my_chunk, 0, 0);
+  };
+  auto fetch_scales = [&](int t, int page, auto edge) {
+    if (r0 != g0) return;
+    const Rows16 w = rows_of(a, it, t * TK + g0, page, wg.hi);
+    v4i sk = resource<4>(a.ks, w), sv = resource<4>(a.vs, w);
+    settled(sk, sv);
+    St::template scale_row<edge>(sk, wg.lo - t * TK - g0, g0, lds_addr(lds_s[t & 7]));
+    St::template scale_row<edge>(sv, wg.lo - t * TK - g0, g0, lds_addr(lds_s[t & 7]) + kScale);
+  };
+  auto put = [&](const v4i& x, uint8_t* to, auto is_v) {
+    const int sw = is_v ? G::v_swz(my_row) : G::k_swz(my_row);
+    uint8_t* base = to + my_row * G::kRow;
+    *reinterpret_cast<v8bf*>(base + 16 * ((2 * my_chunk) ^ sw)) = cvt_fp8x8(x[0], x[1]);
+    *reinterpret_cast<v8bf*>(base + 16 * ((2 * my_chunk + 1) ^ sw)) = cvt_fp8x8(x[2], x[3]);
+  };
   // the end of a phase; no instruction moves from one into another
   auto phase_end = [&] {
     __builtin_amdgcn_sched_barrier(0);
@@ -629,15 +638,32 @@ __global__ __launch_bounds__(512, 2) void attn_chunk_kernel(const AttnArgs a) {
     __builtin_amdgcn_sched_barrier(0);
   };
 
-  if (first && t0 < t1) {
-    const int p0 = page_at(t0), p1 = page_at(t0 + 1);
-    load_k(t0, p0, 0, kEdge);
-    load_v(t0, p0, 0, kEdge);
-    if (t0 + 1 < t1) load_k(t0 + 1, p1, 1, kInner);
-  }
+  // (tiles from t1 on load nothing: no row of theirs is visible)
   int pv = page_at(t0 + 1), pk = page_at(t0 + 2);  // pages of the next V and K loads
-  int at = 0, next = 1, last = 2;                  // places of tiles t, t + 1 and t + 2 (t - 1)
-  dma_wait<0>();
+  v4i fk = {}, fv = {};                            // E4M3: K(t+2) and V(t+1) on their way
+  if (t0 < t1) {
+    const int p0 = page_at(t0);
+    if constexpr (FP8) {
+      fetch_scales(t0, p0, kEdge);
+      fetch_scales(t0 + 1, pv, kInner);
+      const v4i k0 = fetch(t0, p0, kInner, kEdge), k1 = fetch(t0 + 1, pv, kInner, kInner);
+      const v4i v0 = fetch(t0, p0, kEdge, kEdge);
+      fetch_scales(t0 + 2, pk, kInner);
+      fk = fetch(t0 + 2, pk, kInner, kInner);
+      fv = fetch(t0 + 1, pv, kEdge, kInner);
+      put(k0, lds_k[0], kInner);
+      put(k1, lds_k[1], kInner);
+      put(v0, lds_v[0], kEdge);
+      pv = pk;
+      pk = page_at(t0 + 3);
+    } else if (first) {
+      load(t0, p0, lds_k[0], kInner, kEdge);
+      load(t0, p0, lds_v[0], kEdge, kEdge);
+      load(t0 + 1, pv, lds_k[1], kInner, kInner);
+    }
+  }
+  int at = 0, next = 1, last = 2;  // places of tiles t, t + 1 and t + 2 (t - 1)
+  if (!FP8) dma_wait<0>();
   phase_end();
   if (!first) phase_end();
   v16f s[KB];
@@ -649,172 +675,329 @@ __global__ __launch_bounds__(512, 2) void attn_chunk_kernel(const AttnArgs a) {
   // waves in step, so leaving one out would save nothing.
   for (int t = t0; t < t1; ++t) {
     // multiply
-    const bool more = t + 2 < t1;
-    if (first) {
-      // K(t+2) takes K(t-1)'s place, V(t+1) V(t-2)'s
-      if (t + 1 < t1) load_v(t + 1, pv, next, kInner);
-      if (more) load_k(t + 2, pk, last, kInner);
-    }
-    pv = pk;
-    pk = page_at(t + 3);
     __builtin_amdgcn_s_setprio(1);
     // (the first tile adds zero weights times its own values)
-    multiply<D, FP8, KB, true, true>(q, st, s, p, lds_v[t > t0 ? last : at], lds_k[at]);
+    multiply<D, KB, true, true>(q, st, s, p, lds_v[t > t0 ? last : at], lds_k[at]);
     __builtin_amdgcn_s_setprio(0);
     phase_end();
-    // weights
+    // weights. K(t+2) takes K(t-1)'s place, V(t+1) V(t-2)'s
+    if constexpr (FP8) {
+      put(fk, lds_k[last], kInner);
+      put(fv, lds_v[next], kEdge);
+      fetch_scales(t + 3, pk, kInner);
+      fk = fetch(t + 3, pk, kInner, kInner);
+      fv = fetch(t + 2, pv, kEdge, kInner);
+      pv = pk;
+      pk = page_at(t + 4);
+    } else {
+      if (first) {
+        load(t + 1, pv, lds_v[next], kEdge, kInner);
+        load(t + 2, pk, lds_k[last], kInner, kInner);
+      }
+      pv = pk;
+      pk = page_at(t + 3);
+    }
     const int key = t * TK;
     uint32_t bad = 0;
     if (holes)
       for (int g = 0; g < TK / 16; ++g) bad |= (uint32_t)no_page(a, page_of(a, it, key + 16 * g)) << g;
     const bool masked = holes || key + TK > own.all_hi || key < own.all_lo;
-    weight_block<D, FP8, KB, St::kScale>(a, st, s, p, lds_s[t & 3], masked, vlo - key, vhi - key, bad);
-    if (first) {
-      if (more)
-        dma_wait<kOps>();
-      else
-        dma_wait<0>();
-    }
+    weight_block<D, FP8, KB, kScale>(a, st, s, p, lds_s[t & 7], masked, vlo - key, vhi - key, bad);
+    if (!FP8 && first) dma_wait<kOps>();  // what the tile before loaded
     phase_end();
     const int x = last;
     last = at;
     at = next;
     next = x;
   }
-  if (t0 < t1) multiply<D, FP8, KB, true, false>(q, st, s, p, lds_v[last], lds_k[at]);
+  if (t0 < t1) multiply<D, KB, true, false>(q, st, s, p, lds_v[last], lds_k[at]);
+  dma_wait<0>();
   if (first) phase_end();
   store_row<D>(a, it, split, row, st);
 }
 
 // ---------------------------------------------------------------- step
-// At most 32 rows of a (sequence, key/value head): NW waves with the same rows,
-// each with its own key tiles of 32 (wave, wave + NW, ...) and its own two LDS
-// stages, so the loop has no barrier; the waves' results are merged in LDS.
-// With splits, every workgroup takes the same number of tiles, the longest
-// sequence's share (device data: the batch's longest range over the splits), so a
-// batch of many lengths is cut into equal pieces; the last workgroup of a
-// (sequence, head) to arrive joins its parts, in their order.
-template <int D, bool FP8, int NW>
-__global__ __launch_bounds__(NW * 64, 1) void attn_step_kernel(const AttnArgs a) {
-  using St = Stage<D, FP8, 32, 16>;
-  constexpr int kStage = 2 * St::kTile + 2 * St::kScale;      // K, V, scales
-  constexpr int kOps = 2 * (2 * St::kLoads + (FP8 ? 2 : 0));  // loads of a stage
-  constexpr int kOut = D + 4;                                 // floats of a row in the merge
-  constexpr int kMerge = NW * 32 * kOut * 4, kRing = 2 * NW * kStage;
+// At most 32 rows of a (sequence, key/value head), in RB blocks of 16: with so few
+// rows the 16-row products (v_mfma_f32_16x16x32_bf16) do half the work of the
+// 32-row ones, and their small state lets four waves share a SIMD. Lane group g =
+// lane >> 4 holds keys 16 b + 4 g + i of the tile's score block b: P's order for
+// the value product (slot j of group g: key 4 g + j, or 16 + 4 g + j - 4).
+// NW waves have the same rows and take key tiles of 32 in turn (wave, wave + NW,
+// ...), each with a K and a V place of its own in LDS, so the loop has no
+// barrier: the next K tile is loaded as soon as the scores have read this one, the
+// next V tile as soon as the values have, and each load has the other half of a
+// tile's work, and the other waves, to hide behind. The waves' results are merged
+// in LDS.
+// With splits, every workgroup takes the same number of tiles, so a batch of many
+// lengths is cut into equal pieces: about kPieces in all, more if the longest
+// sequence would need more splits than there are (the lengths are device data, so
+// the grid holds the most splits and the ones without tiles leave). The last
+// workgroup of a (sequence, head) to arrive joins its parts, in their order.
+constexpr int kPieces = 512;
+__device__ __forceinline__ float groups_max(float x) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return halves_max(fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1])));
+}
+__device__ __forceinline__ float groups_sum(float x) {
+  x += __shfl_xor(x, 16, kWave);
+  return x + __shfl_xor(x, 32, kWave);
+}
+
+// Waves a SIMD that the LDS places (4 waves a workgroup) leave room for.
+constexpr int step_waves(int D, bool fp8, int rb) {
+  return D == 64 ? 4 : D == 128 ? (fp8 && rb == 1 ? 4 : 2) : (fp8 && rb == 1 ? 2 : 1);
+}
+
+template <int D, bool FP8, int RB, int NW>
+__global__ __launch_bounds__(NW * 64, step_waves(D, FP8, RB)) void attn_step_kernel(const AttnArgs a) {
+  using St = Stage<D, FP8, 32, 16, true>;
+  using G = Geo<D, FP8, true>;
+  constexpr int kStage = 2 * St::kTile + 2 * St::kScale;     // K, V, their scales
+  constexpr int kOps = 2 * (St::kLoads + (FP8 ? 1 : 0));     // loads of a K or V tile
+  constexpr int kRows = 16 * RB, kOut = D + 4;               // floats of a row in the merge
+  constexpr int kMerge = NW * kRows * kOut * 4, kRing = NW * kStage;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[kRing > kMerge ? kRing : kMerge];
-  __shared__ float wm[NW][32], wl[NW][32];
+  __shared__ float wm[NW][kRows], wl[NW][kRows];
   __shared__ int last_flag;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int split = blockIdx.x;
+  const int r = lane & 15, g = lane >> 4;
+  const int split = blockIdx.z;  // slowest: the splits without tiles come last
   Item it;
-  if (!item_of(a, blockIdx.z, blockIdx.y, it)) return;
+  if (!item_of(a, blockIdx.y, blockIdx.x, it)) return;
   it.rows = min(it.rows, a.part_rows);  // max_q promises it
-  const int row = lane & 31;
   const Range rg = range_of(a, it, 0, it.rows);
-  const int vlo = row_lo(a, it, row), vhi = row_hi(a, it, row);
   int t0 = rg.lo / 32, t1 = (rg.hi + 31) / 32;
   int parts = 1;
   if (a.splits > 1) {
-    int span = 0;  // the longest range of keys in the batch
+    int longest = 0;  // the batch's ranges of keys, in tiles
+    float sum = 0.0f;
     for (int b = lane; b < a.B; b += 64) {
       const int n = a.q_start[b + 1] - a.q_start[b];
       int len = (int)min((int64_t)a.kv_len[b], (int64_t)a.cols << a.page_shift);
       if (a.window > 0) len = (int)min((int64_t)len, a.window + n);
-      span = max(span, n > 0 ? len : 0);
+      const int tiles = n > 0 && len > 0 ? len / 32 + 2 : 0;
+      longest = max(longest, tiles);
+      sum += (float)tiles;
     }
 #pragma unroll
-    for (int o = 32; o >= 1; o >>= 1) span = max(span, __shfl_xor(span, o, kWave));
-    const int tiles = __builtin_amdgcn_readfirstlane(span) / 32 + 2;
-    const int n = (tiles + a.splits * NW - 1) / (a.splits * NW) * NW;
+    for (int o = 32; o >= 1; o >>= 1) {
+      longest = max(longest, __shfl_xor(longest, o, kWave));
+      sum += __shfl_xor(sum, o, kWave);
+    }
+    const int share = max((longest + a.splits - 1) / a.splits, (int)(sum * (float)a.kv_heads * (1.0f / kPieces)));
+    const int n = __builtin_amdgcn_readfirstlane((share + NW - 1) / NW * NW);
     parts = max((t1 - t0 + n - 1) / n, 1);
     if (split >= parts) return;
     t0 = t0 + split * n;
     t1 = min(t0 + n, t1);
   }
-  uint8_t* ring = lds + wave * 2 * kStage;
-  auto issue = [&](int t, int buf, int p0, int p1, auto edge) {
-    const uint32_t dst = lds_addr(ring) + buf * kStage;
+  uint8_t* mine = lds + wave * kStage;
+  const uint32_t lk = lds_addr(mine), lv = lk + St::kTile, ls = lv + St::kTile;
+  // K (or V) rows of tile t and their scales
+  auto load = [&](int t, const int (&page)[2], auto is_v, auto edge) {
 #pragma unroll
-    for (int g = 0; g < 2; ++g) {
-      const Rows16 w = rows_of(a, it, t * 32 + 16 * g, g ? p1 : p0, rg.hi);
-      const int skip = rg.lo - t * 32 - 16 * g;
-      v4i rk = resource<St::G::kRow>(a.k, w), rv = resource<St::G::kRow>(a.v, w);
-      settled(rk, rv);
-      St::template rows<false, edge>(rk, skip, 16 * g, dst);
-      St::template rows<true, edge>(rv, skip, 16 * g, dst + St::kTile);
+    for (int n = 0; n < 2; ++n) {
+      const Rows16 w = rows_of(a, it, t * 32 + 16 * n, page[n], rg.hi);
+      const int skip = rg.lo - t * 32 - 16 * n;
+      v4i rs = resource<G::kRow>(is_v ? a.v : a.k, w);
+      settled(rs);
+      St::template rows<is_v, edge>(rs, skip, 16 * n, is_v ? lv : lk);
       if constexpr (FP8) {
-        v4i sk = resource<4>(a.ks, w), sv = resource<4>(a.vs, w);
-        settled(sk, sv);
-        St::template scales<edge>(sk, sv, skip, 16 * g, dst + 2 * St::kTile);
+        v4i sc = resource<4>(is_v ? a.vs : a.ks, w);
+        settled(sc);
+        St::template scale_row<edge>(sc, skip, 16 * n, is_v ? ls + St::kScale : ls);
       }
     }
   };
-  constexpr std::integral_constant<bool, true> kEdge;
-  constexpr std::integral_constant<bool, false> kInner;
+  constexpr std::integral_constant<bool, true> kYes;
+  constexpr std::integral_constant<bool, false> kNo;
+  auto pages = [&](int t, int (&page)[2]) {
+    page[0] = page_of(a, it, t * 32);
+    page[1] = page_of(a, it, t * 32 + 16);
+  };
   int t = t0 + wave;
-  int p0 = page_of(a, it, t * 32), p1 = page_of(a, it, t * 32 + 16);
-  if (t < t1) issue(t, 0, p0, p1, kEdge);
-  v8bf q[D / 16];
-  load_q<D, FP8>(a, it, row, q);
-  State<D> st;
-  st.clear();
-  int n0 = page_of(a, it, (t + NW) * 32), n1 = page_of(a, it, (t + NW) * 32 + 16);
-  int buf = 0;
+  int page[2], next[2];
+  pages(t, page);
+  if (t < t1) {
+    load(t, page, kNo, kYes);
+    load(t, page, kYes, kYes);
+  }
+  pages(t + NW, next);
+  v8bf q[RB][D / 32];
+  int vlo[RB], vhi[RB];
+  float m[RB], l[RB];
+  v4f o[RB][D / 16];
+#pragma unroll
+  for (int rb = 0; rb < RB; ++rb) {
+    const int row = 16 * rb + r;
+    vlo[rb] = row_lo(a, it, row);
+    vhi[rb] = row_hi(a, it, row);
+    m[rb] = -kInf;
+    l[rb] = 0.0f;
+#pragma unroll
+    for (int d = 0; d < D / 16; ++d) o[rb][d] = v4f{};
+    const uint16_t* src = q_row<D>(a, it, row);
+#pragma unroll
+    for (int u = 0; u < D / 32; ++u)
+      q[rb][u] = load_q8(a, src + (FP8 ? 64 * (u / 2) + 16 * g + 8 * (u % 2) : 32 * u + 8 * g));
+  }
   for (; t < t1; t += NW) {
-    lds_reads_done();  // the stage that the next loads overwrite has been read
-    if (t + NW < t1) {
-      issue(t + NW, buf ^ 1, n0, n1, kInner);
-      dma_wait<kOps>();
-    } else {
-      dma_wait<0>();
-    }
-    const uint32_t bad = (no_page(a, p0) ? 1u : 0u) | (no_page(a, p1) ? 2u : 0u);
-    p0 = n0;
-    p1 = n1;
-    n0 = page_of(a, it, (t + 2 * NW) * 32);
-    n1 = page_of(a, it, (t + 2 * NW) * 32 + 16);
+    const bool more = t + NW < t1;
+    const uint32_t bad = (no_page(a, page[0]) ? 1u : 0u) | (no_page(a, page[1]) ? 2u : 0u);
     const int key = t * 32;
-    const bool masked = bad != 0 || key + 32 > rg.all_hi || key < rg.all_lo;
-    const uint8_t* s = ring + buf * kStage;
-    v16f sc[1];
-    v4i w[2];
-    multiply<D, FP8, 1, false, true>(q, st, sc, w, s + St::kTile, s);
-    weight_block<D, FP8, 1, St::kScale>(a, st, sc, w, s + 2 * St::kTile, masked, vlo - key, vhi - key, bad);
-    multiply<D, FP8, 1, true, false>(q, st, sc, w, s + St::kTile, s);
-    buf ^= 1;
+    dma_wait<kOps>();  // K has arrived, V may be under way
+    v4f s[RB][2];
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      const uint8_t* base = mine + (16 * b + r) * G::kRow;
+      const int sw = G::k_swz(16 * b + r);
+#pragma unroll
+      for (int rb = 0; rb < RB; ++rb) s[rb][b] = v4f{};
+#pragma unroll
+      for (int u = 0; u < (FP8 ? D / 64 : D / 32); ++u) {
+        const v4i x = *reinterpret_cast<const v4i*>(base + 16 * ((4 * u + g) ^ sw));
+#pragma unroll
+        for (int rb = 0; rb < RB; ++rb) {
+          if (FP8) {
+            s[rb][b] = mfma_bf16(cvt_fp8x8(x[0], x[1]), q[rb][2 * u], s[rb][b]);
+            s[rb][b] = mfma_bf16(cvt_fp8x8(x[2], x[3]), q[rb][2 * u + 1], s[rb][b]);
+          } else {
+            s[rb][b] = mfma_bf16(as_bf16(x), q[rb][u], s[rb][b]);
+          }
+        }
+      }
+    }
+    if (FP8) {
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const v4f k = *reinterpret_cast<const v4f*>(mine + 2 * St::kTile + 256 * b + 16 * g);
+#pragma unroll
+        for (int rb = 0; rb < RB; ++rb)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s[rb][b][i] *= k[i];
+      }
+    }
+    lds_reads_done();
+    if (more) load(t + NW, next, kNo, kNo);
+    if (bad != 0 || key + 32 > rg.all_hi || key < rg.all_lo) {
+#pragma unroll
+      for (int rb = 0; rb < RB; ++rb)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int j = key + 16 * (i / 4) + 4 * g + i % 4;
+          const bool see = vlo[rb] <= j && vhi[rb] > j && !((bad >> (i / 4)) & 1);
+          s[rb][i / 4][i % 4] = see ? s[rb][i / 4][i % 4] : -kInf;
+        }
+    }
+#pragma unroll
+    for (int rb = 0; rb < RB; ++rb) {
+      float mx = s[rb][0][0];
+#pragma unroll
+      for (int i = 1; i < 8; ++i) mx = fmaxf(mx, s[rb][i / 4][i % 4]);
+      mx = groups_max(mx) * a.c;
+      if (__any(mx > m[rb] + 8.0f)) {
+        const float top = fmaxf(m[rb], mx);
+        const float f = top == -kInf ? 0.0f : exp2_hw(m[rb] - top);
+        m[rb] = top;
+        l[rb] *= f;
+#pragma unroll
+        for (int d = 0; d < D / 16; ++d)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[rb][d][i] *= f;
+      }
+      const float base = m[rb] == -kInf ? 0.0f : m[rb];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float w = exp2_hw(fmaf(s[rb][i / 4][i % 4], a.c, -base));
+        s[rb][i / 4][i % 4] = w;
+        l[rb] += w;
+      }
+    }
+    if (more)
+      dma_wait<kOps>();  // V has arrived, the next K may be under way
+    else
+      dma_wait<0>();
+    v8bf p[RB];
+    v4f sv[2];
+    if (FP8) {
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+        sv[b] = *reinterpret_cast<const v4f*>(mine + 2 * St::kTile + St::kScale + 256 * b + 16 * g);
+    }
+#pragma unroll
+    for (int rb = 0; rb < RB; ++rb) {
+      v4i w;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float x = s[rb][i / 2][2 * (i % 2)], y = s[rb][i / 2][2 * (i % 2) + 1];
+        if (FP8) {
+          x *= sv[i / 2][2 * (i % 2)];
+          y *= sv[i / 2][2 * (i % 2) + 1];
+        }
+        w[i] = (int)pack_bf16x2(x, y);  // one rounding of the weight, as in the chunk kernel
+      }
+      p[rb] = as_bf16(w);
+    }
+    const uint8_t* vt = mine + St::kTile;
+#pragma unroll
+    for (int d = 0; d < D / 16; ++d) {
+      v8bf v;
+      if (FP8) {
+        const int n = r >> 1;
+        const int row = 4 * g + (n & 3) + 16 * (n >> 2);
+        const v2i x = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
+            (QLIN_LDS v2i*)(vt + row * G::kRow + 16 * (d ^ G::v_swz(row)) + 8 * (lane & 1)));
+        v = cvt_fp8x8(x[0], x[1]);
+      } else {
+        const int row = 4 * g + (r >> 2);
+        const int chunk = 2 * d + ((lane & 3) >> 1);
+        const v4s x = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+            (QLIN_LDS v4s*)(vt + row * G::kRow + 16 * (chunk ^ G::v_swz(row)) + 8 * (lane & 1)));
+        const v4s y = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+            (QLIN_LDS v4s*)(vt + (row + 16) * G::kRow + 16 * (chunk ^ G::v_swz(row + 16)) + 8 * (lane & 1)));
+        v = __builtin_bit_cast(v8bf, (v8s){x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]});
+      }
+#pragma unroll
+      for (int rb = 0; rb < RB; ++rb) o[rb][d] = mfma_bf16(v, p[rb], o[rb][d]);
+    }
+    lds_reads_done();
+    if (more) load(t + NW, next, kYes, kNo);
+    page[0] = next[0];
+    page[1] = next[1];
+    pages(t + 2 * NW, next);
   }
   // merge: every wave's rows on the common maximum, then summed over the waves
-  const int hh = lane >> 5;
-  const float l = st.l + __shfl_xor(st.l, 32, kWave);
-  if (hh == 0) {
-    wm[wave][row] = st.m;
-    wl[wave][row] = l;
+#pragma unroll
+  for (int rb = 0; rb < RB; ++rb) {
+    l[rb] = groups_sum(l[rb]);
+    if (g == 0) wm[wave][16 * rb + r] = m[rb];
   }
   __syncthreads();
-  float m = -kInf;
-#pragma unroll
-  for (int w = 0; w < NW; ++w) m = fmaxf(m, wm[w][row]);
-  const float f = st.m == -kInf ? (l == 0.0f ? 0.0f : 1.0f) : exp2_hw(st.m - m);
   float* all = reinterpret_cast<float*>(lds);
-  if (row < it.rows) {
-    float* mine = all + (wave * 32 + row) * kOut;
 #pragma unroll
-    for (int d = 0; d < D / 32; ++d)
+  for (int rb = 0; rb < RB; ++rb) {
+    const int row = 16 * rb + r;
+    float top = -kInf;
 #pragma unroll
-      for (int b = 0; b < 4; ++b)
-        *reinterpret_cast<v4f*>(mine + 32 * d + 8 * b + 4 * hh) =
-            v4f{st.o[d][4 * b] * f, st.o[d][4 * b + 1] * f, st.o[d][4 * b + 2] * f, st.o[d][4 * b + 3] * f};
-    if (hh == 0) wl[wave][row] = l * f;
+    for (int w = 0; w < NW; ++w) top = fmaxf(top, wm[w][row]);
+    const float f = m[rb] == -kInf ? (l[rb] == 0.0f ? 0.0f : 1.0f) : exp2_hw(m[rb] - top);
+    if (row < it.rows) {
+      float* dst = all + (wave * kRows + row) * kOut + 4 * g;
+#pragma unroll
+      for (int d = 0; d < D / 16; ++d)
+        *reinterpret_cast<v4f*>(dst + 16 * d) = v4f{o[rb][d][0] * f, o[rb][d][1] * f, o[rb][d][2] * f, o[rb][d][3] * f};
+      if (g == 0) wl[wave][row] = l[rb] * f;
+    }
   }
   __syncthreads();
   const int64_t heads = (int64_t)a.kv_heads * a.group;
-  auto finish = [&](int r, int c4, const v4f& o, float mm, float ll) {
-    const int64_t tok = it.q0 + r / a.group;
-    const int qh = it.h * a.group + r % a.group;
+  auto finish = [&](int row, int c4, const v4f& x, float mm, float ll) {
+    const int64_t tok = it.q0 + row / a.group;
+    const int qh = it.h * a.group + row % a.group;
     const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
     *reinterpret_cast<uint2*>(a.out + tok * a.ldo + (int64_t)qh * D + c4) =
-        make_uint2(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv));
+        make_uint2(pack_bf16x2(x[0] * inv, x[1] * inv), pack_bf16x2(x[2] * inv, x[3] * inv));
     if (a.lse && c4 == 0) a.lse[tok * heads + qh] = ll == 0.0f ? -kInf : (mm + log2f(ll)) * kLn2;
   };
   // Parts and counter move past the XCDs' own L2 caches (sc1, device scope): a
@@ -827,26 +1010,26 @@ __global__ __launch_bounds__(NW * 64, 1) void attn_step_kernel(const AttnArgs a)
   const __amdgpu_buffer_rsrc_t rm = __builtin_amdgcn_make_buffer_rsrc(
       a.pml + (int64_t)wg * a.splits * a.part_rows * 2, (short)0, a.splits * a.part_rows * 8, 0x00020000);
   for (int i = threadIdx.x; i < it.rows * (D / 4); i += NW * 64) {
-    const int r = i / (D / 4), c4 = i % (D / 4) * 4;
+    const int row = i / (D / 4), c4 = i % (D / 4) * 4;
     float mm = -kInf, ll = 0.0f;
-    v4f o = {};
+    v4f x = {};
 #pragma unroll
     for (int w = 0; w < NW; ++w) {
-      mm = fmaxf(mm, wm[w][r]);
-      ll += wl[w][r];
-      const v4f x = *reinterpret_cast<const v4f*>(all + (w * 32 + r) * kOut + c4);
+      mm = fmaxf(mm, wm[w][row]);
+      ll += wl[w][row];
+      const v4f y = *reinterpret_cast<const v4f*>(all + (w * kRows + row) * kOut + c4);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) o[j] += x[j];
+      for (int j = 0; j < 4; ++j) x[j] += y[j];
     }
     if (parts == 1) {
-      finish(r, c4, o, mm, ll);
+      finish(row, c4, x, mm, ll);
     } else {
-      const int at = split * a.part_rows + r;
+      const int at = split * a.part_rows + row;
       if (c4 == 0) {
-        const v2i x = {(int)__float_as_uint(mm), (int)__float_as_uint(ll)};
-        __builtin_amdgcn_raw_buffer_store_b64(x, rm, at * 8, 0, kSc1);
+        const v2i y = {(int)__float_as_uint(mm), (int)__float_as_uint(ll)};
+        __builtin_amdgcn_raw_buffer_store_b64(y, rm, at * 8, 0, kSc1);
       }
-      __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4i, o), ro, (at * D + c4) * 4, 0, kSc1);
+      __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4i, x), ro, (at * D + c4) * 4, 0, kSc1);
     }
   }
   if (parts == 1) return;
@@ -857,43 +1040,35 @@ __global__ __launch_bounds__(NW * 64, 1) void attn_step_kernel(const AttnArgs a)
                 (uint32_t)(parts - 1);
   __syncthreads();
   if (!last_flag) return;
-  // join, a pass of the maxima and one of the sums, four parts' loads at a time
+  // join: the parts' maxima and sums by all threads at once, then the rows, eight
+  // parts' loads at a time
+  v2i* ml = reinterpret_cast<v2i*>(lds);
+  for (int i = threadIdx.x; i < parts * a.part_rows; i += NW * 64)
+    ml[i] = __builtin_amdgcn_raw_buffer_load_b64(rm, i * 8, 0, kSc1);
+  __syncthreads();
   for (int i = threadIdx.x; i < it.rows * (D / 4); i += NW * 64) {
-    const int r = i / (D / 4), c4 = i % (D / 4) * 4;
-    float mm = -kInf;
-    for (int s0 = 0; s0 < parts; s0 += 4) {
-      float x[4];
+    const int row = i / (D / 4), c4 = i % (D / 4) * 4;
+    float mm = -kInf, ll = 0.0f;
+    for (int s = 0; s < parts; ++s) mm = fmaxf(mm, __uint_as_float((uint32_t)ml[s * a.part_rows + row][0]));
+    v4f x = {};
+    for (int s0 = 0; s0 < parts; s0 += 8) {
+      v4i y[8];
 #pragma unroll
-      for (int b = 0; b < 4; ++b)
-        x[b] = __uint_as_float(
-            __builtin_amdgcn_raw_buffer_load_b32(rm, (min(s0 + b, parts - 1) * a.part_rows + r) * 8, 0, kSc1));
+      for (int b = 0; b < 8; ++b)
+        y[b] = __builtin_amdgcn_raw_buffer_load_b128(ro, ((min(s0 + b, parts - 1) * a.part_rows + row) * D + c4) * 4, 0, kSc1);
 #pragma unroll
-      for (int b = 0; b < 4; ++b) mm = fmaxf(mm, x[b]);
-    }
-    float ll = 0.0f;
-    v4f o = {};
-    for (int s0 = 0; s0 < parts; s0 += 4) {
-      v2i ml[4];
-      v4i x[4];
-#pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        const int at = min(s0 + b, parts - 1) * a.part_rows + r;
-        ml[b] = __builtin_amdgcn_raw_buffer_load_b64(rm, at * 8, 0, kSc1);
-        x[b] = __builtin_amdgcn_raw_buffer_load_b128(ro, (at * D + c4) * 4, 0, kSc1);
-      }
-#pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        const float ms = __uint_as_float((uint32_t)ml[b][0]);
-        const float w = s0 + b >= parts ? 0.0f : ms == -kInf ? 1.0f : exp2_hw(ms - mm);
-        const v4f y = __builtin_bit_cast(v4f, x[b]);
+      for (int b = 0; b < 8; ++b) {
         if (s0 + b < parts) {
-          ll = fmaf(w, __uint_as_float((uint32_t)ml[b][1]), ll);
+          const v2i z = ml[(s0 + b) * a.part_rows + row];
+          const float ms = __uint_as_float((uint32_t)z[0]);
+          const float w = ms == -kInf ? 1.0f : exp2_hw(ms - mm);
+          ll = fmaf(w, __uint_as_float((uint32_t)z[1]), ll);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) o[j] = fmaf(w, y[j], o[j]);
+          for (int j = 0; j < 4; ++j) x[j] = fmaf(w, __builtin_bit_cast(v4f, y[b])[j], x[j]);
         }
       }
     }
-    finish(r, c4, o, mm, ll);
+    finish(row, c4, x, mm, ll);
   }
   if (threadIdx.x == 0) __hip_atomic_store(&a.arrived[wg], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
@@ -950,7 +1125,6 @@ struct Plan {
 constexpr size_t kAttnCounterBytes = kGemmCounterBytes;
 constexpr int kChunkRows = 256;
 constexpr int kCus = 256;
-constexpr int kStepTarget = 1024;  // workgroups
 
 Plan plan_of(const qlin_kv_cache& cache, const qlin_kv_batch& batch, int64_t T, int64_t q_heads, int64_t window) {
   Plan p;
@@ -961,8 +1135,16 @@ Plan plan_of(const qlin_kv_cache& cache, const qlin_kv_batch& batch, int64_t T, 
   if (p.step) {
     p.tiles = batch.batch;
     const int64_t wgs = batch.batch * cache.kv_heads;
-    p.splits = (int)std::max<int64_t>(1, std::min((kStepTarget + wgs - 1) / wgs, (keys + 127) / 128));
-    if (wgs > (int64_t)(kAttnCounterBytes / 4)) p.splits = 1;
+    // A joined part costs about 6 us (its store has to be visible, then counted,
+    // then read). With 64 E4M3 sequences of up to 1536 tokens (512 workgroups,
+    // heads of 128) two parts took 37 us and none 30.5; with eight of 65536
+    // bf16 (64 workgroups) 8 parts took 352 us, 4 357, 16 379. So: one workgroup a
+    // CU; where sequences may be long enough not to notice the join, up to the
+    // most that a ragged batch needs.
+    const int64_t most = keys >= 4096 ? 2048 : kCus;
+    // (64 parts at most: one workgroup reads them all)
+    p.splits = (int)std::max<int64_t>(1, std::min({(most + wgs - 1) / wgs, (keys + 127) / 128, (int64_t)64}));
+    if (wgs >= (keys >= 4096 ? 2048 : kCus)) p.splits = 1;
   } else {
     p.tiles = T * group / kChunkRows + batch.batch;
     const int64_t wgs = p.tiles * cache.kv_heads;
@@ -977,8 +1159,11 @@ Plan plan_of(const qlin_kv_cache& cache, const qlin_kv_batch& batch, int64_t T, 
 template <int D, bool FP8>
 void launch_parts(const AttnArgs& a, const Plan& p, hipStream_t st) {
   if (p.step) {
-    constexpr int NW = D == 256 && !FP8 ? 2 : 4;
-    attn_step_kernel<D, FP8, NW><<<dim3(p.splits, a.kv_heads, a.B), NW * 64, 0, st>>>(a);
+    const dim3 grid(a.kv_heads, a.B, p.splits);
+    if (p.part_rows <= 16)
+      attn_step_kernel<D, FP8, 1, 4><<<grid, 256, 0, st>>>(a);
+    else
+      attn_step_kernel<D, FP8, 2, 4><<<grid, 256, 0, st>>>(a);
   } else {
     const int64_t items = p.tiles * a.kv_heads * p.splits;
     attn_chunk_kernel<D, FP8, D == 256 ? 32 : 64><<<(unsigned)((items + 7) / 8 * 8), 512, 0, st>>>(a);
