@@ -252,16 +252,14 @@ struct State {
 // Operand fragments from LDS (bf16). K: 32 keys of block kb, step u; V^T: 16 keys
 // of step t, columns 32 d.
 template <int D>
-__device__ __forceinline__ v8bf k_frag(const uint8_t* lds_k, int kb, int u) {
+__device__ __forceinline__ v8bf k_frag(const uint8_t* lds_k, int kb, int u, int lane) {
   using G = Geo<D, false>;
-  const int lane = threadIdx.x & 63;
   const int row = 32 * kb + (lane & 31);
   return *reinterpret_cast<const v8bf*>(lds_k + row * G::kRow + 16 * ((2 * u + (lane >> 5)) ^ G::k_swz(row)));
 }
 template <int D>
-__device__ __forceinline__ v8bf v_frag(const uint8_t* lds_v, int t, int d) {
+__device__ __forceinline__ v8bf v_frag(const uint8_t* lds_v, int t, int d, int lane) {
   using G = Geo<D, false>;
-  const int lane = threadIdx.x & 63;
   const int row = 16 * t + 4 * (lane >> 5) + ((lane & 15) >> 2);
   const int chunk = 4 * d + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
   const v4s x = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
@@ -272,40 +270,50 @@ __device__ __forceinline__ v8bf v_frag(const uint8_t* lds_v, int t, int d) {
 }
 __device__ __forceinline__ v8bf as_bf16(const v4i& x) { return __builtin_bit_cast(v8bf, x); }
 
-// The products of KB * 32 keys with a wave's 32 rows: with PV, O^T += V^T P^T of
-// the weights p over lds_v; with QK, the scores S^T of lds_k.
-template <int D, int KB, bool PV, bool QK>
+// Fragment n of the products of KB * 32 keys: first the values', then the keys'.
+template <int D, int KB>
+__device__ __forceinline__ v8bf frag(const uint8_t* lds_v, const uint8_t* lds_k, int n, int lane) {
+  constexpr int nv = 2 * KB * (D / 32);
+  return n < nv ? v_frag<D>(lds_v, n / (D / 32), n % (D / 32), lane)
+                : k_frag<D>(lds_k, (n - nv) % KB, (n - nv) / KB, lane);
+}
+// The lane number, with heads of 256 in a form that keeps the fragments' addresses
+// from being held in registers over the loop (12 of them, which would not fit).
+template <int D>
+__device__ __forceinline__ int frag_lane() {
+  int lane = threadIdx.x & 63;
+  if (D == 256) asm volatile("" : "+v"(lane));
+  return lane;
+}
+
+// The products of KB * 32 keys with a wave's 32 rows: O^T += V^T P^T of the weights p
+// over lds_v, then (QK) the scores S^T of lds_k. fr holds the first N fragments on
+// entry; each product is followed by the read of the fragment N products on (an LDS
+// read takes about as long as 4), and nothing moves past a product: left alone,
+// the scheduler reads two ahead where registers are short.
+// between(i) is called after every second product, for other work to be spread
+// over them.
+template <int D, int KB, int N, bool QK, class F>
 __device__ __forceinline__ void multiply(const v8bf (&q)[D / 16], State<D>& st, v16f (&s)[KB], const v4i (&p)[2 * KB],
-                                         const uint8_t* lds_v, const uint8_t* lds_k) {
-  if (PV) {
-#pragma unroll
-    for (int t = 0; t < 2 * KB; ++t)
-#pragma unroll
-      for (int d = 0; d < D / 32; ++d) st.o[d] = mfma32(v_frag<D>(lds_v, t, d), as_bf16(p[t]), st.o[d]);
-  }
+                                         v8bf (&fr)[N], const uint8_t* lds_v, const uint8_t* lds_k, F between) {
+  constexpr int nv = 2 * KB * (D / 32), all = nv + (QK ? KB * (D / 16) : 0);
+  const int lane = frag_lane<D>();
   if (QK) {
 #pragma unroll
     for (int kb = 0; kb < KB; ++kb) s[kb] = v16f{};
-#pragma unroll
-    for (int u = 0; u < D / 16; ++u)
-#pragma unroll
-      for (int kb = 0; kb < KB; ++kb) s[kb] = mfma32(k_frag<D>(lds_k, kb, u), q[u], s[kb]);
   }
-  // Order of the block's LDS reads and products: kAhead reads first, then each
-  // product followed by the reads that keep kAhead of them under way (an LDS
-  // read takes about as long as 4 products).
-  constexpr int kAhead = 8;
-  constexpr int nv = PV ? 2 * KB * (D / 32) : 0, nk = QK ? KB * (D / 16) : 0;
-  constexpr int reads = 2 * nv + nk;
-  __builtin_amdgcn_sched_group_barrier(0x100, kAhead, 0);
-  int left = reads - kAhead;
 #pragma unroll
-  for (int i = 0; i < nv + nk; ++i) {
-    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-    const int n = left <= 0 ? 0 : (i < nv ? (left < 2 ? left : 2) : 1);
-    if (n == 2) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
-    if (n == 1) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-    left -= n;
+  for (int n = 0; n < all; ++n) {
+    const v8bf x = fr[n % N];
+    if (n < nv)
+      st.o[n % (D / 32)] = mfma32(x, as_bf16(p[n / (D / 32)]), st.o[n % (D / 32)]);
+    else
+      s[(n - nv) % KB] = mfma32(x, q[(n - nv) / KB], s[(n - nv) % KB]);
+    if (n + N < all) fr[n % N] = frag<D, KB>(lds_v, lds_k, n + N, lane);
+    if (n % 2) {
+      between(n / 2);
+      __builtin_amdgcn_sched_barrier(0x4);  // (scalar instructions may move)
+    }
   }
 }
 
@@ -493,44 +501,18 @@ __device__ __forceinline__ void store_row(const AttnArgs& a, const Item& it, int
 }
 
 // ---------------------------------------------------------------- chunk
-// A workgroup of 8 waves has 256 rows of one (sequence, key/value head), 32 a
-// wave, and walks their keys in tiles of TK that all waves share. A tile costs a
-// wave about as many matrix cycles (scores and values) as vector cycles
-// (weights), so the two waves of a SIMD, w and w + 4, work in opposite phases:
-// while one multiplies (values of tile t - 1, scores of tile t), the other takes
-// the weights of its tile; a barrier ends each phase.
-//   phase   waves 0-3           waves 4-7
-//   2t      PV(t-1), QK(t)      weights(t-1)
-//   2t+1    weights(t)          PV(t-1), QK(t)
-// K(t) and V(t-1) are free after phase 2t+1. K and V have three places each: in
-// their weight phase of tile t (the shorter one: products of 32 keys by 32 rows
-// wait for LDS) waves 0-3 issue the loads of K(t+2) and V(t+1) into those of K(t-1)
-// and V(t-2), and by its end have waited for those of the tile before.
-// E4M3 tiles become bf16 on the way into LDS, once a workgroup (converting
-// fragments would cost every wave 8 instructions a product, in the phase in
-// which its partner needs the vector unit: 763 us against TIME_FP8 us for
-// eight chunks of up to 1024 tokens over 9001). They pass through registers: in
-// its weight phase of tile t each wave writes its piece of K(t+2) and V(t+1),
-// loaded one tile before, and loads K(t+3) and V(t+2). Scales come with K and are
-// read in the weight phases: places for 8 tiles.
-template <int D, bool FP8, int TK>
-__global__ __launch_bounds__(512, 2) void attn_chunk_kernel(const AttnArgs a) {
-  using St = Stage<D, false, TK, TK / 4>;
-  using G = Geo<D, false>;
-  constexpr int BM = 256, KB = TK / 32;
-  constexpr int kScale = TK / 16 * 256;  // bytes of one scale area
-  __shared__ __attribute__((aligned(1024))) uint8_t lds_k[3][St::kTile], lds_v[3][St::kTile];
-  __shared__ __attribute__((aligned(1024))) uint8_t lds_s[8][FP8 ? 2 * kScale : 16];
+// A workgroup's BM rows: its sequence and head, its first row and its part of the
+// keys; false: none.
+template <int BM>
+__device__ __forceinline__ bool chunk_item(const AttnArgs& a, Item& it, int& row0, int& split) {
   const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-
   // Work order: consecutive workgroups go to the 8 XCDs in turn; each XCD gets a
   // contiguous run of (head, tile) items, so the tiles of one head share its L2.
   const int items = a.tiles * a.kv_heads * a.splits;
   const int per = (items + 7) / 8;
   const int item = (int)(blockIdx.x % 8) * per + (int)(blockIdx.x / 8);
-  if ((int)(blockIdx.x / 8) >= per || item >= items) return;
-  const int split = item % a.splits;
+  if ((int)(blockIdx.x / 8) >= per || item >= items) return false;
+  split = item % a.splits;
   const int h = item / a.splits / a.tiles;
   int tile = item / a.splits % a.tiles;
   // the tile's sequence: 64 sequences a pass, a lane each, the ones with the most
@@ -560,10 +542,65 @@ __global__ __launch_bounds__(512, 2) void attn_chunk_kernel(const AttnArgs a) {
       tile -= all;
     }
   }
-  if (b < 0) return;
+  if (b < 0 || !item_of(a, __builtin_amdgcn_readfirstlane(b), h, it)) return false;
+  row0 = __builtin_amdgcn_readfirstlane(tile) * BM;
+  return true;
+}
+
+// Tiles [t0, t1) of TK keys of a range of keys that a workgroup takes, and whether
+// some page of them does not exist (every thread of the workgroup calls this).
+template <int TK, int THREADS>
+__device__ __forceinline__ bool chunk_tiles(const AttnArgs& a, const Item& it, const Range& wg, int split, int& t0,
+                                            int& t1) {
+  t0 = wg.lo / TK;
+  t1 = (wg.hi + TK - 1) / TK;
+  if (a.splits > 1) {
+    const int n = max((t1 - t0 + a.splits - 1) / a.splits, 1);
+    t0 = min(t0 + split * n, t1);
+    t1 = min(t0 + n, t1);
+  }
+  t0 = __builtin_amdgcn_readfirstlane(t0);
+  t1 = __builtin_amdgcn_readfirstlane(t1);
+  bool hole = false;
+  const int c1 = t0 < t1 ? (t1 * TK - 1) >> a.page_shift : -1;
+  for (int c = ((t0 * TK) >> a.page_shift) + (int)threadIdx.x; c <= min(c1, a.cols - 1); c += THREADS)
+    hole |= no_page(a, a.table[(int64_t)it.b * a.cols + c]);
+  return __syncthreads_or(hole);
+}
+
+// A workgroup of 8 waves has 256 rows of one (sequence, key/value head), 32 a
+// wave, and walks their keys in tiles of TK that all waves share. A tile costs a
+// wave about as many matrix cycles (scores and values) as vector cycles
+// (weights), so the two waves of a SIMD, w and w + 4, work in opposite phases:
+// while one multiplies (values of tile t - 1, scores of tile t), the other takes
+// the weights of its tile; a barrier ends each phase.
+//   phase   waves 0-3           waves 4-7
+//   2t      PV(t-1), QK(t)      weights(t-1)
+//   2t+1    weights(t)          PV(t-1), QK(t)
+// K(t) and V(t-1) are free after phase 2t+1; K has three places, V four. bf16: in
+// their weight phase of tile t waves 0-3 issue the loads of K(t+2) into the place of
+// K(t-1), waves 4-7 those of V(t+2) into the place of V(t-2), and by its end they have
+// waited for those of the tile before.
+// E4M3 tiles become bf16 on the way into LDS, once a workgroup (converting
+// fragments would cost every wave 8 instructions a product, in the phase in
+// which its partner needs the vector unit). They pass through registers: spread
+// over the products of tile t, each wave writes its piece of K(t+2) or V(t+2), loaded
+// one tile before, and loads that of tile t+3. Scales come along and are read in the
+// weight phases: places for 8 tiles.
+template <int D, bool FP8, int TK>
+__global__ __launch_bounds__(512, 2) void attn_chunk_kernel(const AttnArgs a) {
+  using St = Stage<D, false, TK, TK / 4>;
+  using G = Geo<D, false>;
+  constexpr int BM = 256, KB = TK / 32;
+  constexpr int kScale = TK / 16 * 256;  // bytes of one scale area
+  __shared__ __attribute__((aligned(1024))) uint8_t lds_k[3][St::kTile], lds_v[4][St::kTile];
+  __shared__ __attribute__((aligned(1024))) uint8_t lds_s[8][FP8 ? 2 * kScale : 16];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+
   Item it;
-  if (!item_of(a, __builtin_amdgcn_readfirstlane(b), h, it)) return;
-  const int row0 = __builtin_amdgcn_readfirstlane(tile) * BM;
+  int row0, split;
+  if (!chunk_item<BM>(a, it, row0, split)) return;
 
   const int w0 = row0 + 32 * wave;  // the wave's first row
   const int row = w0 + (lane & 31);
@@ -575,30 +612,18 @@ __global__ __launch_bounds__(512, 2) void attn_chunk_kernel(const AttnArgs a) {
   const Range wg = range_of(a, it, row0, min(row0 + BM, it.rows));
   const Range own = range_of(a, it, w0, max(min(w0 + 32, it.rows), w0 + 1));
   const int vlo = row_lo(a, it, row), vhi = row_hi(a, it, row);
-  int t0 = wg.lo / TK, t1 = (wg.hi + TK - 1) / TK;
-  if (a.splits > 1) {
-    const int n = max((t1 - t0 + a.splits - 1) / a.splits, 1);
-    t0 = min(t0 + split * n, t1);
-    t1 = min(t0 + n, t1);
-  }
-  t0 = __builtin_amdgcn_readfirstlane(t0);
-  t1 = __builtin_amdgcn_readfirstlane(t1);
-  // whether some page of these keys does not exist
-  bool hole = false;
-  const int c1 = t0 < t1 ? (t1 * TK - 1) >> a.page_shift : -1;
-  for (int c = ((t0 * TK) >> a.page_shift) + (int)threadIdx.x; c <= min(c1, a.cols - 1); c += 512)
-    hole |= no_page(a, a.table[(int64_t)it.b * a.cols + c]);
-  const bool holes = __syncthreads_or(hole);
-
+  int t0, t1;
+  const bool holes = chunk_tiles<TK, 512>(a, it, wg, split, t0, t1);
   const bool first = wave < 4;
-  // the rows of a tile that this wave loads, of one 16-row group (bf16: waves 0-3;
-  // E4M3: 16 bytes a lane, with heads of 64 waves 4-7 repeat waves 0-3)
-  const int r0 = FP8 ? wave * (1024 / D) % TK : (wave & 3) * (TK / 4);
+  // the rows of a tile that this wave loads, of one 16-row group (bf16: waves 0-3 of
+  // K and V; E4M3: waves 0-3 of K, 4-7 of V)
+  constexpr int kRows = TK / 4;
+  const int r0 = (wave & 3) * kRows;
   const int g0 = r0 & ~15;
   auto page_at = [&](int t) { return page_of(a, it, t * TK + g0); };
   constexpr std::integral_constant<bool, true> kEdge;
   constexpr std::integral_constant<bool, false> kInner;
-  constexpr int kOps = 2 * St::kLoads;  // loads of an iteration (bf16)
+  constexpr int kOps = St::kLoads;  // loads of an iteration (bf16)
   // bf16: straight into LDS
   auto load = [&](int t, int page, uint8_t* to, auto is_v, auto edge) {
     const Rows16 w = rows_of(a, it, t * TK + g0, page, wg.hi);
@@ -606,96 +631,121 @@ __global__ __launch_bounds__(512, 2) void attn_chunk_kernel(const AttnArgs a) {
     settled(rs);
     St::template rows<is_v, edge>(rs, wg.lo - t * TK - g0, r0, lds_addr(to));
   };
-  // E4M3: this lane's 16 codes of K or V, and the scales of a group
-  const int my_row = r0 + lane / (D / 16), my_chunk = lane % (D / 16);
-  auto fetch = [&](int t, int page, auto is_v, auto edge) {
+  // E4M3: this lane's codes of K (waves 0-3) or V, kMine * 16 of them, where they go as
+  // bf16, and the scales of the wave's group
+  constexpr int kMine = FP8 ? kRows * D / 1024 : 1;
+  const uint8_t* pool = first ? a.k : a.v;
+  const float* pool_s = first ? a.ks : a.vs;
+  int from[kMine], to[kMine][2];
+  if constexpr (FP8) {
+#pragma unroll
+    for (int c = 0; c < kMine; ++c) {
+      const int n = c * 64 + lane, row = r0 + n / (D / 16), chunk = n % (D / 16);
+      const int sw = first ? G::k_swz(row) : G::v_swz(row);
+      from[c] = (row & 15) * D + 16 * chunk;
+      to[c][0] = row * G::kRow + 16 * ((2 * chunk) ^ sw);
+      to[c][1] = row * G::kRow + 16 * ((2 * chunk + 1) ^ sw);
+    }
+  }
+  auto fetch = [&](int t, int page, v4i (&x)[kMine], auto edge) {
     const Rows16 w = rows_of(a, it, t * TK + g0, page, wg.hi);
-    const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
-        const_cast<uint8_t*>(is_v ? a.v : a.k) + w.row * D, (short)0, w.rows * D, 0x00020000);
-    const bool skip = edge && (my_row & 15) < wg.lo - t * TK - g0;
-    return __builtin_amdgcn_raw_buffer_load_b128(rs, skip ? (int)0x80000000 : (my_row & 15) * D + 16 * my_chunk, 0, 0);
+    const int skip = wg.lo - t * TK - g0;
+    if ((r0 & 15) == 0) {
+      v4i rs = resource<4>(pool_s, w);
+      settled(rs);
+      St::template scale_row<edge>(rs, skip, g0, lds_addr(lds_s[t & 7]) + (first ? 0 : kScale));
+    }
+    const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(pool) + w.row * D, (short)0,
+                                                                        w.rows * D, 0x00020000);
+#pragma unroll
+    for (int c = 0; c < kMine; ++c)
+      x[c] = __builtin_amdgcn_raw_buffer_load_b128(rs, edge && from[c] / D < skip ? (int)0x80000000 : from[c], 0, 0);
   };
-  auto fetch_scales = [&](int t, int page, auto edge) {
-    if (r0 != g0) return;
-    const Rows16 w = rows_of(a, it, t * TK + g0, page, wg.hi);
-    v4i sk = resource<4>(a.ks, w), sv = resource<4>(a.vs, w);
-    settled(sk, sv);
-    St::template scale_row<edge>(sk, wg.lo - t * TK - g0, g0, lds_addr(lds_s[t & 7]));
-    St::template scale_row<edge>(sv, wg.lo - t * TK - g0, g0, lds_addr(lds_s[t & 7]) + kScale);
+  auto put = [&](const v4i (&x)[kMine], int t, int k_place, int i) {  // half i % 2 of piece i / 2
+    uint8_t* base = first ? lds_k[k_place] : lds_v[t & 3];
+    *reinterpret_cast<v8bf*>(base + to[i / 2][i % 2]) = cvt_fp8x8(x[i / 2][2 * (i % 2)], x[i / 2][2 * (i % 2) + 1]);
   };
-  auto put = [&](const v4i& x, uint8_t* to, auto is_v) {
-    const int sw = is_v ? G::v_swz(my_row) : G::k_swz(my_row);
-    uint8_t* base = to + my_row * G::kRow;
-    *reinterpret_cast<v8bf*>(base + 16 * ((2 * my_chunk) ^ sw)) = cvt_fp8x8(x[0], x[1]);
-    *reinterpret_cast<v8bf*>(base + 16 * ((2 * my_chunk + 1) ^ sw)) = cvt_fp8x8(x[2], x[3]);
-  };
-  // the end of a phase; no instruction moves from one into another
-  auto phase_end = [&] {
+  // Fragments that a wave holds ahead of its products. With heads of 256, where the
+  // multiply phases are the longer ones, the first of them (values that arrived a
+  // tile before) are read at the end of the weight phase.
+  constexpr int kAhead = D == 256 ? 4 : 8;
+  // the end of a phase; no instruction moves from one into another, and all but the
+  // last `reads` LDS instructions have completed
+  auto phase_end = [&](auto reads) {
     __builtin_amdgcn_sched_barrier(0);
-    lds_reads_done();
+    asm volatile("s_waitcnt lgkmcnt(%0)" ::"n"((int)reads) : "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
     __builtin_amdgcn_sched_barrier(0);
   };
 
+  constexpr std::integral_constant<int, 0> kAll;
+  constexpr std::integral_constant<int, 15> kNone;
+
   // (tiles from t1 on load nothing: no row of theirs is visible)
-  int pv = page_at(t0 + 1), pk = page_at(t0 + 2);  // pages of the next V and K loads
-  v4i fk = {}, fv = {};                            // E4M3: K(t+2) and V(t+1) on their way
+  int p1 = page_at(t0 + 1), p2 = page_at(t0 + 2);  // pages of the next loads
+  v4i fx[kMine];                                   // E4M3: tile t + 2 on its way
   if (t0 < t1) {
     const int p0 = page_at(t0);
     if constexpr (FP8) {
-      fetch_scales(t0, p0, kEdge);
-      fetch_scales(t0 + 1, pv, kInner);
-      const v4i k0 = fetch(t0, p0, kInner, kEdge), k1 = fetch(t0 + 1, pv, kInner, kInner);
-      const v4i v0 = fetch(t0, p0, kEdge, kEdge);
-      fetch_scales(t0 + 2, pk, kInner);
-      fk = fetch(t0 + 2, pk, kInner, kInner);
-      fv = fetch(t0 + 1, pv, kEdge, kInner);
-      put(k0, lds_k[0], kInner);
-      put(k1, lds_k[1], kInner);
-      put(v0, lds_v[0], kEdge);
-      pv = pk;
-      pk = page_at(t0 + 3);
+      v4i x0[kMine], x1[kMine];
+      fetch(t0, p0, x0, kEdge);
+      fetch(t0 + 1, p1, x1, kInner);
+      fetch(t0 + 2, p2, fx, kInner);
+#pragma unroll
+      for (int i = 0; i < 2 * kMine; ++i) {
+        put(x0, t0, 0, i);
+        put(x1, t0 + 1, 1, i);
+      }
     } else if (first) {
       load(t0, p0, lds_k[0], kInner, kEdge);
-      load(t0, p0, lds_v[0], kEdge, kEdge);
-      load(t0 + 1, pv, lds_k[1], kInner, kInner);
+      load(t0 + 1, p1, lds_k[1], kInner, kInner);
+    } else {
+      load(t0, p0, lds_v[t0 & 3], kEdge, kEdge);
+      load(t0 + 1, p1, lds_v[(t0 + 1) & 3], kEdge, kInner);
     }
+    if (FP8) p2 = page_at(t0 + 3);
   }
-  int at = 0, next = 1, last = 2;  // places of tiles t, t + 1 and t + 2 (t - 1)
+  int at = 0, next = 1, last = 2;  // K's places of tiles t, t + 1 and t + 2 (t - 1)
   if (!FP8) dma_wait<0>();
-  phase_end();
-  if (!first) phase_end();
+  phase_end(kAll);
   v16f s[KB];
   v4i p[2 * KB];
+  v8bf fr[kAhead];
 #pragma unroll
   for (int i = 0; i < 2 * KB; ++i) p[i] = v4i{};
+  // (the first tile adds zero weights times its own values)
+  auto prefetch = [&](int t) {
+    const int lane = frag_lane<D>();
+#pragma unroll
+    for (int n = 0; n < kAhead; ++n) fr[n] = frag<D, KB>(lds_v[t & 3], lds_k[0], n, lane);
+  };
+  if (D == 256 && t0 < t1) prefetch(t0);
+  if (!first) phase_end(kAll);
   // Every wave takes every tile, also one that its rows do not see (past their
   // diagonal, before their windows, rows past the end): the phases keep the
   // waves in step, so leaving one out would save nothing.
   for (int t = t0; t < t1; ++t) {
     // multiply
     __builtin_amdgcn_s_setprio(1);
-    // (the first tile adds zero weights times its own values)
-    multiply<D, KB, true, true>(q, st, s, p, lds_v[t > t0 ? last : at], lds_k[at]);
-    __builtin_amdgcn_s_setprio(0);
-    phase_end();
-    // weights. K(t+2) takes K(t-1)'s place, V(t+1) V(t-2)'s
-    if constexpr (FP8) {
-      put(fk, lds_k[last], kInner);
-      put(fv, lds_v[next], kEdge);
-      fetch_scales(t + 3, pk, kInner);
-      fk = fetch(t + 3, pk, kInner, kInner);
-      fv = fetch(t + 2, pv, kEdge, kInner);
-      pv = pk;
-      pk = page_at(t + 4);
-    } else {
-      if (first) {
-        load(t + 1, pv, lds_v[next], kEdge, kInner);
-        load(t + 2, pk, lds_k[last], kInner, kInner);
+    if (D < 256) prefetch(t > t0 ? t - 1 : t);
+    multiply<D, KB, kAhead, true>(q, st, s, p, fr, lds_v[(t > t0 ? t - 1 : t) & 3], lds_k[at], [&](int i) {
+      if constexpr (FP8) {
+        if (i < 2 * kMine) put(fx, t + 2, last, i);
+        if (i == 2 * kMine) fetch(t + 3, p2, fx, kInner);
       }
-      pv = pk;
-      pk = page_at(t + 3);
+    });
+    __builtin_amdgcn_s_setprio(0);
+    phase_end(kAll);
+    // weights
+    if constexpr (FP8) {
+      p2 = page_at(t + 4);
+    } else {
+      if (first)
+        load(t + 2, p2, lds_k[last], kInner, kInner);
+      else
+        load(t + 2, p2, lds_v[(t + 2) & 3], kEdge, kInner);
+      p2 = page_at(t + 3);
     }
     const int key = t * TK;
     uint32_t bad = 0;
@@ -703,16 +753,20 @@ __global__ __launch_bounds__(512, 2) void attn_chunk_kernel(const AttnArgs a) {
       for (int g = 0; g < TK / 16; ++g) bad |= (uint32_t)no_page(a, page_of(a, it, key + 16 * g)) << g;
     const bool masked = holes || key + TK > own.all_hi || key < own.all_lo;
     weight_block<D, FP8, KB, kScale>(a, st, s, p, lds_s[t & 7], masked, vlo - key, vhi - key, bad);
-    if (!FP8 && first) dma_wait<kOps>();  // what the tile before loaded
-    phase_end();
+    if (D == 256) prefetch(t);
+    if (!FP8) dma_wait<kOps>();  // what the tile before loaded
+    phase_end(kNone);  // (no LDS writes in this phase)
     const int x = last;
     last = at;
     at = next;
     next = x;
   }
-  if (t0 < t1) multiply<D, KB, true, false>(q, st, s, p, lds_v[last], lds_k[at]);
+  if (t0 < t1) {
+    if (D < 256) prefetch(t1 - 1);
+    multiply<D, KB, kAhead, false>(q, st, s, p, fr, lds_v[(t1 - 1) & 3], lds_k[at], [](int) {});
+  }
   dma_wait<0>();
-  if (first) phase_end();
+  if (first) phase_end(kAll);
   store_row<D>(a, it, split, row, st);
 }
 
