@@ -450,54 +450,82 @@ __device__ __forceinline__ int32_t page_of(const AttnArgs& a, const Item& it, in
 }
 
 // A sequence's rows and keys from the batch's device data; false: no rows.
-__device__ __forceinline__ bool item_of(const AttnArgs& a, int b, int h, Item& it) {
-  const int64_t s0 = a.q_start[b], s1 = a.q_start[b + 1];
+__device__ __forceinline__ bool item_from(const AttnArgs& a, int b, int h, int64_t s0, int64_t s1, int64_t len,
+                                          Item& it) {
   if (s0 < 0 || s1 > a.T || s1 <= s0) return false;
   it.b = b;
   it.h = h;
   it.q0 = s0;
   it.n = (int)(s1 - s0);
-  const int64_t cap = (int64_t)a.cols << a.page_shift;
-  it.len = (int)max((int64_t)0, min((int64_t)a.kv_len[b], cap));
+  it.len = (int)max((int64_t)0, min(len, (int64_t)a.cols << a.page_shift));
   it.rows = it.n * a.group;
   return true;
 }
+__device__ __forceinline__ bool item_of(const AttnArgs& a, int b, int h, Item& it) {
+  return item_from(a, b, h, a.q_start[b], a.q_start[b + 1], a.kv_len[b], it);
+}
 
-// One row's result: final, or a part for attn_join_kernel. This lane holds the
-// head's values 32 d + 8 (i / 4) + 4 h + i % 4 in o[d][i].
+// One row's part for attn_join_kernel. This lane holds the head's values 32 d +
+// 8 (i / 4) + 4 h + i % 4 in o[d][i].
 template <int D>
-__device__ __forceinline__ void store_row(const AttnArgs& a, const Item& it, int split, int row, const State<D>& st) {
+__device__ __forceinline__ void store_part(const AttnArgs& a, const Item& it, int split, int row, const State<D>& st) {
   const int h = (threadIdx.x & 63) >> 5;
   const float l = st.l + __shfl_xor(st.l, 32, kWave);
   if (row >= it.rows) return;
   const int64_t t = it.q0 + row / a.group;
   const int qh = it.h * a.group + row % a.group;
-  const int64_t heads = (int64_t)a.kv_heads * a.group;
-  if (a.splits > 1) {
-    const int64_t at = (split * a.T + t) * heads + qh;
-    if (h == 0) {
-      a.pml[2 * at] = st.m;
-      a.pml[2 * at + 1] = l;
-    }
-    if (st.m == -kInf && l == 0.0f) return;  // no key: the join does not read it
-#pragma unroll
-    for (int d = 0; d < D / 32; ++d)
-#pragma unroll
-      for (int b = 0; b < 4; ++b)
-        *reinterpret_cast<v4f*>(a.po + at * D + 32 * d + 8 * b + 4 * h) =
-            v4f{st.o[d][4 * b], st.o[d][4 * b + 1], st.o[d][4 * b + 2], st.o[d][4 * b + 3]};
-    return;
+  const int64_t at = (split * a.T + t) * ((int64_t)a.kv_heads * a.group) + qh;
+  if (h == 0) {
+    a.pml[2 * at] = st.m;
+    a.pml[2 * at + 1] = l;
   }
-  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-  uint16_t* dst = a.out + t * a.ldo + (int64_t)qh * D;
+  if (st.m == -kInf && l == 0.0f) return;  // no key: the join does not read it
 #pragma unroll
   for (int d = 0; d < D / 32; ++d)
 #pragma unroll
     for (int b = 0; b < 4; ++b)
-      *reinterpret_cast<uint2*>(dst + 32 * d + 8 * b + 4 * h) =
-          make_uint2(pack_bf16x2(st.o[d][4 * b] * inv, st.o[d][4 * b + 1] * inv),
-                     pack_bf16x2(st.o[d][4 * b + 2] * inv, st.o[d][4 * b + 3] * inv));
-  if (a.lse && h == 0) a.lse[t * heads + qh] = l == 0.0f ? -kInf : (st.m + log2f(l)) * kLn2;
+      *reinterpret_cast<v4f*>(a.po + at * D + 32 * d + 8 * b + 4 * h) =
+          v4f{st.o[d][4 * b], st.o[d][4 * b + 1], st.o[d][4 * b + 2], st.o[d][4 * b + 3]};
+}
+
+// A wave's 32 rows, in whole lines: through 64 D bytes of LDS of its own (128
+// columns at a time), 16-byte chunks exclusive-or-ed by the row.
+template <int D>
+__device__ __forceinline__ void store_rows(const AttnArgs& a, const Item& it, int w0, const State<D>& st,
+                                           uint8_t* lds) {
+  constexpr int kCols = D < 128 ? D : 128, kChunks = kCols / 8, kLine = 2 * kCols;
+  const int lane = threadIdx.x & 63;
+  const int r = lane & 31, h = lane >> 5;
+  const int64_t heads = (int64_t)a.kv_heads * a.group;
+  const float l = st.l + __shfl_xor(st.l, 32, kWave);
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll
+  for (int c0 = 0; c0 < D; c0 += kCols) {
+    if (c0) lds_reads_done();
+#pragma unroll
+    for (int d = 0; d < kCols / 32; ++d)
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        const v16f& o = st.o[c0 / 32 + d];
+        *reinterpret_cast<uint2*>(lds + r * kLine + 16 * ((4 * d + b) ^ (r & (kChunks - 1))) + 8 * h) =
+            make_uint2(pack_bf16x2(o[4 * b] * inv, o[4 * b + 1] * inv),
+                       pack_bf16x2(o[4 * b + 2] * inv, o[4 * b + 3] * inv));
+      }
+    lds_reads_done();  // (and writes; one wave's LDS)
+#pragma unroll
+    for (int i = 0; i < kChunks / 2; ++i) {
+      const int row = i * (64 / kChunks) + lane / kChunks, c = lane % kChunks;
+      const uint4 x = *reinterpret_cast<const uint4*>(lds + row * kLine + 16 * (c ^ (row & (kChunks - 1))));
+      const int gr = w0 + row;
+      if (gr < it.rows)
+        *reinterpret_cast<uint4*>(a.out + (it.q0 + gr / a.group) * a.ldo +
+                                  (int64_t)(it.h * a.group + gr % a.group) * D + c0 + 8 * c) = x;
+    }
+  }
+  const int gr = w0 + r;
+  if (a.lse && h == 0 && gr < it.rows)
+    a.lse[(it.q0 + gr / a.group) * heads + it.h * a.group + gr % a.group] =
+        l == 0.0f ? -kInf : (st.m + log2f(l)) * kLn2;
 }
 
 // ---------------------------------------------------------------- chunk
@@ -519,11 +547,13 @@ __device__ __forceinline__ bool chunk_item(const AttnArgs& a, Item& it, int& row
   // keys first (of a batch of many lengths the longest work must not come last)
   int b = -1;
   for (int b0 = 0; b0 < a.B && b < 0; b0 += 64) {
-    int mine = 0, keys = 0;
+    int mine = 0, keys = 0, from = 0, to = 0;
     if (b0 + lane < a.B) {
-      const int64_t n = (int64_t)a.q_start[b0 + lane + 1] - a.q_start[b0 + lane];
-      mine = n > 0 && n <= a.T ? (int)((n * a.group + BM - 1) / BM) : 0;
+      from = a.q_start[b0 + lane];
+      to = a.q_start[b0 + lane + 1];
       keys = a.kv_len[b0 + lane];
+      const int64_t n = (int64_t)to - from;
+      mine = n > 0 && n <= a.T ? (int)((n * a.group + BM - 1) / BM) : 0;
     }
     int before = 0, all = 0;  // tiles of the pass that come before this lane's; all
     for (int j = 0; j < min(a.B - b0, 64); ++j) {
@@ -538,34 +568,16 @@ __device__ __forceinline__ bool chunk_item(const AttnArgs& a, Item& it, int& row
       tile -= __builtin_amdgcn_readlane(before, j);
       // its last tiles first: with a causal mask they have the most keys
       tile = __builtin_amdgcn_readlane(mine, j) - 1 - tile;
+      if (!item_from(a, b, h, __builtin_amdgcn_readlane(from, j), __builtin_amdgcn_readlane(to, j),
+                     __builtin_amdgcn_readlane(keys, j), it))
+        return false;
     } else {
       tile -= all;
     }
   }
-  if (b < 0 || !item_of(a, __builtin_amdgcn_readfirstlane(b), h, it)) return false;
+  if (b < 0) return false;
   row0 = __builtin_amdgcn_readfirstlane(tile) * BM;
   return true;
-}
-
-// Tiles [t0, t1) of TK keys of a range of keys that a workgroup takes, and whether
-// some page of them does not exist (every thread of the workgroup calls this).
-template <int TK, int THREADS>
-__device__ __forceinline__ bool chunk_tiles(const AttnArgs& a, const Item& it, const Range& wg, int split, int& t0,
-                                            int& t1) {
-  t0 = wg.lo / TK;
-  t1 = (wg.hi + TK - 1) / TK;
-  if (a.splits > 1) {
-    const int n = max((t1 - t0 + a.splits - 1) / a.splits, 1);
-    t0 = min(t0 + split * n, t1);
-    t1 = min(t0 + n, t1);
-  }
-  t0 = __builtin_amdgcn_readfirstlane(t0);
-  t1 = __builtin_amdgcn_readfirstlane(t1);
-  bool hole = false;
-  const int c1 = t0 < t1 ? (t1 * TK - 1) >> a.page_shift : -1;
-  for (int c = ((t0 * TK) >> a.page_shift) + (int)threadIdx.x; c <= min(c1, a.cols - 1); c += THREADS)
-    hole |= no_page(a, a.table[(int64_t)it.b * a.cols + c]);
-  return __syncthreads_or(hole);
 }
 
 // A workgroup of 8 waves has 256 rows of one (sequence, key/value head), 32 a
@@ -604,16 +616,17 @@ __global__ __launch_bounds__(512, 2) void attn_chunk_kernel(const AttnArgs a) {
 
   const int w0 = row0 + 32 * wave;  // the wave's first row
   const int row = w0 + (lane & 31);
-  v8bf q[D / 16];
-  load_q<D>(a, it, row, q);
-  State<D> st;
-  st.clear();
-
   const Range wg = range_of(a, it, row0, min(row0 + BM, it.rows));
   const Range own = range_of(a, it, w0, max(min(w0 + 32, it.rows), w0 + 1));
   const int vlo = row_lo(a, it, row), vhi = row_hi(a, it, row);
-  int t0, t1;
-  const bool holes = chunk_tiles<TK, 512>(a, it, wg, split, t0, t1);
+  int t0 = wg.lo / TK, t1 = (wg.hi + TK - 1) / TK;
+  if (a.splits > 1) {
+    const int n = max((t1 - t0 + a.splits - 1) / a.splits, 1);
+    t0 = min(t0 + split * n, t1);
+    t1 = min(t0 + n, t1);
+  }
+  t0 = __builtin_amdgcn_readfirstlane(t0);
+  t1 = __builtin_amdgcn_readfirstlane(t1);
   const bool first = wave < 4;
   // the rows of a tile that this wave loads, of one 16-row group (bf16: waves 0-3 of
   // K and V; E4M3: waves 0-3 of K, 4-7 of V)
@@ -706,9 +719,19 @@ __global__ __launch_bounds__(512, 2) void attn_chunk_kernel(const AttnArgs a) {
     }
     if (FP8) p2 = page_at(t0 + 3);
   }
+  // whether some page of these keys does not exist
+  bool hole = false;
+  const int c1 = t0 < t1 ? (t1 * TK - 1) >> a.page_shift : -1;
+  for (int c = ((t0 * TK) >> a.page_shift) + (int)threadIdx.x; c <= min(c1, a.cols - 1); c += 512)
+    hole |= no_page(a, a.table[(int64_t)it.b * a.cols + c]);
+  v8bf q[D / 16];
+  load_q<D>(a, it, row, q);
+  State<D> st;
+  st.clear();
   int at = 0, next = 1, last = 2;  // K's places of tiles t, t + 1 and t + 2 (t - 1)
   if (!FP8) dma_wait<0>();
-  phase_end(kAll);
+  lds_reads_done();  // (and writes)
+  const bool holes = __syncthreads_or(hole);
   v16f s[KB];
   v4i p[2 * KB];
   v8bf fr[kAhead];
@@ -767,7 +790,12 @@ __global__ __launch_bounds__(512, 2) void attn_chunk_kernel(const AttnArgs a) {
   }
   dma_wait<0>();
   if (first) phase_end(kAll);
-  store_row<D>(a, it, split, row, st);
+  if (a.splits > 1) {
+    store_part<D>(a, it, split, row, st);
+    return;
+  }
+  __syncthreads();  // V's places are free
+  store_rows<D>(a, it, w0, st, &lds_v[0][0] + wave * (TK * D));
 }
 
 // ---------------------------------------------------------------- step
