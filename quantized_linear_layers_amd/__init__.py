@@ -540,19 +540,25 @@ def _rows_arg(t, name, dev, head_dim, heads=None):
     projection)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a tensor")
-    if t.device != dev:
-        raise ValueError(f"{name} must be a tensor on {dev}, got {t.device}")
     if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-    if t.dim() != 3:
-        raise ValueError(f"{name} must have 3 dims, got {tuple(t.shape)}")
-    T, H, D = t.shape
+    if t.device != dev:
+        raise ValueError(f"{name} must be a tensor on {dev}, got {t.device}")
+    shape = t.shape
+    if len(shape) != 3:
+        raise ValueError(f"{name} must have 3 dims, got {tuple(shape)}")
+    T, H, D = shape
     if D != head_dim or (heads is not None and H != heads):
         raise ValueError(f"{name}: expected {'any' if heads is None else heads} heads of {head_dim}, got {H} of {D}")
     s0, s1, s2 = t.stride()
     if s2 != 1 or (s1 != D and H > 1):
         raise ValueError(f"{name}: the heads of a row must lie together")
     return T, H, s0 if T > 1 else H * D  # (the stride of a single row says nothing)
+
+
+def _like(t):
+    """A new contiguous tensor of t's shape."""
+    return torch.empty_like(t) if t.is_contiguous() else t.new_empty(t.shape)
 
 
 def _positions_arg(t, dev, T):
@@ -567,15 +573,11 @@ def _on(dev, want, name):
         raise ValueError(f"{name} is on {dev}, expected {want}")
 
 
-def _call_on(dev: torch.device, name: str, *args):
-    """A library call on `dev`'s current stream, with `dev` the current device."""
-    if dev.index == torch.cuda.current_device():
-        st = getattr(_lib, name)(*args, _raw_stream(dev.index))
-    else:
-        with torch.cuda.device(dev):
-            st = getattr(_lib, name)(*args, _raw_stream(dev.index))
+def _enqueue(dev: torch.device, fn, *args):
+    """A library call on the current stream of `dev`, the current device."""
+    st = fn(*args, _raw_stream(dev.index))
     if st != OK:
-        raise QlinError(name, st)
+        raise QlinError(fn.__name__, st)
 
 
 # An attention workspace beyond this is not kept between calls.
@@ -698,21 +700,26 @@ class PagedBatch:
         self._c = _KVBatch(q_start.data_ptr(), kv_len.data_ptr(), page_table.data_ptr(), B,
                            page_table.shape[1], self.max_q)
         self._ref = C.byref(self._c)
+        self._ws_bytes = {}
 
 
-def rope(x, positions, rope: Rope, out=None, inverse=False):
-    """Rotary positions of x [T, H, D] (bf16) at positions int32 [T]; `out` may be
-    x. inverse=True turns the other way (the gradient of the rotation)."""
-    D, dev = rope.head_dim, rope.device
+def rope(x, positions, plan: Rope, out=None, inverse=False):
+    """Rotary positions of x [T, H, D] (bf16) at positions int32 [T] by
+    `plan`; `out` may be x. inverse=True turns the other way (the gradient of the
+    rotation)."""
+    D, dev = plan.head_dim, plan.device
     T, H, ldx = _rows_arg(x, "x", dev, D)
+    if dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return rope(x, positions, plan, out, inverse)
     pos = _positions_arg(positions, dev, T)
     if out is None:
-        out, ldy = x.new_empty((T, H, D)), H * D
+        out, ldy = _like(x), H * D
     else:
         T2, _, ldy = _rows_arg(out, "out", dev, D, H)
         if T2 != T:
             raise ValueError("out shape mismatch")
-    _call_on(dev, "qlin_rope", x.data_ptr(), ldx, T, H, D, pos, rope._ref, 1 if inverse else 0, out.data_ptr(), ldy)
+    _enqueue(dev, _lib.qlin_rope, x.data_ptr(), ldx, T, H, D, pos, plan._ref, 1 if inverse else 0, out.data_ptr(), ldy)
     return out
 
 
@@ -725,12 +732,15 @@ def kv_append(cache: PagedKV, batch: PagedBatch, k, v, rope: Rope | None = None,
     D, dev = cache.head_dim, cache.device
     _on(batch.device, dev, "batch")
     T, _, ldk = _rows_arg(k, "k", dev, D, cache.kv_heads)
+    if dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return kv_append(cache, batch, k, v, rope, q, q_out, positions)
     T2, _, ldv = _rows_arg(v, "v", dev, D, cache.kv_heads)
     ldq = ldqo = heads = 0
     if q is not None:
         T3, heads, ldq = _rows_arg(q, "q", dev, D)
         if q_out is None:
-            q_out, ldqo = q.new_empty((T3, heads, D)), heads * D
+            q_out, ldqo = _like(q), heads * D
         else:
             T4, _, ldqo = _rows_arg(q_out, "q_out", dev, D, heads)
             T3 = T3 if T4 == T3 else -1
@@ -744,7 +754,7 @@ def kv_append(cache: PagedKV, batch: PagedBatch, k, v, rope: Rope | None = None,
         _on(rope.device, dev, "rope")
         if rope.head_dim != D:
             raise ValueError("rope and cache differ in head_dim")
-    _call_on(dev, "qlin_kv_append", cache._ref, batch._ref, T, k.data_ptr(), ldk, v.data_ptr(), ldv,
+    _enqueue(dev, _lib.qlin_kv_append, cache._ref, batch._ref, T, k.data_ptr(), ldk, v.data_ptr(), ldv,
              None if rope is None else rope._ref, None if positions is None else _positions_arg(positions, dev, T),
              None if q is None else q.data_ptr(), ldq, heads, None if q is None else q_out.data_ptr(), ldqo)
     return q_out
@@ -761,16 +771,22 @@ def attn_paged(cache: PagedKV, batch: PagedBatch, q, scale=None, causal=True, wi
     D, dev = cache.head_dim, cache.device
     _on(batch.device, dev, "batch")
     T, heads, ldq = _rows_arg(q, "q", dev, D)
+    if dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return attn_paged(cache, batch, q, scale, causal, window, out, return_lse)
     if out is None:
-        out, ldo = q.new_empty((T, heads, D)), heads * D
+        out, ldo = _like(q), heads * D
     else:
         T2, _, ldo = _rows_arg(out, "out", dev, D, heads)
         if T2 != T:
             raise ValueError("out shape mismatch")
     lse = q.new_empty((T, heads), dtype=torch.float32) if return_lse else None
-    nb = _lib.qlin_attn_workspace_bytes(cache._ref, batch._ref, T, heads)
+    key = (T, heads, D, cache.kv_heads, cache.page_size)  # what the size depends on beside the batch's own
+    nb = batch._ws_bytes.get(key)
+    if nb is None:
+        nb = batch._ws_bytes[key] = _lib.qlin_attn_workspace_bytes(cache._ref, batch._ref, T, heads)
     ws = _attn_workspace(nb, dev) if nb else None
-    _call_on(dev, "qlin_attn_paged", cache._ref, batch._ref, T, q.data_ptr(), ldq, heads,
+    _enqueue(dev, _lib.qlin_attn_paged, cache._ref, batch._ref, T, q.data_ptr(), ldq, heads,
              D ** -0.5 if scale is None else float(scale), 1 if causal else 0, int(window), out.data_ptr(), ldo,
              None if lse is None else lse.data_ptr(), None if ws is None else ws.data_ptr(), nb)
     return (out, lse) if return_lse else out
