@@ -369,14 +369,18 @@ int qlin_moe_w4a16_workspace_layout(int64_t T, int64_t H, int64_t I, int64_t E, 
  *             row: an idle slot). Rows outside every sequence (padding behind
  *             the last one) are neither read nor written;
  *   kv_len    [batch] int32: tokens of sequence b in the cache, its new ones
- *             included (they are the last ones). A length over
- *             table_cols * page_size counts as that;
+ *             included (they are the last ones). Of a sequence that is longer
+ *             than its row of the page table the tokens behind the table's
+ *             reach are neither stored nor seen;
  *   page_table [batch][table_cols] int32: page of each page_size tokens;
  *   max_q     at least the longest sequence's count of new tokens (a host
  *             value, it selects kernels; with fewer the result is the same).
  * The arrays are device data, read when the kernels run (a captured graph
  * sees the values of each replay), so their values are no errors: the keys of
  * a page outside [0, pages) are not written and not seen.
+ * Limits (QLIN_ERR_SHAPE beyond): batch <= 65535, pages * kv_heads < 2^31,
+ * table_cols * page_size < 2^31 - 65536, T * q_heads < 2^30, batch * kv_heads <
+ * 2^24.
  * ------------------------------------------------------------------------ */
 enum { QLIN_KV_BF16 = 0, QLIN_KV_E4M3 = 1 };
 
@@ -448,8 +452,11 @@ int qlin_rope(const qlin_bf16* x, int64_t ldx, int64_t T, int64_t H, int64_t D,
  * q [T][ldq] (q_heads heads), turned the same way, goes to q_out [T][ldqo] in
  * bf16; q = q_out = NULL leaves the queries out, q_out may be q itself. A
  * token whose slot lies before 0 or outside the page table, or in a page
- * outside [0, pages), is not stored (its query is still turned). No two
- * sequences may store into one page's same slot. */
+ * outside [0, pages), is not stored (its query is still turned). Sequences may
+ * share pages of earlier tokens, but no two may store into the same slot (either's
+ * row may remain). Values that are not finite are stored as they are in bf16; an
+ * E4M3 row that has one is not defined. k and v must not overlap q_out or the
+ * cache. */
 int qlin_kv_append(const qlin_kv_cache* cache, const qlin_kv_batch* batch, int64_t T,
                    const qlin_bf16* k, int64_t ldk, const qlin_bf16* v, int64_t ldv,
                    const qlin_rope_plan* rope, const int32_t* positions, const qlin_bf16* q,
@@ -465,8 +472,11 @@ int qlin_kv_append(const qlin_kv_cache* cache, const qlin_kv_batch* batch, int64
  * with a window > 0 (which needs causal). A row that sees no key gets zeros and
  * lse = -inf. Scores, softmax statistics and sums are fp32, products are bf16
  * MFMA: the weights exp(z_j - max) (times v's scale) are rounded to bf16
- * before they multiply the values. Cached values behind a sequence's end and
- * outside every page that it uses never reach its result, NaN included.
+ * before they multiply the values. What lies in the cache behind a sequence's
+ * end, in pages that it does not use, or before the window of its first new token
+ * never reaches its result, NaN included; a value (of v) that one of its new
+ * tokens sees must be finite, else it may reach the rows of all of them. q and
+ * out must not overlap.
  *   q, out [T][ldq], [T][ldo] bf16 (ld >= q_heads * head_dim, multiples of 8);
  *   lse [T][q_heads] fp32 or NULL; scale finite.
  * Workspace: qlin_attn_workspace_bytes bytes, 256-byte aligned (0 when the key

@@ -882,14 +882,13 @@ void qo_rope(const uint16_t* x, int64_t ldx, int64_t T, int64_t H, int64_t D, co
 }
 
 /* For each of T rows its sequence (-1: none) and its place in it. */
-static void row_places(const int32_t* q_start, const int32_t* kv_len, int64_t B, int64_t T, int64_t cap,
-                       int64_t* seq, int64_t* place) {
+static void row_places(const int32_t* q_start, const int32_t* kv_len, int64_t B, int64_t T, int64_t* seq,
+                       int64_t* place) {
   for (int64_t t = 0; t < T; ++t) seq[t] = -1;
   for (int64_t b = 0; b < B; ++b)
     for (int64_t t = q_start[b]; t < q_start[b + 1] && t < T; ++t) {
-      int64_t len = kv_len[b] < cap ? kv_len[b] : cap;
       seq[t] = b;
-      place[t] = len - (q_start[b + 1] - q_start[b]) + (t - q_start[b]);
+      place[t] = (int64_t)kv_len[b] - (q_start[b + 1] - q_start[b]) + (t - q_start[b]);
     }
 }
 
@@ -899,7 +898,7 @@ static void row_places(const int32_t* q_start, const int32_t* kv_len, int64_t B,
 void qo_kv_slots(const int32_t* q_start, const int32_t* kv_len, const int32_t* table, int64_t B, int64_t cols,
                  int64_t page_size, int64_t pages, int64_t T, int64_t* slot, int64_t* place) {
   int64_t* seq = malloc(sizeof(int64_t) * (size_t)(T > 0 ? T : 1));
-  row_places(q_start, kv_len, B, T, cols * page_size, seq, place);
+  row_places(q_start, kv_len, B, T, seq, place);
   for (int64_t t = 0; t < T; ++t) {
     slot[t] = -1;
     if (seq[t] < 0) {
@@ -931,7 +930,7 @@ void qo_attn_paged(const uint16_t* q, int64_t ldq, int64_t T, int64_t Hq, int64_
   int64_t* seq = malloc(sizeof(int64_t) * (size_t)(T > 0 ? T : 1));
   int64_t* place = malloc(sizeof(int64_t) * (size_t)(T > 0 ? T : 1));
   const int64_t cap = cols * page_size;
-  row_places(q_start, kv_len, B, T, cap, seq, place);
+  row_places(q_start, kv_len, B, T, seq, place);
 #pragma omp parallel for schedule(dynamic, 1) collapse(2)
   for (int64_t t = 0; t < T; ++t)
     for (int64_t h = 0; h < Hq; ++h) {

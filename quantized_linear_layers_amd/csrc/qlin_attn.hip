@@ -120,7 +120,9 @@ struct Geo {
 struct Item {
   int b, h;     // sequence, key/value head
   int64_t q0;   // its first row in q
-  int n, len;   // new tokens, keys
+  int n;        // new tokens
+  int first;    // the first one's place in the sequence (below 0: before it)
+  int len;      // keys: the sequence's, at most what its page table reaches
   int rows;     // packed rows
 };
 
@@ -417,11 +419,11 @@ __device__ __forceinline__ void load_q(const AttnArgs& a, const Item& it, int ro
 // Keys [row_lo, row_hi) that a packed row sees (none: row_hi <= row_lo).
 __device__ __forceinline__ int row_hi(const AttnArgs& a, const Item& it, int row) {
   if (row >= it.rows) return 0;
-  return a.causal ? it.len - it.n + row / a.group + 1 : it.len;
+  return a.causal ? min(it.first + row / a.group + 1, it.len) : it.len;
 }
 __device__ __forceinline__ int row_lo(const AttnArgs& a, const Item& it, int row) {
   if (a.window <= 0) return 0;
-  const int64_t lo = (int64_t)it.len - it.n + row / a.group + 1 - a.window;
+  const int64_t lo = (int64_t)it.first + row / a.group + 1 - a.window;
   return lo > 0 ? (int)lo : 0;
 }
 // Of rows [row0, row1): keys [lo, hi) that some row sees, and [all_lo, all_hi)
@@ -431,8 +433,8 @@ struct Range {
 };
 __device__ __forceinline__ Range range_of(const AttnArgs& a, const Item& it, int row0, int row1) {
   Range r;
-  r.lo = row_lo(a, it, row0);
   r.hi = max(row_hi(a, it, row1 - 1), 0);
+  r.lo = min(row_lo(a, it, row0), r.hi);
   r.all_lo = row_lo(a, it, row1 - 1);
   r.all_hi = row_hi(a, it, row0);
   r.lo = __builtin_amdgcn_readfirstlane(r.lo);
@@ -457,7 +459,9 @@ __device__ __forceinline__ bool item_from(const AttnArgs& a, int b, int h, int64
   it.h = h;
   it.q0 = s0;
   it.n = (int)(s1 - s0);
-  it.len = (int)max((int64_t)0, min(len, (int64_t)a.cols << a.page_shift));
+  len = max(len, (int64_t)0);
+  it.first = (int)(len - it.n);
+  it.len = (int)min(len, (int64_t)a.cols << a.page_shift);
   it.rows = it.n * a.group;
   return true;
 }
@@ -867,7 +871,8 @@ __global__ __launch_bounds__(NW * 64, step_waves(D, FP8, RB)) void attn_step_ker
       longest = max(longest, __shfl_xor(longest, o, kWave));
       sum += __shfl_xor(sum, o, kWave);
     }
-    const int share = max((longest + a.splits - 1) / a.splits, (int)(sum * (float)a.kv_heads * (1.0f / kPieces)));
+    // (at least 1: a batch without any key has rows to write too)
+    const int share = max(max((longest + a.splits - 1) / a.splits, 1), (int)(sum * (float)a.kv_heads * (1.0f / kPieces)));
     const int n = __builtin_amdgcn_readfirstlane((share + NW - 1) / NW * NW);
     parts = max((t1 - t0 + n - 1) / n, 1);
     if (split >= parts) return;
@@ -1283,7 +1288,7 @@ int launch_attn(const qlin_kv_cache& cache, const qlin_kv_batch& batch, int64_t 
   a.ldo = ldo;
   a.pages = (int)cache.pages;
   a.T = T;
-  a.window = window;
+  a.window = std::min<int64_t>(window, (int64_t)1 << 32);  // (more is all keys; sums of it must not overflow)
   a.B = (int)batch.batch;
   a.cols = (int)batch.table_cols;
   a.page_shift = __builtin_ctzll((unsigned long long)cache.page_size);

@@ -83,8 +83,7 @@ __global__ __launch_bounds__(kRopeThreads) void rope_kernel(const RopeArgs a) {
     while (b < a.B && (int64_t)a.q_start[b + 1] <= t) ++b;
     if (b >= a.B || t < (int64_t)a.q_start[b]) return;  // padding: left as it is
     const int64_t s0 = a.q_start[b], s1 = a.q_start[b + 1];
-    const int64_t len = min((int64_t)a.kv_len[b], a.cols << a.page_shift);
-    index = len - (s1 - s0) + (t - s0);
+    index = a.kv_len[b] - (s1 - s0) + (t - s0);
     const int64_t col = index >> a.page_shift;
     if (index >= 0 && col < a.cols) {
       page = a.table[b * a.cols + col];

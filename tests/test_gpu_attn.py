@@ -299,6 +299,79 @@ def test_length_over_the_table(q, oracle):
     assert (host(got) == 0).all() and (host(lse) == -np.inf).all()
 
 
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("new,G,window", [(3, 4, 0), (3, 4, 2), (3, 4, 40), (90, 2, 0), (90, 2, 25), (5, 16, 3)])
+def test_sequences_longer_than_their_tables(q, oracle, new, G, window, fmt):
+    """The tokens behind the table's reach are not stored and not seen; the others
+    keep their places."""
+    rng = np.random.default_rng(new + window)
+    D, Hkv, page, cols = 128, 2, 16, 8
+    kv = [cols * page + 2, cols * page + new + 40, 100]
+    table = rng.permutation(3 * cols).reshape(3, cols).astype(np.int32)
+    start = (np.arange(4) * new).astype(np.int32)
+    pages, T, Hq = 3 * cols, 3 * new, Hkv * G
+    cache = q.PagedKV.empty(pages, Hkv, D, page, fmt)
+    fill_cache(q, rng, cache, None, np.array([cols * page] * 3), table)
+    before = [host(t) for t in (cache.k, cache.v)]
+    b = q.PagedBatch(dev(start), dev(np.array(kv, np.int32)), dev(table), new)
+    qkv = projections(rng, (T, Hq + 2 * Hkv, D))
+    d, plan = dev(qkv), q.Rope(D)
+    qq = q.kv_append(cache, b, d[:, Hq:Hq + Hkv], d[:, Hq + Hkv:], rope=plan, q=d[:, :Hq])
+    slot, place = oracle.kv_slots(start, kv, table, page, pages, T)
+    assert (slot >= 0).sum() == (new - 2) + new and place[new - 1] == cols * page + 1
+    y, mag = oracle.rope(qkv, place, host(plan.turns), D)
+    rope_check(host(qq), y[:, :Hq], mag[:, :Hq], "queries")
+    kept = np.ones((pages, page), bool)
+    kept[slot[slot >= 0] // page, slot[slot >= 0] % page] = False
+    for t, o in zip((cache.k, cache.v), before):
+        assert np.array_equal(host(t).transpose(0, 2, 1, 3)[kept], o.transpose(0, 2, 1, 3)[kept])
+    got, lse = q.attn_paged(cache, b, qq, window=window, return_lse=True)
+    e4 = fmt == "e4m3"
+    r = oracle.attn_paged(host(qq), host(cache.k), host(cache.v), host(cache.k_scale) if e4 else None,
+                          host(cache.v_scale) if e4 else None, start, kv, table, D ** -0.5, True, window)
+    attn_check(r, host(got), host(lse), D, f"longer than the table {fmt}")
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("new,G", [(1, 4), (40, 2)])
+def test_no_key_at_all_and_the_next_call(q, oracle, new, G, fmt):
+    """A batch of empty sequences over tables that split the key axis: zeros, and
+    the workspace serves the next call."""
+    rng = np.random.default_rng(new)
+    B, Hkv, D, page, cols = 3, 2, 128, 16, 64
+    T, Hq = B * new, Hkv * G
+    cache = q.PagedKV.empty(B * cols, Hkv, D, page, fmt)
+    table = rng.permutation(B * cols).reshape(B, cols).astype(np.int32)
+    fill_cache(q, rng, cache, None, np.array([cols * page] * B), table)
+    start = (np.arange(B + 1) * new).astype(np.int32)
+    x = projections(rng, (T, Hq, D))
+    lens = torch.zeros(B, dtype=torch.int32, device="cuda")
+    b = q.PagedBatch(dev(start), lens, dev(table), new)
+    nbytes = q.lib().qlin_attn_workspace_bytes(cache._c, b._c, T, Hq)
+    assert nbytes > 0
+    e4 = fmt == "e4m3"
+    for kv in ([0, 0, 0], [0, 900, 3], [-5, 0, 0], [1000, 1, 400]):
+        lens.copy_(torch.tensor(kv, dtype=torch.int32))
+        got, lse = q.attn_paged(cache, b, dev(x), return_lse=True)
+        r = oracle.attn_paged(x, host(cache.k), host(cache.v), host(cache.k_scale) if e4 else None,
+                              host(cache.v_scale) if e4 else None, start, kv, table, D ** -0.5)
+        attn_check(r, host(got), host(lse), D, f"{kv} {fmt}")
+        assert not q.workspace(nbytes, got.device)[:65536].any().item(), "counters"
+
+
+@pytest.mark.parametrize("new,G", [(2, 4), (40, 2)])
+def test_window_of_any_size(q, new, G):
+    rng = np.random.default_rng(3)
+    cache = q.PagedKV.empty(64, 1, 128, 16)
+    table = rng.permutation(64)[None].astype(np.int32)
+    fill_cache(q, rng, cache, None, np.array([1000]), table)
+    b = q.PagedBatch(dev(np.array([0, new], np.int32)), dev(np.array([1000], np.int32)), dev(table), new)
+    x = dev(projections(rng, (new, G, 128)))
+    ref = q.attn_paged(cache, b, x)
+    for window in (1000, 1024, 2 ** 31 - 1, 2 ** 31, 2 ** 32 + 5, 2 ** 63 - 1):
+        assert torch.equal(q.attn_paged(cache, b, x, window=window), ref), window
+
+
 @pytest.mark.parametrize("new,G", [(1, 4), (80, 2)])
 @pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
 def test_pool_beyond_32_bit_offsets(q, oracle, fmt, new, G):
@@ -535,6 +608,76 @@ def test_two_streams_and_two_graphs(q):
         torch.cuda.synchronize()
         for i, (o, l) in enumerate(outs):
             assert np.array_equal(host(o), refs[i][0]) and np.array_equal(host(l), refs[i][1])
+
+
+def chunk_setup(q, seed, fmt):
+    rng = np.random.default_rng(seed)
+    Hkv, G, D, page, cols = 2, 4, 128, 16, 80
+    new, kv = [70, 0, 33], [1100, 5, 700]
+    table = rng.permutation(3 * cols).reshape(3, cols).astype(np.int32)
+    cache = stale_pool(q, 3 * cols, Hkv, page, D, fmt)
+    fill_cache(q, rng, cache, None, np.array(kv), table)
+    start = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+    batch = q.PagedBatch(dev(start), dev(np.array(kv, np.int32)), dev(table), 70)
+    qkv = dev(projections(rng, (sum(new), (G + 2) * Hkv, D)))
+    assert q.lib().qlin_attn_workspace_bytes(cache._c, batch._c, sum(new), G * Hkv) > 0
+    return cache, batch, qkv, q.Rope(D), G * Hkv
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+def test_chunks_in_graphs_on_two_streams(q, fmt):
+    """Chunks whose key axis is split (parts in a workspace, a second launch that
+    joins them), eager on two streams and as two graphs replayed at once."""
+    sets = [chunk_setup(q, 21, fmt), chunk_setup(q, 22, fmt)]
+    refs = [tuple(host(t) for t in decode_step(q, *s)) for s in sets]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(4):
+        for i, s in enumerate(sets):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(decode_step(q, *s))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(np.array_equal(host(o), refs[i][0]) and np.array_equal(host(z), refs[i][1]) for o, z in got[i])
+    graphs, outs = [], []
+    for s in sets:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(decode_step(q, *s))
+        graphs.append(g)
+    for _ in range(4):
+        for o, z in outs:
+            o.zero_()
+            z.zero_()
+        decode_step(q, *sets[0])
+        torch.cuda.synchronize()
+        for i, g in enumerate(graphs):
+            with torch.cuda.stream(streams[i]):
+                g.replay()
+        torch.cuda.synchronize()
+        for i, (o, z) in enumerate(outs):
+            assert np.array_equal(host(o), refs[i][0]) and np.array_equal(host(z), refs[i][1])
+
+
+def test_one_workspace_with_the_products(q):
+    """Attention (split steps and chunks) and split-K products take turns in one
+    stream's workspace."""
+    rng = np.random.default_rng(8)
+    step, chunk = decode_setup(q, 23), chunk_setup(q, 24, "bf16")
+    M, N, K = 8, 512, 8192
+    assert q.workspace_bytes(q.OP_GEMM_FP8, M, N, K) > 0
+    w, ws = q.quant_weight(dev(bits(rng.standard_normal((N, K)))))
+    a, sa = q.quant_act(dev(bits(rng.standard_normal((M, K)))))
+
+    def turn():
+        return [*decode_step(q, *step), q.gemm_fp8(a, sa, w, ws), *decode_step(q, *chunk), q.gemm_fp8(a, sa, w, ws)]
+
+    ref = [host(t) for t in turn()]
+    for _ in range(4):
+        assert all(np.array_equal(host(x), y) for x, y in zip(turn(), ref))
+    r = q.linear_fp8(dev(bits(rng.standard_normal((M, K)))), w, ws)
+    assert torch.isfinite(r.float()).all()
 
 
 def test_same_result_every_time(q):

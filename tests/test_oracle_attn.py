@@ -67,9 +67,9 @@ def test_slots(oracle):
     # fewer keys than new tokens: the first lie before the sequence
     slot, _ = oracle.kv_slots([0, 3], [1], [[0]], 16, 1, 3)
     assert slot.tolist() == [-1, -1, 0]
-    # a length over the table's reach counts as that
-    slot, _ = oracle.kv_slots([0, 1], [99], [[0]], 16, 1, 1)
-    assert slot.tolist() == [15]
+    # what lies behind the table's reach is not stored
+    slot, place = oracle.kv_slots([0, 3], [17], [[0]], 16, 1, 3)
+    assert slot.tolist() == [14, 15, -1] and place.tolist() == [14, 15, 16]
 
 
 @pytest.mark.parametrize("fp8", [False, True])
