@@ -319,24 +319,36 @@ __device__ __forceinline__ void multiply(const v8bf (&q)[D / 16], State<D>& st, 
   }
 }
 
+// A tile's E4M3 scales of keys 8 n + 4 h + 0..3, h the lane's half.
+__device__ __forceinline__ v4f scales(const uint8_t* lds_s, int n) {
+  return *reinterpret_cast<const v4f*>(lds_s + n / 2 * 256 + (8 * (n & 1) + 4 * ((threadIdx.x & 63) >> 5)) * 4);
+}
+
 // The weights of a score block, rounded to bf16, and the running maximum and
 // sum (and with a raised maximum O) that go with them.
 //   vis_lo, vis_hi: keys that this lane's row sees, relative to the first
 //   masked: whether some row sees only part of them; bad: bit g = the 16-row
 //   group g lies in no page
-template <int D, bool FP8, int KB, int SCALE>
+//   E4M3: lds_s, lds_s + SCALE: the keys' and values' scales; with HOLD the keys' are in
+//   ks already, and the values' are read ahead of the work
+template <int D, bool FP8, int KB, int SCALE, bool HOLD>
 __device__ __forceinline__ void weight_block(const AttnArgs& a, State<D>& st, v16f (&s)[KB], v4i (&p)[2 * KB],
-                                             const uint8_t* lds_s, bool masked, int vis_lo, int vis_hi, uint32_t bad) {
+                                             const v4f (&ks)[4 * KB], const uint8_t* lds_s, bool masked, int vis_lo,
+                                             int vis_hi, uint32_t bad) {
   const int h = (threadIdx.x & 63) >> 5;
+  v4f vs[4 * KB];
   if (FP8) {
+    if (HOLD) {
 #pragma unroll
-    for (int kb = 0; kb < KB; ++kb)
+      for (int n = 0; n < 4 * KB; ++n) vs[n] = scales(lds_s + SCALE, n);
+      __builtin_amdgcn_sched_barrier(0);
+    }
 #pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        const v4f k = *reinterpret_cast<const v4f*>(lds_s + (2 * kb + b / 2) * 256 + (8 * (b & 1) + 4 * h) * 4);
+    for (int n = 0; n < 4 * KB; ++n) {
+      const v4f k = HOLD ? ks[n] : scales(lds_s, n);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) s[kb][4 * b + i] *= k[i];
-      }
+      for (int i = 0; i < 4; ++i) s[n / 4][n % 4 * 4 + i] *= k[i];
+    }
   }
   if (masked) {
     const int lo = vis_lo - 4 * h, hi = vis_hi - 4 * h;
@@ -375,14 +387,11 @@ __device__ __forceinline__ void weight_block(const AttnArgs& a, State<D>& st, v1
     }
   if (FP8) {
 #pragma unroll
-    for (int kb = 0; kb < KB; ++kb)
+    for (int n = 0; n < 4 * KB; ++n) {
+      const v4f v = HOLD ? vs[n] : scales(lds_s + SCALE, n);
 #pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        const v4f v =
-            *reinterpret_cast<const v4f*>(lds_s + SCALE + (2 * kb + b / 2) * 256 + (8 * (b & 1) + 4 * h) * 4);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) s[kb][4 * b + i] *= v[i];
-      }
+      for (int i = 0; i < 4; ++i) s[n / 4][n % 4 * 4 + i] *= v[i];
+    }
   }
   // P rounded to bf16 for the product (at most 2^-8 of a weight; the sum l
   // keeps the unrounded weights)
@@ -601,10 +610,13 @@ __device__ __forceinline__ bool chunk_item(const AttnArgs& a, Item& it, int& row
 // fragments would cost every wave 8 instructions a product, in the phase in
 // which its partner needs the vector unit). They pass through registers: spread
 // over the products of tile t, each wave writes its piece of K(t+2) or V(t+2), loaded
-// one tile before, and loads that of tile t+3. Scales come along and are read in the
-// weight phases: places for 8 tiles.
+// one tile before, and loads that of tile t+3. Scales come along: places for 8 tiles.
+//
+// Heads of 64 need few enough registers for two workgroups a CU (four waves a SIMD):
+// each fills the other's waits, so the priority of the multiplying wave, which is
+// worth 3 % with heads of 128, costs 3 % there.
 template <int D, bool FP8, int TK>
-__global__ __launch_bounds__(512, 2) void attn_chunk_kernel(const AttnArgs a) {
+__global__ __launch_bounds__(512, D == 64 ? 4 : 2) void attn_chunk_kernel(const AttnArgs a) {
   using St = Stage<D, false, TK, TK / 4>;
   using G = Geo<D, false>;
   constexpr int BM = 256, KB = TK / 32;
@@ -641,6 +653,13 @@ __global__ __launch_bounds__(512, 2) void attn_chunk_kernel(const AttnArgs a) {
   constexpr std::integral_constant<bool, true> kEdge;
   constexpr std::integral_constant<bool, false> kInner;
   constexpr int kOps = St::kLoads;  // loads of an iteration (bf16)
+  // E4M3: read the key scales over the last products and the values' ahead of the
+  // weights, where registers allow; else where they are used, an LDS read's time
+  // exposed eight times a tile (eight chunks of up to 1024 tokens, 32 heads of
+  // 128, in prompts of up to 9001: 610 us and 663; heads of 256 would spill: four such
+  // chunks 1600 us and 790).
+  constexpr bool kHold = D == 128;
+  constexpr int kProducts = 2 * KB * (D / 32) + KB * (D / 16);  // of a tile
   // bf16: straight into LDS
   auto load = [&](int t, int page, uint8_t* to, auto is_v, auto edge) {
     const Rows16 w = rows_of(a, it, t * TK + g0, page, wg.hi);
@@ -672,8 +691,13 @@ __global__ __launch_bounds__(512, 2) void attn_chunk_kernel(const AttnArgs a) {
       settled(rs);
       St::template scale_row<edge>(rs, skip, g0, lds_addr(lds_s[t & 7]) + (first ? 0 : kScale));
     }
-    const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(pool) + w.row * D, (short)0,
-                                                                        w.rows * D, 0x00020000);
+    // (uniform, which the compiler cannot see: without readfirstlane it loops over
+    // the lanes' resources)
+    const uint64_t base = (uint64_t)(uintptr_t)pool + w.row * D;
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((int)(uint32_t)base);
+    const uint32_t hi = __builtin_amdgcn_readfirstlane((int)(uint32_t)(base >> 32));
+    const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+        (void*)(uintptr_t)((uint64_t)hi << 32 | lo), (short)0, __builtin_amdgcn_readfirstlane(w.rows * D), 0x00020000);
 #pragma unroll
     for (int c = 0; c < kMine; ++c)
       x[c] = __builtin_amdgcn_raw_buffer_load_b128(rs, edge && from[c] / D < skip ? (int)0x80000000 : from[c], 0, 0);
@@ -682,10 +706,11 @@ __global__ __launch_bounds__(512, 2) void attn_chunk_kernel(const AttnArgs a) {
     uint8_t* base = first ? lds_k[k_place] : lds_v[t & 3];
     *reinterpret_cast<v8bf*>(base + to[i / 2][i % 2]) = cvt_fp8x8(x[i / 2][2 * (i % 2)], x[i / 2][2 * (i % 2) + 1]);
   };
-  // Fragments that a wave holds ahead of its products. With heads of 256, where the
-  // multiply phases are the longer ones, the first of them (values that arrived a
-  // tile before) are read at the end of the weight phase.
-  constexpr int kAhead = D == 256 ? 4 : 8;
+  // Fragments that a wave holds ahead of its products (heads of 64 and 256: as many
+  // as the registers allow). With heads of 256, where the multiply phases are the
+  // longer ones, the first of them (values that arrived a tile before) are read at
+  // the end of the weight phase.
+  constexpr int kAhead = D == 128 ? 8 : 4;
   // the end of a phase; no instruction moves from one into another, and all but the
   // last `reads` LDS instructions have completed
   auto phase_end = [&](auto reads) {
@@ -739,6 +764,7 @@ __global__ __launch_bounds__(512, 2) void attn_chunk_kernel(const AttnArgs a) {
   v16f s[KB];
   v4i p[2 * KB];
   v8bf fr[kAhead];
+  v4f ks[4 * KB];  // E4M3: the tile's key scales, read over the last products
 #pragma unroll
   for (int i = 0; i < 2 * KB; ++i) p[i] = v4i{};
   // (the first tile adds zero weights times its own values)
@@ -754,15 +780,17 @@ __global__ __launch_bounds__(512, 2) void attn_chunk_kernel(const AttnArgs a) {
   // waves in step, so leaving one out would save nothing.
   for (int t = t0; t < t1; ++t) {
     // multiply
-    __builtin_amdgcn_s_setprio(1);
+    if (D == 128) __builtin_amdgcn_s_setprio(1);
     if (D < 256) prefetch(t > t0 ? t - 1 : t);
     multiply<D, KB, kAhead, true>(q, st, s, p, fr, lds_v[(t > t0 ? t - 1 : t) & 3], lds_k[at], [&](int i) {
       if constexpr (FP8) {
         if (i < 2 * kMine) put(fx, t + 2, last, i);
         if (i == 2 * kMine) fetch(t + 3, p2, fx, kInner);
+        if (kHold && i >= kProducts / 2 - 4 * KB)
+          ks[i - (kProducts / 2 - 4 * KB)] = scales(lds_s[t & 7], i - (kProducts / 2 - 4 * KB));
       }
     });
-    __builtin_amdgcn_s_setprio(0);
+    if (D == 128) __builtin_amdgcn_s_setprio(0);
     phase_end(kAll);
     // weights
     if constexpr (FP8) {
@@ -779,7 +807,7 @@ __global__ __launch_bounds__(512, 2) void attn_chunk_kernel(const AttnArgs a) {
     if (holes)
       for (int g = 0; g < TK / 16; ++g) bad |= (uint32_t)no_page(a, page_of(a, it, key + 16 * g)) << g;
     const bool masked = holes || key + TK > own.all_hi || key < own.all_lo;
-    weight_block<D, FP8, KB, kScale>(a, st, s, p, lds_s[t & 7], masked, vlo - key, vhi - key, bad);
+    weight_block<D, FP8, KB, kScale, kHold>(a, st, s, p, ks, lds_s[t & 7], masked, vlo - key, vhi - key, bad);
     if (D == 256) prefetch(t);
     if (!FP8) dma_wait<kOps>();  // what the tile before loaded
     phase_end(kNone);  // (no LDS writes in this phase)
