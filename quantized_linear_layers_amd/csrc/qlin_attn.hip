@@ -28,10 +28,10 @@
 // exclusive-or-ed by row bits (k_swz, v_swz), so that both the row reads of K and
 // the transposing reads of V touch every bank once.
 //
-// Two kernels share this: attn_step_kernel (at most 32 rows: one decode step),
-// where each wave takes its own key tiles and the waves merge at the end, and
-// attn_chunk_kernel, where each wave has its own rows and the workgroup shares the
-// tiles. Either splits the key axis over workgroups when the rows alone do not
+// Two kernels share this: attn_step_kernel (32 rows a workgroup: a decode step, a
+// small chunk), where each wave takes its own key tiles and the waves merge at the
+// end, and attn_chunk_kernel (256 rows), where each wave has its own rows and the
+// workgroup shares the tiles. Either splits the key axis over workgroups when the rows alone do not
 // fill the device; the parts are joined by the last workgroup to arrive (step) or
 // by attn_join_kernel (chunk, whose parts are many rows).
 #include "qlin_internal.h"
@@ -70,10 +70,10 @@ struct AttnArgs {
   float c;     // |scale| * log2(e)
   // with splits > 1, parts of the key axis: unnormalised O rows and their running
   // maximum (log2) and sum. Chunk: [splits][T][q_heads][D] and [..][2]; step:
-  // [batch * kv_heads][splits][part_rows][D] and [..][2], and arrival counters
+  // [batch * kv_heads * row_tiles][splits][part_rows][D] and [..][2], and arrival counters
   float *po, *pml;
-  uint32_t* arrived;  // [batch * kv_heads], 0 between calls
-  int part_rows;
+  uint32_t* arrived;  // [batch * kv_heads * row_tiles], 0 between calls
+  int part_rows, row_tiles;  // step: rows of a workgroup, workgroups for a sequence's rows
 };
 
 __device__ __forceinline__ v16f mfma32(v8bf a, v8bf b, v16f c) {
@@ -831,8 +831,8 @@ __global__ __launch_bounds__(512, D == 64 ? 4 : 2) void attn_chunk_kernel(const 
 }
 
 // ---------------------------------------------------------------- step
-// At most 32 rows of a (sequence, key/value head), in RB blocks of 16: with so few
-// rows the 16-row products (v_mfma_f32_16x16x32_bf16) do half the work of the
+// A workgroup has up to 32 rows of a (sequence, key/value head), in RB blocks of 16:
+// with so few rows the 16-row products (v_mfma_f32_16x16x32_bf16) do half the work of the
 // 32-row ones, and their small state lets four waves share a SIMD. Lane group g =
 // lane >> 4 holds keys 16 b + 4 g + i of the tile's score block b: P's order for
 // the value product (slot j of group g: key 4 g + j, or 16 + 4 g + j - 4).
@@ -878,9 +878,11 @@ __global__ __launch_bounds__(NW * 64, step_waves(D, FP8, RB)) void attn_step_ker
   const int r = lane & 15, g = lane >> 4;
   const int split = blockIdx.z;  // slowest: the splits without tiles come last
   Item it;
-  if (!item_of(a, blockIdx.y, blockIdx.x, it)) return;
-  it.rows = min(it.rows, a.part_rows);  // max_q promises it
-  const Range rg = range_of(a, it, 0, it.rows);
+  // (heads fastest: with eight or sixteen the row tiles of one share an XCD's L2)
+  const int h = blockIdx.x % a.kv_heads, row0 = blockIdx.x / a.kv_heads * a.part_rows;
+  if (!item_of(a, blockIdx.y, h, it) || row0 >= it.rows) return;
+  const int rows = min(it.rows - row0, a.part_rows);  // this workgroup's
+  const Range rg = range_of(a, it, row0, row0 + rows);
   int t0 = rg.lo / 32, t1 = (rg.hi + 31) / 32;
   int parts = 1;
   if (a.splits > 1) {
@@ -892,7 +894,7 @@ __global__ __launch_bounds__(NW * 64, step_waves(D, FP8, RB)) void attn_step_ker
       if (a.window > 0) len = (int)min((int64_t)len, a.window + n);
       const int tiles = n > 0 && len > 0 ? len / 32 + 2 : 0;
       longest = max(longest, tiles);
-      sum += (float)tiles;
+      sum += (float)tiles * (float)max((n * a.group + a.part_rows - 1) / a.part_rows, 0);
     }
 #pragma unroll
     for (int o = 32; o >= 1; o >>= 1) {
@@ -946,13 +948,13 @@ __global__ __launch_bounds__(NW * 64, step_waves(D, FP8, RB)) void attn_step_ker
 #pragma unroll
   for (int rb = 0; rb < RB; ++rb) {
     const int row = 16 * rb + r;
-    vlo[rb] = row_lo(a, it, row);
-    vhi[rb] = row_hi(a, it, row);
+    vlo[rb] = row_lo(a, it, row0 + row);
+    vhi[rb] = row_hi(a, it, row0 + row);
     m[rb] = -kInf;
     l[rb] = 0.0f;
 #pragma unroll
     for (int d = 0; d < D / 16; ++d) o[rb][d] = v4f{};
-    const uint16_t* src = q_row<D>(a, it, row);
+    const uint16_t* src = q_row<D>(a, it, row0 + row);
 #pragma unroll
     for (int u = 0; u < D / 32; ++u)
       q[rb][u] = load_q8(a, src + (FP8 ? 64 * (u / 2) + 16 * g + 8 * (u % 2) : 32 * u + 8 * g));
@@ -1097,7 +1099,7 @@ __global__ __launch_bounds__(NW * 64, step_waves(D, FP8, RB)) void attn_step_ker
 #pragma unroll
     for (int w = 0; w < NW; ++w) top = fmaxf(top, wm[w][row]);
     const float f = m[rb] == -kInf ? (l[rb] == 0.0f ? 0.0f : 1.0f) : exp2_hw(m[rb] - top);
-    if (row < it.rows) {
+    if (row < rows) {
       float* dst = all + (wave * kRows + row) * kOut + 4 * g;
 #pragma unroll
       for (int d = 0; d < D / 16; ++d)
@@ -1108,8 +1110,8 @@ __global__ __launch_bounds__(NW * 64, step_waves(D, FP8, RB)) void attn_step_ker
   __syncthreads();
   const int64_t heads = (int64_t)a.kv_heads * a.group;
   auto finish = [&](int row, int c4, const v4f& x, float mm, float ll) {
-    const int64_t tok = it.q0 + row / a.group;
-    const int qh = it.h * a.group + row % a.group;
+    const int64_t tok = it.q0 + (row0 + row) / a.group;
+    const int qh = it.h * a.group + (row0 + row) % a.group;
     const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
     *reinterpret_cast<uint2*>(a.out + tok * a.ldo + (int64_t)qh * D + c4) =
         make_uint2(pack_bf16x2(x[0] * inv, x[1] * inv), pack_bf16x2(x[2] * inv, x[3] * inv));
@@ -1119,12 +1121,12 @@ __global__ __launch_bounds__(NW * 64, step_waves(D, FP8, RB)) void attn_step_ker
   // part is visible everywhere once its store has completed, so the wait before
   // the counter orders them without flushing a cache.
   constexpr int kSc1 = 16;
-  const int wg = it.b * a.kv_heads + it.h;
+  const int wg = it.b * gridDim.x + blockIdx.x;
   const __amdgpu_buffer_rsrc_t ro = __builtin_amdgcn_make_buffer_rsrc(
       a.po + (int64_t)wg * a.splits * a.part_rows * D, (short)0, a.splits * a.part_rows * D * 4, 0x00020000);
   const __amdgpu_buffer_rsrc_t rm = __builtin_amdgcn_make_buffer_rsrc(
       a.pml + (int64_t)wg * a.splits * a.part_rows * 2, (short)0, a.splits * a.part_rows * 8, 0x00020000);
-  for (int i = threadIdx.x; i < it.rows * (D / 4); i += NW * 64) {
+  for (int i = threadIdx.x; i < rows * (D / 4); i += NW * 64) {
     const int row = i / (D / 4), c4 = i % (D / 4) * 4;
     float mm = -kInf, ll = 0.0f;
     v4f x = {};
@@ -1161,7 +1163,7 @@ __global__ __launch_bounds__(NW * 64, step_waves(D, FP8, RB)) void attn_step_ker
   for (int i = threadIdx.x; i < parts * a.part_rows; i += NW * 64)
     ml[i] = __builtin_amdgcn_raw_buffer_load_b64(rm, i * 8, 0, kSc1);
   __syncthreads();
-  for (int i = threadIdx.x; i < it.rows * (D / 4); i += NW * 64) {
+  for (int i = threadIdx.x; i < rows * (D / 4); i += NW * 64) {
     const int row = i / (D / 4), c4 = i % (D / 4) * 4;
     float mm = -kInf, ll = 0.0f;
     for (int s = 0; s < parts; ++s) mm = fmaxf(mm, __uint_as_float((uint32_t)ml[s * a.part_rows + row][0]));
@@ -1189,51 +1191,69 @@ __global__ __launch_bounds__(NW * 64, step_waves(D, FP8, RB)) void attn_step_ker
 }
 
 // ---------------------------------------------------------------- join
-// The parts of the key axis to one result: a wave a (token, query head).
+// The parts of the key axis to one result: four values of a (token, query head) a
+// thread. Everything that a row needs is loaded at once, before it is known which
+// parts have a key (what a part without one holds is not used): bound by that
+// one round trip, then by the parts' bytes.
 template <int D>
 __global__ __launch_bounds__(256) void attn_join_kernel(const AttnArgs a) {
-  constexpr int V = D / 64;  // values a lane
+  constexpr int kRow = D / 4, kRows = 64 / kRow;  // threads of a row, rows of a wave
   const int lane = threadIdx.x & 63;
-  const int64_t heads = (int64_t)a.kv_heads * a.group;
-  const int64_t at = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (at >= a.T * heads) return;
+  const int64_t heads = (int64_t)a.kv_heads * a.group, all = a.T * heads;
+  const int64_t at0 = ((int64_t)blockIdx.x * 4 + (threadIdx.x >> 6)) * kRows;  // the wave's first row
+  if (at0 >= all) return;
+  const int64_t mine = at0 + lane / kRow, at = min(mine, all - 1);
+  const int c = 4 * (lane % kRow);
   // rows of no sequence have no parts (and are left as they are)
-  const int64_t t = at / heads;
   bool in = false;
-  for (int b0 = 0; b0 < a.B && !in; b0 += 64) {
-    const int b = b0 + lane;
-    in = __any(b < a.B && a.q_start[b] >= 0 && a.q_start[b] <= t && t < a.q_start[b + 1] && a.q_start[b + 1] <= a.T);
-  }
-  if (!in) return;
-  float m = -kInf;
-  for (int s = lane; s < a.splits; s += 64) m = fmaxf(m, a.pml[2 * (s * a.T * heads + at)]);
-  m = wave_max(m);
-  float l = 0.0f, o[V] = {};
-  for (int s = 0; s < a.splits; ++s) {
-    const int64_t p = s * a.T * heads + at;
-    const float ms = a.pml[2 * p], ls = a.pml[2 * p + 1];
-    if (ms == -kInf && ls == 0.0f) continue;  // a part without a key
-    const float w = ms == -kInf ? 1.0f : exp2_hw(ms - m);
-    l += w * ls;
+  for (int b0 = 0; b0 < a.B; b0 += 64) {
+    const int b = min(b0 + lane, a.B - 1);
+    const int from = a.q_start[b], to = a.q_start[b + 1];
 #pragma unroll
-    for (int i = 0; i < V; ++i) o[i] += w * a.po[p * D + V * lane + i];
+    for (int i = 0; i < kRows; ++i) {
+      const int64_t t = (at0 + i) / heads;
+      const bool here = __any(from >= 0 && from <= t && t < to && to <= a.T);
+      in |= here && lane / kRow == i;
+    }
   }
+  float m = -kInf, l = 0.0f;
+  v4f o = {};
+  for (int s0 = 0; s0 < a.splits; s0 += 4) {
+    float ms[4], ls[4];
+    v4f x[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t p = min(s0 + i, a.splits - 1) * all + at;
+      const float2 z = *reinterpret_cast<const float2*>(a.pml + 2 * p);
+      ms[i] = z.x;
+      ls[i] = z.y;
+      x[i] = *reinterpret_cast<const v4f*>(a.po + p * D + c);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (s0 + i >= a.splits || (ms[i] == -kInf && ls[i] == 0.0f)) continue;  // no such part, or one without a key
+      const float top = fmaxf(m, ms[i]);
+      const float f = m == -kInf ? 1.0f : exp2_hw(m - top), w = ms[i] == -kInf ? 1.0f : exp2_hw(ms[i] - top);
+      m = top;
+      l = l * f + ls[i] * w;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) o[j] = o[j] * f + x[i][j] * w;
+    }
+  }
+  if (!in || mine >= all) return;
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const __bf16 y = (__bf16)(o[i] * inv);
-    a.out[t * a.ldo + at % heads * D + V * lane + i] = __builtin_bit_cast(uint16_t, y);
-  }
-  if (a.lse && lane == 0) a.lse[at] = l == 0.0f ? -kInf : (m + log2f(l)) * kLn2;
+  *reinterpret_cast<uint2*>(a.out + at / heads * a.ldo + at % heads * D + c) =
+      make_uint2(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv));
+  if (a.lse && c == 0) a.lse[at] = l == 0.0f ? -kInf : (m + log2f(l)) * kLn2;
 }
 
 // ---------------------------------------------------------------- host
 struct Plan {
   bool step;
   int splits;
-  int64_t tiles;
-  int part_rows;
-  size_t parts;  // rows of parts in the workspace
+  int64_t tiles;             // chunk: workgroups for the rows, at most
+  int part_rows, row_tiles;  // step
+  size_t parts;              // rows of parts in the workspace
 };
 
 // Arrival counters at the start of the workspace, as the GEMMs' split-K.
@@ -1241,40 +1261,75 @@ constexpr size_t kAttnCounterBytes = kGemmCounterBytes;
 constexpr int kChunkRows = 256;
 constexpr int kCus = 256;
 
+Plan step_plan(const qlin_kv_cache& cache, const qlin_kv_batch& batch, int64_t rows, int64_t keys) {
+  Plan p = {};
+  p.step = true;
+  p.part_rows = (int)std::min<int64_t>(32, rows);
+  p.row_tiles = (int)((rows + 31) / 32);
+  const int64_t wgs = batch.batch * cache.kv_heads * p.row_tiles;
+  // A joined part costs about 6 us (its store has to be visible, then counted,
+  // then read). With 64 E4M3 sequences of up to 1536 tokens (512 workgroups,
+  // heads of 128) two parts took 37 us and none 30.5; with eight of 65536
+  // bf16 (64 workgroups) 8 parts took 352 us, 4 357, 16 379. So: one workgroup a
+  // CU; where sequences may be long enough not to notice the join, up to the
+  // most that a ragged batch needs.
+  const int64_t most = keys >= 4096 ? 2048 : kCus;
+  const int64_t piece = p.row_tiles > 1 ? 512 : 128;  // keys of a part, at least (more rows, a dearer join)
+  // (64 parts at most: one workgroup reads them all)
+  p.splits = (int)std::max<int64_t>(1, std::min({(most + wgs - 1) / wgs, (keys + piece - 1) / piece, (int64_t)64}));
+  if (wgs >= most) p.splits = 1;
+  p.parts = p.splits <= 1 ? 0 : (size_t)p.splits * wgs * p.part_rows;
+  return p;
+}
+
+Plan chunk_plan(const qlin_kv_cache& cache, const qlin_kv_batch& batch, int64_t T, int64_t rows, int64_t group,
+                int64_t keys) {
+  Plan p = {};
+  p.tiles = std::min(T * group / kChunkRows + batch.batch, (rows + kChunkRows - 1) / kChunkRows * batch.batch);
+  const int64_t wgs = p.tiles * cache.kv_heads, room = cache.head_dim == 64 ? 2 * kCus : kCus;
+  // A chunk of 512 tokens (32 heads of 128, a group of 4) of 4096: 4 parts 49.2 us, 2
+  // 63.6, 8 (more workgroups than CUs) 67.5; 1024 of 1024: 2 parts 38.8, none 31.7.
+  p.splits = (int)std::max<int64_t>(1, std::min(room / wgs, keys / 1024));
+  p.parts = p.splits <= 1 ? 0 : (size_t)p.splits * T * cache.kv_heads * group;
+  return p;
+}
+
+// Workgroups of 32 rows (a step's kernel) or of 256 (a chunk's). The chunk's does
+// about twice the work a second once it fills the device, but a call of few rows
+// leaves most of its workgroups' rows or most CUs idle. Heads of 128, a group of 4,
+// 8 key/value heads, us of 32 and of 256 rows:
+//   up to 128 rows a sequence: 200 sequences of 16 tokens (4 key/value heads) of up to
+//     1024: 79 and 167; 40 of 32 of 16384: 526 and 551; one of 16 of 32768: 47 and 54;
+//   more, at most 4096 keys and 1024 workgroups of 32 rows, as long as these times
+//     the keys are at most 2 M: 512 tokens of 512: 13 and 21; 1024 of 1024: 29 and 32 (no
+//     causal mask: 35 and 31); four chunks of 64 of 4096: 27 and 32; 512 of 4096: 51 and 49;
+//   the others: 2048 of 2048: 75 and 55; 1024 of 4096: 93 and 77; 256 of 8192: 56 and 49,
+//     of 32768: 194 and 135.
+// Heads of 64 have four of these workgroups on a CU, twice as many: 1500 of 1500: 28 and
+// 40, 2048 of 2048: 41 and 43.
+// Here: the most keys for which 32 rows are taken (0: never).
+int64_t few_rows_keys(const qlin_kv_cache& cache, const qlin_kv_batch& batch, int64_t T, int64_t rows,
+                      int64_t group) {
+  if (rows <= 128) return INT64_MAX;
+  const int64_t room = cache.head_dim == 64 ? 2 : 1;
+  const int64_t tiles = (rows + 31) / 32 * batch.batch;  // (the grid: also those that a ragged batch leaves empty)
+  const int64_t wgs = std::min(tiles, T * group / 32 + batch.batch) * cache.kv_heads;
+  if (wgs > 1024 * room || tiles * cache.kv_heads > 8192) return 0;
+  return std::min((int64_t)4096, ((int64_t)room << 21) / wgs);
+}
+
 Plan plan_of(const qlin_kv_cache& cache, const qlin_kv_batch& batch, int64_t T, int64_t q_heads, int64_t window) {
-  Plan p;
-  const int64_t group = q_heads / cache.kv_heads;
+  const int64_t group = q_heads / cache.kv_heads, rows = std::min(batch.max_q, T) * group;
   int64_t keys = batch.table_cols * cache.page_size;
   if (window > 0) keys = std::min(keys, std::min(window, keys) + batch.max_q);
-  p.step = batch.max_q * group <= 32;
-  if (p.step) {
-    p.tiles = batch.batch;
-    const int64_t wgs = batch.batch * cache.kv_heads;
-    // A joined part costs about 6 us (its store has to be visible, then counted,
-    // then read). With 64 E4M3 sequences of up to 1536 tokens (512 workgroups,
-    // heads of 128) two parts took 37 us and none 30.5; with eight of 65536
-    // bf16 (64 workgroups) 8 parts took 352 us, 4 357, 16 379. So: one workgroup a
-    // CU; where sequences may be long enough not to notice the join, up to the
-    // most that a ragged batch needs.
-    const int64_t most = keys >= 4096 ? 2048 : kCus;
-    // (64 parts at most: one workgroup reads them all)
-    p.splits = (int)std::max<int64_t>(1, std::min({(most + wgs - 1) / wgs, (keys + 127) / 128, (int64_t)64}));
-    if (wgs >= (keys >= 4096 ? 2048 : kCus)) p.splits = 1;
-  } else {
-    p.tiles = T * group / kChunkRows + batch.batch;
-    const int64_t wgs = p.tiles * cache.kv_heads;
-    p.splits = wgs >= kCus ? 1 : (int)std::max<int64_t>(1, std::min(2 * kCus / wgs, (keys + 255) / 256));
-  }
-  p.part_rows = (int)std::min<int64_t>(32, batch.max_q * group);
-  p.parts = p.splits <= 1 ? 0 : p.step ? (size_t)p.splits * batch.batch * cache.kv_heads * p.part_rows
-                                       : (size_t)p.splits * T * q_heads;
-  return p;
+  return keys <= few_rows_keys(cache, batch, T, rows, group) ? step_plan(cache, batch, rows, keys)
+                                                             : chunk_plan(cache, batch, T, rows, group, keys);
 }
 
 template <int D, bool FP8>
 void launch_parts(const AttnArgs& a, const Plan& p, hipStream_t st) {
   if (p.step) {
-    const dim3 grid(a.kv_heads, a.B, p.splits);
+    const dim3 grid(a.kv_heads * p.row_tiles, a.B, p.splits);
     if (p.part_rows <= 16)
       attn_step_kernel<D, FP8, 1, 4><<<grid, 256, 0, st>>>(a);
     else
@@ -1284,16 +1339,22 @@ void launch_parts(const AttnArgs& a, const Plan& p, hipStream_t st) {
     attn_chunk_kernel<D, FP8, D == 256 ? 32 : 64><<<(unsigned)((items + 7) / 8 * 8), 512, 0, st>>>(a);
   }
   if (p.splits > 1 && !p.step) {
-    const int64_t rows = a.T * a.kv_heads * a.group;
-    attn_join_kernel<D><<<(unsigned)((rows + 3) / 4), 256, 0, st>>>(a);
+    const int64_t rows = a.T * a.kv_heads * a.group, wg = 1024 / D;  // rows of a workgroup
+    attn_join_kernel<D><<<(unsigned)((rows + wg - 1) / wg), 256, 0, st>>>(a);
   }
 }
 
 }  // namespace
 
 size_t attn_workspace_bytes(const qlin_kv_cache& cache, const qlin_kv_batch& batch, int64_t T, int64_t q_heads) {
-  const Plan p = plan_of(cache, batch, T, q_heads, 0);
-  if (p.splits <= 1) return 0;
+  // Enough for a call with any window: a window lowers the keys, which may also turn
+  // a chunk into workgroups of 32 rows (either plan's parts only fall with the keys).
+  Plan p = plan_of(cache, batch, T, q_heads, 0);
+  if (!p.step) {
+    const int64_t group = q_heads / cache.kv_heads, rows = std::min(batch.max_q, T) * group;
+    p.parts = std::max(p.parts, step_plan(cache, batch, rows, few_rows_keys(cache, batch, T, rows, group)).parts);
+  }
+  if (p.parts == 0) return 0;
   return kAttnCounterBytes + round_up(p.parts * cache.head_dim * 4, 256) + round_up(p.parts * 8, 256);
 }
 
@@ -1325,6 +1386,7 @@ int launch_attn(const qlin_kv_cache& cache, const qlin_kv_batch& batch, int64_t 
   a.causal = causal;
   a.splits = p.splits;
   a.part_rows = p.part_rows;
+  a.row_tiles = p.row_tiles;
   a.tiles = (int)p.tiles;
   a.negate = scale < 0.0f;
   // a scale of 0 must keep masked scores at -inf (0 * -inf is NaN): a positive

@@ -247,6 +247,64 @@ def test_chunk_split_over_keys(q, oracle, fmt):
     run_attn(q, oracle, 43, [150], [900], 1, 2, 256, 32, fmt, window=300)
 
 
+# Chunks over tables of more than 4096 tokens, which have workgroups of 256 rows (the
+# shorter ones above: of 32): the key axis in parts, and with many heads whole.
+def long_table(page):
+    return 4096 // page + 1
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("D,page,Hkv,G", [(64, 16, 2, 2), (128, 16, 1, 4), (128, 64, 2, 1), (128, 256, 1, 3),
+                                          (256, 32, 1, 2), (64, 128, 1, 8), (256, 16, 1, 4), (64, 32, 70, 2),
+                                          (128, 32, 40, 2), (256, 64, 40, 2)])
+def test_chunk_long_table(q, oracle, D, page, Hkv, G, fmt):
+    run_attn(q, oracle, 20 + D + page, [33, 0, 64, 129, 1], [33, 17, 200, 150, 90], Hkv, G, D, page, fmt, pad=2,
+             extra_cols=long_table(page))
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("causal,window", [(False, 0), (True, 0), (True, 10 ** 15)])
+@pytest.mark.parametrize("D,Hkv", [(64, 1), (128, 1), (256, 1), (64, 40), (128, 24), (256, 24)])
+def test_chunk_masks_long_table(q, oracle, causal, window, fmt, D, Hkv):
+    run_attn(q, oracle, 31, [100, 40, 35, 70], [260, 7, 0, 70], Hkv, 4, D, 16, fmt, causal, window, pad=1,
+             extra_cols=long_table(16))
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("D,Hkv", [(128, 1), (256, 1), (64, 8), (128, 8)])
+@pytest.mark.parametrize("window", [4500, 4096])
+def test_chunk_windows_of_many_keys(q, oracle, D, Hkv, window, fmt):
+    run_attn(q, oracle, 33, [150, 3], [4700, 20], Hkv, 1, D, 128, fmt, True, window, pad=1, extra_cols=2)
+
+
+def test_chunk_window_inside(q, oracle):
+    """A window in chunks of so many rows that they have workgroups of 256."""
+    run_attn(q, oracle, 34, [700, 300], [900, 300], 20, 4, 64, 32, "bf16", window=77)
+    run_attn(q, oracle, 35, [700, 300], [900, 300], 16, 4, 128, 32, "e4m3", window=130)
+    run_attn(q, oracle, 36, [500, 600], [900, 600], 16, 4, 256, 64, "bf16", window=33)
+
+
+def test_chunk_split_over_keys_long_table(q, oracle):
+    run_attn(q, oracle, 41, [40], [1333], 2, 4, 128, 64, "bf16", extra_cols=100)
+    run_attn(q, oracle, 42, [70, 9], [1333, 600], 1, 4, 64, 16, "e4m3", causal=False, extra_cols=400)
+    run_attn(q, oracle, 43, [150], [4900], 1, 2, 256, 32, "bf16")
+
+
+@pytest.mark.parametrize("scale", [-0.09, 0.0, 1e-6, 1.5])
+def test_scales_long_table(q, oracle, scale):
+    run_attn(q, oracle, 51, [100, 40], [190, 61], 1, 2, 128, 16, "bf16", scale=scale, extra_cols=long_table(16))
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+def test_pages_that_do_not_exist_long_table(q, oracle, fmt):
+    def edit(t):
+        t[0, 1] = -1
+        t[0, 3] = 10 ** 9
+        t[1, :] = 2 ** 31 - 1
+
+    run_attn(q, oracle, 61, [80, 70], [90, 71], 2, 2, 128, 16, fmt, table_edit=edit, extra_cols=long_table(16))
+
+
 @pytest.mark.parametrize("scale", [-0.09, 0.0, 1e-6, 1.5])
 @pytest.mark.parametrize("new,G", [([1, 1], 4), ([60, 40], 2)])
 def test_scales(q, oracle, scale, new, G):
@@ -300,12 +358,13 @@ def test_length_over_the_table(q, oracle):
 
 
 @pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
-@pytest.mark.parametrize("new,G,window", [(3, 4, 0), (3, 4, 2), (3, 4, 40), (90, 2, 0), (90, 2, 25), (5, 16, 3)])
-def test_sequences_longer_than_their_tables(q, oracle, new, G, window, fmt):
+@pytest.mark.parametrize("new,G,window,cols", [(3, 4, 0, 8), (3, 4, 2, 8), (3, 4, 40, 8), (90, 2, 0, 8), (90, 2, 25, 8),
+                                               (5, 16, 3, 8), (90, 2, 0, 257), (90, 2, 4090, 257)])
+def test_sequences_longer_than_their_tables(q, oracle, new, G, window, cols, fmt):
     """The tokens behind the table's reach are not stored and not seen; the others
     keep their places."""
     rng = np.random.default_rng(new + window)
-    D, Hkv, page, cols = 128, 2, 16, 8
+    D, Hkv, page = 128, 2, 16
     kv = [cols * page + 2, cols * page + new + 40, 100]
     table = rng.permutation(3 * cols).reshape(3, cols).astype(np.int32)
     start = (np.arange(4) * new).astype(np.int32)
@@ -333,12 +392,12 @@ def test_sequences_longer_than_their_tables(q, oracle, new, G, window, fmt):
 
 
 @pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
-@pytest.mark.parametrize("new,G", [(1, 4), (40, 2)])
-def test_no_key_at_all_and_the_next_call(q, oracle, new, G, fmt):
+@pytest.mark.parametrize("new,G,cols", [(1, 4, 64), (40, 2, 64), (90, 2, 260)])
+def test_no_key_at_all_and_the_next_call(q, oracle, new, G, cols, fmt):
     """A batch of empty sequences over tables that split the key axis: zeros, and
     the workspace serves the next call."""
     rng = np.random.default_rng(new)
-    B, Hkv, D, page, cols = 3, 2, 128, 16, 64
+    B, Hkv, D, page = 3, 2, 128, 16
     T, Hq = B * new, Hkv * G
     cache = q.PagedKV.empty(B * cols, Hkv, D, page, fmt)
     table = rng.permutation(B * cols).reshape(B, cols).astype(np.int32)
@@ -359,29 +418,30 @@ def test_no_key_at_all_and_the_next_call(q, oracle, new, G, fmt):
         assert not q.workspace(nbytes, got.device)[:65536].any().item(), "counters"
 
 
-@pytest.mark.parametrize("new,G", [(2, 4), (40, 2)])
-def test_window_of_any_size(q, new, G):
+@pytest.mark.parametrize("new,G,cols", [(2, 4, 64), (40, 2, 64), (40, 8, 300)])
+def test_window_of_any_size(q, new, G, cols):
     rng = np.random.default_rng(3)
-    cache = q.PagedKV.empty(64, 1, 128, 16)
-    table = rng.permutation(64)[None].astype(np.int32)
+    cache = q.PagedKV.empty(cols, 1, 128, 16)
+    table = rng.permutation(cols)[None].astype(np.int32)
     fill_cache(q, rng, cache, None, np.array([1000]), table)
     b = q.PagedBatch(dev(np.array([0, new], np.int32)), dev(np.array([1000], np.int32)), dev(table), new)
     x = dev(projections(rng, (new, G, 128)))
     ref = q.attn_paged(cache, b, x)
-    for window in (1000, 1024, 2 ** 31 - 1, 2 ** 31, 2 ** 32 + 5, 2 ** 63 - 1):
+    # (the same kernel with and without a window of at least the table's tokens)
+    for window in (16 * cols, 2 ** 31 - 1, 2 ** 31, 2 ** 32 + 5, 2 ** 63 - 1):
         assert torch.equal(q.attn_paged(cache, b, x, window=window), ref), window
 
 
-@pytest.mark.parametrize("new,G", [(1, 4), (80, 2)])
+@pytest.mark.parametrize("new,G,more", [(1, 4, 0), (80, 2, 0), (80, 2, 20)])
 @pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
-def test_pool_beyond_32_bit_offsets(q, oracle, fmt, new, G):
+def test_pool_beyond_32_bit_offsets(q, oracle, fmt, new, G, more):
     """Pages whose byte offsets pass 2^32."""
     D, Hkv, page = 256, 8, 256
     one = Hkv * page * D * (2 if fmt == "bf16" else 1)
     pages = (1 << 32) // one + 40
     rng = np.random.default_rng(12)
     cache = q.PagedKV.empty(pages, Hkv, D, page, fmt)
-    table = np.array([[pages - 1, pages - 7, 3]], np.int32)
+    table = np.array([[pages - 1, pages - 7, 3] + [-1] * more], np.int32)
     kv = np.array([600])
     start = np.array([0, new], np.int32)
     fill_cache(q, rng, cache, start, kv, table)
@@ -389,7 +449,7 @@ def test_pool_beyond_32_bit_offsets(q, oracle, fmt, new, G):
     b = q.PagedBatch(dev(start), dev(kv.astype(np.int32)), dev(table), new)
     got, lse = q.attn_paged(cache, b, dev(x), return_lse=True)
     e4 = fmt == "e4m3"
-    small = [host(t[table[0].tolist()]) if t is not None else None
+    small = [host(t[table[0, :3].tolist()]) if t is not None else None
              for t in (cache.k, cache.v, cache.k_scale, cache.v_scale)]
     r = oracle.attn_paged(x, small[0], small[1], small[2] if e4 else None, small[3] if e4 else None, start, kv,
                           np.array([[0, 1, 2]]), D ** -0.5)
@@ -610,9 +670,9 @@ def test_two_streams_and_two_graphs(q):
             assert np.array_equal(host(o), refs[i][0]) and np.array_equal(host(l), refs[i][1])
 
 
-def chunk_setup(q, seed, fmt):
+def chunk_setup(q, seed, fmt, cols):
     rng = np.random.default_rng(seed)
-    Hkv, G, D, page, cols = 2, 4, 128, 16, 80
+    Hkv, G, D, page = 2, 4, 128, 16
     new, kv = [70, 0, 33], [1100, 5, 700]
     table = rng.permutation(3 * cols).reshape(3, cols).astype(np.int32)
     cache = stale_pool(q, 3 * cols, Hkv, page, D, fmt)
@@ -625,10 +685,12 @@ def chunk_setup(q, seed, fmt):
 
 
 @pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
-def test_chunks_in_graphs_on_two_streams(q, fmt):
-    """Chunks whose key axis is split (parts in a workspace, a second launch that
-    joins them), eager on two streams and as two graphs replayed at once."""
-    sets = [chunk_setup(q, 21, fmt), chunk_setup(q, 22, fmt)]
+@pytest.mark.parametrize("cols", [80, 260])
+def test_chunks_in_graphs_on_two_streams(q, fmt, cols):
+    """Chunks whose key axis is split (parts in a workspace, joined by the last
+    workgroup or by a second launch), eager on two streams and as two graphs
+    replayed at once."""
+    sets = [chunk_setup(q, 21, fmt, cols), chunk_setup(q, 22, fmt, cols)]
     refs = [tuple(host(t) for t in decode_step(q, *s)) for s in sets]
     streams = [torch.cuda.Stream(), torch.cuda.Stream()]
     torch.cuda.synchronize()
@@ -660,11 +722,12 @@ def test_chunks_in_graphs_on_two_streams(q, fmt):
             assert np.array_equal(host(o), refs[i][0]) and np.array_equal(host(z), refs[i][1])
 
 
-def test_one_workspace_with_the_products(q):
+@pytest.mark.parametrize("cols", [80, 260])
+def test_one_workspace_with_the_products(q, cols):
     """Attention (split steps and chunks) and split-K products take turns in one
     stream's workspace."""
     rng = np.random.default_rng(8)
-    step, chunk = decode_setup(q, 23), chunk_setup(q, 24, "bf16")
+    step, chunk = decode_setup(q, 23), chunk_setup(q, 24, "bf16", cols)
     M, N, K = 8, 512, 8192
     assert q.workspace_bytes(q.OP_GEMM_FP8, M, N, K) > 0
     w, ws = q.quant_weight(dev(bits(rng.standard_normal((N, K)))))
