@@ -1287,9 +1287,11 @@ Plan chunk_plan(const qlin_kv_cache& cache, const qlin_kv_batch& batch, int64_t 
   Plan p = {};
   p.tiles = std::min(T * group / kChunkRows + batch.batch, (rows + kChunkRows - 1) / kChunkRows * batch.batch);
   const int64_t wgs = p.tiles * cache.kv_heads, room = cache.head_dim == 64 ? 2 * kCus : kCus;
-  // A chunk of 512 tokens (32 heads of 128, a group of 4) of 4096: 4 parts 49.2 us, 2
-  // 63.6, 8 (more workgroups than CUs) 67.5; 1024 of 1024: 2 parts 38.8, none 31.7.
-  p.splits = (int)std::max<int64_t>(1, std::min(room / wgs, keys / 1024));
+  // One workgroup a CU, equal parts. A chunk of 512 tokens (32 heads of 128, a group of
+  // 4) of 4096: 4 parts 49.2 us, 2 63.6, 8 (more workgroups than CUs) 67.5; 1024 of 1024:
+  // 2 parts 38.8, none 31.7. (Parts by each sequence's length instead: 1024 of 4096 90 us
+  // and more, where two equal ones take 77, and no gain over ragged batches.)
+  p.splits = keys < 2048 ? 1 : (int)std::max<int64_t>(1, std::min(room / wgs, keys / 512));
   p.parts = p.splits <= 1 ? 0 : (size_t)p.splits * T * cache.kv_heads * group;
   return p;
 }
@@ -1300,8 +1302,8 @@ Plan chunk_plan(const qlin_kv_cache& cache, const qlin_kv_batch& batch, int64_t 
 // 8 key/value heads, us of 32 and of 256 rows:
 //   up to 128 rows a sequence: 200 sequences of 16 tokens (4 key/value heads) of up to
 //     1024: 79 and 167; 40 of 32 of 16384: 526 and 551; one of 16 of 32768: 47 and 54;
-//   more, at most 4096 keys and 1024 workgroups of 32 rows, as long as these times
-//     the keys are at most 2 M: 512 tokens of 512: 13 and 21; 1024 of 1024: 29 and 32 (no
+//   more, at most 1024 workgroups of 32 rows, as long as these times the keys are at most
+//     2 M: 512 tokens of 512: 13 and 21; 1024 of 1024: 29 and 32 (no
 //     causal mask: 35 and 31); four chunks of 64 of 4096: 27 and 32; 512 of 4096: 51 and 49;
 //   the others: 2048 of 2048: 75 and 55; 1024 of 4096: 93 and 77; 256 of 8192: 56 and 49,
 //     of 32768: 194 and 135.
@@ -1315,7 +1317,7 @@ int64_t few_rows_keys(const qlin_kv_cache& cache, const qlin_kv_batch& batch, in
   const int64_t tiles = (rows + 31) / 32 * batch.batch;  // (the grid: also those that a ragged batch leaves empty)
   const int64_t wgs = std::min(tiles, T * group / 32 + batch.batch) * cache.kv_heads;
   if (wgs > 1024 * room || tiles * cache.kv_heads > 8192) return 0;
-  return std::min((int64_t)4096, ((int64_t)room << 21) / wgs);
+  return ((int64_t)room << 21) / wgs;
 }
 
 Plan plan_of(const qlin_kv_cache& cache, const qlin_kv_batch& batch, int64_t T, int64_t q_heads, int64_t window) {
