@@ -1277,6 +1277,11 @@ Plan step_plan(const qlin_kv_cache& cache, const qlin_kv_batch& batch, int64_t r
   const int64_t piece = p.row_tiles > 1 ? 512 : 128;  // keys of a part, at least (more rows, a dearer join)
   // (64 parts at most: one workgroup reads them all)
   p.splits = (int)std::max<int64_t>(1, std::min({(most + wgs - 1) / wgs, (keys + piece - 1) / piece, (int64_t)64}));
+  // The last workgroup reads all parts, a part's keys and its rows cost about the same
+  // time at keys * 32 = parts^2 * rows * head_dim: 2 sequences of 50 rows, heads of 128,
+  // 28454 keys: 36 us, 54 with 64 parts; 16 tokens of 32 heads, 32768 keys: 39 and 47.
+  const int even = (int)std::sqrt(32.0 * (double)keys / (double)(p.part_rows * cache.head_dim));
+  p.splits = std::max(1, std::min(p.splits, even));
   if (wgs >= most) p.splits = 1;
   p.parts = p.splits <= 1 ? 0 : (size_t)p.splits * wgs * p.part_rows;
   return p;
