@@ -375,6 +375,9 @@ int qlin_moe_w4a16_workspace_layout(int64_t T, int64_t H, int64_t I, int64_t E, 
  *   page_table [batch][table_cols] int32: page of each page_size tokens;
  *   max_q     at least the longest sequence's count of new tokens (a host
  *             value, it selects kernels; with fewer the result is the same).
+ * Kernels and the split of the key axis are chosen on the host from these sizes,
+ * table_cols * page_size standing for the longest sequence: a table much wider
+ * than the sequences need costs speed, not correctness.
  * The arrays are device data, read when the kernels run (a captured graph
  * sees the values of each replay), so their values are no errors: the keys of
  * a page outside [0, pages) are not written and not seen.

@@ -615,6 +615,14 @@ __device__ __forceinline__ bool chunk_item(const AttnArgs& a, Item& it, int& row
 // Heads of 64 need few enough registers for two workgroups a CU (four waves a SIMD):
 // each fills the other's waits, so the priority of the multiplying wave, which is
 // worth 3 % with heads of 128, costs 3 % there.
+//
+// Measured, 32 + 8 heads of 128: a prompt of 8192, bf16 491 us (1119 TFLOP/s, 86 % of a
+// large library matrix product's 1294); 2048 of 32768 902 us (1181); eight E4M3 chunks of
+// up to 1024 of up to 9001 557 us (917). 16 + 8 heads of 256, window 1024, four prompts of
+// 4096: 223 us (735). Bound by the phases: a tile takes about 2900 cycles (E4M3 3700) of
+// the 2048 that its products need, because one wave a SIMD issues the weights' vector
+// instructions in 5 cycles where two would take 4; and a workgroup by its start (first
+// tiles, queries) and its end, 14 to 26 thousand cycles, which nothing else on the CU hides.
 template <int D, bool FP8, int TK>
 __global__ __launch_bounds__(512, D == 64 ? 4 : 2) void attn_chunk_kernel(const AttnArgs a) {
   using St = Stage<D, false, TK, TK / 4>;
@@ -847,6 +855,10 @@ __global__ __launch_bounds__(512, D == 64 ? 4 : 2) void attn_chunk_kernel(const 
 // sequence would need more splits than there are (the lengths are device data, so
 // the grid holds the most splits and the ones without tiles leave). The last
 // workgroup of a (sequence, head) to arrive joins its parts, in their order.
+//
+// Bound by memory: eight bf16 sequences of 65536, 32 + 8 heads of 128, 362 us (5.93 TB/s
+// read); 64 E4M3 ones of up to 1536 30.7 us (4.57 TB/s). One of 1025: 9.4 us, of which the
+// launch, four dependent loads (lengths, page, keys, values) and the join are all but 1.
 constexpr int kPieces = 512;
 __device__ __forceinline__ float groups_max(float x) {
   const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
@@ -1279,7 +1291,7 @@ Plan step_plan(const qlin_kv_cache& cache, const qlin_kv_batch& batch, int64_t r
   p.splits = (int)std::max<int64_t>(1, std::min({(most + wgs - 1) / wgs, (keys + piece - 1) / piece, (int64_t)64}));
   // The last workgroup reads all parts, a part's keys and its rows cost about the same
   // time at keys * 32 = parts^2 * rows * head_dim: 2 sequences of 50 rows, heads of 128,
-  // 28454 keys: 36 us, 54 with 64 parts; 16 tokens of 32 heads, 32768 keys: 39 and 47.
+  // 28454 keys: 36 us, 54 with 64 parts; 16 tokens of 32 heads, 32768 keys: 38 and 47.
   const int even = (int)std::sqrt(32.0 * (double)keys / (double)(p.part_rows * cache.head_dim));
   p.splits = std::max(1, std::min(p.splits, even));
   if (wgs >= most) p.splits = 1;
@@ -1306,12 +1318,12 @@ Plan chunk_plan(const qlin_kv_cache& cache, const qlin_kv_batch& batch, int64_t 
 // leaves most of its workgroups' rows or most CUs idle. Heads of 128, a group of 4,
 // 8 key/value heads, us of 32 and of 256 rows:
 //   up to 128 rows a sequence: 200 sequences of 16 tokens (4 key/value heads) of up to
-//     1024: 79 and 167; 40 of 32 of 16384: 526 and 551; one of 16 of 32768: 47 and 54;
-//   more, at most 1024 workgroups of 32 rows, as long as these times the keys are at most
-//     2 M: 512 tokens of 512: 13 and 21; 1024 of 1024: 29 and 32 (no
-//     causal mask: 35 and 31); four chunks of 64 of 4096: 27 and 32; 512 of 4096: 51 and 49;
-//   the others: 2048 of 2048: 75 and 55; 1024 of 4096: 93 and 77; 256 of 8192: 56 and 49,
-//     of 32768: 194 and 135.
+//     1024: 79 and 167; 40 of 32 of 16384: 526 and 551; one of 16 of 32768: 38 and 54;
+//   more, at most 1024 workgroups of 32 rows and these times the keys below 2^21: 512
+//     tokens of 512: 13 and 21; 1024 of 1024: 29 and 32 (no causal mask: 35 and 31); four
+//     chunks of 64 of 4096: 27 and 32;
+//   the others: 512 of 4096: 51 and 49; 256 of 8192: 56 and 49, of 32768: 194 and 135;
+//     1024 of 4096: 93 and 77; 2048 of 2048: 75 and 55.
 // Heads of 64 have four of these workgroups on a CU, twice as many: 1500 of 1500: 28 and
 // 40, 2048 of 2048: 41 and 43.
 // Here: the most keys for which 32 rows are taken (0: never).
@@ -1322,7 +1334,7 @@ int64_t few_rows_keys(const qlin_kv_cache& cache, const qlin_kv_batch& batch, in
   const int64_t tiles = (rows + 31) / 32 * batch.batch;  // (the grid: also those that a ragged batch leaves empty)
   const int64_t wgs = std::min(tiles, T * group / 32 + batch.batch) * cache.kv_heads;
   if (wgs > 1024 * room || tiles * cache.kv_heads > 8192) return 0;
-  return ((int64_t)room << 21) / wgs;
+  return ((room << 21) - 1) / wgs;
 }
 
 Plan plan_of(const qlin_kv_cache& cache, const qlin_kv_batch& batch, int64_t T, int64_t q_heads, int64_t window) {
