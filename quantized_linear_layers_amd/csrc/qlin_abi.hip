@@ -458,19 +458,21 @@ int qlin_rope(const qlin_bf16* x, int64_t ldx, int64_t T, int64_t H, int64_t D,
   return launch_rope(x, ldx, T, H, D, positions, *rope, inverse, y, ldy, as_stream(stream));
 }
 
+static bool kv_shape_ok(const qlin_kv_cache* c, const qlin_kv_batch* b, int64_t T) {
+  return (c->head_dim == 64 || c->head_dim == 128 || c->head_dim == 256) && c->page_size >= 16 &&
+         c->page_size <= 256 && (c->page_size & (c->page_size - 1)) == 0 && c->pages >= 1 &&
+         c->pages <= 0x7FFFFFFF && c->kv_heads >= 1 && c->kv_heads <= 0xFFFF &&
+         c->pages * c->kv_heads <= 0x7FFFFFFF && T >= 0 && T <= 0x7FFFFFFF && b->batch >= 0 &&
+         b->batch <= 0xFFFF && b->max_q >= 0 && b->table_cols >= 0 &&
+         b->table_cols <= (0x7FFFFFFF - 65536) / c->page_size;
+}
+
 // The cache and batch of a call with T rows; the arrays of an empty call (T == 0
 // or no sequence) may be NULL.
 static int kv_args(const qlin_kv_cache* c, const qlin_kv_batch* b, int64_t T) {
   QLIN_CHECK(c && b, QLIN_ERR_ARG);
   QLIN_CHECK(c->fmt == QLIN_KV_BF16 || c->fmt == QLIN_KV_E4M3, QLIN_ERR_ARG);
-  QLIN_CHECK((c->head_dim == 64 || c->head_dim == 128 || c->head_dim == 256) && c->page_size >= 16 &&
-                 c->page_size <= 256 && (c->page_size & (c->page_size - 1)) == 0 && c->pages >= 1 &&
-                 c->pages <= 0x7FFFFFFF && c->kv_heads >= 1 && c->kv_heads <= 0xFFFF &&
-                 c->pages * c->kv_heads <= 0x7FFFFFFF,
-             QLIN_ERR_SHAPE);
-  QLIN_CHECK(T >= 0 && T <= 0x7FFFFFFF && b->batch >= 0 && b->batch <= 0xFFFF && b->max_q >= 0 &&
-                 b->table_cols >= 0 && b->table_cols <= (0x7FFFFFFF - 65536) / c->page_size,
-             QLIN_ERR_SHAPE);
+  QLIN_CHECK(kv_shape_ok(c, b, T), QLIN_ERR_SHAPE);
   if (T == 0 || b->batch == 0) return QLIN_OK;
   QLIN_CHECK(b->table_cols >= 1 && b->max_q >= 1, QLIN_ERR_SHAPE);
   QLIN_CHECK(c->k && c->v && b->q_start && b->kv_len && b->page_table, QLIN_ERR_ARG);
@@ -520,8 +522,8 @@ static bool attn_shape_ok(const qlin_kv_cache* c, const qlin_kv_batch* b, int64_
 
 size_t qlin_attn_workspace_bytes(const qlin_kv_cache* cache, const qlin_kv_batch* batch, int64_t T,
                                  int64_t q_heads) {
-  if (!cache || !batch || T <= 0 || batch->batch <= 0 || cache->kv_heads <= 0 || cache->page_size <= 0 ||
-      batch->table_cols <= 0 || batch->max_q <= 0 || !attn_shape_ok(cache, batch, T, q_heads))
+  if (!cache || !batch || !kv_shape_ok(cache, batch, T) || T == 0 || batch->batch == 0 ||
+      batch->table_cols == 0 || batch->max_q == 0 || !attn_shape_ok(cache, batch, T, q_heads))
     return 0;
   return attn_workspace_bytes(*cache, *batch, T, q_heads);
 }

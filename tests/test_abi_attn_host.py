@@ -156,6 +156,12 @@ def test_attn_workspace(q):
             assert q.lib().qlin_attn_workspace_bytes(c, bb, B * mq, 4) >= 0
     assert q.lib().qlin_attn_workspace_bytes(c, b, 0, 4) == 0
     assert q.lib().qlin_attn_workspace_bytes(None, b, 1, 4) == 0
+    # sizes that the call refuses need none
+    for over, _ in BAD_CACHE:
+        if set(over) & {"head_dim", "page_size", "pages", "kv_heads"}:
+            assert q.lib().qlin_attn_workspace_bytes(cache(q, **over), b, 1, 4) == 0, over
+    assert q.lib().qlin_attn_workspace_bytes(c, b, 1 << 62, 4) == 0
+    assert q.lib().qlin_attn_workspace_bytes(c, batch(q, batch=1, table_cols=1 << 60), 1, 4) == 0
     assert q.lib().qlin_attn_workspace_bytes(c, b, 1, 3) == 0
 
 
