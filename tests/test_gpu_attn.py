@@ -525,6 +525,28 @@ def test_append(q, oracle, D, page, Hkv, Hq, rot, inter, fmt):
             assert np.array_equal(a, bb)
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_append_codes_of_any_magnitude(q, oracle, D):
+    """E4M3 rows from the smallest to the largest magnitudes, ties among their
+    quotients: the per-token quantiser's scales and codes, bit for bit."""
+    rng = np.random.default_rng(D)
+    T, Hkv, page = 4096, 2, 64
+    x = rng.standard_normal((T, Hkv, D)) * 2.0 ** rng.integers(-126, 127, (T, Hkv, 1))
+    x[:512] = 2.0 ** rng.integers(-100, 100, (512, Hkv, 1)) * rng.integers(-448, 449, (512, Hkv, D)) / 16  # exact quotients
+    k = bits(np.clip(x, -3e38, 3e38))
+    cache = q.PagedKV.empty(T // page, Hkv, D, page, "e4m3")
+    table = rng.permutation(T // page)[None].astype(np.int32)
+    b = q.PagedBatch(dev(np.array([0, T], np.int32)), dev(np.array([T], np.int32)), dev(table), T)
+    q.kv_append(cache, b, dev(k), dev(k[::-1].copy()))
+    slot, _ = oracle.kv_slots([0, T], [T], table, page, T // page, T)
+    for name, rows in (("k", k), ("v", k[::-1])):
+        want, ws = oracle.quant_act(np.ascontiguousarray(rows).reshape(-1, D), oracle.OCP)
+        got = host(getattr(cache, name))[slot // page, :, slot % page].reshape(-1, D)
+        sc = host(getattr(cache, name + "_scale"))[slot // page, :, slot % page].ravel()
+        assert np.array_equal(sc, ws), name
+        assert np.array_equal(got, want), name
+
+
 def test_append_in_place_queries(q):
     rng = np.random.default_rng(8)
     start, table, pages = make_batch(rng, [20], [60], 16)
