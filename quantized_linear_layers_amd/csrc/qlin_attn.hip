@@ -614,7 +614,7 @@ __device__ __forceinline__ bool chunk_item(const AttnArgs& a, Item& it, int& row
 //
 // Heads of 64 need few enough registers for two workgroups a CU (four waves a SIMD):
 // each fills the other's waits, so the priority of the multiplying wave, which is
-// worth 3 % with heads of 128, costs 3 % there.
+// worth 2 to 4 % with wider heads, costs 3 % there.
 //
 // Measured, 32 + 8 heads of 128: a prompt of 8192, bf16 491 us (1119 TFLOP/s, 86 % of a
 // large library matrix product's 1294); 2048 of 32768 902 us (1181); eight E4M3 chunks of
@@ -788,7 +788,7 @@ __global__ __launch_bounds__(512, D == 64 ? 4 : 2) void attn_chunk_kernel(const 
   // waves in step, so leaving one out would save nothing.
   for (int t = t0; t < t1; ++t) {
     // multiply
-    if (D == 128) __builtin_amdgcn_s_setprio(1);
+    if (D > 64) __builtin_amdgcn_s_setprio(1);
     if (D < 256) prefetch(t > t0 ? t - 1 : t);
     multiply<D, KB, kAhead, true>(q, st, s, p, fr, lds_v[(t > t0 ? t - 1 : t) & 3], lds_k[at], [&](int i) {
       if constexpr (FP8) {
@@ -798,7 +798,7 @@ __global__ __launch_bounds__(512, D == 64 ? 4 : 2) void attn_chunk_kernel(const 
           ks[i - (kProducts / 2 - 4 * KB)] = scales(lds_s[t & 7], i - (kProducts / 2 - 4 * KB));
       }
     });
-    if (D == 128) __builtin_amdgcn_s_setprio(0);
+    if (D > 64) __builtin_amdgcn_s_setprio(0);
     phase_end(kAll);
     // weights
     if constexpr (FP8) {

@@ -340,6 +340,18 @@ def test_many_sequences(q, oracle):
     run_attn(q, oracle, 82, new, kv, 1, 2, 64, 16, "bf16", pad=2)
 
 
+@pytest.mark.parametrize("B", [70, 150])
+def test_chunk_of_many_sequences(q, oracle, B):
+    """The same in workgroups of 256 rows, with the key axis split (70) and whole."""
+    rng = np.random.default_rng(B)
+    new = rng.integers(0, 3, B).tolist()
+    kv = [n + int(x) for n, x in zip(new, rng.integers(0, 60, B))]
+    for b, n, more in ((2, 300, 40), (66, 200, 500), (B - 1, 140, 0)):
+        new[b], kv[b] = n, n + more
+    run_attn(q, oracle, 83, new, kv, 1, 2, 128, 16, "bf16", pad=2, extra_cols=long_table(16))
+    run_attn(q, oracle, 84, new, kv, 1, 2, 64, 32, "e4m3", window=90, extra_cols=long_table(16))
+
+
 def test_length_over_the_table(q, oracle):
     rng = np.random.default_rng(4)
     start, table, pages = make_batch(rng, [1], [64], 16)
