@@ -593,103 +593,214 @@ __device__ __forceinline__ bool chunk_item(const AttnArgs& a, Item& it, int& row
   return true;
 }
 
-// A workgroup of 8 waves has 256 rows of one (sequence, key/value head), 32 a
-// wave, and walks their keys in tiles of TK that all waves share. A tile costs a
-// wave about as many matrix cycles (scores and values) as vector cycles
-// (weights), so the two waves of a SIMD, w and w + 4, work in opposite phases:
-// while one multiplies (values of tile t - 1, scores of tile t), the other takes
-// the weights of its tile; a barrier ends each phase.
-//   phase   waves 0-3           waves 4-7
-//   2t      PV(t-1), QK(t)      weights(t-1)
-//   2t+1    weights(t)          PV(t-1), QK(t)
-// K(t) and V(t-1) are free after phase 2t+1; K has three places, V four. bf16: in
-// their weight phase of tile t waves 0-3 issue the loads of K(t+2) into the place of
-// K(t-1), waves 4-7 those of V(t+2) into the place of V(t-2), and by its end they have
-// waited for those of the tile before.
-// E4M3 tiles become bf16 on the way into LDS, once a workgroup (converting
-// fragments would cost every wave 8 instructions a product, in the phase in
-// which its partner needs the vector unit). They pass through registers: spread
-// over the products of tile t, each wave writes its piece of K(t+2) or V(t+2), loaded
-// one tile before, and loads that of tile t+3. Scales come along: places for 8 tiles.
-//
-// Heads of 64 need few enough registers for two workgroups a CU (four waves a SIMD):
-// each fills the other's waits, so the priority of the multiplying wave, which is
-// worth 2 to 4 % with wider heads, costs 3 % there.
-//
-// Measured, 32 + 8 heads of 128: a prompt of 8192, bf16 491 us (1119 TFLOP/s, 86 % of a
-// large library matrix product's 1294); 2048 of 32768 902 us (1181); eight E4M3 chunks of
-// up to 1024 of up to 9001 557 us (917). 16 + 8 heads of 256, window 1024, four prompts of
-// 4096: 223 us (735). Bound by the phases: a tile takes about 2900 cycles (E4M3 3700) of
-// the 2048 that its products need, because one wave a SIMD issues the weights' vector
-// instructions in 5 cycles where two would take 4; and a workgroup by its start (first
-// tiles, queries) and its end, 14 to 26 thousand cycles, which nothing else on the CU hides.
-template <int D, bool FP8, int TK>
-__global__ __launch_bounds__(512, D == 64 ? 4 : 2) void attn_chunk_kernel(const AttnArgs a) {
-  using St = Stage<D, false, TK, TK / 4>;
-  using G = Geo<D, false>;
-  constexpr int BM = 256, KB = TK / 32;
-  constexpr int kScale = TK / 16 * 256;  // bytes of one scale area
-  __shared__ __attribute__((aligned(1024))) uint8_t lds_k[3][St::kTile], lds_v[4][St::kTile];
-  __shared__ __attribute__((aligned(1024))) uint8_t lds_s[8][FP8 ? 2 * kScale : 16];
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-
+// What a wave of a workgroup of BM rows has to do: its first row w0, its lane's row, the
+// keys that the workgroup's and the wave's rows see, those of the lane's row, and the
+// tiles of TK keys of this part.
+struct ChunkJob {
   Item it;
-  int row0, split;
-  if (!chunk_item<BM>(a, it, row0, split)) return;
-
-  const int w0 = row0 + 32 * wave;  // the wave's first row
-  const int row = w0 + (lane & 31);
-  const Range wg = range_of(a, it, row0, min(row0 + BM, it.rows));
-  const Range own = range_of(a, it, w0, max(min(w0 + 32, it.rows), w0 + 1));
-  const int vlo = row_lo(a, it, row), vhi = row_hi(a, it, row);
-  int t0 = wg.lo / TK, t1 = (wg.hi + TK - 1) / TK;
+  int split, w0, row;
+  Range wg, own;
+  int vlo, vhi, t0, t1;
+};
+template <int BM, int TK>
+__device__ __forceinline__ bool chunk_job(const AttnArgs& a, int wave, ChunkJob& j) {
+  int row0;
+  if (!chunk_item<BM>(a, j.it, row0, j.split)) return false;
+  j.w0 = row0 + 32 * wave;
+  j.row = j.w0 + ((int)threadIdx.x & 31);
+  j.wg = range_of(a, j.it, row0, min(row0 + BM, j.it.rows));
+  j.own = range_of(a, j.it, j.w0, max(min(j.w0 + 32, j.it.rows), j.w0 + 1));
+  j.vlo = row_lo(a, j.it, j.row);
+  j.vhi = row_hi(a, j.it, j.row);
+  int t0 = j.wg.lo / TK, t1 = (j.wg.hi + TK - 1) / TK;
   if (a.splits > 1) {
     const int n = max((t1 - t0 + a.splits - 1) / a.splits, 1);
-    t0 = min(t0 + split * n, t1);
+    t0 = min(t0 + j.split * n, t1);
     t1 = min(t0 + n, t1);
   }
-  t0 = __builtin_amdgcn_readfirstlane(t0);
-  t1 = __builtin_amdgcn_readfirstlane(t1);
-  const bool first = wave < 4;
-  // the rows of a tile that this wave loads, of one 16-row group (bf16: waves 0-3 of
-  // K and V; E4M3: waves 0-3 of K, 4-7 of V)
+  j.t0 = __builtin_amdgcn_readfirstlane(t0);
+  j.t1 = __builtin_amdgcn_readfirstlane(t1);
+  return true;
+}
+
+// bf16: a workgroup of 4 waves has 128 rows of one (sequence, key/value head), 32 a
+// wave, and walks their keys in tiles of TK that its waves share. A wave multiplies
+// (values of tile t - 1, scores of tile t), then takes the weights of tile t; a tile
+// costs it about as many matrix cycles as vector cycles. Two workgroups share a CU
+// (heads of 64: four), one wave of each a SIMD, so that while one multiplies another
+// takes weights, and one's start and end hide behind the other's tiles.
+// K and V have two places each. After the barrier that ends the products of tile t,
+// K(t) and V(t-1) are free: the loads of K(t+2) and V(t+1) go there, and have until the
+// end of the products of tile t+1, where the wave waits for them before the barrier.
+// (One workgroup of 256 rows a CU, its wave pairs held in opposite phases by barriers,
+// as below: 231 us for 213 with heads of 256 and a window, 83 for 73 for eight prompts
+// of 1024 with heads of 128, 945 for 962 for 2048 tokens of 32768.)
+template <int D, int TK>
+__global__ __launch_bounds__(256, D == 64 ? 4 : 2) void attn_chunk_kernel(const AttnArgs a) {
+  using St = Stage<D, false, TK, TK / 4>;
+  using G = Geo<D, false>;
+  constexpr int BM = 128, KB = TK / 32;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds_k[2][St::kTile], lds_v[2][St::kTile];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  ChunkJob job;
+  if (!chunk_job<BM, TK>(a, wave, job)) return;
+  const Item it = job.it;
+  const Range wg = job.wg, own = job.own;
+  const int w0 = job.w0, row = job.row, vlo = job.vlo, vhi = job.vhi, t0 = job.t0, t1 = job.t1;
+  // the rows of a tile that this wave loads, of one 16-row group
   constexpr int kRows = TK / 4;
-  const int r0 = (wave & 3) * kRows;
+  const int r0 = wave * kRows;
   const int g0 = r0 & ~15;
   auto page_at = [&](int t) { return page_of(a, it, t * TK + g0); };
   constexpr std::integral_constant<bool, true> kEdge;
   constexpr std::integral_constant<bool, false> kInner;
-  constexpr int kOps = St::kLoads;  // loads of an iteration (bf16)
-  // E4M3: read the key scales over the last products and the values' ahead of the
-  // weights, where registers allow; else where they are used, an LDS read's time
-  // exposed eight times a tile (eight chunks of up to 1024 tokens, 32 heads of
-  // 128, in prompts of up to 9001: 610 us and 663; heads of 256 would spill: four such
-  // chunks 1600 us and 790).
-  constexpr bool kHold = D == 128;
-  constexpr int kProducts = 2 * KB * (D / 32) + KB * (D / 16);  // of a tile
-  // bf16: straight into LDS
   auto load = [&](int t, int page, uint8_t* to, auto is_v, auto edge) {
     const Rows16 w = rows_of(a, it, t * TK + g0, page, wg.hi);
     v4i rs = resource<G::kRow>(is_v ? a.v : a.k, w);
     settled(rs);
     St::template rows<is_v, edge>(rs, wg.lo - t * TK - g0, r0, lds_addr(to));
   };
-  // E4M3: this lane's codes of K (waves 0-3) or V, kMine * 16 of them, where they go as
+  constexpr int kAhead = D == 128 ? 8 : 4;  // fragments ahead of the products (64, 256: as registers allow)
+  // the end of the products: this wave's loads have arrived, its LDS reads are done, and
+  // nothing moves across
+  auto products_end = [&] {
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  // (tiles from t1 on load nothing: no row of theirs is visible)
+  int p1 = page_at(t0 + 1), p2 = page_at(t0 + 2);  // pages of the next loads
+  if (t0 < t1) {
+    const int p0 = page_at(t0);
+    load(t0, p0, lds_k[0], kInner, kEdge);
+    load(t0, p0, lds_v[0], kEdge, kEdge);
+    load(t0 + 1, p1, lds_k[1], kInner, kInner);
+  }
+  // whether some page of these keys does not exist
+  bool hole = false;
+  const int c1 = t0 < t1 ? (t1 * TK - 1) >> a.page_shift : -1;
+  for (int c = ((t0 * TK) >> a.page_shift) + (int)threadIdx.x; c <= min(c1, a.cols - 1); c += 256)
+    hole |= no_page(a, a.table[(int64_t)it.b * a.cols + c]);
+  v8bf q[D / 16];
+  load_q<D>(a, it, row, q);
+  State<D> st;
+  st.clear();
+  dma_wait<0>();
+  lds_reads_done();
+  const bool holes = __syncthreads_or(hole);
+  v16f s[KB];
+  v4i p[2 * KB];
+  v8bf fr[kAhead];
+  const v4f none[4 * KB] = {};
+#pragma unroll
+  for (int i = 0; i < 2 * KB; ++i) p[i] = v4i{};
+  // (the first tile adds zero weights times its own values)
+  auto prefetch = [&](int place) {  // (all of the values')
+    static_assert(kAhead <= 2 * KB * (D / 32), "");
+    const int lane = frag_lane<D>();
+#pragma unroll
+    for (int n = 0; n < kAhead; ++n) fr[n] = frag<D, KB>(lds_v[place], lds_k[0], n, lane);
+  };
+  int at = 0;  // the place of K(t) and V(t)
+  for (int t = t0; t < t1; ++t) {
+    const int vat = t > t0 ? at ^ 1 : at;
+    prefetch(vat);
+    __builtin_amdgcn_s_setprio(1);
+    multiply<D, KB, kAhead, true>(q, st, s, p, fr, lds_v[vat], lds_k[at], [](int) {});
+    __builtin_amdgcn_s_setprio(0);
+    products_end();
+    load(t + 2, p2, lds_k[at], kInner, kInner);
+    load(t + 1, p1, lds_v[at ^ 1], kEdge, kInner);
+    p1 = p2;
+    p2 = page_at(t + 3);
+    const int key = t * TK;
+    uint32_t bad = 0;
+    if (holes)
+      for (int g = 0; g < TK / 16; ++g) bad |= (uint32_t)no_page(a, page_of(a, it, key + 16 * g)) << g;
+    const bool masked = holes || key + TK > own.all_hi || key < own.all_lo;
+    weight_block<D, false, KB, 0, false>(a, st, s, p, none, nullptr, masked, vlo - key, vhi - key, bad);
+    __builtin_amdgcn_sched_barrier(0);
+    at ^= 1;
+  }
+  if (t0 < t1) {
+    prefetch(at ^ 1);
+    multiply<D, KB, kAhead, false>(q, st, s, p, fr, lds_v[at ^ 1], lds_k[at], [](int) {});
+  }
+  dma_wait<0>();
+  if (a.splits > 1) {
+    store_part<D>(a, it, job.split, row, st);
+    return;
+  }
+  __syncthreads();  // V's places are free
+  store_rows<D>(a, it, w0, st, &lds_v[0][0] + wave * (TK * D));
+}
+
+// E4M3: tiles become bf16 on the way into LDS, once a workgroup (converting fragments
+// would cost every wave 8 instructions a product), so a workgroup has 8 waves and 256
+// rows. The two waves of a SIMD, w and w + 4, work in opposite phases: while one
+// multiplies, the other takes the weights of its tile; a barrier ends each phase.
+//   phase   waves 0-3           waves 4-7
+//   2t      PV(t-1), QK(t)      weights(t-1)
+//   2t+1    weights(t)          PV(t-1), QK(t)
+// K(t) and V(t-1) are free after phase 2t+1; K has three places, V four. Tiles pass
+// through registers: spread over the products of tile t, each wave writes its piece of
+// K(t+2) (waves 0-3) or V(t+2), loaded one tile before, and loads that of tile t+3.
+// Scales come along: places for 8 tiles.
+//
+// Heads of 64 need few enough registers for two workgroups a CU (four waves a SIMD):
+// each fills the other's waits, so the priority of the multiplying wave, which is
+// worth 2 to 4 % with wider heads, costs 3 % there.
+//
+// Measured, 32 + 8 heads of 128: eight chunks of up to 1024 tokens in prompts of up to
+// 9001 557 us (917 TFLOP/s). Bound by the phases: a tile takes about 3700 cycles of the
+// 2048 that its products need: the scales are 64 multiplications a lane, and one wave a
+// SIMD issues the vector instructions of its weights in 5 cycles where two would take 4.
+template <int D, int TK>
+__global__ __launch_bounds__(512, D == 64 ? 4 : 2) void attn_chunk_e4m3_kernel(const AttnArgs a) {
+  using St = Stage<D, false, TK, TK / 4>;
+  using G = Geo<D, false>;
+  constexpr int BM = 256, KB = TK / 32;
+  constexpr int kScale = TK / 16 * 256;  // bytes of one scale area
+  __shared__ __attribute__((aligned(1024))) uint8_t lds_k[3][St::kTile], lds_v[4][St::kTile];
+  __shared__ __attribute__((aligned(1024))) uint8_t lds_s[8][2 * kScale];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+
+  ChunkJob job;
+  if (!chunk_job<BM, TK>(a, wave, job)) return;
+  const Item it = job.it;
+  const Range wg = job.wg, own = job.own;
+  const int w0 = job.w0, row = job.row, vlo = job.vlo, vhi = job.vhi, t0 = job.t0, t1 = job.t1;
+  const bool first = wave < 4;
+  // the rows of a tile that this wave loads, of one 16-row group (waves 0-3 of K, 4-7 of V)
+  constexpr int kRows = TK / 4;
+  const int r0 = (wave & 3) * kRows;
+  const int g0 = r0 & ~15;
+  auto page_at = [&](int t) { return page_of(a, it, t * TK + g0); };
+  constexpr std::integral_constant<bool, true> kEdge;
+  constexpr std::integral_constant<bool, false> kInner;
+  // Read the key scales over the last products and the values' ahead of the
+  // weights, where registers allow; else where they are used, an LDS read's time
+  // exposed eight times a tile (eight chunks of up to 1024 tokens, 32 heads of
+  // 128, in prompts of up to 9001: 610 us and 663; heads of 256 would spill: four such
+  // chunks 1600 us and 790).
+  constexpr bool kHold = D == 128;
+  constexpr int kProducts = 2 * KB * (D / 32) + KB * (D / 16);  // of a tile
+  // This lane's codes of K (waves 0-3) or V, kMine * 16 of them, where they go as
   // bf16, and the scales of the wave's group
-  constexpr int kMine = FP8 ? kRows * D / 1024 : 1;
+  constexpr int kMine = kRows * D / 1024;
   const uint8_t* pool = first ? a.k : a.v;
   const float* pool_s = first ? a.ks : a.vs;
   int from[kMine], to[kMine][2];
-  if constexpr (FP8) {
 #pragma unroll
-    for (int c = 0; c < kMine; ++c) {
-      const int n = c * 64 + lane, row = r0 + n / (D / 16), chunk = n % (D / 16);
-      const int sw = first ? G::k_swz(row) : G::v_swz(row);
-      from[c] = (row & 15) * D + 16 * chunk;
-      to[c][0] = row * G::kRow + 16 * ((2 * chunk) ^ sw);
-      to[c][1] = row * G::kRow + 16 * ((2 * chunk + 1) ^ sw);
-    }
+  for (int c = 0; c < kMine; ++c) {
+    const int n = c * 64 + lane, r = r0 + n / (D / 16), chunk = n % (D / 16);
+    const int sw = first ? G::k_swz(r) : G::v_swz(r);
+    from[c] = (r & 15) * D + 16 * chunk;
+    to[c][0] = r * G::kRow + 16 * ((2 * chunk) ^ sw);
+    to[c][1] = r * G::kRow + 16 * ((2 * chunk + 1) ^ sw);
   }
   auto fetch = [&](int t, int page, v4i (&x)[kMine], auto edge) {
     const Rows16 w = rows_of(a, it, t * TK + g0, page, wg.hi);
@@ -734,27 +845,19 @@ __global__ __launch_bounds__(512, D == 64 ? 4 : 2) void attn_chunk_kernel(const 
 
   // (tiles from t1 on load nothing: no row of theirs is visible)
   int p1 = page_at(t0 + 1), p2 = page_at(t0 + 2);  // pages of the next loads
-  v4i fx[kMine];                                   // E4M3: tile t + 2 on its way
+  v4i fx[kMine];                                   // tile t + 2 on its way
   if (t0 < t1) {
     const int p0 = page_at(t0);
-    if constexpr (FP8) {
-      v4i x0[kMine], x1[kMine];
-      fetch(t0, p0, x0, kEdge);
-      fetch(t0 + 1, p1, x1, kInner);
-      fetch(t0 + 2, p2, fx, kInner);
+    v4i x0[kMine], x1[kMine];
+    fetch(t0, p0, x0, kEdge);
+    fetch(t0 + 1, p1, x1, kInner);
+    fetch(t0 + 2, p2, fx, kInner);
 #pragma unroll
-      for (int i = 0; i < 2 * kMine; ++i) {
-        put(x0, t0, 0, i);
-        put(x1, t0 + 1, 1, i);
-      }
-    } else if (first) {
-      load(t0, p0, lds_k[0], kInner, kEdge);
-      load(t0 + 1, p1, lds_k[1], kInner, kInner);
-    } else {
-      load(t0, p0, lds_v[t0 & 3], kEdge, kEdge);
-      load(t0 + 1, p1, lds_v[(t0 + 1) & 3], kEdge, kInner);
+    for (int i = 0; i < 2 * kMine; ++i) {
+      put(x0, t0, 0, i);
+      put(x1, t0 + 1, 1, i);
     }
-    if (FP8) p2 = page_at(t0 + 3);
+    p2 = page_at(t0 + 3);
   }
   // whether some page of these keys does not exist
   bool hole = false;
@@ -766,13 +869,12 @@ __global__ __launch_bounds__(512, D == 64 ? 4 : 2) void attn_chunk_kernel(const 
   State<D> st;
   st.clear();
   int at = 0, next = 1, last = 2;  // K's places of tiles t, t + 1 and t + 2 (t - 1)
-  if (!FP8) dma_wait<0>();
   lds_reads_done();  // (and writes)
   const bool holes = __syncthreads_or(hole);
   v16f s[KB];
   v4i p[2 * KB];
   v8bf fr[kAhead];
-  v4f ks[4 * KB];  // E4M3: the tile's key scales, read over the last products
+  v4f ks[4 * KB];  // the tile's key scales, read over the last products
 #pragma unroll
   for (int i = 0; i < 2 * KB; ++i) p[i] = v4i{};
   // (the first tile adds zero weights times its own values)
@@ -791,33 +893,22 @@ __global__ __launch_bounds__(512, D == 64 ? 4 : 2) void attn_chunk_kernel(const 
     if (D > 64) __builtin_amdgcn_s_setprio(1);
     if (D < 256) prefetch(t > t0 ? t - 1 : t);
     multiply<D, KB, kAhead, true>(q, st, s, p, fr, lds_v[(t > t0 ? t - 1 : t) & 3], lds_k[at], [&](int i) {
-      if constexpr (FP8) {
-        if (i < 2 * kMine) put(fx, t + 2, last, i);
-        if (i == 2 * kMine) fetch(t + 3, p2, fx, kInner);
-        if (kHold && i >= kProducts / 2 - 4 * KB)
-          ks[i - (kProducts / 2 - 4 * KB)] = scales(lds_s[t & 7], i - (kProducts / 2 - 4 * KB));
-      }
+      if (i < 2 * kMine) put(fx, t + 2, last, i);
+      if (i == 2 * kMine) fetch(t + 3, p2, fx, kInner);
+      if (kHold && i >= kProducts / 2 - 4 * KB)
+        ks[i - (kProducts / 2 - 4 * KB)] = scales(lds_s[t & 7], i - (kProducts / 2 - 4 * KB));
     });
     if (D > 64) __builtin_amdgcn_s_setprio(0);
     phase_end(kAll);
     // weights
-    if constexpr (FP8) {
-      p2 = page_at(t + 4);
-    } else {
-      if (first)
-        load(t + 2, p2, lds_k[last], kInner, kInner);
-      else
-        load(t + 2, p2, lds_v[(t + 2) & 3], kEdge, kInner);
-      p2 = page_at(t + 3);
-    }
+    p2 = page_at(t + 4);
     const int key = t * TK;
     uint32_t bad = 0;
     if (holes)
       for (int g = 0; g < TK / 16; ++g) bad |= (uint32_t)no_page(a, page_of(a, it, key + 16 * g)) << g;
     const bool masked = holes || key + TK > own.all_hi || key < own.all_lo;
-    weight_block<D, FP8, KB, kScale, kHold>(a, st, s, p, ks, lds_s[t & 7], masked, vlo - key, vhi - key, bad);
+    weight_block<D, true, KB, kScale, kHold>(a, st, s, p, ks, lds_s[t & 7], masked, vlo - key, vhi - key, bad);
     if (D == 256) prefetch(t);
-    if (!FP8) dma_wait<kOps>();  // what the tile before loaded
     phase_end(kNone);  // (no LDS writes in this phase)
     const int x = last;
     last = at;
@@ -831,7 +922,7 @@ __global__ __launch_bounds__(512, D == 64 ? 4 : 2) void attn_chunk_kernel(const 
   dma_wait<0>();
   if (first) phase_end(kAll);
   if (a.splits > 1) {
-    store_part<D>(a, it, split, row, st);
+    store_part<D>(a, it, job.split, row, st);
     return;
   }
   __syncthreads();  // V's places are free
@@ -1270,7 +1361,9 @@ struct Plan {
 
 // Arrival counters at the start of the workspace, as the GEMMs' split-K.
 constexpr size_t kAttnCounterBytes = kGemmCounterBytes;
-constexpr int kChunkRows = 256;
+// Rows of a chunk's workgroup, and its workgroups a CU.
+int64_t chunk_rows(const qlin_kv_cache& c) { return c.fmt == QLIN_KV_E4M3 ? 256 : 128; }
+int64_t chunk_room(const qlin_kv_cache& c) { return (c.head_dim == 64 ? 2 : 1) * (c.fmt == QLIN_KV_E4M3 ? 1 : 2); }
 constexpr int kCus = 256;
 
 Plan step_plan(const qlin_kv_cache& cache, const qlin_kv_batch& batch, int64_t rows, int64_t keys) {
@@ -1302,8 +1395,9 @@ Plan step_plan(const qlin_kv_cache& cache, const qlin_kv_batch& batch, int64_t r
 Plan chunk_plan(const qlin_kv_cache& cache, const qlin_kv_batch& batch, int64_t T, int64_t rows, int64_t group,
                 int64_t keys) {
   Plan p = {};
-  p.tiles = std::min(T * group / kChunkRows + batch.batch, (rows + kChunkRows - 1) / kChunkRows * batch.batch);
-  const int64_t wgs = p.tiles * cache.kv_heads, room = cache.head_dim == 64 ? 2 * kCus : kCus;
+  const int64_t bm = chunk_rows(cache), room = chunk_room(cache) * kCus;
+  p.tiles = std::min(T * group / bm + batch.batch, (rows + bm - 1) / bm * batch.batch);
+  const int64_t wgs = p.tiles * cache.kv_heads;
   // One workgroup a CU, equal parts. A chunk of 512 tokens (32 heads of 128, a group of
   // 4) of 4096: 4 parts 49.2 us, 2 63.6, 8 (more workgroups than CUs) 67.5; 1024 of 1024:
   // 2 parts 38.8, none 31.7. (Parts by each sequence's length instead: 1024 of 4096 90 us
@@ -1355,7 +1449,12 @@ void launch_parts(const AttnArgs& a, const Plan& p, hipStream_t st) {
       attn_step_kernel<D, FP8, 2, 4><<<grid, 256, 0, st>>>(a);
   } else {
     const int64_t items = p.tiles * a.kv_heads * p.splits;
-    attn_chunk_kernel<D, FP8, D == 256 ? 32 : 64><<<(unsigned)((items + 7) / 8 * 8), 512, 0, st>>>(a);
+    const unsigned grid = (unsigned)((items + 7) / 8 * 8);
+    constexpr int TK = D == 256 ? 32 : 64;
+    if constexpr (FP8)
+      attn_chunk_e4m3_kernel<D, TK><<<grid, 512, 0, st>>>(a);
+    else
+      attn_chunk_kernel<D, TK><<<grid, 256, 0, st>>>(a);
   }
   if (p.splits > 1 && !p.step) {
     const int64_t rows = a.T * a.kv_heads * a.group, wg = 1024 / D;  // rows of a workgroup
