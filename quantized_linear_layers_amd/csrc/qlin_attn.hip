@@ -30,10 +30,11 @@
 //
 // Two kernels share this: attn_step_kernel (32 rows a workgroup: a decode step, a
 // small chunk), where each wave takes its own key tiles and the waves merge at the
-// end, and attn_chunk_kernel (256 rows), where each wave has its own rows and the
-// workgroup shares the tiles. Either splits the key axis over workgroups when the rows alone do not
-// fill the device; the parts are joined by the last workgroup to arrive (step) or
-// by attn_join_kernel (chunk, whose parts are many rows).
+// end, and attn_chunk_kernel (128 rows; E4M3 attn_chunk_e4m3_kernel, 256), where each
+// wave has its own rows and the workgroup shares the tiles. All split the key axis
+// over workgroups when the rows alone do not fill the device; the parts are joined by
+// the last workgroup to arrive (step) or by attn_join_kernel (chunk, whose parts are
+// many rows).
 #include "qlin_internal.h"
 #include "qlin_device.h"
 
@@ -635,6 +636,12 @@ __device__ __forceinline__ bool chunk_job(const AttnArgs& a, int wave, ChunkJob&
 // (One workgroup of 256 rows a CU, its wave pairs held in opposite phases by barriers,
 // as below: 231 us for 213 with heads of 256 and a window, 83 for 73 for eight prompts
 // of 1024 with heads of 128, 945 for 962 for 2048 tokens of 32768.)
+//
+// Measured, 32 + 8 heads of 128: a prompt of 8192 515 us (1067 TFLOP/s, 82 % of a large
+// library matrix product's 1294); 2048 tokens of 32768 965 us (1103). 16 + 8 heads of 256,
+// window 1024, four prompts of up to 4096: 208 us (786). Bound by the issue of vector
+// instructions, about as many cycles as the products', and by what the two waves of a SIMD
+// take from each other.
 template <int D, int TK>
 __global__ __launch_bounds__(256, D == 64 ? 4 : 2) void attn_chunk_kernel(const AttnArgs a) {
   using St = Stage<D, false, TK, TK / 4>;
@@ -739,7 +746,8 @@ __global__ __launch_bounds__(256, D == 64 ? 4 : 2) void attn_chunk_kernel(const 
 
 // E4M3: tiles become bf16 on the way into LDS, once a workgroup (converting fragments
 // would cost every wave 8 instructions a product), so a workgroup has 8 waves and 256
-// rows. The two waves of a SIMD, w and w + 4, work in opposite phases: while one
+// rows (with 128 and the kernel above, twice the conversions: 655 us for 600 for the chunks
+// below, 1220 for 1015 for 2048 tokens of 32768). The two waves of a SIMD, w and w + 4, work in opposite phases: while one
 // multiplies, the other takes the weights of its tile; a barrier ends each phase.
 //   phase   waves 0-3           waves 4-7
 //   2t      PV(t-1), QK(t)      weights(t-1)
@@ -1398,37 +1406,37 @@ Plan chunk_plan(const qlin_kv_cache& cache, const qlin_kv_batch& batch, int64_t 
   const int64_t bm = chunk_rows(cache), room = chunk_room(cache) * kCus;
   p.tiles = std::min(T * group / bm + batch.batch, (rows + bm - 1) / bm * batch.batch);
   const int64_t wgs = p.tiles * cache.kv_heads;
-  // One workgroup a CU, equal parts. A chunk of 512 tokens (32 heads of 128, a group of
-  // 4) of 4096: 4 parts 49.2 us, 2 63.6, 8 (more workgroups than CUs) 67.5; 1024 of 1024:
-  // 2 parts 38.8, none 31.7. (Parts by each sequence's length instead: 1024 of 4096 90 us
-  // and more, where two equal ones take 77, and no gain over ragged batches.)
-  p.splits = keys < 2048 ? 1 : (int)std::max<int64_t>(1, std::min(room / wgs, keys / 512));
+  // As many equal parts as fill the device once. bf16, 32 + 8 heads of 128: 512 tokens of
+  // 4096 with 4 parts 49 us, 2 55, 8 (more workgroups than fit) 63; 1024 of 1024: 2 parts 34,
+  // none 26. (Parts by each sequence's length instead: no gain over ragged batches, and
+  // 1024 of 4096 90 us for 77.)
+  p.splits = keys <= 2048 ? 1 : (int)std::max<int64_t>(1, std::min(room / wgs, keys / 512));
   p.parts = p.splits <= 1 ? 0 : (size_t)p.splits * T * cache.kv_heads * group;
   return p;
 }
 
-// Workgroups of 32 rows (a step's kernel) or of 256 (a chunk's). The chunk's does
-// about twice the work a second once it fills the device, but a call of few rows
-// leaves most of its workgroups' rows or most CUs idle. Heads of 128, a group of 4,
-// 8 key/value heads, us of 32 and of 256 rows:
-//   up to 128 rows a sequence: 200 sequences of 16 tokens (4 key/value heads) of up to
-//     1024: 79 and 167; 40 of 32 of 16384: 526 and 551; one of 16 of 32768: 38 and 54;
-//   more, at most 1024 workgroups of 32 rows and these times the keys below 2^21: 512
-//     tokens of 512: 13 and 21; 1024 of 1024: 29 and 32 (no causal mask: 35 and 31); four
-//     chunks of 64 of 4096: 27 and 32;
-//   the others: 512 of 4096: 51 and 49; 256 of 8192: 56 and 49, of 32768: 194 and 135;
-//     1024 of 4096: 93 and 77; 2048 of 2048: 75 and 55.
-// Heads of 64 have four of these workgroups on a CU, twice as many: 1500 of 1500: 28 and
-// 40, 2048 of 2048: 41 and 43.
+// Workgroups of 32 rows (a step's kernel) or of 128 (E4M3: 256; a chunk's). The chunk's
+// do about twice the work a second once they fill the device, but a call of few rows
+// leaves most of their rows or most CUs idle. 32 + 8 heads of 128, us of 32 rows and of
+// 128 in bf16:
+//   up to 64 rows a sequence: 200 of 16 tokens (16 + 4 heads) of up to 1024: 79 and 91;
+//   more, at most 1024 workgroups of 32 rows and these times the keys below 2^20: 512
+//     tokens of 512: 13 and 17; four chunks of 64 of 4000: 27 and 28;
+//   the others: 1024 of 1024: 29 and 26; 512 of 4096: 52 and 49; 256 of 8192: 57 and 50;
+//     8 of 32 of 4096: 41 and 31; 2048 of 2048: 74 and 51.
+// Heads of 64 have four workgroups of 32 rows on a CU, twice as many: 1024 of 1024: 17 and
+// 20, 2048 of 2048: 41 and 35. E4M3, 32 and 256 rows, up to 128 rows or below 2^21: 14 of 33
+// of up to 3203 (16 + 4 heads): 38 and 46; 1024 of 1024: 31 and 36; 1024 of 4096: 105 and 84.
 // Here: the most keys for which 32 rows are taken (0: never).
 int64_t few_rows_keys(const qlin_kv_cache& cache, const qlin_kv_batch& batch, int64_t T, int64_t rows,
                       int64_t group) {
-  if (rows <= 128) return INT64_MAX;
+  const bool e4m3 = cache.fmt == QLIN_KV_E4M3;
+  if (rows <= (e4m3 ? 128 : 64)) return INT64_MAX;
   const int64_t room = cache.head_dim == 64 ? 2 : 1;
   const int64_t tiles = (rows + 31) / 32 * batch.batch;  // (the grid: also those that a ragged batch leaves empty)
   const int64_t wgs = std::min(tiles, T * group / 32 + batch.batch) * cache.kv_heads;
   if (wgs > 1024 * room || tiles * cache.kv_heads > 8192) return 0;
-  return ((room << 21) - 1) / wgs;
+  return ((room << (e4m3 ? 21 : 20)) - 1) / wgs;
 }
 
 Plan plan_of(const qlin_kv_cache& cache, const qlin_kv_batch& batch, int64_t T, int64_t q_heads, int64_t window) {
