@@ -637,9 +637,9 @@ __device__ __forceinline__ bool chunk_job(const AttnArgs& a, int wave, ChunkJob&
 // as below: 231 us for 213 with heads of 256 and a window, 83 for 73 for eight prompts
 // of 1024 with heads of 128, 945 for 962 for 2048 tokens of 32768.)
 //
-// Measured, 32 + 8 heads of 128: a prompt of 8192 515 us (1067 TFLOP/s, 82 % of a large
-// library matrix product's 1294); 2048 tokens of 32768 965 us (1103). 16 + 8 heads of 256,
-// window 1024, four prompts of up to 4096: 208 us (786). Bound by the issue of vector
+// Measured, 32 + 8 heads of 128: a prompt of 8192 507 us (1085 TFLOP/s, 84 % of a large
+// library matrix product's 1294); 2048 tokens of 32768 943 us (1130). 16 + 8 heads of 256,
+// window 1024, four prompts of up to 4096: 205 us (801). Bound by the issue of vector
 // instructions, about as many cycles as the products', and by what the two waves of a SIMD
 // take from each other.
 template <int D, int TK>
@@ -762,7 +762,7 @@ __global__ __launch_bounds__(256, D == 64 ? 4 : 2) void attn_chunk_kernel(const 
 // worth 2 to 4 % with wider heads, costs 3 % there.
 //
 // Measured, 32 + 8 heads of 128: eight chunks of up to 1024 tokens in prompts of up to
-// 9001 557 us (917 TFLOP/s). Bound by the phases: a tile takes about 3700 cycles of the
+// 9001 560 us (914 TFLOP/s). Bound by the phases: a tile takes about 3700 cycles of the
 // 2048 that its products need: the scales are 64 multiplications a lane, and one wave a
 // SIMD issues the vector instructions of its weights in 5 cycles where two would take 4.
 template <int D, int TK>

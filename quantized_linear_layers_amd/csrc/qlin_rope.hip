@@ -9,7 +9,7 @@
 // (5.10 TB/s read and written); queries, keys and values of eight prompts of up to 1024
 // tokens into a bf16 cache 30.3 us (4.81 TB/s). E4M3 rows are short of that (2249 tokens,
 // heads of 256: 14.1 us, 3.60 TB/s): absmax, quotients that equal the per-token
-// quantiser's, and encoding take the vector unit as long. A decode step takes 3.7 us (8 tokens) to 5.5 (64
+// quantiser's, and encoding take the vector unit as long. A decode step takes 3.7 us (8 tokens) to 5.2 (64
 // with the append), the launch and three dependent loads.
 #include "qlin_internal.h"
 #include "qlin_device.h"
