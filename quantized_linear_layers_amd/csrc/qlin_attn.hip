@@ -667,7 +667,7 @@ __global__ __launch_bounds__(256, D == 64 ? 4 : 2) void attn_chunk_kernel(const 
     settled(rs);
     St::template rows<is_v, edge>(rs, wg.lo - t * TK - g0, r0, lds_addr(to));
   };
-  constexpr int kAhead = D == 128 ? 8 : 4;  // fragments ahead of the products (64, 256: as registers allow)
+  constexpr int kAhead = 4;  // fragments ahead of the products (6, 8 and 12 with heads of 128: the same time)
   // the end of the products: this wave's loads have arrived, its LDS reads are done, and
   // nothing moves across
   auto products_end = [&] {
