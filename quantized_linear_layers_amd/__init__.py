@@ -781,7 +781,7 @@ def attn_paged(cache: PagedKV, batch: PagedBatch, q, scale=None, causal=True, wi
         if T2 != T:
             raise ValueError("out shape mismatch")
     lse = q.new_empty((T, heads), dtype=torch.float32) if return_lse else None
-    key = (T, heads, D, cache.kv_heads, cache.page_size)  # what the size depends on beside the batch's own
+    key = (T, heads, D, cache.kv_heads, cache.page_size, cache.fmt)  # what the size depends on beside the batch's own
     nb = batch._ws_bytes.get(key)
     if nb is None:
         nb = batch._ws_bytes[key] = _lib.qlin_attn_workspace_bytes(cache._ref, batch._ref, T, heads)

@@ -778,6 +778,33 @@ def test_one_workspace_with_the_products(q, cols):
     assert torch.isfinite(r.float()).all()
 
 
+@pytest.mark.parametrize("first", ["bf16", "e4m3"])
+@pytest.mark.parametrize("lens,new", [([20000], [64]), ([8192, 700, 64, 3000], [100, 100, 64, 99])])
+def test_one_batch_over_caches_of_both_types(q, oracle, lens, new, first):
+    """Layers of one model may keep their caches in different types: a batch serves
+    both, in either order, although the calls' workspaces differ in size."""
+    rng = np.random.default_rng(len(lens))
+    Hkv, G, D, page = 8, 4, 128, 16
+    start, table, pages = make_batch(rng, new, lens, page)
+    T = int(start[-1])
+    batch = q.PagedBatch(dev(start), dev(np.array(lens, np.int32)), dev(table), max(new))
+    x = projections(rng, (T, Hkv * G, D))
+    caches = {f: stale_pool(q, pages, Hkv, page, D, f) for f in ("bf16", "e4m3")}
+    sizes = {f: q.lib().qlin_attn_workspace_bytes(c._c, batch._c, T, Hkv * G) for f, c in caches.items()}
+    assert sizes["bf16"] != sizes["e4m3"]
+    rows = [0, T // 2, T - 1]  # checked against the oracle, as sequences of one token of their own
+    b = np.searchsorted(start, rows, side="right") - 1
+    upto = [lens[i] - new[i] + r - start[i] + 1 for i, r in zip(b, rows)]
+    for f in sorted(caches, key=lambda f: f != first):
+        c = caches[f]
+        fill_cache(q, rng, c, None, np.array(lens), table)
+        got, lse = q.attn_paged(c, batch, dev(x), return_lse=True)
+        e4 = f == "e4m3"
+        r = oracle.attn_paged(x[rows], host(c.k), host(c.v), host(c.k_scale) if e4 else None,
+                              host(c.v_scale) if e4 else None, np.arange(4), upto, table[b], D ** -0.5)
+        attn_check(r, host(got)[rows], host(lse)[rows], D, f"{f} after {first}")
+
+
 def test_same_result_every_time(q):
     """No atomics: repeated calls agree bit for bit, with and without other
     work on the device."""
