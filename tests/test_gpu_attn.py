@@ -559,6 +559,33 @@ def test_append_codes_of_any_magnitude(q, oracle, D):
         assert np.array_equal(got, want), name
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_append_codes_of_negative_zeros(q, oracle, D):
+    """A zero keeps its sign in its E4M3 code at every scale, as in the per-token
+    quantiser: rows of any magnitude with zeros of both signs among them, and values
+    so small that their codes are zeros."""
+    rng = np.random.default_rng(D + 1)
+    T, Hkv, page = 509, 3, 16
+    x = rng.standard_normal((T, Hkv, D)) * 2.0 ** rng.integers(-126, 127, (T, Hkv, 1))
+    x *= np.where(rng.random(x.shape) < 0.2, 2.0 ** -30, 1.0)
+    k = bits(np.clip(x, -3e38, 3e38))
+    k[rng.random(k.shape) < 0.2] = 0x8000
+    k[rng.random(k.shape) < 0.1] = 0x0000
+    k[7] = 0x8000  # rows of nothing else: scale 0, codes 0
+    pages = -(-T // page)
+    cache = q.PagedKV.empty(pages, Hkv, D, page, "e4m3")
+    table = rng.permutation(pages)[None].astype(np.int32)
+    b = q.PagedBatch(dev(np.array([0, T], np.int32)), dev(np.array([T], np.int32)), dev(table), T)
+    q.kv_append(cache, b, dev(k), dev(k[::-1].copy()))
+    slot, _ = oracle.kv_slots([0, T], [T], table, page, pages, T)
+    for name, rows in (("k", k), ("v", k[::-1])):
+        want, ws = oracle.quant_act(np.ascontiguousarray(rows).reshape(-1, D), oracle.OCP)
+        assert (want == 0x80).sum() > T * Hkv * D // 8
+        got = host(getattr(cache, name))[slot // page, :, slot % page].reshape(-1, D)
+        assert np.array_equal(host(getattr(cache, name + "_scale"))[slot // page, :, slot % page].ravel(), ws), name
+        assert np.array_equal(got, want), name
+
+
 def test_append_in_place_queries(q):
     rng = np.random.default_rng(8)
     start, table, pages = make_batch(rng, [20], [60], 16)
