@@ -481,7 +481,8 @@ int qlin_kv_append(const qlin_kv_cache* cache, const qlin_kv_batch* batch, int64
  * tokens sees must be finite, else it may reach the rows of all of them. q and
  * out must not overlap.
  *   q, out [T][ldq], [T][ldo] bf16 (ld >= q_heads * head_dim, multiples of 8);
- *   lse [T][q_heads] fp32 or NULL; scale finite.
+ *   lse [T][q_heads] fp32 or NULL; scale * log2(e) finite in fp32 (|scale| below
+ *   2.35e38; else QLIN_ERR_ARG).
  * Workspace: qlin_attn_workspace_bytes bytes, 256-byte aligned (0 when the key
  * axis is not split). As the GEMMs', it starts with 64 KiB of arrival counters
  * that must be zero before the first call that uses it (qlin_workspace_init);

@@ -534,7 +534,7 @@ int qlin_attn_paged(const qlin_kv_cache* cache, const qlin_kv_batch* batch, int6
                     size_t ws_bytes, qlin_stream_t stream) {
   int rc = kv_args(cache, batch, T);
   if (rc) return rc;
-  QLIN_CHECK(std::isfinite(scale) && window >= 0 && (window == 0 || causal), QLIN_ERR_ARG);
+  QLIN_CHECK(std::isfinite(attn_factor(scale)) && window >= 0 && (window == 0 || causal), QLIN_ERR_ARG);
   QLIN_CHECK(attn_shape_ok(cache, batch, T, q_heads) && ldq >= q_heads * cache->head_dim &&
                  ldo >= q_heads * cache->head_dim,
              QLIN_ERR_SHAPE);

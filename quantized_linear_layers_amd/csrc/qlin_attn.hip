@@ -40,6 +40,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <limits>
 #include <type_traits>
 
 namespace qlin {
@@ -1515,9 +1516,10 @@ int launch_attn(const qlin_kv_cache& cache, const qlin_kv_batch& batch, int64_t 
   a.row_tiles = p.row_tiles;
   a.tiles = (int)p.tiles;
   a.negate = scale < 0.0f;
-  // a scale of 0 must keep masked scores at -inf (0 * -inf is NaN): a positive
-  // one so small that every finite score gets the weight 1
-  a.c = std::max(std::fabs(scale) * 1.44269504088896340736f, 1e-37f);
+  // a scale of 0 must keep masked scores at -inf (0 * -inf is NaN): the smallest factor,
+  // 2^-149, gives every finite score a weight within 2^-21 of 1. (Factors below fp32's
+  // normal range are off by at most 2^-150, which moves no exponent by more than 2^-22.)
+  a.c = std::max(attn_factor(scale), std::numeric_limits<float>::denorm_min());
   if (p.splits > 1) {
     a.arrived = (uint32_t*)ws;
     a.po = (float*)((uint8_t*)ws + kAttnCounterBytes);

@@ -102,6 +102,8 @@ int launch_kv_append(const qlin_kv_cache& cache, const qlin_kv_batch& batch, int
                      int64_t ldq, int64_t q_heads, uint16_t* q_out, int64_t ldqo, hipStream_t st);
 
 // ---- attention over the paged cache (qlin_attn.hip)
+// What scores are multiplied with, as powers of two: must be finite.
+inline float attn_factor(float scale) { return (scale < 0.0f ? -scale : scale) * 1.44269504088896340736f; }
 size_t attn_workspace_bytes(const qlin_kv_cache& cache, const qlin_kv_batch& batch, int64_t T,
                             int64_t q_heads);
 int launch_attn(const qlin_kv_cache& cache, const qlin_kv_batch& batch, int64_t T, const uint16_t* q,

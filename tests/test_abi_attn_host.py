@@ -189,3 +189,13 @@ def test_binding_refuses_host_tensors(q):
 
     with pytest.raises(ValueError):
         q.rope(x, torch.zeros(4, dtype=torch.int32), P)
+
+
+def test_attn_scales_whose_factor_overflows(q):
+    """Scores are multiplied by |scale| * log2(e) in fp32: a scale for which that is
+    infinite would turn a score of 0 into NaN."""
+    assert attn_call(q, T=0, scale=2.3e38) == q.OK
+    assert attn_call(q, T=0, scale=-2.3e38) == q.OK
+    for scale in (2.4e38, -2.4e38, 3.4e38, math.nan, -math.inf):
+        assert attn_call(q, T=0, scale=scale) == q.ERR_ARG, scale
+        assert attn_call(q, scale=scale) == q.ERR_ARG, scale

@@ -310,6 +310,35 @@ def test_scales(q, oracle, scale, new, G):
     run_attn(q, oracle, 51, new, [90, 61], 1, G, 128, 16, "bf16", scale=scale)
 
 
+@pytest.mark.parametrize("scale,gain", [(0.0, 60), (1e-38, 60), (-1e-38, 60), (1e-40, 60), (2.3e38, -62), (-2.3e38, -62)])
+@pytest.mark.parametrize("new,G,more", [([1, 3], 4, 0), ([60, 40], 2, 0), ([60, 40], 2, long_table(16))])
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+def test_scales_at_the_ends_of_fp32(q, oracle, scale, gain, new, G, more, fmt):
+    """Scores up to 2^126 under scales of 0 and of about their inverse, and scores of
+    2^-121 (and of 0) under the largest scales: queries and keys are signs times
+    2^gain, so that products are exact and within fp32's normal range."""
+    rng = np.random.default_rng(52)
+    D, page, kv = 64, 16, [90, 61]
+    start, table, pages = make_batch(rng, new, kv, page)
+    table = np.concatenate([table, np.full((2, more), -1, np.int32)], 1)
+    cache = stale_pool(q, pages, 1, page, D, fmt)
+    b = q.PagedBatch(dev(np.array([0, 90, 151], np.int32)), dev(np.array(kv, np.int32)), dev(table), 90)
+
+    def signs(*shape):
+        return bits(np.where(rng.random(shape) < 0.5, 1.0, -1.0) * 2.0 ** gain)
+
+    q.kv_append(cache, b, dev(signs(151, 1, D)), dev(projections(rng, (151, 1, D))))
+    T = int(start[-1])
+    x = signs(T, G, D)
+    x[T - 1, 0] = 0  # a row of scores 0
+    b = q.PagedBatch(dev(start), dev(np.array(kv, np.int32)), dev(table), max(new))
+    got, lse = q.attn_paged(cache, b, dev(x), scale=scale, return_lse=True)
+    e4 = fmt == "e4m3"
+    r = oracle.attn_paged(x, host(cache.k), host(cache.v), host(cache.k_scale) if e4 else None,
+                          host(cache.v_scale) if e4 else None, start, kv, table, scale)
+    attn_check(r, host(got), host(lse), D, f"scale {scale}")
+
+
 @pytest.mark.parametrize("new,G", [([1, 1], 4), ([60, 70], 2)])
 @pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
 def test_pages_that_do_not_exist(q, oracle, new, G, fmt):
