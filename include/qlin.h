@@ -495,6 +495,14 @@ int qlin_attn_paged(const qlin_kv_cache* cache, const qlin_kv_batch* batch, int6
                     int64_t window, qlin_bf16* out, int64_t ldo, float* lse, void* ws,
                     size_t ws_bytes, qlin_stream_t stream);
 
+/* What qlin_attn_paged chooses for a call, on the host (the arrays are not looked
+ * at and may be NULL): plan[0] rows of a workgroup (32: the kernel of decode steps
+ * and small chunks; 128 or, E4M3, 256: chunks; 0: an empty call), plan[1] parts of
+ * the key axis, at most, plan[2] bytes of the workspace that the call uses, never
+ * more than qlin_attn_workspace_bytes, which has to hold for every window. */
+int qlin_attn_plan(const qlin_kv_cache* cache, const qlin_kv_batch* batch, int64_t T, int64_t q_heads,
+                   int64_t window, int64_t plan[3]);
+
 #ifdef __cplusplus
 }
 #endif

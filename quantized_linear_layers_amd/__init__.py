@@ -92,6 +92,7 @@ _SIGS = {
     "qlin_attn_workspace_bytes": (_SZ, [C.POINTER(_KVCache), C.POINTER(_KVBatch), _I64, _I64]),
     "qlin_attn_paged": (_INT, [C.POINTER(_KVCache), C.POINTER(_KVBatch), _I64, _P, _I64, _I64, _F32,
                                _INT, _I64, _P, _I64, _P, _P, _SZ, _P]),
+    "qlin_attn_plan": (_INT, [C.POINTER(_KVCache), C.POINTER(_KVBatch), _I64, _I64, _I64, C.POINTER(_I64)]),
 }
 for _name, (_res, _args) in _SIGS.items():
     _f = getattr(_lib, _name)

@@ -547,7 +547,19 @@ int qlin_attn_paged(const qlin_kv_cache* cache, const qlin_kv_batch* batch, int6
   rc = device_ok();
   if (rc) return rc;
   return launch_attn(*cache, *batch, T, q, ldq, q_heads, scale, causal, window, out, ldo, lse, ws,
-                     as_stream(stream));
+                     ws_bytes, as_stream(stream));
+}
+
+int qlin_attn_plan(const qlin_kv_cache* cache, const qlin_kv_batch* batch, int64_t T, int64_t q_heads,
+                   int64_t window, int64_t plan[3]) {
+  QLIN_CHECK(cache && batch && plan && window >= 0, QLIN_ERR_ARG);
+  QLIN_CHECK(cache->fmt == QLIN_KV_BF16 || cache->fmt == QLIN_KV_E4M3, QLIN_ERR_ARG);
+  QLIN_CHECK(kv_shape_ok(cache, batch, T) && attn_shape_ok(cache, batch, T, q_heads), QLIN_ERR_SHAPE);
+  plan[0] = plan[1] = plan[2] = 0;
+  if (T == 0 || batch->batch == 0) return QLIN_OK;
+  QLIN_CHECK(batch->table_cols >= 1 && batch->max_q >= 1, QLIN_ERR_SHAPE);
+  attn_plan(*cache, *batch, T, q_heads, window, plan);
+  return QLIN_OK;
 }
 
 }  // extern "C"

@@ -1473,6 +1473,10 @@ void launch_parts(const AttnArgs& a, const Plan& p, hipStream_t st) {
 
 }  // namespace
 
+static size_t parts_bytes(size_t parts, int64_t head_dim) {
+  return parts == 0 ? 0 : kAttnCounterBytes + round_up(parts * head_dim * 4, 256) + round_up(parts * 8, 256);
+}
+
 size_t attn_workspace_bytes(const qlin_kv_cache& cache, const qlin_kv_batch& batch, int64_t T, int64_t q_heads) {
   // Enough for a call with any window: a window lowers the keys, which may also turn
   // a chunk into workgroups of 32 rows (either plan's parts only fall with the keys).
@@ -1481,14 +1485,23 @@ size_t attn_workspace_bytes(const qlin_kv_cache& cache, const qlin_kv_batch& bat
     const int64_t group = q_heads / cache.kv_heads, rows = std::min(batch.max_q, T) * group;
     p.parts = std::max(p.parts, step_plan(cache, batch, rows, few_rows_keys(cache, batch, T, rows, group)).parts);
   }
-  if (p.parts == 0) return 0;
-  return kAttnCounterBytes + round_up(p.parts * cache.head_dim * 4, 256) + round_up(p.parts * 8, 256);
+  return parts_bytes(p.parts, cache.head_dim);
+}
+
+void attn_plan(const qlin_kv_cache& cache, const qlin_kv_batch& batch, int64_t T, int64_t q_heads, int64_t window,
+               int64_t out[3]) {
+  const Plan p = plan_of(cache, batch, T, q_heads, window);
+  out[0] = p.step ? 32 : chunk_rows(cache);
+  out[1] = p.splits;
+  out[2] = (int64_t)parts_bytes(p.parts, cache.head_dim);
 }
 
 int launch_attn(const qlin_kv_cache& cache, const qlin_kv_batch& batch, int64_t T, const uint16_t* q, int64_t ldq,
                 int64_t q_heads, float scale, int causal, int64_t window, uint16_t* out, int64_t ldo, float* lse,
-                void* ws, hipStream_t st) {
+                void* ws, size_t ws_bytes, hipStream_t st) {
   const Plan p = plan_of(cache, batch, T, q_heads, window);
+  const size_t used = parts_bytes(p.parts, cache.head_dim);
+  if (used > ws_bytes || (used && !ws)) return QLIN_ERR_WORKSPACE;
   AttnArgs a = {};
   a.k = (const uint8_t*)cache.k;
   a.v = (const uint8_t*)cache.v;

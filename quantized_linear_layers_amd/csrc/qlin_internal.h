@@ -108,6 +108,9 @@ size_t attn_workspace_bytes(const qlin_kv_cache& cache, const qlin_kv_batch& bat
                             int64_t q_heads);
 int launch_attn(const qlin_kv_cache& cache, const qlin_kv_batch& batch, int64_t T, const uint16_t* q,
                 int64_t ldq, int64_t q_heads, float scale, int causal, int64_t window, uint16_t* out,
-                int64_t ldo, float* lse, void* ws, hipStream_t st);
+                int64_t ldo, float* lse, void* ws, size_t ws_bytes, hipStream_t st);
+// Rows of a workgroup, parts of the key axis, bytes of the workspace that a call uses.
+void attn_plan(const qlin_kv_cache& cache, const qlin_kv_batch& batch, int64_t T, int64_t q_heads,
+               int64_t window, int64_t out[3]);
 
 }  // namespace qlin

@@ -199,3 +199,92 @@ def test_attn_scales_whose_factor_overflows(q):
     for scale in (2.4e38, -2.4e38, 3.4e38, math.nan, -math.inf):
         assert attn_call(q, T=0, scale=scale) == q.ERR_ARG, scale
         assert attn_call(q, scale=scale) == q.ERR_ARG, scale
+
+
+def attn_plan(q, c, b, T, heads, window=0):
+    out = (C.c_int64 * 3)(-1, -1, -1)
+    assert q.lib().qlin_attn_plan(c, b, T, heads, window, out) == q.OK
+    return tuple(out)
+
+
+def any_cache(q, fmt, D, Hkv, page):
+    e4 = fmt == "e4m3"
+    return cache(q, head_dim=D, kv_heads=Hkv, page_size=page, pages=1 << 20, fmt=q.KV_E4M3 if e4 else q.KV_BF16,
+                 k_scale=A if e4 else None, v_scale=A if e4 else None)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_no_window_needs_more_workspace_than_reported(q, fmt, D):
+    """A call plans with its window, and its parts have to fit the workspace that is
+    sized without one, also where the window turns a chunk's kernel into a step's."""
+    page, turned, calls = 64, 0, 0
+    windows = (1, 33, 500, 511, 512, 1500, 2048, 4000, 8191, 20000, 65536, 10 ** 6, 2 ** 62)
+    for Hkv in (1, 2, 8, 40):
+        for G in (1, 4, 8):
+            c = any_cache(q, fmt, D, Hkv, page)
+            for B in (1, 2, 5, 64, 700):
+                for mq in (1, 3, 16, 17, 40, 129, 1024, 5000):
+                    for cols in (1, 9, 64, 65, 128, 513, 4096):
+                        b = batch(q, batch=B, max_q=mq, table_cols=cols)
+                        for T in {mq, B * mq, B * (mq // 2 + 1)}:
+                            if T * Hkv * G >= 1 << 30:  # (the call's limit)
+                                continue
+                            have = q.lib().qlin_attn_workspace_bytes(c, b, T, Hkv * G)
+                            whole = attn_plan(q, c, b, T, Hkv * G)
+                            assert whole[2] <= have
+                            for w in windows:
+                                rows, parts, used = attn_plan(q, c, b, T, Hkv * G, w)
+                                assert used <= have, (Hkv, G, B, mq, cols, T, w)
+                                assert (parts > 1) == (used > 0)
+                                calls += 1
+                                turned += whole[0] > 32 and rows == 32 and parts > 1
+    assert turned > 0 and calls > 100000
+
+
+def test_attn_plan_refusals(q):
+    out = (C.c_int64 * 3)()
+    c, b = cache(q), batch(q)
+    f = q.lib().qlin_attn_plan
+    assert f(None, b, 1, 4, 0, out) == q.ERR_ARG and f(c, None, 1, 4, 0, out) == q.ERR_ARG
+    assert f(c, b, 1, 4, -1, out) == q.ERR_ARG and f(c, b, 1, 4, 0, None) == q.ERR_ARG
+    assert f(cache(q, fmt=2), b, 1, 4, 0, out) == q.ERR_ARG
+    for cc, bb, T, heads in ((cache(q, head_dim=96), b, 1, 4), (c, batch(q, max_q=0), 1, 4), (c, b, -1, 4), (c, b, 1, 3),
+                             (c, batch(q, table_cols=0), 1, 4), (c, batch(q, table_cols=1 << 60), 1, 4),
+                             (c, b, 1 << 30, 4), (c, b, 1, 0)):
+        assert f(cc, bb, T, heads, 0, out) == q.ERR_SHAPE
+    assert attn_plan(q, c, b, 0, 4) == (0, 0, 0) and attn_plan(q, c, batch(q, batch=0), 1, 4) == (0, 0, 0)
+    # no array is looked at
+    assert attn_plan(q, cache(q, k=None, v=None), batch(q, q_start=None, kv_len=None, page_table=None), 1, 4)[0] == 32
+
+
+# Which kernel runs in the GPU tests that are meant for one of them, and whether the key
+# axis is in parts: (rows of a workgroup in bf16, in E4M3, parts), for batches of `new`
+# tokens over tables of `keys`.
+LONG = 1 << 18
+PLANS = [
+    # decode steps, whole (2304 keys: two tokens a head beyond a table of 2049) and in parts
+    (64, 2, 4, 16, [1] * 13, 321 + 15, (32, 32, True)), (128, 1, 4, 32, [3], 2049 + 31 + 160, (32, 32, True)),
+    (64, 1, 2, 16, [2] * 150, 64, (32, 32, False)),
+    # chunks over their own tables: 32 rows
+    (128, 1, 4, 16, [33, 0, 64, 129, 1], 208, (32, 32, False)), (128, 2, 4, 64, [40], 1344 + 576, (32, 32, True)),
+    # over long tables: the chunks' kernels, with few heads in parts, with many whole
+    (64, 2, 2, 16, [33, 0, 64, 129, 1], LONG + 208, (128, 256, True)),
+    (128, 1, 4, 16, [33, 0, 64, 129, 1], LONG + 208, (128, 256, True)),
+    (256, 1, 2, 32, [33, 0, 64, 129, 1], LONG + 224, (128, 256, True)),
+    (64, 70, 2, 32, [33, 0, 64, 129, 1], LONG + 224, (128, 256, False)),
+    (128, 40, 2, 32, [33, 0, 64, 129, 1], LONG + 224, (128, 256, False)),
+    (256, 40, 2, 64, [33, 0, 64, 129, 1], LONG + 256, (128, 256, False)),
+    (128, 24, 4, 16, [100, 40, 35, 70], LONG + 272, (128, 256, False)),
+    (128, 1, 2, 16, [300] + [1] * 69, LONG + 352, (128, 256, True)),
+    # whole prompts with windows
+    (64, 20, 4, 32, [700, 300], 928, (128, 256, False)), (256, 16, 4, 64, [500, 600], 960, (128, 256, False)),
+]
+
+
+@pytest.mark.parametrize("D,Hkv,G,page,new,keys,want", PLANS)
+def test_kernels_that_the_gpu_tests_are_for(q, D, Hkv, G, page, new, keys, want):
+    for fmt, rows in (("bf16", want[0]), ("e4m3", want[1])):
+        b = batch(q, batch=len(new), max_q=max(new), table_cols=keys // page)
+        got = attn_plan(q, any_cache(q, fmt, D, Hkv, page), b, sum(new), Hkv * G)
+        assert (got[0], got[1] > 1) == (rows, want[2]), (fmt, got)
