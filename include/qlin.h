@@ -427,9 +427,10 @@ typedef struct {
  *                     turns between (YaRN: low 1, high 32 and a magnitude of
  *                     0.1 ln(factor) + 1).
  * trained_len, low and high are read by the ramp alone. Errors: QLIN_ERR_ARG
- * for an unknown rule, a NULL out or a parameter that is not finite or not in
- * range (base > 1, factor > 0, trained_len > 0, 0 <= low < high);
- * QLIN_ERR_SHAPE for a rot that is no multiple of 16. */
+ * for an unknown rule, a NULL out, a parameter that is not finite or not in
+ * range (base > 1, factor > 0, trained_len > 0, 0 <= low < high) or a frequency
+ * that comes out infinite (out is then not defined); QLIN_ERR_SHAPE for a rot that
+ * is no multiple of 16. */
 enum { QLIN_ROPE_PLAIN = 0, QLIN_ROPE_LINEAR = 1, QLIN_ROPE_BASE = 2, QLIN_ROPE_RAMP = 3 };
 int qlin_rope_turns(int64_t rot, double base, int rule, double factor, double trained_len, double low,
                     double high, double* out);

@@ -427,6 +427,7 @@ int qlin_rope_turns(int64_t rot, double base, int rule, double factor, double tr
       const double keep = std::min(1.0, std::max(0.0, (trained_len * f - low) / (high - low)));
       f = f * keep + f / factor * (1.0 - keep);
     }
+    QLIN_CHECK(std::isfinite(f), QLIN_ERR_ARG);
     out[i] = f;
   }
   return QLIN_OK;

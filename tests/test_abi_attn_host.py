@@ -63,6 +63,16 @@ def test_turns_refusals(q, args, status):
     assert q.lib().qlin_rope_turns(16, 1e4, 0, 1.0, 1.0, 0.0, 1.0, None) == q.ERR_ARG
 
 
+@pytest.mark.parametrize("args", [(1e4, 1, 5e-324, 1, 0, 1), (1e4, 2, 1e-308, 1, 0, 1), (1e4, 3, 1e-313, 8192, 1, 32)])
+def test_turns_that_overflow(q, args):
+    """Parameters within their ranges whose frequencies are infinite: no NaN angles."""
+    base, rule, *rest = args
+    out = (C.c_double * 8)()
+    assert q.lib().qlin_rope_turns(16, base, rule, *map(float, rest), out) == q.ERR_ARG
+    assert q.lib().qlin_rope_turns(16, base, rule, 1e-30, *map(float, rest[1:]), out) == q.OK
+    assert all(math.isfinite(x) for x in out)
+
+
 def rope_call(q, x=A, ldx=128, T=4, H=2, D=64, pos=A, pl="", inverse=0, y=2 * A, ldy=128):
     pl = plan(q) if pl == "" else pl
     return q.lib().qlin_rope(p(x), ldx, T, H, D, p(pos), pl, inverse, p(y), ldy, None)
