@@ -562,6 +562,14 @@ def _like(t):
     return torch.empty_like(t) if t.is_contiguous() else t.new_empty(t.shape)
 
 
+def _int64(x, name):
+    """x as an int that ctypes hands over whole (beyond 64 bits it would wrap)."""
+    x = int(x)
+    if not -1 << 63 <= x < 1 << 63:
+        raise ValueError(f"{name} must fit 64 bits, got {x}")
+    return x
+
+
 def _positions_arg(t, dev, T):
     _check(t, "positions", torch.int32, 1)
     if t.device != dev or t.numel() != T:
@@ -696,7 +704,8 @@ class PagedBatch:
         self.device = q_start.device
         _on(kv_len.device, self.device, "kv_len")
         _on(page_table.device, self.device, "page_table")
-        self.q_start, self.kv_len, self.page_table, self.max_q = q_start, kv_len, page_table, int(max_q)
+        self.q_start, self.kv_len, self.page_table = q_start, kv_len, page_table
+        self.max_q = _int64(max_q, "max_q")
         self.batch = B
         self._c = _KVBatch(q_start.data_ptr(), kv_len.data_ptr(), page_table.data_ptr(), B,
                            page_table.shape[1], self.max_q)
@@ -788,6 +797,6 @@ def attn_paged(cache: PagedKV, batch: PagedBatch, q, scale=None, causal=True, wi
         nb = batch._ws_bytes[key] = _lib.qlin_attn_workspace_bytes(cache._ref, batch._ref, T, heads)
     ws = _attn_workspace(nb, dev) if nb else None
     _enqueue(dev, _lib.qlin_attn_paged, cache._ref, batch._ref, T, q.data_ptr(), ldq, heads,
-             D ** -0.5 if scale is None else float(scale), 1 if causal else 0, int(window), out.data_ptr(), ldo,
-             None if lse is None else lse.data_ptr(), None if ws is None else ws.data_ptr(), nb)
+             D ** -0.5 if scale is None else float(scale), 1 if causal else 0, _int64(window, "window"),
+             out.data_ptr(), ldo, None if lse is None else lse.data_ptr(), None if ws is None else ws.data_ptr(), nb)
     return (out, lse) if return_lse else out

@@ -922,3 +922,15 @@ def test_binding_refusals(q):
     none = torch.zeros(0, 8, 128, dtype=torch.bfloat16, device="cuda")
     assert q.attn_paged(cache, batch, none).shape == (0, 8, 128)
     assert q.rope(none, torch.zeros(0, dtype=torch.int32, device="cuda"), plan).shape == (0, 8, 128)
+
+
+def test_integers_beyond_64_bits_are_refused(q):
+    """Not taken modulo 2^64: a window of 2^64 + 5 is not one of 5."""
+    cache, batch, qkv, plan, Hq = decode_setup(q, 6)
+    for window in (1 << 63, (1 << 64) + 5, -(1 << 63) - 1):
+        with pytest.raises(ValueError):
+            q.attn_paged(cache, batch, qkv[:, :Hq], window=window)
+    with pytest.raises(q.QlinError):
+        q.attn_paged(cache, batch, qkv[:, :Hq], window=-(1 << 63))
+    with pytest.raises(ValueError):
+        q.PagedBatch(batch.q_start, batch.kv_len, batch.page_table, (1 << 64) + 1)
