@@ -425,7 +425,9 @@ typedef struct {
  *   QLIN_ROPE_RAMP    f_i / factor below `low` turns over trained_len tokens,
  *                     f_i above `high`, blended linearly in the number of
  *                     turns between (YaRN: low 1, high 32 and a magnitude of
- *                     0.1 ln(factor) + 1).
+ *                     0.1 ln(factor) + 1; model code that blends linearly in
+ *                     the pair's index between two limits has other frequencies
+ *                     there: write those to `turns` oneself).
  * trained_len, low and high are read by the ramp alone. Errors: QLIN_ERR_ARG
  * for an unknown rule, a NULL out, a parameter that is not finite or not in
  * range (base > 1, factor > 0, trained_len > 0, 0 <= low < high) or a frequency

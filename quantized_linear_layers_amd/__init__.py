@@ -611,24 +611,35 @@ class Rope:
     rot_dim/2), or (2i, 2i + 1) if `interleaved`. `scaling` is None, ("linear",
     factor), ("base", factor) or ("ramp", factor, trained_len, low, high): see
     qlin_rope_turns. `magnitude` scales the rotated values (YaRN: 0.1 ln(factor)
-    + 1 with ("ramp", factor, trained_len, 1, 32))."""
+    + 1 with ("ramp", factor, trained_len, 1, 32)). The ramp blends linearly in
+    the number of turns, as YaRN's text defines it; model code that blends
+    linearly in the pair's index gives other frequencies: take such a
+    checkpoint's own by `turns` [rot_dim / 2] (tensor or sequence of floats: turns
+    a position, inv_freq / 2 pi), which replaces base and scaling."""
 
     _RULES = {"linear": (ROPE_LINEAR, 1), "base": (ROPE_BASE, 1), "ramp": (ROPE_RAMP, 4)}
 
     def __init__(self, head_dim: int, rot_dim: int | None = None, base: float = 10000.0,
-                 interleaved: bool = False, scaling=None, magnitude: float = 1.0, device="cuda"):
+                 interleaved: bool = False, scaling=None, magnitude: float = 1.0, device="cuda", turns=None):
         self.head_dim, self.rot_dim = int(head_dim), int(head_dim if rot_dim is None else rot_dim)
         self.interleaved, self.magnitude = bool(interleaved), float(magnitude)
         if self.rot_dim > self.head_dim:
             raise ValueError("rot_dim must not exceed head_dim")
         rule, args = ROPE_PLAIN, []
         if scaling is not None:
+            if turns is not None:
+                raise ValueError("turns replaces the frequency rule: no scaling with it")
             if scaling[0] not in self._RULES or len(scaling) - 1 != self._RULES[scaling[0]][1]:
                 raise ValueError(f"scaling {scaling!r}: expected one of {sorted(self._RULES)} and its arguments")
             rule, args = self._RULES[scaling[0]][0], [float(x) for x in scaling[1:]]
         args += [1.0, 1.0, 0.0, 1.0][len(args):]
         out = (_F64 * max(self.rot_dim // 2, 1))()
         _call("qlin_rope_turns", self.rot_dim, float(base), rule, *args, out)
+        if turns is not None:
+            given = torch.as_tensor(turns, dtype=torch.float64)
+            if tuple(given.shape) != (self.rot_dim // 2,) or not bool(torch.isfinite(given).all()):
+                raise ValueError("turns must be rot_dim / 2 finite values")
+            out = given.tolist()
         self.turns = torch.tensor(list(out), dtype=torch.float64, device=device)
         if not self.turns.is_cuda:
             raise ValueError("device must be a GPU")

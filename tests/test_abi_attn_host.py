@@ -298,3 +298,13 @@ def test_kernels_that_the_gpu_tests_are_for(q, D, Hkv, G, page, new, keys, want)
         b = batch(q, batch=len(new), max_q=max(new), table_cols=keys // page)
         got = attn_plan(q, any_cache(q, fmt, D, Hkv, page), b, sum(new), Hkv * G)
         assert (got[0], got[1] > 1) == (rows, want[2]), (fmt, got)
+
+
+def test_given_turns_refusals(q):
+    for turns in ([0.1] * 31, [0.1] * 33, [[0.1] * 32], 0.1, [math.nan] * 32, [0.1] * 31 + [math.inf]):
+        with pytest.raises(ValueError):
+            q.Rope(64, turns=turns, device="cpu")
+    with pytest.raises(ValueError):
+        q.Rope(64, turns=[0.1] * 32, scaling=("linear", 2.0), device="cpu")
+    with pytest.raises(q.QlinError):
+        q.Rope(64, rot_dim=24, turns=[0.1] * 12, device="cpu")

@@ -90,6 +90,27 @@ def test_rope_large_folds_heads_and_strides(q, oracle):
     assert torch.equal(qkv[:, H:].view(torch.int16), tail.view(torch.int16))
 
 
+@pytest.mark.parametrize("as_tensor", [False, True])
+@pytest.mark.parametrize("rot", [64, 32])
+def test_rope_given_turns(q, oracle, rot, as_tensor):
+    """Frequencies of one's own: a blend that is linear in the pair's index, which
+    the ramp rule (linear in turns) does not give."""
+    rng = np.random.default_rng(rot)
+    i = np.arange(rot // 2)
+    f = 10000.0 ** (-2.0 * i / rot) / (2 * np.pi)
+    keep = 1.0 - np.clip((i - 3) / (rot // 2 - 8), 0.0, 1.0)
+    turns = f * keep + f / 8.0 * (1.0 - keep)
+    given = torch.from_numpy(turns).float().cuda().double() if as_tensor else turns.tolist()
+    plan = q.Rope(64, rot_dim=rot, turns=given, magnitude=1.1)
+    want = host(given) if as_tensor else turns
+    assert np.array_equal(host(plan.turns), want)
+    if as_tensor:
+        given.zero_()  # the plan has its own
+    x, pos = projections(rng, (9, 3, 64)), rng.integers(0, 100000, 9).astype(np.int32)
+    y, mag = oracle.rope(x, pos, want, rot, False, 1.1)
+    rope_check(host(q.rope(dev(x), dev(pos), plan)), y, mag, "own turns")
+
+
 def test_rope_gradient(q):
     """The inverse rotation is the gradient: <R x, g> differenced in every
     direction of a small x, in exact arithmetic of its linear map."""
