@@ -383,7 +383,10 @@ int qlin_moe_w4a16_workspace_layout(int64_t T, int64_t H, int64_t I, int64_t E, 
  * a page outside [0, pages) are not written and not seen.
  * Limits (QLIN_ERR_SHAPE beyond): batch <= 65535, pages * kv_heads < 2^31,
  * table_cols * page_size < 2^31 - 65536, T * q_heads < 2^30, batch * kv_heads <
- * 2^24.
+ * 2^24, and what fits a grid of 2^32 threads: for the rotation and the append about
+ * T * ceil(heads / 8) * head_dim < 2^36, for attention with max_q * q_heads / kv_heads
+ * > 64 about T * q_heads / 128 + batch * kv_heads < 2^24 (E4M3: T * q_heads / 256 +
+ * batch * kv_heads < 2^23).
  * ------------------------------------------------------------------------ */
 enum { QLIN_KV_BF16 = 0, QLIN_KV_E4M3 = 1 };
 

@@ -446,7 +446,7 @@ int qlin_rope(const qlin_bf16* x, int64_t ldx, int64_t T, int64_t H, int64_t D,
               int64_t ldy, qlin_stream_t stream) {
   QLIN_CHECK(rope, QLIN_ERR_ARG);
   QLIN_CHECK(T >= 0 && H >= 0 && D >= 16 && D % 16 == 0 && D <= 1024 && T <= 0x7FFFFFFF && H <= 0xFFFF &&
-                 ldx >= H * D && ldy >= H * D && (x != y || ldx == ldy),
+                 ldx >= H * D && ldy >= H * D && (x != y || ldx == ldy) && rope_grid_ok(T, H, D),
              QLIN_ERR_SHAPE);
   int rc = rope_plan_args(rope, D);
   if (rc) return rc;
@@ -505,6 +505,7 @@ int qlin_kv_append(const qlin_kv_cache* cache, const qlin_kv_batch* batch, int64
     QLIN_CHECK(q_heads >= 1 && q_heads <= 0xFFFF && ldq >= q_heads * D && ldqo >= q_heads * D &&
                    (q != q_out || ldq == ldqo),
                QLIN_ERR_SHAPE);
+  QLIN_CHECK(rope_grid_ok(T, (q ? q_heads : 0) + 2 * cache->kv_heads, D), QLIN_ERR_SHAPE);
   if (T == 0 || batch->batch == 0) return QLIN_OK;
   QLIN_CHECK(k && v, QLIN_ERR_ARG);
   QLIN_CHECK(a16(k) && a16(v) && ldk % 8 == 0 && ldv % 8 == 0 && ((uintptr_t)positions & 3) == 0,
@@ -518,7 +519,7 @@ int qlin_kv_append(const qlin_kv_cache* cache, const qlin_kv_batch* batch, int64
 
 static bool attn_shape_ok(const qlin_kv_cache* c, const qlin_kv_batch* b, int64_t T, int64_t q_heads) {
   return q_heads >= 1 && q_heads <= 0xFFFF && q_heads % c->kv_heads == 0 && T * q_heads <= 0x3FFFFFFF &&
-         b->max_q <= 0x7FFFFFFF && b->batch * c->kv_heads <= 0xFFFFFF;
+         b->max_q <= 0x7FFFFFFF && b->batch * c->kv_heads <= 0xFFFFFF && attn_grid_ok(*c, *b, T, q_heads);
 }
 
 size_t qlin_attn_workspace_bytes(const qlin_kv_cache* cache, const qlin_kv_batch* batch, int64_t T,

@@ -1473,6 +1473,13 @@ void launch_parts(const AttnArgs& a, const Plan& p, hipStream_t st) {
 
 }  // namespace
 
+bool attn_grid_ok(const qlin_kv_cache& cache, const qlin_kv_batch& batch, int64_t T, int64_t q_heads) {
+  // (with one part: calls of more have at most chunk_room * 256 workgroups)
+  if (std::min(batch.max_q, T) * (q_heads / cache.kv_heads) <= 64) return true;
+  const int64_t wgs = T * q_heads / chunk_rows(cache) + batch.batch * cache.kv_heads;
+  return (wgs + 7) / 8 * 8 * (cache.fmt == QLIN_KV_E4M3 ? 512 : 256) <= 0xFFFFFFFF;
+}
+
 static size_t parts_bytes(size_t parts, int64_t head_dim) {
   return parts == 0 ? 0 : kAttnCounterBytes + round_up(parts * head_dim * 4, 256) + round_up(parts * 8, 256);
 }

@@ -96,6 +96,8 @@ int launch_moe_w4a16(const uint16_t* x, int64_t T, int64_t H, int64_t I, int64_t
 int launch_rope(const uint16_t* x, int64_t ldx, int64_t T, int64_t H, int64_t D,
                 const int32_t* positions, const qlin_rope_plan& rope, int inverse, uint16_t* y,
                 int64_t ldy, hipStream_t st);
+// Whether T rows of heads of D values (queries, keys and values together) fit a grid.
+bool rope_grid_ok(int64_t T, int64_t heads, int64_t D);
 int launch_kv_append(const qlin_kv_cache& cache, const qlin_kv_batch& batch, int64_t T,
                      const uint16_t* k, int64_t ldk, const uint16_t* v, int64_t ldv,
                      const qlin_rope_plan* rope, const int32_t* positions, const uint16_t* q,
@@ -109,6 +111,8 @@ size_t attn_workspace_bytes(const qlin_kv_cache& cache, const qlin_kv_batch& bat
 int launch_attn(const qlin_kv_cache& cache, const qlin_kv_batch& batch, int64_t T, const uint16_t* q,
                 int64_t ldq, int64_t q_heads, float scale, int causal, int64_t window, uint16_t* out,
                 int64_t ldo, float* lse, void* ws, size_t ws_bytes, hipStream_t st);
+// Whether the workgroups of a chunk's kernel fit a grid.
+bool attn_grid_ok(const qlin_kv_cache& cache, const qlin_kv_batch& batch, int64_t T, int64_t q_heads);
 // Rows of a workgroup, parts of the key axis, bytes of the workspace that a call uses.
 void attn_plan(const qlin_kv_cache& cache, const qlin_kv_batch& batch, int64_t T, int64_t q_heads,
                int64_t window, int64_t out[3]);

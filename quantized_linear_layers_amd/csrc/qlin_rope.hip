@@ -251,6 +251,17 @@ void rope_shape(RopeArgs& a, dim3& grid) {
 
 }  // namespace
 
+bool rope_grid_ok(int64_t T, int64_t heads, int64_t D) {
+  RopeArgs a = {};
+  a.T = T;
+  a.D = (int)D;
+  a.heads[0] = (int)heads;
+  if (T == 0 || heads == 0) return true;
+  dim3 grid;
+  rope_shape(a, grid);
+  return (int64_t)grid.x * kRopeThreads <= 0xFFFFFFFF && grid.y <= 0xFFFF;
+}
+
 int launch_rope(const uint16_t* x, int64_t ldx, int64_t T, int64_t H, int64_t D,
                 const int32_t* positions, const qlin_rope_plan& rope, int inverse, uint16_t* y,
                 int64_t ldy, hipStream_t st) {

@@ -308,3 +308,29 @@ def test_given_turns_refusals(q):
         q.Rope(64, turns=[0.1] * 32, scaling=("linear", 2.0), device="cpu")
     with pytest.raises(q.QlinError):
         q.Rope(64, rot_dim=24, turns=[0.1] * 12, device="cpu")
+
+
+def test_grids_that_would_pass_32_bits(q):
+    """Threads of a grid are counted in 32 bits: calls beyond are refused, not cut."""
+    # rotation: pieces of 16 values, eight heads a thread
+    assert rope_call(q, T=(1 << 31) - 1, H=1, D=64, ldx=64, ldy=64) == q.ERR_SHAPE
+    assert rope_call(q, T=1 << 30, H=16, D=64, ldx=1024, ldy=1024) == q.ERR_SHAPE
+    assert rope_call(q, T=1 << 27, H=9, D=1024, ldx=9216, ldy=9216, pl=plan(q)) == q.ERR_SHAPE
+    # (the largest sizes that fit get as far as the next check)
+    assert rope_call(q, T=(1 << 30) - 64, H=1, D=64, ldx=64, ldy=64, x=A + 2) == q.ERR_ALIGN
+    big = cache(q, kv_heads=8, head_dim=256)
+    assert append_call(q, c=big, T=1 << 28, ldk=2048, ldv=2048) == q.ERR_SHAPE
+    assert append_call(q, c=big, T=1 << 25, ldk=2048, ldv=2048, k=A + 2) == q.ERR_ALIGN
+    # chunks: 256 (E4M3 512) threads for 128 (256) rows, and a workgroup for every
+    # (sequence, head) that ends inside one
+    for fmt, most in (("bf16", 1 << 24), ("e4m3", 1 << 23)):
+        c = any_cache(q, fmt, 64, 255, 16)
+        out = (C.c_int64 * 3)()
+        for B, T, rows, ok in ((65535, 65535, 100, (65535 * 255 + 65535 * 255 // 128) < most), (65535, 65535, 64, True),
+                               (32000, 65535, 100, True), (65535, 4000000, 100, False)):
+            b = batch(q, batch=B, max_q=rows)
+            status = q.lib().qlin_attn_plan(c, b, T, 255, 0, out)
+            assert status == (q.OK if ok else q.ERR_SHAPE), (fmt, B, T, rows)
+            if not ok:
+                assert attn_call(q, c=c, b=b, T=T, heads=255, ldq=255 * 64, ldo=255 * 64) == q.ERR_SHAPE
+                assert q.lib().qlin_attn_workspace_bytes(c, b, T, 255) == 0
