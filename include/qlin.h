@@ -374,10 +374,13 @@ int qlin_moe_w4a16_workspace_layout(int64_t T, int64_t H, int64_t I, int64_t E, 
  *             reach are neither stored nor seen;
  *   page_table [batch][table_cols] int32: page of each page_size tokens;
  *   max_q     at least the longest sequence's count of new tokens (a host
- *             value, it selects kernels; with fewer the result is the same).
+ *             value, it selects kernels and sizes grids; the result is the same
+ *             for any max_q that is large enough; of a sequence with more new
+ *             tokens the rows of the others are not defined).
  * Kernels and the split of the key axis are chosen on the host from these sizes,
  * table_cols * page_size standing for the longest sequence: a table much wider
- * than the sequences need costs speed, not correctness.
+ * than the sequences need costs speed (a decode step of 64 sequences of up to 1536
+ * keys 34.6 us for 30.7), not correctness.
  * The arrays are device data, read when the kernels run (a captured graph
  * sees the values of each replay), so their values are no errors: the keys of
  * a page outside [0, pages) are not written and not seen.

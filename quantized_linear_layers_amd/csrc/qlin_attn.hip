@@ -635,14 +635,18 @@ __device__ __forceinline__ bool chunk_job(const AttnArgs& a, int wave, ChunkJob&
 // K(t) and V(t-1) are free: the loads of K(t+2) and V(t+1) go there, and have until the
 // end of the products of tile t+1, where the wave waits for them before the barrier.
 // (One workgroup of 256 rows a CU, its wave pairs held in opposite phases by barriers,
-// as below: 231 us for 213 with heads of 256 and a window, 83 for 73 for eight prompts
-// of 1024 with heads of 128, 945 for 962 for 2048 tokens of 32768.)
+// as below, on one machine: 234 us for 218 with heads of 256 and a window, 80 for 75 for
+// eight prompts of up to 1024 with heads of 128, but 523 for 536 for a prompt of 8192 and
+// 965 for 995 for 2048 tokens of 32768.)
 //
-// Measured, 32 + 8 heads of 128: a prompt of 8192 507 us (1085 TFLOP/s, 84 % of a large
-// library matrix product's 1294); 2048 tokens of 32768 943 us (1130). 16 + 8 heads of 256,
-// window 1024, four prompts of up to 4096: 205 us (801). Bound by the issue of vector
-// instructions, about as many cycles as the products', and by what the two waves of a SIMD
-// take from each other.
+// Measured, 32 + 8 heads of 128: a prompt of 8192 534 us (1029 TFLOP/s, 79 % of a large
+// library matrix product's 1298); 2048 tokens of 32768 994 us (1072). 16 + 8 heads of 256,
+// window 1024, four prompts of up to 4096: 219 us (750). (Another machine, with the same
+// matrix product: 507, 943 and 205.) Bound by the issue of vector instructions, with heads
+// of 128 about as many cycles as the products' (27 a tile beside the 32 products, about 140
+// for the weights), and by what the two waves of a SIMD take from each other. With heads of
+// 256 a tile has half the scores, but 102 vector instructions beside its 32 products: the
+// fragments' LDS addresses, which there are computed anew for each (frag_lane).
 template <int D, int TK>
 __global__ __launch_bounds__(256, D == 64 ? 4 : 2) void attn_chunk_kernel(const AttnArgs a) {
   using St = Stage<D, false, TK, TK / 4>;
@@ -758,14 +762,18 @@ __global__ __launch_bounds__(256, D == 64 ? 4 : 2) void attn_chunk_kernel(const 
 // K(t+2) (waves 0-3) or V(t+2), loaded one tile before, and loads that of tile t+3.
 // Scales come along: places for 8 tiles.
 //
-// Heads of 64 need few enough registers for two workgroups a CU (four waves a SIMD):
-// each fills the other's waits, so the priority of the multiplying wave, which is
-// worth 2 to 4 % with wider heads, costs 3 % there.
+// Heads of 64 leave room for two workgroups a CU (four waves a SIMD) at the price of 6
+// spilled registers, written before and read after the tile loop: each workgroup fills the
+// other's waits, so the priority of the multiplying wave, which is worth 2 to 4 % with
+// wider heads, costs 3 % there. Heads of 256 spill 7, one of which is read back in every
+// tile; heads of 128 none.
 //
-// Measured, 32 + 8 heads of 128: eight chunks of up to 1024 tokens in prompts of up to
-// 9001 560 us (914 TFLOP/s). Bound by the phases: a tile takes about 3700 cycles of the
-// 2048 that its products need: the scales are 64 multiplications a lane, and one wave a
-// SIMD issues the vector instructions of its weights in 5 cycles where two would take 4.
+// Measured, eight chunks of up to 1024 tokens in prompts of up to 9001: 32 + 8 heads of
+// 128 597 us (856 TFLOP/s; bf16 532), heads of 64 437 (585; bf16 326), 16 + 8 heads of 256
+// 659 (776; bf16 560). (Another machine: 560 with heads of 128.) Bound by the phases: a tile
+// takes the two waves of a SIMD about 4000 cycles, of which their products need 2048 and
+// their 240 vector instructions each (bf16: 168) 2400 at 5 cycles, so the most of what is
+// missing goes to the two barriers a tile that hold the phases.
 template <int D, int TK>
 __global__ __launch_bounds__(512, D == 64 ? 4 : 2) void attn_chunk_e4m3_kernel(const AttnArgs a) {
   using St = Stage<D, false, TK, TK / 4>;
@@ -958,7 +966,8 @@ __global__ __launch_bounds__(512, D == 64 ? 4 : 2) void attn_chunk_e4m3_kernel(c
 //
 // Bound by memory: eight bf16 sequences of 65536, 32 + 8 heads of 128, 362 us (5.93 TB/s
 // read); 64 E4M3 ones of up to 1536 30.7 us (4.57 TB/s). One of 1025: 9.4 us, of which the
-// launch, four dependent loads (lengths, page, keys, values) and the join are all but 1.
+// launch, three loads that each need the one before (lengths, page, keys and values) and
+// the join are all but 1.
 constexpr int kPieces = 512;
 __device__ __forceinline__ float groups_max(float x) {
   const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
@@ -1386,7 +1395,9 @@ Plan step_plan(const qlin_kv_cache& cache, const qlin_kv_batch& batch, int64_t r
   // heads of 128) two parts took 37 us and none 30.5; with eight of 65536
   // bf16 (64 workgroups) 8 parts took 352 us, 4 357, 16 379. So: one workgroup a
   // CU; where sequences may be long enough not to notice the join, up to the
-  // most that a ragged batch needs.
+  // most that a ragged batch needs. (`keys` is what the page table reaches: the same
+  // 64 sequences cost 30.7 us with a table of 1536 tokens and 34.6, with the longer ones
+  // in two parts, with any of 4096 or more.)
   const int64_t most = keys >= 4096 ? 2048 : kCus;
   const int64_t piece = p.row_tiles > 1 ? 512 : 128;  // keys of a part, at least (more rows, a dearer join)
   // (64 parts at most: one workgroup reads them all)

@@ -5,12 +5,14 @@
 // head over all heads that it handles, so its eight sines and cosines are
 // computed once and used for every one of them.
 //
-// Bound by memory from about 1000 tokens on: 8192 tokens of 32 heads of 128 26.3 us
-// (5.10 TB/s read and written); queries, keys and values of eight prompts of up to 1024
-// tokens into a bf16 cache 30.3 us (4.81 TB/s). E4M3 rows are short of that (2249 tokens,
-// heads of 256: 14.1 us, 3.60 TB/s): absmax, quotients that equal the per-token
-// quantiser's, and encoding take the vector unit as long. A decode step takes 3.7 us (8 tokens) to 5.2 (64
-// with the append), the launch and three dependent loads.
+// Bound by memory from about 1000 tokens on: 8192 tokens of 32 heads of 128 26.5 us
+// (5.07 TB/s read and written); queries, keys and values of eight prompts of up to 1024
+// tokens into a bf16 cache 30.2 us (4.81 TB/s). E4M3 rows are short of that (2249 tokens,
+// heads of 256: 14.0 us, 3.61 TB/s): absmax, quotients that equal the per-token
+// quantiser's, and encoding take the vector unit as long. A decode step takes 3.7 us (8
+// tokens) to 5.2 (64 with the append): the launch and its loads, which are waited for one
+// after the other (positions or lengths and page, frequencies, heads) although of these
+// only the page needs the one before.
 #include "qlin_internal.h"
 #include "qlin_device.h"
 #include "qlin_quant_row.h"

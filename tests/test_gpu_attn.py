@@ -268,8 +268,8 @@ def test_chunk_split_over_keys(q, oracle, fmt):
     run_attn(q, oracle, 43, [150], [900], 1, 2, 256, 32, fmt, window=300)
 
 
-# Chunks over tables of 2^18 tokens, which have workgroups of 256 rows (the shorter
-# ones above: of 32): the key axis in parts, and with many heads whole.
+# Chunks over tables of 2^18 tokens, which have workgroups of 128 rows, E4M3 256 (the
+# shorter ones above: of 32): the key axis in parts, and with many heads whole.
 def long_table(page):
     return (1 << 18) // page
 
