@@ -955,3 +955,84 @@ def test_integers_beyond_64_bits_are_refused(q):
         q.attn_paged(cache, batch, qkv[:, :Hq], window=-(1 << 63))
     with pytest.raises(ValueError):
         q.PagedBatch(batch.q_start, batch.kv_len, batch.page_table, (1 << 64) + 1)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("new,kv,G,D,more,window", [
+    ([1, 2, 0, 1], [300, 70, 5, 1], 4, 128, 0, 0), ([1], [2000], 4, 128, 100, 0), ([60, 3, 40], [90, 3, 400], 5, 128, 0, 0),
+    ([60, 3, 40], [90, 3, 400], 3, 64, long_table(16), 0), ([130, 7], [1130, 7], 2, 256, long_table(16), 90),
+    ([1], [777], 71, 64, 0, 0), ([1, 1], [777, 30], 71, 128, long_table(16), 0), ([3, 1], [400, 400], 40, 256, 0, 17)])
+def test_strided_rows_and_rows_before_the_first_sequence(q, oracle, new, kv, G, D, more, window, fmt):
+    """Queries and outputs inside wider rows, groups of heads of any size, padding on
+    both sides of the sequences: nothing else is written."""
+    rng = np.random.default_rng(G + D)
+    Hkv, page, lead, pad = 2, 16, 3, 2
+    start, table, pages = make_batch(rng, new, kv, page)
+    cache = stale_pool(q, pages, Hkv, page, D, fmt)
+    fill_cache(q, rng, cache, start, np.array(kv), table)
+    table = np.concatenate([table, np.full((len(kv), more), -1, np.int32)], 1)
+    start = (start + lead).astype(np.int32)
+    T, Hq, e4 = int(start[-1]) + pad, Hkv * G, fmt == "e4m3"
+    wide = projections(rng, (T, Hq + 2 * Hkv, D))
+    d = dev(wide)
+    b = q.PagedBatch(dev(start), dev(np.array(kv, np.int32)), dev(table), max(new))
+    buf = torch.full((T, Hq + 1, D), 7.0, dtype=torch.bfloat16, device="cuda")
+
+    def untouched():
+        h = host(buf)
+        return (h[:, 0] == 0x40E0).all() and (h[:lead] == 0x40E0).all() and (h[T - pad:] == 0x40E0).all()
+
+    out, lse = q.attn_paged(cache, b, d[:, Hkv:Hkv + Hq], window=window, out=buf[:, 1:], return_lse=True)
+    x = np.ascontiguousarray(wide[:, Hkv:Hkv + Hq])
+    r = oracle.attn_paged(x, host(cache.k), host(cache.v), host(cache.k_scale) if e4 else None,
+                          host(cache.v_scale) if e4 else None, start, kv, table, D ** -0.5, True, window)
+    attn_check(r, host(out), host(lse), D, "strided")
+    assert untouched()
+    before, plan = [host(t) for t in (cache.k, cache.v)], q.Rope(D)
+    buf.fill_(7.0)
+    q.kv_append(cache, b, d[:, Hq:Hq + Hkv], d[:, Hq + Hkv:], rope=plan, q=d[:, :Hq], q_out=buf[:, 1:])
+    slot, place = oracle.kv_slots(start, kv, table, page, pages, T)
+    y, mag = oracle.rope(wide, place, host(plan.turns), D)
+    rope_check(host(buf)[lead:T - pad, 1:], y[lead:T - pad, :Hq], mag[lead:T - pad, :Hq], "queries")
+    assert untouched()
+    kept = np.ones((pages, page), bool)
+    kept[slot[slot >= 0] // page, slot[slot >= 0] % page] = False
+    for t, o in zip((cache.k, cache.v), before):
+        assert np.array_equal(host(t).transpose(0, 2, 1, 3)[kept], o.transpose(0, 2, 1, 3)[kept])
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("new,G,more", [([3, 1], 4, 0), ([60, 40], 2, 0), ([60, 40], 2, long_table(16))])
+def test_queries_and_keys_that_are_not_finite(q, new, G, more, fmt):
+    """They reach their own rows, or the rows that see them, and no other, by a bit."""
+    rng = np.random.default_rng(5)
+    D, Hkv, page, kv = 128, 1, 16, [90, 61]
+    start, table, pages = make_batch(rng, new, kv, page)
+    cache = stale_pool(q, pages, Hkv, page, D, fmt)
+    fill_cache(q, rng, cache, start, np.array(kv), table)
+    T, last = int(start[-1]), new[0] - 1
+    b = q.PagedBatch(dev(start), dev(np.array(kv, np.int32)),
+                     dev(np.concatenate([table, np.full((2, more), -1, np.int32)], 1)), max(new))
+
+    def run(x, rows):  # rows: what must differ from the finite call
+        got, lse = (host(t) for t in q.attn_paged(cache, b, dev(x), return_lse=True))
+        keep = np.ones((T, G), bool)
+        for i in rows:
+            keep[i] = False
+            assert np.isnan(bf16_to_f32(got[i])).all() and np.isnan(lse[i]).all()
+        return got[keep], lse[keep], keep
+
+    x = projections(rng, (T, G, D))
+    out, lse, _ = run(x, [])
+    out, lse = out.reshape(T, G, D), lse.reshape(T, G)
+    bad = x.copy()
+    bad[1, 0, 5] = 0x7FC0  # NaN
+    got, gl, keep = run(bad, [(1, 0)])
+    assert np.array_equal(got, out[keep]) and np.array_equal(gl, lse[keep])
+    page_of, row = table[0, 89 // page], 89 % page  # the first sequence's last key: its last token's own
+    if fmt == "bf16":
+        cache.k[page_of, 0, row, 3] = float("nan")
+    else:
+        cache.k_scale[page_of, 0, row] = float("nan")
+    got, gl, keep = run(x, [last])
+    assert np.array_equal(got, out[keep]) and np.array_equal(gl, lse[keep])
