@@ -128,3 +128,12 @@ def test_clock_summary_bounds(bench, tmp_path, capsys):
     assert len(lines) == 1 and lines[0][0] == "a"
     n, us, lo, hi = int(lines[0][2]), float(lines[0][3]), float(lines[0][4]), float(lines[0][5])
     assert n == 3 and us == 100.0 and lo == 2.0 and hi == 2.2
+
+
+@pytest.mark.parametrize("which", ["decode", "prefill", "moe"])
+def test_committed_counters_describe_the_sources(bench, which):
+    """The counter summaries carry a hash of the kernels' sources, and the benchmark
+    reports no traffic where it differs: after a change to one of these files the
+    counters are taken again."""
+    table = bench.traffic_table(which)
+    assert table is not None and table["rows"]
