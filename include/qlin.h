@@ -475,6 +475,38 @@ int qlin_kv_append(const qlin_kv_cache* cache, const qlin_kv_batch* batch, int64
                    int64_t ldq, int64_t q_heads, qlin_bf16* q_out, int64_t ldqo,
                    qlin_stream_t stream);
 
+/* Norms of single heads, as models have them whose queries and keys (and values) are
+ * normalised before the rotation: each head's D values become
+ *   x / sqrt(mean(x^2) + eps) * (offset + w),
+ * with the part's own weight w [head_dim] (bf16; NULL: no weight, the factor is 1).
+ * offset is 0, or 1 for weights that are stored less one. Queries and keys always are
+ * normalised, values with values != 0. Everything up to the one rounding of the
+ * output (or to the E4M3 scale and codes) is fp32, squares beyond its range (values
+ * from 1.8e19 on) included. weights 16-byte aligned; eps from 2^-100 to 2^100, offset
+ * finite (QLIN_ERR_ARG). */
+typedef struct {
+  const qlin_bf16 *q_weight, *k_weight, *v_weight;
+  float eps, offset;
+  int values;
+} qlin_head_norm;
+
+/* qlin_kv_append of heads that are normalised first (in the same pass): by norm,
+ * never NULL, which the queries' and keys' rotation follows if there is one. An E4M3
+ * row is quantised from the normalised (and rotated) fp32 values. */
+int qlin_kv_append_norm(const qlin_kv_cache* cache, const qlin_kv_batch* batch, int64_t T,
+                        const qlin_bf16* k, int64_t ldk, const qlin_bf16* v, int64_t ldv,
+                        const qlin_head_norm* norm, const qlin_rope_plan* rope, const int32_t* positions,
+                        const qlin_bf16* q, int64_t ldq, int64_t q_heads, qlin_bf16* q_out, int64_t ldqo,
+                        qlin_stream_t stream);
+
+/* qlin_rope of heads that are normalised first, by norm's q_weight: the queries of a
+ * layer that stores no keys (it reads another layer's cache). With a NULL rope they
+ * are only normalised, and positions may be NULL. D is a power of two from 16 to 1024
+ * (QLIN_ERR_SHAPE); the rest as for qlin_rope. */
+int qlin_norm_rope(const qlin_bf16* x, int64_t ldx, int64_t T, int64_t H, int64_t D,
+                   const qlin_head_norm* norm, const int32_t* positions, const qlin_rope_plan* rope,
+                   qlin_bf16* y, int64_t ldy, qlin_stream_t stream);
+
 /* Attention of the new tokens over the cache, after qlin_kv_append. With g =
  * q_heads / kv_heads, query head h of new token i (position p = kv_len - new
  * tokens + i) gives, over the keys j it sees,

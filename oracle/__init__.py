@@ -71,6 +71,8 @@ def _load():
         "qo_rope_turns": (None, [I64, C.c_double, C.c_int, C.c_double, C.c_double, C.c_double, C.c_double,
                                  P]),
         "qo_rope": (None, [P, I64, I64, I64, I64, P, P, I64, C.c_int, C.c_double, C.c_int, P, P]),
+        "qo_norm_rope": (None, [P, I64, I64, I64, I64, P, C.c_double, C.c_double, P, P, I64, C.c_int, C.c_double, P,
+                                P]),
         "qo_kv_slots": (None, [P, P, P, I64, I64, I64, I64, I64, P, P]),
         "qo_attn_paged": (None, [P, I64, I64, I64, I64, P, P, P, P, C.c_int, I64, I64, I64, P, P, P, I64,
                                  I64, C.c_double, C.c_int, I64, P, P, P, P, P]),
@@ -411,6 +413,18 @@ def rope(x_bf16, positions, turns, rot, interleaved=False, magnitude=1.0, invers
     y, mag = np.empty((T, H, D)), np.empty((T, H, D))
     _load().qo_rope(_p(x), H * D, T, H, D, _p(pos), _p(turns), rot, int(interleaved), magnitude,
                     int(inverse), _p(y), _p(mag))
+    return y, mag
+
+
+def norm_rope(x_bf16, w, eps, offset, positions, turns, rot, interleaved=False, magnitude=1.0):
+    """x [T,H,D] bf16 bits, w [D] bf16 bits or None -> (y, mag) f64 [T,H,D]: the
+    normalised and turned values and the magnitudes that their sums are made of."""
+    x, pos, turns = _c(x_bf16, np.uint16), _c(positions, np.int32), _c(turns, np.float64)
+    w = None if w is None else _c(w, np.uint16)
+    T, H, D = x.shape
+    y, mag = np.empty((T, H, D)), np.empty((T, H, D))
+    _load().qo_norm_rope(_p(x), H * D, T, H, D, _p(w), eps, offset, _p(pos), _p(turns), rot, int(interleaved),
+                         magnitude, _p(y), _p(mag))
     return y, mag
 
 

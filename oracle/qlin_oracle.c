@@ -881,6 +881,39 @@ void qo_rope(const uint16_t* x, int64_t ldx, int64_t T, int64_t H, int64_t D, co
     }
 }
 
+/* x [T][ldx] bf16 (H heads of D) normalised: v / sqrt(mean(v^2) + eps) * (offset + w),
+ * w [D] bf16 or NULL (factor 1), then turned as by qo_rope (rot 0: not at all). Outputs
+ * as there. */
+void qo_norm_rope(const uint16_t* x, int64_t ldx, int64_t T, int64_t H, int64_t D, const uint16_t* w, double eps,
+                  double offset, const int32_t* pos, const double* turns, int64_t rot, int interleaved,
+                  double magnitude, double* y, double* mag) {
+  const double two_pi = 2.0 * acos(-1.0);
+  for (int64_t t = 0; t < T; ++t)
+    for (int64_t h = 0; h < H; ++h) {
+      double* dst = y + (t * H + h) * D;
+      double* m = mag + (t * H + h) * D;
+      double sum = 0.0;
+      for (int64_t d = 0; d < D; ++d) {
+        dst[d] = bf16_value(x[t * ldx + h * D + d]);
+        sum += dst[d] * dst[d];
+      }
+      const double root = sqrt(sum / (double)D + eps);
+      for (int64_t d = 0; d < D; ++d) {
+        dst[d] = dst[d] / root * (w ? offset + bf16_value(w[d]) : 1.0);
+        m[d] = fabs(dst[d]);
+      }
+      for (int64_t i = 0; i < rot / 2; ++i) {
+        const int64_t ia = interleaved ? 2 * i : i, ib = interleaved ? 2 * i + 1 : i + rot / 2;
+        const double part = (double)pos[t] * turns[i];
+        const double angle = two_pi * (part - floor(part));
+        const double a = dst[ia], b = dst[ib];
+        dst[ia] = magnitude * (a * cos(angle) - b * sin(angle));
+        dst[ib] = magnitude * (b * cos(angle) + a * sin(angle));
+        m[ia] = m[ib] = fabs(magnitude) * (fabs(a) + fabs(b));
+      }
+    }
+}
+
 /* For each of T rows its sequence (-1: none) and its place in it. */
 static void row_places(const int32_t* q_start, const int32_t* kv_len, int64_t B, int64_t T, int64_t* seq,
                        int64_t* place) {

@@ -53,6 +53,11 @@ class _RopePlan(C.Structure):
     _fields_ = [("turns", _P), ("rot", _I64), ("interleaved", _INT), ("magnitude", _F32)]
 
 
+class _HeadNorm(C.Structure):
+    _fields_ = [("q_weight", _P), ("k_weight", _P), ("v_weight", _P), ("eps", _F32), ("offset", _F32),
+                ("values", _INT)]
+
+
 _SIGS = {
     "qlin_abi_version": (_INT, []),
     "qlin_status_str": (C.c_char_p, [_INT]),
@@ -89,6 +94,10 @@ _SIGS = {
     "qlin_rope": (_INT, [_P, _I64, _I64, _I64, _I64, _P, C.POINTER(_RopePlan), _INT, _P, _I64, _P]),
     "qlin_kv_append": (_INT, [C.POINTER(_KVCache), C.POINTER(_KVBatch), _I64, _P, _I64, _P, _I64,
                               C.POINTER(_RopePlan), _P, _P, _I64, _I64, _P, _I64, _P]),
+    "qlin_kv_append_norm": (_INT, [C.POINTER(_KVCache), C.POINTER(_KVBatch), _I64, _P, _I64, _P, _I64,
+                                   C.POINTER(_HeadNorm), C.POINTER(_RopePlan), _P, _P, _I64, _I64, _P, _I64, _P]),
+    "qlin_norm_rope": (_INT, [_P, _I64, _I64, _I64, _I64, C.POINTER(_HeadNorm), _P, C.POINTER(_RopePlan), _P, _I64,
+                              _P]),
     "qlin_attn_workspace_bytes": (_SZ, [C.POINTER(_KVCache), C.POINTER(_KVBatch), _I64, _I64]),
     "qlin_attn_paged": (_INT, [C.POINTER(_KVCache), C.POINTER(_KVBatch), _I64, _P, _I64, _I64, _F32,
                                _INT, _I64, _P, _I64, _P, _P, _SZ, _P]),
@@ -648,6 +657,44 @@ class Rope:
         self._ref = C.byref(self._c)
 
 
+class HeadNorm:
+    """Norms of single heads: x / sqrt(mean(x^2) + eps) * (offset + weight), weights
+    bf16 [D] on the GPU, or None for a part without one. Queries and keys are
+    normalised, values if `values` or if they have a weight. offset=1.0 for weights
+    that are stored less one. Without any weight, head_dim and device are taken from
+    the arguments."""
+
+    def __init__(self, q_weight=None, k_weight=None, v_weight=None, eps: float = 1e-6, offset: float = 0.0,
+                 values=None, head_dim: int | None = None, device="cuda"):
+        if values is not None and not values and v_weight is not None:
+            raise ValueError("v_weight without values")
+        self.values = v_weight is not None if values is None else bool(values)
+        self.weights = {"q_weight": q_weight, "k_weight": k_weight, "v_weight": v_weight}
+        self.eps, self.offset = float(eps), float(offset)
+        self.head_dim = None if head_dim is None else int(head_dim)
+        self.device = None
+        for name, w in self.weights.items():
+            if w is None:
+                continue
+            _check(w, name, torch.bfloat16, 1)
+            if self.head_dim is None:
+                self.head_dim = w.numel()
+            if w.numel() != self.head_dim:
+                raise ValueError(f"{name} must be [{self.head_dim}]")
+            if self.device is None:
+                self.device = w.device
+            _on(w.device, self.device, name)
+        if self.head_dim is None:
+            raise ValueError("head_dim is needed without weights")
+        if self.device is None:
+            self.device = torch.empty(0, device=device).device
+        if self.device.type != "cuda":
+            raise ValueError("device must be a GPU")
+        self._c = _HeadNorm(*(None if w is None else w.data_ptr() for w in self.weights.values()), self.eps,
+                            self.offset, int(self.values))
+        self._ref = C.byref(self._c)
+
+
 class PagedKV:
     """A paged key/value cache: k, v [pages, kv_heads, page_size, head_dim], bf16,
     or uint8 E4M3 codes with k_scale, v_scale f32 [pages, kv_heads, page_size].
@@ -744,18 +791,46 @@ def rope(x, positions, plan: Rope, out=None, inverse=False):
     return out
 
 
+def norm_rope(x, norm: HeadNorm, positions=None, plan: Rope | None = None, out=None):
+    """Heads x [T, H, D] (bf16) normalised by `norm` (its q_weight), then turned by
+    `plan` at positions int32 [T] if there is one: the queries of a layer that stores
+    no keys. `out` may be x."""
+    D, dev = norm.head_dim, norm.device
+    T, H, ldx = _rows_arg(x, "x", dev, D)
+    if dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return norm_rope(x, norm, positions, plan, out)
+    if plan is not None:
+        _on(plan.device, dev, "plan")
+        if plan.head_dim != D:
+            raise ValueError("plan and norm differ in head_dim")
+        if positions is None:
+            raise ValueError("a rotation needs positions")
+    if out is None:
+        out, ldy = _like(x), H * D
+    else:
+        T2, _, ldy = _rows_arg(out, "out", dev, D, H)
+        if T2 != T:
+            raise ValueError("out shape mismatch")
+    _enqueue(dev, _lib.qlin_norm_rope, x.data_ptr(), ldx, T, H, D, norm._ref,
+             None if positions is None else _positions_arg(positions, dev, T), None if plan is None else plan._ref,
+             out.data_ptr(), ldy)
+    return out
+
+
 def kv_append(cache: PagedKV, batch: PagedBatch, k, v, rope: Rope | None = None, q=None, q_out=None,
-              positions=None):
+              positions=None, norm: HeadNorm | None = None):
     """The new tokens' keys (turned by `rope`) and values [T, kv_heads, D] into the
     cache. With q [T, q_heads, D] also turns the queries: returned, or written to
     q_out (which may be q). positions int32 [T] replaces each token's place in
-    its sequence as what the rotation uses."""
+    its sequence as what the rotation uses. With `norm`, queries, keys (and values)
+    are normalised head by head before."""
     D, dev = cache.head_dim, cache.device
     _on(batch.device, dev, "batch")
     T, _, ldk = _rows_arg(k, "k", dev, D, cache.kv_heads)
     if dev.index != torch.cuda.current_device():
         with torch.cuda.device(dev):
-            return kv_append(cache, batch, k, v, rope, q, q_out, positions)
+            return kv_append(cache, batch, k, v, rope, q, q_out, positions, norm)
     T2, _, ldv = _rows_arg(v, "v", dev, D, cache.kv_heads)
     ldq = ldqo = heads = 0
     if q is not None:
@@ -775,9 +850,16 @@ def kv_append(cache: PagedKV, batch: PagedBatch, k, v, rope: Rope | None = None,
         _on(rope.device, dev, "rope")
         if rope.head_dim != D:
             raise ValueError("rope and cache differ in head_dim")
-    _enqueue(dev, _lib.qlin_kv_append, cache._ref, batch._ref, T, k.data_ptr(), ldk, v.data_ptr(), ldv,
-             None if rope is None else rope._ref, None if positions is None else _positions_arg(positions, dev, T),
-             None if q is None else q.data_ptr(), ldq, heads, None if q is None else q_out.data_ptr(), ldqo)
+    args = (None if rope is None else rope._ref, None if positions is None else _positions_arg(positions, dev, T),
+            None if q is None else q.data_ptr(), ldq, heads, None if q is None else q_out.data_ptr(), ldqo)
+    if norm is None:
+        _enqueue(dev, _lib.qlin_kv_append, cache._ref, batch._ref, T, k.data_ptr(), ldk, v.data_ptr(), ldv, *args)
+    else:
+        _on(norm.device, dev, "norm")
+        if norm.head_dim != D:
+            raise ValueError("norm and cache differ in head_dim")
+        _enqueue(dev, _lib.qlin_kv_append_norm, cache._ref, batch._ref, T, k.data_ptr(), ldk, v.data_ptr(), ldv,
+                 norm._ref, *args)
     return q_out
 
 

@@ -92,7 +92,34 @@ int qlin_rope(const qlin_bf16* x, int64_t ldx, int64_t T, int64_t H, int64_t D,
              QLIN_ERR_ALIGN);
   rc = device_ok();
   if (rc) return rc;
-  return launch_rope(x, ldx, T, H, D, positions, *rope, inverse, y, ldy, as_stream(stream));
+  return launch_rope(x, ldx, T, H, D, nullptr, positions, rope, inverse, y, ldy, as_stream(stream));
+}
+
+static int head_norm_args(const qlin_head_norm* n) {
+  QLIN_CHECK(n && n->eps >= 0x1p-100f && n->eps <= 0x1p+100f && std::isfinite(n->offset), QLIN_ERR_ARG);
+  QLIN_CHECK(a16(n->q_weight) && a16(n->k_weight) && a16(n->v_weight), QLIN_ERR_ALIGN);
+  return QLIN_OK;
+}
+
+int qlin_norm_rope(const qlin_bf16* x, int64_t ldx, int64_t T, int64_t H, int64_t D, const qlin_head_norm* norm,
+                   const int32_t* positions, const qlin_rope_plan* rope, qlin_bf16* y, int64_t ldy,
+                   qlin_stream_t stream) {
+  int rc = head_norm_args(norm);
+  if (rc) return rc;
+  QLIN_CHECK(T >= 0 && H >= 0 && D >= 16 && D <= 1024 && (D & (D - 1)) == 0 && T <= 0x7FFFFFFF && H <= 0xFFFF &&
+                 ldx >= H * D && ldy >= H * D && (x != y || ldx == ldy) && rope_grid_ok(T, H, D),
+             QLIN_ERR_SHAPE);
+  if (rope) {
+    rc = rope_plan_args(rope, D);
+    if (rc) return rc;
+  }
+  if (T == 0 || H == 0) return QLIN_OK;
+  QLIN_CHECK(x && y && (positions || !rope), QLIN_ERR_ARG);
+  QLIN_CHECK(a16(x) && a16(y) && ldx % 8 == 0 && ldy % 8 == 0 && ((uintptr_t)positions & 3) == 0,
+             QLIN_ERR_ALIGN);
+  rc = device_ok();
+  if (rc) return rc;
+  return launch_rope(x, ldx, T, H, D, norm, positions, rope, 0, y, ldy, as_stream(stream));
 }
 
 static bool kv_shape_ok(const qlin_kv_cache* c, const qlin_kv_batch* b, int64_t T) {
@@ -123,11 +150,10 @@ static int kv_args(const qlin_kv_cache* c, const qlin_kv_batch* b, int64_t T) {
   return QLIN_OK;
 }
 
-int qlin_kv_append(const qlin_kv_cache* cache, const qlin_kv_batch* batch, int64_t T,
-                   const qlin_bf16* k, int64_t ldk, const qlin_bf16* v, int64_t ldv,
-                   const qlin_rope_plan* rope, const int32_t* positions, const qlin_bf16* q,
-                   int64_t ldq, int64_t q_heads, qlin_bf16* q_out, int64_t ldqo,
-                   qlin_stream_t stream) {
+static int kv_append(const qlin_kv_cache* cache, const qlin_kv_batch* batch, int64_t T, const qlin_bf16* k,
+                     int64_t ldk, const qlin_bf16* v, int64_t ldv, const qlin_head_norm* norm,
+                     const qlin_rope_plan* rope, const int32_t* positions, const qlin_bf16* q, int64_t ldq,
+                     int64_t q_heads, qlin_bf16* q_out, int64_t ldqo, qlin_stream_t stream) {
   int rc = kv_args(cache, batch, T);
   if (rc) return rc;
   const int64_t D = cache->head_dim, kvd = cache->kv_heads * D;
@@ -149,8 +175,26 @@ int qlin_kv_append(const qlin_kv_cache* cache, const qlin_kv_batch* batch, int64
   if (q) QLIN_CHECK(a16(q) && a16(q_out) && ldq % 8 == 0 && ldqo % 8 == 0, QLIN_ERR_ALIGN);
   rc = device_ok();
   if (rc) return rc;
-  return launch_kv_append(*cache, *batch, T, k, ldk, v, ldv, rope, positions, q, ldq, q_heads, q_out, ldqo,
+  return launch_kv_append(*cache, *batch, T, k, ldk, v, ldv, norm, rope, positions, q, ldq, q_heads, q_out, ldqo,
                           as_stream(stream));
+}
+
+int qlin_kv_append(const qlin_kv_cache* cache, const qlin_kv_batch* batch, int64_t T,
+                   const qlin_bf16* k, int64_t ldk, const qlin_bf16* v, int64_t ldv,
+                   const qlin_rope_plan* rope, const int32_t* positions, const qlin_bf16* q,
+                   int64_t ldq, int64_t q_heads, qlin_bf16* q_out, int64_t ldqo,
+                   qlin_stream_t stream) {
+  return kv_append(cache, batch, T, k, ldk, v, ldv, nullptr, rope, positions, q, ldq, q_heads, q_out, ldqo, stream);
+}
+
+int qlin_kv_append_norm(const qlin_kv_cache* cache, const qlin_kv_batch* batch, int64_t T,
+                        const qlin_bf16* k, int64_t ldk, const qlin_bf16* v, int64_t ldv,
+                        const qlin_head_norm* norm, const qlin_rope_plan* rope, const int32_t* positions,
+                        const qlin_bf16* q, int64_t ldq, int64_t q_heads, qlin_bf16* q_out, int64_t ldqo,
+                        qlin_stream_t stream) {
+  const int rc = head_norm_args(norm);
+  if (rc) return rc;
+  return kv_append(cache, batch, T, k, ldk, v, ldv, norm, rope, positions, q, ldq, q_heads, q_out, ldqo, stream);
 }
 
 static bool attn_shape_ok(const qlin_kv_cache* c, const qlin_kv_batch* b, int64_t T, int64_t q_heads) {

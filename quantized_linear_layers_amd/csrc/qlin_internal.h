@@ -93,13 +93,14 @@ int launch_moe_w4a16(const uint16_t* x, int64_t T, int64_t H, int64_t I, int64_t
                      const uint8_t* p2, const uint16_t* st2, uint16_t* y, void* ws, hipStream_t st);
 
 // ---- rotary positions and the paged cache's append (qlin_rope.hip)
-int launch_rope(const uint16_t* x, int64_t ldx, int64_t T, int64_t H, int64_t D,
-                const int32_t* positions, const qlin_rope_plan& rope, int inverse, uint16_t* y,
+// (norm: NULL without head norms; rope: NULL without a rotation)
+int launch_rope(const uint16_t* x, int64_t ldx, int64_t T, int64_t H, int64_t D, const qlin_head_norm* norm,
+                const int32_t* positions, const qlin_rope_plan* rope, int inverse, uint16_t* y,
                 int64_t ldy, hipStream_t st);
 // Whether T rows of heads of D values (queries, keys and values together) fit a grid.
 bool rope_grid_ok(int64_t T, int64_t heads, int64_t D);
 int launch_kv_append(const qlin_kv_cache& cache, const qlin_kv_batch& batch, int64_t T,
-                     const uint16_t* k, int64_t ldk, const uint16_t* v, int64_t ldv,
+                     const uint16_t* k, int64_t ldk, const uint16_t* v, int64_t ldv, const qlin_head_norm* norm,
                      const qlin_rope_plan* rope, const int32_t* positions, const uint16_t* q,
                      int64_t ldq, int64_t q_heads, uint16_t* q_out, int64_t ldqo, hipStream_t st);
 

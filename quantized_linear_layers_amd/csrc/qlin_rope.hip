@@ -48,6 +48,11 @@ struct RopeArgs {
   int64_t B, cols;
   int slots;  // heads of one token that a workgroup handles at a time
   int toks;   // tokens of a workgroup
+  // head norms: weights of queries, keys and values (NULL: 1), parts that are
+  // normalised (bit 0 queries, 1 keys, 2 values)
+  const uint16_t* w[3];
+  float eps, offset;
+  int normed;
 };
 
 // The sequence of token t: the number of sequences that end at or before it.
@@ -101,8 +106,52 @@ __device__ __forceinline__ void divide(Piece& p, float sc) {
   }
 }
 
-// APPEND: keys and values go to the cache; FP8: as E4M3 codes with a scale.
-template <bool APPEND, bool FP8>
+// The sum of x over the n lanes (a power of two, aligned) that share a head, in each.
+// Lanes trade within a row of 16 by DPP: after each step the lanes that a mirror
+// trades between hold one value already.
+template <int CTRL>
+__device__ __forceinline__ float dpp_add(float x) {
+  return x + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), CTRL, 0xF, 0xF, false));
+}
+__device__ __forceinline__ float head_sum(float x, int n) {
+  if (n >= 2) x = dpp_add<0xB1>(x);    // quad_perm 1 0 3 2
+  if (n >= 4) x = dpp_add<0x4E>(x);    // quad_perm 2 3 0 1
+  if (n >= 8) x = dpp_add<0x141>(x);   // the two quads of eight lanes
+  if (n >= 16) x = dpp_add<0x140>(x);  // the two eights of a row
+  if (n >= 32) x += __shfl_xor(x, 16, kWave);
+  if (n >= 64) x += __shfl_xor(x, 32, kWave);
+  return x;
+}
+
+// A head's piece over the head's root mean square: p / sqrt(sum of squares / D + eps),
+// the sum over the head's n lanes in fp32. Squares that pass fp32's range (a value
+// above 1.8e19) are summed again of values times 2^-72.
+__device__ __forceinline__ void normalise(Piece& p, int n, float inv_d, float eps) {
+  auto squares = [&] {
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s = fmaf(p.hi[i], p.hi[i], fmaf(p.lo[i], p.lo[i], s));
+    return head_sum(s, n);
+  };
+  auto times = [&](float f) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      p.lo[i] *= f;
+      p.hi[i] *= f;
+    }
+  };
+  float s = squares();
+  if (s > 0x1.fffffep+127f) {
+    times(0x1p-72f);
+    s = squares();
+    eps = eps * 0x1p-72f * 0x1p-72f;
+  }
+  times(__builtin_amdgcn_rsqf(fmaf(s, inv_d, eps)));
+}
+
+// APPEND: keys and values go to the cache; FP8: as E4M3 codes with a scale. NORM:
+// heads are normalised first.
+template <bool APPEND, bool FP8, bool NORM>
 __global__ __launch_bounds__(kRopeThreads) void rope_kernel(const RopeArgs a) {
   const int per_head = a.D / 16;
   const int c = threadIdx.x % per_head;       // this thread's piece of a head
@@ -155,13 +204,21 @@ __global__ __launch_bounds__(kRopeThreads) void rope_kernel(const RopeArgs a) {
   auto head_of = [&](int h, int part) {
     return h - (part > 0 ? a.heads[0] : 0) - (part > 1 ? a.heads[1] : 0);
   };
-  uint4 n0 = make_uint4(0, 0, 0, 0), n1 = n0;
+  uint4 n0 = make_uint4(0, 0, 0, 0), n1 = n0, w0 = n0, w1 = n0;
   auto next = [&](int h) {  // the head after this one is read before this one is worked on
     if (h >= h_all) return;
     const int part = part_of(h);
     const uint16_t* src = a.x[part] + t * a.ld[part] + (int64_t)head_of(h, part) * a.D;
     n0 = ldg16(src + o0);
     n1 = ldg16(src + o1);
+    if (NORM) {
+      const uint16_t* w = part == 0 ? a.w[0] : part == 1 ? a.w[1] : a.w[2];
+      w0 = w1 = make_uint4(0, 0, 0, 0);
+      if (w) {
+        w0 = ldg16(w + o0);
+        w1 = ldg16(w + o1);
+      }
+    }
   };
   const int step = gridDim.y * a.slots;
   int h = blockIdx.y * a.slots + slot;
@@ -169,11 +226,26 @@ __global__ __launch_bounds__(kRopeThreads) void rope_kernel(const RopeArgs a) {
   for (; h < h_all; h += step) {
     const int part = part_of(h), hh = head_of(h, part);
     uint4 r0 = n0, r1 = n1;
+    const uint4 g0 = w0, g1 = w1;
     next(h + step);
     if (part > 0 && page < 0) continue;
     Piece p;
     unpack_bf16x8(r0, p.lo);
     unpack_bf16x8(r1, p.hi);
+    const bool normed = NORM && ((a.normed >> part) & 1);
+    if (normed) {
+      normalise(p, per_head, 1.0f / (float)a.D, a.eps);
+      // (fp32 from here to the one rounding at the end, the weights exact)
+      const float offset = (part == 0 ? a.w[0] : part == 1 ? a.w[1] : a.w[2]) ? a.offset : 1.0f;
+      Piece w;
+      unpack_bf16x8(g0, w.lo);
+      unpack_bf16x8(g1, w.hi);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        p.lo[i] *= w.lo[i] + offset;
+        p.hi[i] *= w.hi[i] + offset;
+      }
+    }
     if (turning && part < 2) {
       if (halves) {
 #pragma unroll
@@ -194,6 +266,8 @@ __global__ __launch_bounds__(kRopeThreads) void rope_kernel(const RopeArgs a) {
           p.hi[2 * i + 1] = fmaf(y, cs[4 + i], x * sn[4 + i]);
         }
       }
+    }
+    if (normed || (turning && part < 2)) {
       r0 = pack8(p.lo);
       r1 = pack8(p.hi);
     }
@@ -264,8 +338,25 @@ bool rope_grid_ok(int64_t T, int64_t heads, int64_t D) {
   return (int64_t)grid.x * kRopeThreads <= 0xFFFFFFFF && grid.y <= 0xFFFF;
 }
 
-int launch_rope(const uint16_t* x, int64_t ldx, int64_t T, int64_t H, int64_t D,
-                const int32_t* positions, const qlin_rope_plan& rope, int inverse, uint16_t* y,
+static void norm_args(RopeArgs& a, const qlin_head_norm& n) {
+  a.w[0] = n.q_weight;
+  a.w[1] = n.k_weight;
+  a.w[2] = n.v_weight;
+  a.eps = n.eps;
+  a.offset = n.offset;
+  a.normed = n.values ? 7 : 3;
+}
+static void rope_args(RopeArgs& a, const qlin_rope_plan* rope) {
+  a.sign = 1.0f;
+  if (!rope) return;
+  a.rot16 = (int)(rope->rot / 16);
+  a.interleaved = rope->interleaved;
+  a.magnitude = rope->magnitude;
+  a.turns = rope->turns;
+}
+
+int launch_rope(const uint16_t* x, int64_t ldx, int64_t T, int64_t H, int64_t D, const qlin_head_norm* norm,
+                const int32_t* positions, const qlin_rope_plan* rope, int inverse, uint16_t* y,
                 int64_t ldy, hipStream_t st) {
   RopeArgs a = {};
   a.x[0] = x;
@@ -275,20 +366,22 @@ int launch_rope(const uint16_t* x, int64_t ldx, int64_t T, int64_t H, int64_t D,
   a.ldy = ldy;
   a.T = T;
   a.D = (int)D;
-  a.rot16 = (int)(rope.rot / 16);
-  a.interleaved = rope.interleaved;
-  a.magnitude = rope.magnitude;
-  a.sign = inverse ? -1.0f : 1.0f;
-  a.turns = rope.turns;
+  rope_args(a, rope);
+  if (inverse) a.sign = -1.0f;
   a.positions = positions;
   dim3 grid;
   rope_shape(a, grid);
-  rope_kernel<false, false><<<grid, kRopeThreads, 0, st>>>(a);
+  if (norm) {
+    norm_args(a, *norm);
+    rope_kernel<false, false, true><<<grid, kRopeThreads, 0, st>>>(a);
+  } else {
+    rope_kernel<false, false, false><<<grid, kRopeThreads, 0, st>>>(a);
+  }
   return launch_status();
 }
 
 int launch_kv_append(const qlin_kv_cache& cache, const qlin_kv_batch& batch, int64_t T,
-                     const uint16_t* k, int64_t ldk, const uint16_t* v, int64_t ldv,
+                     const uint16_t* k, int64_t ldk, const uint16_t* v, int64_t ldv, const qlin_head_norm* norm,
                      const qlin_rope_plan* rope, const int32_t* positions, const uint16_t* q,
                      int64_t ldq, int64_t q_heads, uint16_t* q_out, int64_t ldqo, hipStream_t st) {
   RopeArgs a = {};
@@ -304,13 +397,7 @@ int launch_kv_append(const qlin_kv_cache& cache, const qlin_kv_batch& batch, int
   a.ldy = ldqo;
   a.T = T;
   a.D = (int)cache.head_dim;
-  if (rope) {
-    a.rot16 = (int)(rope->rot / 16);
-    a.interleaved = rope->interleaved;
-    a.magnitude = rope->magnitude;
-    a.turns = rope->turns;
-  }
-  a.sign = 1.0f;
+  rope_args(a, rope);
   a.positions = positions;
   a.kc = (uint8_t*)cache.k;
   a.vc = (uint8_t*)cache.v;
@@ -326,10 +413,18 @@ int launch_kv_append(const qlin_kv_cache& cache, const qlin_kv_batch& batch, int
   a.cols = batch.table_cols;
   dim3 grid;
   rope_shape(a, grid);
-  if (cache.fmt == QLIN_KV_E4M3)
-    rope_kernel<true, true><<<grid, kRopeThreads, 0, st>>>(a);
-  else
-    rope_kernel<true, false><<<grid, kRopeThreads, 0, st>>>(a);
+  const bool f8 = cache.fmt == QLIN_KV_E4M3;
+  if (norm) {
+    norm_args(a, *norm);
+    if (f8)
+      rope_kernel<true, true, true><<<grid, kRopeThreads, 0, st>>>(a);
+    else
+      rope_kernel<true, false, true><<<grid, kRopeThreads, 0, st>>>(a);
+  } else if (f8) {
+    rope_kernel<true, true, false><<<grid, kRopeThreads, 0, st>>>(a);
+  } else {
+    rope_kernel<true, false, false><<<grid, kRopeThreads, 0, st>>>(a);
+  }
   return launch_status();
 }
 

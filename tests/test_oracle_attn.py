@@ -111,3 +111,32 @@ def test_attn_is_a_dense_softmax(oracle, fp8, causal, window):
                 np.testing.assert_allclose(r["lse"][t, h], np.log(e.sum()), rtol=1e-12)
     # the last sequence has more new tokens than keys: its first two see nothing when causal
     assert (r["seen"][4:6] == 0).all() == causal
+
+
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("weighted", [False, True])
+def test_norm_then_rotation(oracle, inter, weighted):
+    """Normalised heads have a root mean square of 1 (without eps and weight), and the
+    rotation of the normalised values is the rotation that is pinned above."""
+    rng = np.random.default_rng(12)
+    T, H, D, rot = 6, 3, 64, 48
+    x = bits(rng.standard_normal((T, H, D)) * 2.0 ** rng.integers(-60, 60, (T, H, 1)))
+    w = bits(rng.standard_normal(D)) if weighted else None
+    pos = rng.integers(0, 1 << 20, T).astype(np.int32)
+    turns = oracle.rope_turns(rot)
+    f = bf16_to_f32(x).astype(np.float64)
+    n, _ = oracle.norm_rope(x, None, 0.0, 3.0, pos, turns, 0)
+    np.testing.assert_allclose((n ** 2).mean(-1), 1.0, rtol=1e-12)
+    np.testing.assert_allclose(n * np.sqrt((f ** 2).mean(-1, keepdims=True)), f, rtol=1e-12)
+    g, mag = oracle.norm_rope(x, w, 0.25, 1.0, pos, turns, rot, inter, 1.5)
+    m = f / np.sqrt((f * f).sum(-1, keepdims=True) / D + 0.25)
+    if weighted:
+        m = m * (1.0 + bf16_to_f32(w).astype(np.float64))
+    a, b = (m[..., 0:rot:2], m[..., 1:rot:2]) if inter else (m[..., :rot // 2], m[..., rot // 2:rot])
+    part = pos.astype(np.float64)[:, None] * turns
+    z = 1.5 * (a + 1j * b) * np.exp(2j * math.pi * (part - np.rint(part)))[:, None]
+    ya, yb = (g[..., 0:rot:2], g[..., 1:rot:2]) if inter else (g[..., :rot // 2], g[..., rot // 2:rot])
+    np.testing.assert_allclose(ya, z.real, atol=1e-11)
+    np.testing.assert_allclose(yb, z.imag, atol=1e-11)
+    np.testing.assert_allclose(g[..., rot:], m[..., rot:], rtol=1e-12)
+    assert (mag >= np.abs(g) - 1e-12).all()
