@@ -536,6 +536,43 @@ int qlin_attn_paged(const qlin_kv_cache* cache, const qlin_kv_batch* batch, int6
                     int64_t window, qlin_bf16* out, int64_t ldo, float* lse, void* ws,
                     size_t ws_bytes, qlin_stream_t stream);
 
+/* Attention of trees of new tokens (drafted tokens that are verified in one step):
+ * qlin_attn_paged, except that a new token sees, beside the tokens that were in its
+ * sequence before the new ones, those new ones that its mask names.
+ *   mask      [T][words] uint64: bit u % 64 of word u / 64 of row t: the token sees
+ *             its sequence's new token u (its own bit among them; without any, and no
+ *             earlier token, its row is empty). words is 1 to 8 and max_q at most
+ *             64 * words (QLIN_ERR_SHAPE); bits from the sequence's count of new tokens
+ *             on are not looked at;
+ *   positions [T] int32, read with a window > 0 alone (else it may be NULL): a token sees
+ *             the earlier keys j > positions[t] - window, the position taken as the
+ *             nearest of first .. first + new tokens - 1. The window is at least max_q
+ *             (QLIN_ERR_ARG), so that a token's ancestors all lie inside it: the mask
+ *             alone decides about new tokens.
+ * Keys and values of the new tokens lie where qlin_kv_append puts them, in the order
+ * of the rows (rotated at positions[t], which is the depth's, not the slot's). The
+ * rest, workspace and plan included, as for qlin_attn_paged with causal != 0. */
+typedef struct {
+  const uint64_t* mask;
+  const int32_t* positions;
+  int64_t words;
+} qlin_tree;
+
+int qlin_attn_tree(const qlin_kv_cache* cache, const qlin_kv_batch* batch, int64_t T,
+                   const qlin_bf16* q, int64_t ldq, int64_t q_heads, float scale, const qlin_tree* tree,
+                   int64_t window, qlin_bf16* out, int64_t ldo, float* lse, void* ws,
+                   size_t ws_bytes, qlin_stream_t stream);
+
+/* A tree's masks and positions from its parents: parents [T] int32, of each new token
+ * the number among its sequence's new tokens of the one that it follows; any value
+ * that is not an earlier new token's (-1) starts from the tokens before. mask [T][words]
+ * gets the token's ancestors and itself, positions [T] (or NULL) the sequence's
+ * length before the new tokens plus the number of ancestors. Of the batch q_start,
+ * kv_len, batch and max_q are used; rows of no sequence are left as they are. mask
+ * 8-byte aligned. */
+int qlin_tree_plan(const qlin_kv_batch* batch, int64_t T, const int32_t* parents, int64_t words, uint64_t* mask,
+                   int32_t* positions, qlin_stream_t stream);
+
 /* What qlin_attn_paged chooses for a call, on the host (the arrays are not looked
  * at and may be NULL): plan[0] rows of a workgroup (32: the kernel of decode steps
  * and small chunks; 128 or, E4M3, 256: chunks; 0: an empty call), plan[1] parts of

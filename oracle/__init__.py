@@ -76,6 +76,9 @@ def _load():
         "qo_kv_slots": (None, [P, P, P, I64, I64, I64, I64, I64, P, P]),
         "qo_attn_paged": (None, [P, I64, I64, I64, I64, P, P, P, P, C.c_int, I64, I64, I64, P, P, P, I64,
                                  I64, C.c_double, C.c_int, I64, P, P, P, P, P]),
+        "qo_attn_tree": (None, [P, I64, I64, I64, I64, P, P, P, P, C.c_int, I64, I64, I64, P, P, P, I64,
+                                I64, C.c_double, I64, P, I64, P, P, P, P, P, P]),
+        "qo_tree_plan": (None, [P, P, I64, I64, P, I64, P, P]),
         "qo_max_threads": (C.c_int, []),
         "qo_set_threads": (None, [C.c_int]),
     }
@@ -437,10 +440,18 @@ def kv_slots(q_start, kv_len, table, page_size, pages, T):
     return slot, place
 
 
-def attn_paged(q_bf16, k, v, ks, vs, q_start, kv_len, table, scale, causal=True, window=0):
+def tree_plan(q_start, kv_len, parents, words, mask, positions):
+    """Fills mask [T, words] uint64 and positions [T] int32 (rows of no sequence stay)."""
+    qs, kl, pa = _c(q_start, np.int32), _c(kv_len, np.int32), _c(parents, np.int32)
+    assert mask.dtype == np.uint64 and positions.dtype == np.int32 and mask.flags.c_contiguous
+    _load().qo_tree_plan(_p(qs), _p(kl), kl.size, pa.size, _p(pa), words, _p(mask), _p(positions))
+
+
+def attn_paged(q_bf16, k, v, ks, vs, q_start, kv_len, table, scale, causal=True, window=0, mask=None,
+               positions=None):
     """q [T,Hq,D] bf16 bits over pools [pages,Hkv,page,D] (bf16 bits, or u8 codes
     with f32 scales). Returns dict(out, lse, mag, zmag, seen); rows of no
-    sequence hold NaN (seen 0)."""
+    sequence hold NaN (seen 0). mask [T, words] uint64: trees of new tokens."""
     fp8 = ks is not None
     q = _c(q_bf16, np.uint16)
     k, v = (_c(a, np.uint8 if fp8 else np.uint16) for a in (k, v))
@@ -450,9 +461,14 @@ def attn_paged(q_bf16, k, v, ks, vs, q_start, kv_len, table, scale, causal=True,
     pages, Hkv, page, _ = k.shape
     r = dict(out=np.full((T, Hq, D), np.nan), lse=np.full((T, Hq), np.nan), mag=np.zeros((T, Hq, D)),
              zmag=np.zeros((T, Hq)), seen=np.zeros((T, Hq), np.int64))
-    _load().qo_attn_paged(_p(q), Hq * D, T, Hq, D, _p(k), _p(v), _p(ks), _p(vs), int(fp8), pages, Hkv, page,
-                          _p(qs), _p(kl), _p(tb), kl.size, tb.shape[1], scale, int(causal), window,
-                          _p(r["out"]), _p(r["lse"]), _p(r["mag"]), _p(r["zmag"]), _p(r["seen"]))
+    args = (_p(q), Hq * D, T, Hq, D, _p(k), _p(v), _p(ks), _p(vs), int(fp8), pages, Hkv, page,
+            _p(qs), _p(kl), _p(tb), kl.size, tb.shape[1], scale)
+    out = (_p(r["out"]), _p(r["lse"]), _p(r["mag"]), _p(r["zmag"]), _p(r["seen"]))
+    if mask is None:
+        _load().qo_attn_paged(*args, int(causal), window, *out)
+    else:
+        mask, positions = _c(mask, np.uint64), None if positions is None else _c(positions, np.int32)
+        _load().qo_attn_tree(*args, window, _p(mask), mask.shape[1], _p(positions), *out)
     return r
 
 

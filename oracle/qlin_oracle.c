@@ -954,12 +954,14 @@ static double pool_value(const void* pool, const float* scale, int fp8, int64_t 
  * pools [pages][Hkv][page_size][D]. Outputs, where a row belongs to a
  * sequence: out [T][Hq][D] unrounded, lse [T][Hq], mag [T][Hq][D] (the mean of
  * |v| under the weights), zmag [T][Hq] (the largest |scale| sum |q_d k_d|
- * of a seen key), seen [T][Hq] (keys that the row sees). */
-void qo_attn_paged(const uint16_t* q, int64_t ldq, int64_t T, int64_t Hq, int64_t D, const void* k, const void* v,
+ * of a seen key), seen [T][Hq] (keys that the row sees). With a mask [T][words] (and
+ * positions for a window) the new tokens are trees: of the keys from the first new token
+ * on a row sees those whose bits are set. */
+static void attn_rows(const uint16_t* q, int64_t ldq, int64_t T, int64_t Hq, int64_t D, const void* k, const void* v,
                    const float* ks, const float* vs, int fp8, int64_t pages, int64_t Hkv, int64_t page_size,
                    const int32_t* q_start, const int32_t* kv_len, const int32_t* table, int64_t B, int64_t cols,
-                   double scale, int causal, int64_t window, double* out, double* lse, double* mag, double* zmag,
-                   int64_t* seen) {
+                   double scale, int causal, int64_t window, const uint64_t* mask, int64_t words,
+                   const int32_t* positions, double* out, double* lse, double* mag, double* zmag, int64_t* seen) {
   int64_t* seq = malloc(sizeof(int64_t) * (size_t)(T > 0 ? T : 1));
   int64_t* place = malloc(sizeof(int64_t) * (size_t)(T > 0 ? T : 1));
   const int64_t cap = cols * page_size;
@@ -976,8 +978,19 @@ void qo_attn_paged(const uint16_t* q, int64_t ldq, int64_t T, int64_t Hq, int64_
       double top = -INFINITY, zm = 0.0;
       int64_t n = 0;
       for (int64_t j = 0; j < len; ++j) {
-        if (causal && j > place[t]) continue;
-        if (window > 0 && j <= place[t] - window) continue;
+        if (mask) {
+          const int64_t n = q_start[b + 1] - q_start[b], first = kv_len[b] - n, u = j - first;
+          if (u >= 64 * words || (u >= 0 && !((mask[t * words + u / 64] >> (u % 64)) & 1))) continue;
+          if (u < 0 && window > 0) {
+            int64_t p = positions[t];
+            if (p < first) p = first;
+            if (p > first + n - 1) p = first + n - 1;
+            if (j <= p - window) continue;
+          }
+        } else {
+          if (causal && j > place[t]) continue;
+          if (window > 0 && j <= place[t] - window) continue;
+        }
         const int64_t page = table[b * cols + j / page_size];
         if (page < 0 || page >= pages) continue;
         const int64_t r = (page * Hkv + hk) * page_size + j % page_size;
@@ -1013,6 +1026,45 @@ void qo_attn_paged(const uint16_t* q, int64_t ldq, int64_t T, int64_t Hq, int64_
     }
   free(seq);
   free(place);
+}
+
+void qo_attn_paged(const uint16_t* q, int64_t ldq, int64_t T, int64_t Hq, int64_t D, const void* k, const void* v,
+                   const float* ks, const float* vs, int fp8, int64_t pages, int64_t Hkv, int64_t page_size,
+                   const int32_t* q_start, const int32_t* kv_len, const int32_t* table, int64_t B, int64_t cols,
+                   double scale, int causal, int64_t window, double* out, double* lse, double* mag, double* zmag,
+                   int64_t* seen) {
+  attn_rows(q, ldq, T, Hq, D, k, v, ks, vs, fp8, pages, Hkv, page_size, q_start, kv_len, table, B, cols, scale,
+            causal, window, NULL, 0, NULL, out, lse, mag, zmag, seen);
+}
+void qo_attn_tree(const uint16_t* q, int64_t ldq, int64_t T, int64_t Hq, int64_t D, const void* k, const void* v,
+                  const float* ks, const float* vs, int fp8, int64_t pages, int64_t Hkv, int64_t page_size,
+                  const int32_t* q_start, const int32_t* kv_len, const int32_t* table, int64_t B, int64_t cols,
+                  double scale, int64_t window, const uint64_t* mask, int64_t words, const int32_t* positions,
+                  double* out, double* lse, double* mag, double* zmag, int64_t* seen) {
+  attn_rows(q, ldq, T, Hq, D, k, v, ks, vs, fp8, pages, Hkv, page_size, q_start, kv_len, table, B, cols, scale, 1,
+            window, mask, words, positions, out, lse, mag, zmag, seen);
+}
+
+/* Masks [T][words] and positions [T] of trees, a token's ancestors one by one. Rows of no
+ * sequence, and of a sequence the tokens from 64 words on, are left alone. */
+void qo_tree_plan(const int32_t* q_start, const int32_t* kv_len, int64_t B, int64_t T, const int32_t* parents,
+                  int64_t words, uint64_t* mask, int32_t* positions) {
+  for (int64_t b = 0; b < B; ++b) {
+    const int64_t s0 = q_start[b], n = q_start[b + 1] - s0;
+    if (s0 < 0 || s0 + n > T) continue;
+    for (int64_t i = 0; i < n && i < 64 * words; ++i) {
+      int64_t depth = 0, u = i;
+      for (int64_t w = 0; w < words; ++w) mask[(s0 + i) * words + w] = 0;
+      for (;;) {
+        mask[(s0 + i) * words + u / 64] |= (uint64_t)1 << (u % 64);
+        const int64_t p = parents[s0 + u];
+        if (p < 0 || p >= u) break;
+        u = p;
+        depth++;
+      }
+      positions[s0 + i] = (int32_t)(kv_len[b] - n + depth);
+    }
+  }
 }
 
 int qo_max_threads(void) {

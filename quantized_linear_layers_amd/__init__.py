@@ -53,6 +53,10 @@ class _RopePlan(C.Structure):
     _fields_ = [("turns", _P), ("rot", _I64), ("interleaved", _INT), ("magnitude", _F32)]
 
 
+class _Tree(C.Structure):
+    _fields_ = [("mask", _P), ("positions", _P), ("words", _I64)]
+
+
 class _HeadNorm(C.Structure):
     _fields_ = [("q_weight", _P), ("k_weight", _P), ("v_weight", _P), ("eps", _F32), ("offset", _F32),
                 ("values", _INT)]
@@ -101,6 +105,9 @@ _SIGS = {
     "qlin_attn_workspace_bytes": (_SZ, [C.POINTER(_KVCache), C.POINTER(_KVBatch), _I64, _I64]),
     "qlin_attn_paged": (_INT, [C.POINTER(_KVCache), C.POINTER(_KVBatch), _I64, _P, _I64, _I64, _F32,
                                _INT, _I64, _P, _I64, _P, _P, _SZ, _P]),
+    "qlin_attn_tree": (_INT, [C.POINTER(_KVCache), C.POINTER(_KVBatch), _I64, _P, _I64, _I64, _F32,
+                              C.POINTER(_Tree), _I64, _P, _I64, _P, _P, _SZ, _P]),
+    "qlin_tree_plan": (_INT, [C.POINTER(_KVBatch), _I64, _P, _I64, _P, _P, _P]),
     "qlin_attn_plan": (_INT, [C.POINTER(_KVCache), C.POINTER(_KVBatch), _I64, _I64, _I64, C.POINTER(_I64)]),
 }
 for _name, (_res, _args) in _SIGS.items():
@@ -771,6 +778,52 @@ class PagedBatch:
         self._ws_bytes = {}
 
 
+class Tree:
+    """Trees of a batch's new tokens: mask int64 [T, words] (bit u % 64 of word u / 64:
+    the token sees its sequence's new token u) and positions int32 [T], or None (no
+    window then). Contents as at qlin_tree; `Tree.empty` allocates them for
+    `tree_plan`."""
+
+    def __init__(self, mask, positions=None):
+        _check(mask, "mask", torch.int64, 2)
+        self.device, (self.tokens, self.words) = mask.device, mask.shape
+        if positions is not None:
+            _check(positions, "positions", torch.int32, 1)
+            _on(positions.device, self.device, "positions")
+            if positions.numel() != self.tokens:
+                raise ValueError("mask must be [T, words] and positions [T]")
+        self.mask, self.positions = mask, positions
+        self._c = _Tree(mask.data_ptr(), None if positions is None else positions.data_ptr(), self.words)
+        self._ref = C.byref(self._c)
+
+    @classmethod
+    def empty(cls, tokens: int, words: int = 1, device="cuda"):
+        """Uninitialised masks of `words` * 64 new tokens a sequence, and positions."""
+        return cls(torch.empty((tokens, words), dtype=torch.int64, device=device),
+                   torch.empty((tokens,), dtype=torch.int32, device=device))
+
+
+def tree_plan(batch: PagedBatch, parents, tree: Tree | None = None):
+    """The masks and positions of a batch's trees from the tokens' parents int32 [T]
+    (numbers among a sequence's new tokens, -1: it follows the tokens before): into
+    `tree`, which is returned, or into a new one."""
+    dev = batch.device
+    _check(parents, "parents", torch.int32, 1)
+    _on(parents.device, dev, "parents")
+    T = parents.numel()
+    if dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return tree_plan(batch, parents, tree)
+    if tree is None:
+        tree = Tree.empty(T, max(1, -(-batch.max_q // 64)), dev)
+    _on(tree.device, dev, "tree")
+    if tree.tokens != T:
+        raise ValueError("parents and tree differ in tokens")
+    _enqueue(dev, _lib.qlin_tree_plan, batch._ref, T, parents.data_ptr(), tree.words, tree._c.mask,
+             tree._c.positions)
+    return tree
+
+
 def rope(x, positions, plan: Rope, out=None, inverse=False):
     """Rotary positions of x [T, H, D] (bf16) at positions int32 [T] by
     `plan`; `out` may be x. inverse=True turns the other way (the gradient of the
@@ -864,32 +917,41 @@ def kv_append(cache: PagedKV, batch: PagedBatch, k, v, rope: Rope | None = None,
 
 
 def attn_paged(cache: PagedKV, batch: PagedBatch, q, scale=None, causal=True, window=0, out=None,
-               return_lse=False):
+               return_lse=False, tree: Tree | None = None):
     """Attention of the new tokens' queries q [T, q_heads, D] over the cache, which
     holds their keys already (kv_append): [T, q_heads, D] bf16, and with
     return_lse the rows' ln of the sum of exponentials, f32 [T, q_heads]. scale
     defaults to D ** -0.5; window > 0 limits each token to its last `window` keys.
-    Rows of q outside every sequence are left as they are in `out` (undefined
-    in a new one)."""
+    With `tree`, each new token sees the earlier ones of its sequence and those new
+    ones that its mask names (qlin_attn_tree; a window is then at least max_q). Rows
+    of q outside every sequence are left as they are in `out` (undefined in a new
+    one)."""
     D, dev = cache.head_dim, cache.device
     _on(batch.device, dev, "batch")
     T, heads, ldq = _rows_arg(q, "q", dev, D)
     if dev.index != torch.cuda.current_device():
         with torch.cuda.device(dev):
-            return attn_paged(cache, batch, q, scale, causal, window, out, return_lse)
+            return attn_paged(cache, batch, q, scale, causal, window, out, return_lse, tree)
     if out is None:
         out, ldo = _like(q), heads * D
     else:
         T2, _, ldo = _rows_arg(out, "out", dev, D, heads)
         if T2 != T:
             raise ValueError("out shape mismatch")
+    if tree is not None:
+        _on(tree.device, dev, "tree")
+        if tree.tokens != T:
+            raise ValueError("q and tree differ in tokens")
+        if not causal:
+            raise ValueError("a tree's masks replace causal")
     lse = q.new_empty((T, heads), dtype=torch.float32) if return_lse else None
     key = (T, heads, D, cache.kv_heads, cache.page_size, cache.fmt)  # what the size depends on beside the batch's own
     nb = batch._ws_bytes.get(key)
     if nb is None:
         nb = batch._ws_bytes[key] = _lib.qlin_attn_workspace_bytes(cache._ref, batch._ref, T, heads)
     ws = _attn_workspace(nb, dev) if nb else None
-    _enqueue(dev, _lib.qlin_attn_paged, cache._ref, batch._ref, T, q.data_ptr(), ldq, heads,
-             D ** -0.5 if scale is None else float(scale), 1 if causal else 0, _int64(window, "window"),
+    fn, mask = (_lib.qlin_attn_paged, 1 if causal else 0) if tree is None else (_lib.qlin_attn_tree, tree._ref)
+    _enqueue(dev, fn, cache._ref, batch._ref, T, q.data_ptr(), ldq, heads,
+             D ** -0.5 if scale is None else float(scale), mask, _int64(window, "window"),
              out.data_ptr(), ldo, None if lse is None else lse.data_ptr(), None if ws is None else ws.data_ptr(), nb)
     return (out, lse) if return_lse else out

@@ -210,10 +210,10 @@ size_t qlin_attn_workspace_bytes(const qlin_kv_cache* cache, const qlin_kv_batch
   return attn_workspace_bytes(*cache, *batch, T, q_heads);
 }
 
-int qlin_attn_paged(const qlin_kv_cache* cache, const qlin_kv_batch* batch, int64_t T,
-                    const qlin_bf16* q, int64_t ldq, int64_t q_heads, float scale, int causal,
-                    int64_t window, qlin_bf16* out, int64_t ldo, float* lse, void* ws,
-                    size_t ws_bytes, qlin_stream_t stream) {
+static int attn_paged(const qlin_kv_cache* cache, const qlin_kv_batch* batch, int64_t T,
+                      const qlin_bf16* q, int64_t ldq, int64_t q_heads, float scale, int causal,
+                      int64_t window, const qlin_tree* tree, qlin_bf16* out, int64_t ldo, float* lse, void* ws,
+                      size_t ws_bytes, qlin_stream_t stream) {
   int rc = kv_args(cache, batch, T);
   if (rc) return rc;
   QLIN_CHECK(std::isfinite(attn_factor(scale)) && window >= 0 && (window == 0 || causal), QLIN_ERR_ARG);
@@ -228,8 +228,51 @@ int qlin_attn_paged(const qlin_kv_cache* cache, const qlin_kv_batch* batch, int6
   QLIN_CHECK(need == 0 || ((uintptr_t)ws & 255) == 0, QLIN_ERR_ALIGN);
   rc = device_ok();
   if (rc) return rc;
-  return launch_attn(*cache, *batch, T, q, ldq, q_heads, scale, causal, window, out, ldo, lse, ws,
+  return launch_attn(*cache, *batch, T, q, ldq, q_heads, scale, causal, window, tree, out, ldo, lse, ws,
                      ws_bytes, as_stream(stream));
+}
+
+int qlin_attn_paged(const qlin_kv_cache* cache, const qlin_kv_batch* batch, int64_t T,
+                    const qlin_bf16* q, int64_t ldq, int64_t q_heads, float scale, int causal,
+                    int64_t window, qlin_bf16* out, int64_t ldo, float* lse, void* ws,
+                    size_t ws_bytes, qlin_stream_t stream) {
+  return attn_paged(cache, batch, T, q, ldq, q_heads, scale, causal, window, nullptr, out, ldo, lse, ws, ws_bytes,
+                    stream);
+}
+
+static bool tree_words_ok(const qlin_kv_batch* b, int64_t words) {
+  return words >= 1 && words <= 8 && b->max_q <= 64 * words;
+}
+
+int qlin_attn_tree(const qlin_kv_cache* cache, const qlin_kv_batch* batch, int64_t T,
+                   const qlin_bf16* q, int64_t ldq, int64_t q_heads, float scale, const qlin_tree* tree,
+                   int64_t window, qlin_bf16* out, int64_t ldo, float* lse, void* ws,
+                   size_t ws_bytes, qlin_stream_t stream) {
+  QLIN_CHECK(cache && batch && tree, QLIN_ERR_ARG);
+  QLIN_CHECK(tree_words_ok(batch, tree->words), QLIN_ERR_SHAPE);
+  QLIN_CHECK(window >= 0 && (window == 0 || window >= batch->max_q), QLIN_ERR_ARG);
+  if (T > 0 && batch->batch > 0) {
+    QLIN_CHECK(tree->mask && (window == 0 || tree->positions), QLIN_ERR_ARG);
+    QLIN_CHECK(((uintptr_t)tree->mask & 7) == 0 && ((uintptr_t)tree->positions & 3) == 0, QLIN_ERR_ALIGN);
+  }
+  return attn_paged(cache, batch, T, q, ldq, q_heads, scale, 1, window, tree, out, ldo, lse, ws, ws_bytes, stream);
+}
+
+int qlin_tree_plan(const qlin_kv_batch* batch, int64_t T, const int32_t* parents, int64_t words, uint64_t* mask,
+                   int32_t* positions, qlin_stream_t stream) {
+  QLIN_CHECK(batch, QLIN_ERR_ARG);
+  QLIN_CHECK(T >= 0 && T <= 0x7FFFFFFF && batch->batch >= 0 && batch->batch <= 0xFFFF && batch->max_q >= 0 &&
+                 tree_words_ok(batch, words),
+             QLIN_ERR_SHAPE);
+  if (T == 0 || batch->batch == 0) return QLIN_OK;
+  QLIN_CHECK(batch->max_q >= 1, QLIN_ERR_SHAPE);
+  QLIN_CHECK(batch->q_start && batch->kv_len && parents && mask, QLIN_ERR_ARG);
+  QLIN_CHECK(((uintptr_t)mask & 7) == 0 && (((uintptr_t)batch->q_start | (uintptr_t)batch->kv_len |
+                                             (uintptr_t)parents | (uintptr_t)positions) & 3) == 0,
+             QLIN_ERR_ALIGN);
+  const int rc = device_ok();
+  if (rc) return rc;
+  return launch_tree_plan(*batch, T, parents, words, mask, positions, as_stream(stream));
 }
 
 int qlin_attn_plan(const qlin_kv_cache* cache, const qlin_kv_batch* batch, int64_t T, int64_t q_heads,

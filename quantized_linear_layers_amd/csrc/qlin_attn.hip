@@ -76,6 +76,11 @@ struct AttnArgs {
   float *po, *pml;
   uint32_t* arrived;  // [batch * kv_heads * row_tiles], 0 between calls
   int part_rows, row_tiles;  // step: rows of a workgroup, workgroups for a sequence's rows
+  // a tree: masks [T][words] of the new tokens that each one sees, 32 bits a word, and
+  // positions [T] (with a window)
+  const uint32_t* mask;
+  const int32_t* positions;
+  int words;
 };
 
 __device__ __forceinline__ v16f mfma32(v8bf a, v8bf b, v16f c) {
@@ -331,12 +336,13 @@ __device__ __forceinline__ v4f scales(const uint8_t* lds_s, int n) {
 //   vis_lo, vis_hi: keys that this lane's row sees, relative to the first
 //   masked: whether some row sees only part of them; bad: bit g = the 16-row
 //   group g lies in no page
+//   TREE: tree[kb], the keys of block kb that the row's mask lets it see (if masked)
 //   E4M3: lds_s, lds_s + SCALE: the keys' and values' scales; with HOLD the keys' are in
 //   ks already, and the values' are read ahead of the work
-template <int D, bool FP8, int KB, int SCALE, bool HOLD>
+template <int D, bool FP8, bool TREE, int KB, int SCALE, bool HOLD>
 __device__ __forceinline__ void weight_block(const AttnArgs& a, State<D>& st, v16f (&s)[KB], v4i (&p)[2 * KB],
                                              const v4f (&ks)[4 * KB], const uint8_t* lds_s, bool masked, int vis_lo,
-                                             int vis_hi, uint32_t bad) {
+                                             int vis_hi, uint32_t bad, const uint32_t (&tree)[KB]) {
   const int h = (threadIdx.x & 63) >> 5;
   v4f vs[4 * KB];
   if (FP8) {
@@ -355,13 +361,16 @@ __device__ __forceinline__ void weight_block(const AttnArgs& a, State<D>& st, v1
   if (masked) {
     const int lo = vis_lo - 4 * h, hi = vis_hi - 4 * h;
 #pragma unroll
-    for (int kb = 0; kb < KB; ++kb)
+    for (int kb = 0; kb < KB; ++kb) {
+      const uint32_t mine = TREE ? tree[kb] >> (4 * h) : 0;
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         const int key = 32 * kb + 8 * (i / 4) + i % 4;
-        const bool see = lo <= key && hi > key && !((bad >> (2 * kb + i / 8)) & 1);
+        bool see = lo <= key && hi > key && !((bad >> (2 * kb + i / 8)) & 1);
+        if (TREE) see = see && ((mine >> (8 * (i / 4) + i % 4)) & 1);
         s[kb][i] = see ? s[kb][i] : -kInf;
       }
+    }
   }
   float mx = s[0][0];
 #pragma unroll
@@ -427,32 +436,64 @@ __device__ __forceinline__ void load_q(const AttnArgs& a, const Item& it, int ro
   for (int u = 0; u < D / 16; ++u) q[u] = load_q8(a, src + 16 * u);
 }
 
-// Keys [row_lo, row_hi) that a packed row sees (none: row_hi <= row_lo).
+// Keys [row_lo, row_hi) that a packed row sees (none: row_hi <= row_lo). Of a TREE the
+// keys from the first new token on are seen by the row's mask (tree_bits) beside, and
+// the window ends at the token's position, which is that of one of the new tokens.
+template <bool TREE>
 __device__ __forceinline__ int row_hi(const AttnArgs& a, const Item& it, int row) {
   if (row >= it.rows) return 0;
-  return a.causal ? min(it.first + row / a.group + 1, it.len) : it.len;
+  return !TREE && a.causal ? min(it.first + row / a.group + 1, it.len) : it.len;
 }
+template <bool TREE>
 __device__ __forceinline__ int row_lo(const AttnArgs& a, const Item& it, int row) {
   if (a.window <= 0) return 0;
-  const int64_t lo = (int64_t)it.first + row / a.group + 1 - a.window;
+  int64_t p = (int64_t)it.first + row / a.group;
+  if (TREE) {
+    const int64_t own = a.positions[it.q0 + min(row, it.rows - 1) / a.group];
+    p = min(max(own, (int64_t)it.first), (int64_t)it.first + it.n - 1);
+  }
+  const int64_t lo = p + 1 - a.window;
   return lo > 0 ? (int)lo : 0;
 }
 // Of rows [row0, row1): keys [lo, hi) that some row sees, and [all_lo, all_hi)
-// that every row sees.
+// that every row sees (of a tree: at least these, at most those).
 struct Range {
   int lo, hi, all_lo, all_hi;
 };
+template <bool TREE>
 __device__ __forceinline__ Range range_of(const AttnArgs& a, const Item& it, int row0, int row1) {
   Range r;
-  r.hi = max(row_hi(a, it, row1 - 1), 0);
-  r.lo = min(row_lo(a, it, row0), r.hi);
-  r.all_lo = row_lo(a, it, row1 - 1);
-  r.all_hi = row_hi(a, it, row0);
+  r.hi = max(row_hi<TREE>(a, it, row1 - 1), 0);
+  if (TREE) {
+    const int64_t lo = a.window > 0 ? (int64_t)it.first + 1 - a.window : 0;
+    r.lo = lo > 0 ? min((int)lo, r.hi) : 0;
+    r.all_lo = a.window > 0 ? (int)max(lo + it.n - 1, (int64_t)0) : 0;
+    r.all_hi = row0 < it.rows ? min(it.first, it.len) : 0;
+  } else {
+    r.lo = min(row_lo<TREE>(a, it, row0), r.hi);
+    r.all_lo = row_lo<TREE>(a, it, row1 - 1);
+    r.all_hi = row_hi<TREE>(a, it, row0);
+  }
   r.lo = __builtin_amdgcn_readfirstlane(r.lo);
   r.hi = __builtin_amdgcn_readfirstlane(r.hi);
   r.all_lo = __builtin_amdgcn_readfirstlane(r.all_lo);
   r.all_hi = __builtin_amdgcn_readfirstlane(r.all_hi);
   return r;
+}
+
+// A packed row's mask (rows past the end: the last one's).
+__device__ __forceinline__ const uint32_t* mask_row(const AttnArgs& a, const Item& it, int row) {
+  return a.mask + (it.q0 + min(row, it.rows - 1) / a.group) * a.words;
+}
+// Of the 32 keys from `key` on, those that the mask lets the row see: all before the
+// first new token, none behind the mask's end.
+__device__ __forceinline__ uint32_t tree_bits(const AttnArgs& a, const Item& it, const uint32_t* mask, int key) {
+  const int64_t u = (int64_t)key - it.first;
+  if (u <= -32) return ~0u;
+  if (u < 0) return mask[0] << (int)-u | ((1u << (int)-u) - 1);
+  const int64_t w = u >> 5;
+  const uint32_t lo = w < a.words ? mask[w] : 0, hi = w + 1 < a.words ? mask[w + 1] : 0;
+  return (uint32_t)(((uint64_t)hi << 32 | lo) >> (u & 31));
 }
 
 // The page of a key, read through the scalar cache (keys outside the table:
@@ -604,16 +645,16 @@ struct ChunkJob {
   Range wg, own;
   int vlo, vhi, t0, t1;
 };
-template <int BM, int TK>
+template <bool TREE, int BM, int TK>
 __device__ __forceinline__ bool chunk_job(const AttnArgs& a, int wave, ChunkJob& j) {
   int row0;
   if (!chunk_item<BM>(a, j.it, row0, j.split)) return false;
   j.w0 = row0 + 32 * wave;
   j.row = j.w0 + ((int)threadIdx.x & 31);
-  j.wg = range_of(a, j.it, row0, min(row0 + BM, j.it.rows));
-  j.own = range_of(a, j.it, j.w0, max(min(j.w0 + 32, j.it.rows), j.w0 + 1));
-  j.vlo = row_lo(a, j.it, j.row);
-  j.vhi = row_hi(a, j.it, j.row);
+  j.wg = range_of<TREE>(a, j.it, row0, min(row0 + BM, j.it.rows));
+  j.own = range_of<TREE>(a, j.it, j.w0, max(min(j.w0 + 32, j.it.rows), j.w0 + 1));
+  j.vlo = row_lo<TREE>(a, j.it, j.row);
+  j.vhi = row_hi<TREE>(a, j.it, j.row);
   int t0 = j.wg.lo / TK, t1 = (j.wg.hi + TK - 1) / TK;
   if (a.splits > 1) {
     const int n = max((t1 - t0 + a.splits - 1) / a.splits, 1);
@@ -647,7 +688,7 @@ __device__ __forceinline__ bool chunk_job(const AttnArgs& a, int wave, ChunkJob&
 // for the weights), and by what the two waves of a SIMD take from each other. With heads of
 // 256 a tile has half the scores, but 102 vector instructions beside its 32 products: the
 // fragments' LDS addresses, which there are computed anew for each (frag_lane).
-template <int D, int TK>
+template <int D, int TK, bool TREE>
 __global__ __launch_bounds__(256, D == 64 ? 4 : 2) void attn_chunk_kernel(const AttnArgs a) {
   using St = Stage<D, false, TK, TK / 4>;
   using G = Geo<D, false>;
@@ -655,7 +696,7 @@ __global__ __launch_bounds__(256, D == 64 ? 4 : 2) void attn_chunk_kernel(const 
   __shared__ __attribute__((aligned(1024))) uint8_t lds_k[2][St::kTile], lds_v[2][St::kTile];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   ChunkJob job;
-  if (!chunk_job<BM, TK>(a, wave, job)) return;
+  if (!chunk_job<TREE, BM, TK>(a, wave, job)) return;
   const Item it = job.it;
   const Range wg = job.wg, own = job.own;
   const int w0 = job.w0, row = job.row, vlo = job.vlo, vhi = job.vhi, t0 = job.t0, t1 = job.t1;
@@ -732,7 +773,12 @@ __global__ __launch_bounds__(256, D == 64 ? 4 : 2) void attn_chunk_kernel(const 
     if (holes)
       for (int g = 0; g < TK / 16; ++g) bad |= (uint32_t)no_page(a, page_of(a, it, key + 16 * g)) << g;
     const bool masked = holes || key + TK > own.all_hi || key < own.all_lo;
-    weight_block<D, false, KB, 0, false>(a, st, s, p, none, nullptr, masked, vlo - key, vhi - key, bad);
+    uint32_t tree[KB] = {};
+    if (TREE && masked) {
+#pragma unroll
+      for (int kb = 0; kb < KB; ++kb) tree[kb] = tree_bits(a, it, mask_row(a, it, row), key + 32 * kb);
+    }
+    weight_block<D, false, TREE, KB, 0, false>(a, st, s, p, none, nullptr, masked, vlo - key, vhi - key, bad, tree);
     __builtin_amdgcn_sched_barrier(0);
     at ^= 1;
   }
@@ -774,7 +820,7 @@ __global__ __launch_bounds__(256, D == 64 ? 4 : 2) void attn_chunk_kernel(const 
 // takes the two waves of a SIMD about 4000 cycles, of which their products need 2048 and
 // their 240 vector instructions each (bf16: 168) 2400 at 5 cycles, so the most of what is
 // missing goes to the two barriers a tile that hold the phases.
-template <int D, int TK>
+template <int D, int TK, bool TREE>
 __global__ __launch_bounds__(512, D == 64 ? 4 : 2) void attn_chunk_e4m3_kernel(const AttnArgs a) {
   using St = Stage<D, false, TK, TK / 4>;
   using G = Geo<D, false>;
@@ -786,7 +832,7 @@ __global__ __launch_bounds__(512, D == 64 ? 4 : 2) void attn_chunk_e4m3_kernel(c
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 
   ChunkJob job;
-  if (!chunk_job<BM, TK>(a, wave, job)) return;
+  if (!chunk_job<TREE, BM, TK>(a, wave, job)) return;
   const Item it = job.it;
   const Range wg = job.wg, own = job.own;
   const int w0 = job.w0, row = job.row, vlo = job.vlo, vhi = job.vhi, t0 = job.t0, t1 = job.t1;
@@ -924,7 +970,13 @@ __global__ __launch_bounds__(512, D == 64 ? 4 : 2) void attn_chunk_e4m3_kernel(c
     if (holes)
       for (int g = 0; g < TK / 16; ++g) bad |= (uint32_t)no_page(a, page_of(a, it, key + 16 * g)) << g;
     const bool masked = holes || key + TK > own.all_hi || key < own.all_lo;
-    weight_block<D, true, KB, kScale, kHold>(a, st, s, p, ks, lds_s[t & 7], masked, vlo - key, vhi - key, bad);
+    uint32_t tree[KB] = {};
+    if (TREE && masked) {
+#pragma unroll
+      for (int kb = 0; kb < KB; ++kb) tree[kb] = tree_bits(a, it, mask_row(a, it, row), key + 32 * kb);
+    }
+    weight_block<D, true, TREE, KB, kScale, kHold>(a, st, s, p, ks, lds_s[t & 7], masked, vlo - key, vhi - key, bad,
+                                                   tree);
     if (D == 256) prefetch(t);
     phase_end(kNone);  // (no LDS writes in this phase)
     const int x = last;
@@ -983,7 +1035,7 @@ constexpr int step_waves(int D, bool fp8, int rb) {
   return D == 64 ? 4 : D == 128 ? (fp8 && rb == 1 ? 4 : 2) : (fp8 && rb == 1 ? 2 : 1);
 }
 
-template <int D, bool FP8, int RB, int NW>
+template <int D, bool FP8, int RB, int NW, bool TREE>
 __global__ __launch_bounds__(NW * 64, step_waves(D, FP8, RB)) void attn_step_kernel(const AttnArgs a) {
   using St = Stage<D, FP8, 32, 16, true>;
   using G = Geo<D, FP8, true>;
@@ -1003,7 +1055,7 @@ __global__ __launch_bounds__(NW * 64, step_waves(D, FP8, RB)) void attn_step_ker
   const int h = blockIdx.x % a.kv_heads, row0 = blockIdx.x / a.kv_heads * a.part_rows;
   if (!item_of(a, blockIdx.y, h, it) || row0 >= it.rows) return;
   const int rows = min(it.rows - row0, a.part_rows);  // this workgroup's
-  const Range rg = range_of(a, it, row0, row0 + rows);
+  const Range rg = range_of<TREE>(a, it, row0, row0 + rows);
   int t0 = rg.lo / 32, t1 = (rg.hi + 31) / 32;
   int parts = 1;
   if (a.splits > 1) {
@@ -1069,8 +1121,8 @@ __global__ __launch_bounds__(NW * 64, step_waves(D, FP8, RB)) void attn_step_ker
 #pragma unroll
   for (int rb = 0; rb < RB; ++rb) {
     const int row = 16 * rb + r;
-    vlo[rb] = row_lo(a, it, row0 + row);
-    vhi[rb] = row_hi(a, it, row0 + row);
+    vlo[rb] = row_lo<TREE>(a, it, row0 + row);
+    vhi[rb] = row_hi<TREE>(a, it, row0 + row);
     m[rb] = -kInf;
     l[rb] = 0.0f;
 #pragma unroll
@@ -1120,13 +1172,16 @@ __global__ __launch_bounds__(NW * 64, step_waves(D, FP8, RB)) void attn_step_ker
     if (more) load(t + NW, next, kNo, kNo);
     if (bad != 0 || key + 32 > rg.all_hi || key < rg.all_lo) {
 #pragma unroll
-      for (int rb = 0; rb < RB; ++rb)
+      for (int rb = 0; rb < RB; ++rb) {
+        const uint32_t tree = TREE ? tree_bits(a, it, mask_row(a, it, row0 + 16 * rb + r), key) >> (4 * g) : 0;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const int j = key + 16 * (i / 4) + 4 * g + i % 4;
-          const bool see = vlo[rb] <= j && vhi[rb] > j && !((bad >> (i / 4)) & 1);
+          bool see = vlo[rb] <= j && vhi[rb] > j && !((bad >> (i / 4)) & 1);
+          if (TREE) see = see && ((tree >> (16 * (i / 4) + i % 4)) & 1);
           s[rb][i / 4][i % 4] = see ? s[rb][i / 4][i % 4] : -kInf;
         }
+      }
     }
 #pragma unroll
     for (int rb = 0; rb < RB; ++rb) {
@@ -1459,27 +1514,32 @@ Plan plan_of(const qlin_kv_cache& cache, const qlin_kv_batch& batch, int64_t T, 
                                                              : chunk_plan(cache, batch, T, rows, group, keys);
 }
 
-template <int D, bool FP8>
+template <int D, bool FP8, bool TREE>
 void launch_parts(const AttnArgs& a, const Plan& p, hipStream_t st) {
   if (p.step) {
     const dim3 grid(a.kv_heads * p.row_tiles, a.B, p.splits);
     if (p.part_rows <= 16)
-      attn_step_kernel<D, FP8, 1, 4><<<grid, 256, 0, st>>>(a);
+      attn_step_kernel<D, FP8, 1, 4, TREE><<<grid, 256, 0, st>>>(a);
     else
-      attn_step_kernel<D, FP8, 2, 4><<<grid, 256, 0, st>>>(a);
+      attn_step_kernel<D, FP8, 2, 4, TREE><<<grid, 256, 0, st>>>(a);
   } else {
     const int64_t items = p.tiles * a.kv_heads * p.splits;
     const unsigned grid = (unsigned)((items + 7) / 8 * 8);
     constexpr int TK = D == 256 ? 32 : 64;
     if constexpr (FP8)
-      attn_chunk_e4m3_kernel<D, TK><<<grid, 512, 0, st>>>(a);
+      attn_chunk_e4m3_kernel<D, TK, TREE><<<grid, 512, 0, st>>>(a);
     else
-      attn_chunk_kernel<D, TK><<<grid, 256, 0, st>>>(a);
+      attn_chunk_kernel<D, TK, TREE><<<grid, 256, 0, st>>>(a);
   }
   if (p.splits > 1 && !p.step) {
     const int64_t rows = a.T * a.kv_heads * a.group, wg = 1024 / D;  // rows of a workgroup
     attn_join_kernel<D><<<(unsigned)((rows + wg - 1) / wg), 256, 0, st>>>(a);
   }
+}
+
+template <int D, bool FP8>
+void launch_heads(const AttnArgs& a, const Plan& p, hipStream_t st) {
+  a.mask ? launch_parts<D, FP8, true>(a, p, st) : launch_parts<D, FP8, false>(a, p, st);
 }
 
 }  // namespace
@@ -1515,8 +1575,8 @@ void attn_plan(const qlin_kv_cache& cache, const qlin_kv_batch& batch, int64_t T
 }
 
 int launch_attn(const qlin_kv_cache& cache, const qlin_kv_batch& batch, int64_t T, const uint16_t* q, int64_t ldq,
-                int64_t q_heads, float scale, int causal, int64_t window, uint16_t* out, int64_t ldo, float* lse,
-                void* ws, size_t ws_bytes, hipStream_t st) {
+                int64_t q_heads, float scale, int causal, int64_t window, const qlin_tree* tree, uint16_t* out,
+                int64_t ldo, float* lse, void* ws, size_t ws_bytes, hipStream_t st) {
   const Plan p = plan_of(cache, batch, T, q_heads, window);
   const size_t used = parts_bytes(p.parts, cache.head_dim);
   if (used > ws_bytes || (used && !ws)) return QLIN_ERR_WORKSPACE;
@@ -1556,11 +1616,16 @@ int launch_attn(const qlin_kv_cache& cache, const qlin_kv_batch& batch, int64_t 
     a.po = (float*)((uint8_t*)ws + kAttnCounterBytes);
     a.pml = (float*)((uint8_t*)a.po + round_up(p.parts * cache.head_dim * 4, 256));
   }
+  if (tree) {
+    a.mask = (const uint32_t*)tree->mask;
+    a.positions = tree->positions;
+    a.words = (int)(2 * tree->words);
+  }
   const bool f8 = cache.fmt == QLIN_KV_E4M3;
   switch (cache.head_dim) {
-    case 64: f8 ? launch_parts<64, true>(a, p, st) : launch_parts<64, false>(a, p, st); break;
-    case 128: f8 ? launch_parts<128, true>(a, p, st) : launch_parts<128, false>(a, p, st); break;
-    default: f8 ? launch_parts<256, true>(a, p, st) : launch_parts<256, false>(a, p, st); break;
+    case 64: f8 ? launch_heads<64, true>(a, p, st) : launch_heads<64, false>(a, p, st); break;
+    case 128: f8 ? launch_heads<128, true>(a, p, st) : launch_heads<128, false>(a, p, st); break;
+    default: f8 ? launch_heads<256, true>(a, p, st) : launch_heads<256, false>(a, p, st); break;
   }
   return launch_status();
 }

@@ -109,13 +109,18 @@ int launch_kv_append(const qlin_kv_cache& cache, const qlin_kv_batch& batch, int
 inline float attn_factor(float scale) { return (scale < 0.0f ? -scale : scale) * 1.44269504088896340736f; }
 size_t attn_workspace_bytes(const qlin_kv_cache& cache, const qlin_kv_batch& batch, int64_t T,
                             int64_t q_heads);
+// (tree: NULL for the order of the tokens)
 int launch_attn(const qlin_kv_cache& cache, const qlin_kv_batch& batch, int64_t T, const uint16_t* q,
-                int64_t ldq, int64_t q_heads, float scale, int causal, int64_t window, uint16_t* out,
-                int64_t ldo, float* lse, void* ws, size_t ws_bytes, hipStream_t st);
+                int64_t ldq, int64_t q_heads, float scale, int causal, int64_t window, const qlin_tree* tree,
+                uint16_t* out, int64_t ldo, float* lse, void* ws, size_t ws_bytes, hipStream_t st);
 // Whether the workgroups of a chunk's kernel fit a grid.
 bool attn_grid_ok(const qlin_kv_cache& cache, const qlin_kv_batch& batch, int64_t T, int64_t q_heads);
 // Rows of a workgroup, parts of the key axis, bytes of the workspace that a call uses.
 void attn_plan(const qlin_kv_cache& cache, const qlin_kv_batch& batch, int64_t T, int64_t q_heads,
                int64_t window, int64_t out[3]);
+
+// ---- a step's tables (qlin_tables.hip)
+int launch_tree_plan(const qlin_kv_batch& batch, int64_t T, const int32_t* parents, int64_t words,
+                     uint64_t* mask, int32_t* positions, hipStream_t st);
 
 }  // namespace qlin

@@ -140,3 +140,32 @@ def test_norm_then_rotation(oracle, inter, weighted):
     np.testing.assert_allclose(yb, z.imag, atol=1e-11)
     np.testing.assert_allclose(g[..., rot:], m[..., rot:], rtol=1e-12)
     assert (mag >= np.abs(g) - 1e-12).all()
+
+
+def test_tree_masks_and_attention(oracle):
+    """Masks and positions by hand, and attention under them as a dense softmax over
+    the keys that a set of ancestors names."""
+    start, kv = np.array([0, 5, 5, 8], np.int32), np.array([9, 4, 3], np.int32)
+    parents = np.array([-1, 0, 0, 1, 7, -1, -1, 1], np.int32)  # (7 is no earlier token)
+    mask, pos = np.zeros((8, 2), np.uint64), np.zeros(8, np.int32)
+    oracle.tree_plan(start, kv, parents, 2, mask, pos)
+    assert mask[:, 0].tolist() == [1, 3, 5, 11, 16, 1, 2, 6] and (mask[:, 1] == 0).all()
+    assert pos.tolist() == [4, 5, 5, 6, 4, 0, 0, 1]
+    rng = np.random.default_rng(13)
+    D, page = 64, 16
+    k, v = (bits(rng.standard_normal((4, 1, page, D))) for _ in range(2))
+    x = bits(rng.standard_normal((8, 2, D)))
+    table = np.array([[2], [1], [0]], np.int32)
+    for window in (0, 5):
+        r = oracle.attn_paged(x, k, v, None, None, start, kv, table, 0.3, True, window, mask, pos)
+        kf, vf, xf = (bf16_to_f32(a).astype(np.float64) for a in (k, v, x))
+        for b, (s0, s1) in enumerate(zip(start[:-1], start[1:])):
+            first = kv[b] - (s1 - s0)
+            for t in range(s0, s1):
+                keys = [j for j in range(first) if not window or j > pos[t] - window]
+                keys += [first + u for u in range(s1 - s0) if (int(mask[t, 0]) >> u) & 1]
+                z = xf[t] @ kf[table[b, 0], 0, keys].T * 0.3
+                w = np.exp(z - z.max(-1, keepdims=True))
+                np.testing.assert_allclose(r["out"][t], w @ vf[table[b, 0], 0, keys] / w.sum(-1, keepdims=True), rtol=1e-9, atol=1e-12)
+                np.testing.assert_allclose(r["lse"][t], z.max(-1) + np.log(w.sum(-1)), rtol=1e-12)
+                assert (r["seen"][t] == len(keys)).all()
