@@ -409,6 +409,58 @@ typedef struct {
   int64_t batch, table_cols, max_q;
 } qlin_kv_batch;
 
+/* Tables of a step, built on the device from the requests' lengths.
+ *
+ * A pool keeps the pages that no request has, in a list that is taken from and given
+ * back to at its end: free_pages [pages] int32, of which the first count[0] are free;
+ * count[1] is what the last reservation lacked. pages is the cache's (a slot, page *
+ * page_size + row, fits int32: pages * page_size < 2^31), page_size a power of two from
+ * 16 to 256.
+ *
+ * Tables hold what qlin_kv_batch points to: page_table [batch][table_cols], q_start
+ * [batch + 1], kv_len [batch]; and slots, positions [T] (either may be NULL). */
+typedef struct {
+  int32_t* free_pages;
+  int32_t* count;
+  int64_t pages, page_size;
+} qlin_kv_pool;
+
+typedef struct {
+  int32_t *page_table, *q_start, *kv_len, *slots, *positions;
+  int64_t batch, table_cols;
+} qlin_kv_tables;
+
+/* Room for new_tokens [batch] behind lengths [batch] cached tokens (negative numbers
+ * count as none). Writes
+ *   q_start    the new tokens' starts, one request behind the other;
+ *   kv_len     lengths + new_tokens (may be `lengths` itself);
+ *   page_table the entries from the first page without cached tokens to the last one
+ *              with a new token: request by request, from the end of the free list,
+ *              which gets that much shorter; -1 where the list is exhausted (count[1]
+ *              is then the number of such entries, else 0);
+ *   slots      of row t its token's place in the cache, page * page_size + row: -1 if
+ *              its page is none of the pool's or lies behind the table's reach (no page
+ *              is taken there);
+ *   positions  of row t its token's place in its sequence.
+ * Other entries of the page table, and rows of slots and positions from q_start[batch] on,
+ * are left as they are; rows from T on are not written. The sum of new_tokens has to be
+ * below 2^31. Everything else in the pool and the tables is device data of any value:
+ * nothing outside the arrays is read or written for it.
+ * Calls that share a pool must be ordered on one stream. */
+int qlin_kv_reserve(const qlin_kv_pool* pool, const qlin_kv_tables* tables, int64_t T, const int32_t* lengths,
+                    const int32_t* new_tokens, qlin_stream_t stream);
+
+/* Pages back to the pool: of every request the entries from the first page without one
+ * of its first lengths[b] tokens to the last one of its kv_len[b]. They go to the end
+ * of the list, the last request's last page first, so that giving back what was
+ * reserved last restores the list. Entries that are no page of the pool are passed
+ * over, and so is what would not fit the list. Tables are left as they are (kv_len
+ * too: the next reservation is told the lengths). A page that several requests share must
+ * lie within the lengths that all but one of them keep: it is given back as often as
+ * it is released. */
+int qlin_kv_release(const qlin_kv_pool* pool, const qlin_kv_tables* tables, const int32_t* lengths,
+                    qlin_stream_t stream);
+
 /* Rotary positions: pair i of the first `rot` values of a head is turned by
  * position * turns[i] whole turns and scaled by `magnitude`:
  *   a' = m (a cos t - b sin t), b' = m (b cos t + a sin t),
@@ -572,6 +624,22 @@ int qlin_attn_tree(const qlin_kv_cache* cache, const qlin_kv_batch* batch, int64
  * 8-byte aligned. */
 int qlin_tree_plan(const qlin_kv_batch* batch, int64_t T, const int32_t* parents, int64_t words, uint64_t* mask,
                    int32_t* positions, qlin_stream_t stream);
+
+/* Accepted tokens moved together: of sequence b the new tokens path[b][0 .. kept[b]-1]
+ * (numbers among its new tokens, ascending) become its first new tokens, in every one
+ * of n_caches caches (a model's layers, all of one size and format) that share the
+ * batch's page table: keys, values and E4M3 scales of token path[b][i] are copied to the
+ * place of token i, as if all had been read before any is written. path [batch]
+ * [path_cols] and kept [batch] int32; kept beyond path_cols or the new tokens counts as
+ * those. lengths [batch] gets the cached tokens then: kv_len less the new tokens plus
+ * the kept ones; it must not overlap the batch's arrays (QLIN_ERR_ARG for kv_len
+ * itself). Rows of other tokens, the dropped ones among them, are left as they are. A
+ * number outside the new tokens, or a place that the table does not reach or whose page
+ * is none of the pool's, moves nothing; of a path that does not ascend the moved rows
+ * are not defined. No two sequences may share a page of new tokens. n_caches is 1 to
+ * 65535; of the batch max_q is not used. */
+int qlin_kv_keep(const qlin_kv_cache* caches, int64_t n_caches, const qlin_kv_batch* batch, const int32_t* path,
+                 int64_t path_cols, const int32_t* kept, int32_t* lengths, qlin_stream_t stream);
 
 /* What qlin_attn_paged chooses for a call, on the host (the arrays are not looked
  * at and may be NULL): plan[0] rows of a workgroup (32: the kernel of decode steps

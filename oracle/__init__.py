@@ -78,6 +78,9 @@ def _load():
                                  I64, C.c_double, C.c_int, I64, P, P, P, P, P]),
         "qo_attn_tree": (None, [P, I64, I64, I64, I64, P, P, P, P, C.c_int, I64, I64, I64, P, P, P, I64,
                                 I64, C.c_double, I64, P, I64, P, P, P, P, P, P]),
+        "qo_kv_reserve": (None, [P, P, I64, I64, I64, I64, I64, P, P, P, P, P, P, P]),
+        "qo_kv_release": (None, [P, P, I64, I64, I64, I64, P, P, P]),
+        "qo_kv_keep": (None, [P, I64, I64, I64, I64, P, P, P, I64, I64, P, I64, P, P]),
         "qo_tree_plan": (None, [P, P, I64, I64, P, I64, P, P]),
         "qo_max_threads": (C.c_int, []),
         "qo_set_threads": (None, [C.c_int]),
@@ -438,6 +441,37 @@ def kv_slots(q_start, kv_len, table, page_size, pages, T):
     _load().qo_kv_slots(_p(qs), _p(kl), _p(tb), kl.size, tb.shape[1], page_size, pages, T, _p(slot),
                         _p(place))
     return slot, place
+
+
+def kv_reserve(lengths, new, table, free, count, page_size, slots, positions):
+    """Updates table, count, slots and positions (int32 arrays); -> (q_start, kv_len)."""
+    ln, nw = _c(lengths, np.int32), _c(new, np.int32)
+    q_start, kv_len = np.empty(ln.size + 1, np.int32), np.empty(ln.size, np.int32)
+    assert all(a.dtype == np.int32 and a.flags.c_contiguous for a in (table, free, count, slots, positions))
+    _load().qo_kv_reserve(_p(ln), _p(nw), ln.size, table.shape[1], page_size, free.size, slots.size, _p(table),
+                          _p(free), _p(count), _p(q_start), _p(kv_len), _p(slots), _p(positions))
+    return q_start, kv_len
+
+
+def kv_release(keep, kv_len, table, free, count, page_size):
+    """Updates free and count."""
+    kp, kl = _c(keep, np.int32), _c(kv_len, np.int32)
+    assert all(a.dtype == np.int32 and a.flags.c_contiguous for a in (table, free, count))
+    _load().qo_kv_release(_p(kp), _p(kl), kl.size, table.shape[1], page_size, free.size, _p(table), _p(free),
+                          _p(count))
+
+
+def kv_keep(pools, q_start, kv_len, table, path, kept):
+    """Moves rows of the pools (arrays [pages, heads, page(, values)]) -> lengths."""
+    qs, kl, tb = _c(q_start, np.int32), _c(kv_len, np.int32), _c(table, np.int32)
+    pa, kp = _c(path, np.int32), _c(kept, np.int32)
+    lengths = np.empty(kl.size, np.int32)
+    for pool in pools:
+        assert pool.flags.c_contiguous
+        pages, heads, page = pool.shape[:3]
+        _load().qo_kv_keep(_p(pool), pool[0, 0, 0].nbytes, pages, heads, page, _p(qs), _p(kl), _p(tb), kl.size,
+                           tb.shape[1], _p(pa), pa.shape[1], _p(kp), _p(lengths))
+    return lengths
 
 
 def tree_plan(q_start, kv_len, parents, words, mask, positions):

@@ -1045,6 +1045,79 @@ void qo_attn_tree(const uint16_t* q, int64_t ldq, int64_t T, int64_t Hq, int64_t
             window, mask, words, positions, out, lse, mag, zmag, seen);
 }
 
+/* A step's tables, request by request and token by token. table, free_pages and count
+ * [2] in and out; q_start, kv_len, slots, positions out (rows of no token stay). */
+void qo_kv_reserve(const int32_t* lengths, const int32_t* fresh, int64_t B, int64_t cols, int64_t page_size,
+                   int64_t pages, int64_t T, int32_t* table, const int32_t* free_pages, int32_t* count,
+                   int32_t* q_start, int32_t* kv_len, int32_t* slots, int32_t* positions) {
+  int64_t left = count[0] < 0 ? 0 : count[0] > pages ? pages : count[0], lacking = 0, t = 0;
+  for (int64_t b = 0; b < B; ++b) {
+    const int64_t len = lengths[b] > 0 ? lengths[b] : 0, n = fresh[b] > 0 ? fresh[b] : 0;
+    for (int64_t c = 0; c < cols; ++c) {
+      /* a column is new if it begins at or behind the cached tokens and before the new ones' end */
+      if (c * page_size < len || c * page_size >= len + n) continue;
+      if (left > 0) {
+        table[b * cols + c] = free_pages[--left];
+      } else {
+        table[b * cols + c] = -1;
+        lacking++;
+      }
+    }
+    q_start[b] = (int32_t)t;
+    kv_len[b] = (int32_t)(len + n);
+    for (int64_t p = len; p < len + n; ++p, ++t) {
+      if (t >= T) continue;
+      const int64_t page = p / page_size < cols ? table[b * cols + p / page_size] : -1;
+      slots[t] = page >= 0 && page < pages ? (int32_t)(page * page_size + p % page_size) : -1;
+      positions[t] = (int32_t)p;
+    }
+  }
+  q_start[B] = (int32_t)t;
+  count[0] = (int32_t)left;
+  count[1] = (int32_t)lacking;
+}
+void qo_kv_release(const int32_t* keep, const int32_t* kv_len, int64_t B, int64_t cols, int64_t page_size,
+                   int64_t pages, const int32_t* table, int32_t* free_pages, int32_t* count) {
+  int64_t left = count[0] < 0 ? 0 : count[0] > pages ? pages : count[0];
+  for (int64_t b = B - 1; b >= 0; --b)
+    for (int64_t c = cols - 1; c >= 0; --c) {
+      const int64_t at = c * page_size, page = table[b * cols + c];
+      if (at < keep[b] || at < 0 || at >= kv_len[b] || page < 0 || page >= pages) continue;
+      if (left < pages) free_pages[left++] = (int32_t)page;
+    }
+  count[0] = (int32_t)left;
+}
+
+/* Rows of one pool (`row` bytes a token and head, [pages][heads][page_size]) moved, and the
+ * lengths that are left. */
+void qo_kv_keep(uint8_t* pool, int64_t row, int64_t pages, int64_t heads, int64_t page_size, const int32_t* q_start,
+                const int32_t* kv_len, const int32_t* table, int64_t B, int64_t cols, const int32_t* path,
+                int64_t width, const int32_t* kept, int32_t* lengths) {
+  for (int64_t b = 0; b < B; ++b) {
+    const int64_t n = q_start[b + 1] - q_start[b], first = (kv_len[b] > 0 ? kv_len[b] : 0) - n;
+    int64_t count = kept[b] < 0 ? 0 : kept[b];
+    if (count > n) count = n;
+    if (count > width) count = width;
+    lengths[b] = (int32_t)(first + count > 0 ? first + count : 0);
+    uint8_t* was = malloc((size_t)(count * heads * row + 1));
+    for (int pass = 0; pass < 2; ++pass)
+      for (int64_t i = 0; i < count; ++i) {
+        const int64_t u = path[b * width + i], from = first + u, to = first + i;
+        if (u < 0 || u >= n || from < 0 || to < 0 || from / page_size >= cols || to / page_size >= cols) continue;
+        const int64_t pf = table[b * cols + from / page_size], pt = table[b * cols + to / page_size];
+        if (pf < 0 || pf >= pages || pt < 0 || pt >= pages) continue;
+        for (int64_t h = 0; h < heads; ++h) {
+          uint8_t* mine = was + (i * heads + h) * row;
+          if (pass == 0)
+            memcpy(mine, pool + ((pf * heads + h) * page_size + from % page_size) * row, (size_t)row);
+          else
+            memcpy(pool + ((pt * heads + h) * page_size + to % page_size) * row, mine, (size_t)row);
+        }
+      }
+    free(was);
+  }
+}
+
 /* Masks [T][words] and positions [T] of trees, a token's ancestors one by one. Rows of no
  * sequence, and of a sequence the tokens from 64 words on, are left alone. */
 void qo_tree_plan(const int32_t* q_start, const int32_t* kv_len, int64_t B, int64_t T, const int32_t* parents,

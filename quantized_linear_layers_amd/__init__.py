@@ -53,6 +53,15 @@ class _RopePlan(C.Structure):
     _fields_ = [("turns", _P), ("rot", _I64), ("interleaved", _INT), ("magnitude", _F32)]
 
 
+class _KVPool(C.Structure):
+    _fields_ = [("free_pages", _P), ("count", _P), ("pages", _I64), ("page_size", _I64)]
+
+
+class _KVTables(C.Structure):
+    _fields_ = [("page_table", _P), ("q_start", _P), ("kv_len", _P), ("slots", _P), ("positions", _P),
+                ("batch", _I64), ("table_cols", _I64)]
+
+
 class _Tree(C.Structure):
     _fields_ = [("mask", _P), ("positions", _P), ("words", _I64)]
 
@@ -107,6 +116,9 @@ _SIGS = {
                                _INT, _I64, _P, _I64, _P, _P, _SZ, _P]),
     "qlin_attn_tree": (_INT, [C.POINTER(_KVCache), C.POINTER(_KVBatch), _I64, _P, _I64, _I64, _F32,
                               C.POINTER(_Tree), _I64, _P, _I64, _P, _P, _SZ, _P]),
+    "qlin_kv_reserve": (_INT, [C.POINTER(_KVPool), C.POINTER(_KVTables), _I64, _P, _P, _P]),
+    "qlin_kv_release": (_INT, [C.POINTER(_KVPool), C.POINTER(_KVTables), _P, _P]),
+    "qlin_kv_keep": (_INT, [C.POINTER(_KVCache), _I64, C.POINTER(_KVBatch), _P, _I64, _P, _P, _P]),
     "qlin_tree_plan": (_INT, [C.POINTER(_KVBatch), _I64, _P, _I64, _P, _P, _P]),
     "qlin_attn_plan": (_INT, [C.POINTER(_KVCache), C.POINTER(_KVBatch), _I64, _I64, _I64, C.POINTER(_I64)]),
 }
@@ -753,6 +765,23 @@ class PagedKV:
         return cls(*t)
 
 
+class PagedLayers:
+    """The caches of a model's layers, of one size and format, that share a page table:
+    what `kv_keep` moves rows of in one call."""
+
+    def __init__(self, caches):
+        self.caches = tuple(caches)
+        if not self.caches:
+            raise ValueError("at least one cache")
+        one = self.caches[0]
+        for c in self.caches:
+            _on(c.device, one.device, "cache")
+            if c.k.shape != one.k.shape or c.fmt != one.fmt:
+                raise ValueError("the caches must have one size and format")
+        self.device = one.device
+        self._c = (_KVCache * len(self.caches))(*(c._c for c in self.caches))
+
+
 class PagedBatch:
     """New tokens of a batch of sequences: q_start int32 [B+1], kv_len int32 [B],
     page_table int32 [B, cols] (device tensors, read when a call runs) and
@@ -776,6 +805,81 @@ class PagedBatch:
                            page_table.shape[1], self.max_q)
         self._ref = C.byref(self._c)
         self._ws_bytes = {}
+
+
+class PagePool:
+    """The pages of a cache that no request has: free int32 [pages], of which the first
+    count[0] are free, and count int32 [2] (count[1]: pages that the last reservation
+    lacked). Wraps device tensors; `PagePool.full` makes a pool with all pages free."""
+
+    def __init__(self, free, count, page_size: int):
+        _check(free, "free", torch.int32, 1)
+        _check(count, "count", torch.int32, 1)
+        self.device = free.device
+        _on(count.device, self.device, "count")
+        if count.numel() != 2:
+            raise ValueError("count must be [2]")
+        self.page_size = int(page_size)
+        if self.page_size not in (16, 32, 64, 128, 256):
+            raise ValueError("page_size must be 16, 32, 64, 128 or 256")
+        self.free, self.count, self.pages = free, count, free.numel()
+        self._c = _KVPool(free.data_ptr(), count.data_ptr(), self.pages, self.page_size)
+        self._ref = C.byref(self._c)
+
+    @classmethod
+    def full(cls, pages: int, page_size: int = 64, device="cuda"):
+        """All `pages` free, the lowest taken first."""
+        return cls(torch.arange(pages - 1, -1, -1, dtype=torch.int32, device=device),
+                   torch.tensor([pages, 0], dtype=torch.int32, device=device), page_size)
+
+
+class PageTables:
+    """The tables of a batch of requests over `pool`: page_table int32 [B, cols] (the
+    requests' pages), and q_start, kv_len, slots and positions of at most max_tokens new
+    tokens, max_q of one request, which `reserve` writes. `batch` is the PagedBatch of
+    them. All of them stay in place, so a captured graph may hold the calls."""
+
+    def __init__(self, pool: PagePool, page_table, max_tokens: int, max_q: int):
+        _check(page_table, "page_table", torch.int32, 2)
+        dev = self.device = pool.device
+        _on(page_table.device, dev, "page_table")
+        B, cols = page_table.shape
+        self.pool, self.page_table, self.max_tokens = pool, page_table, int(max_tokens)
+        self.q_start = torch.zeros(B + 1, dtype=torch.int32, device=dev)
+        self.kv_len = torch.zeros(B, dtype=torch.int32, device=dev)
+        self.slots = torch.full((self.max_tokens,), -1, dtype=torch.int32, device=dev)
+        self.positions = torch.zeros(self.max_tokens, dtype=torch.int32, device=dev)
+        self.batch = PagedBatch(self.q_start, self.kv_len, page_table, max_q)
+        self._c = _KVTables(page_table.data_ptr(), self.q_start.data_ptr(), self.kv_len.data_ptr(),
+                            self.slots.data_ptr(), self.positions.data_ptr(), B, cols)
+        self._ref = C.byref(self._c)
+
+    def _lengths(self, t, name):
+        _check(t, name, torch.int32, 1)
+        if t.device != self.device or t.numel() != self._c.batch:
+            raise ValueError(f"{name} must be [{self._c.batch}] on {self.device}")
+        return t.data_ptr()
+
+    def reserve(self, lengths, new_tokens) -> PagedBatch:
+        """Room for new_tokens int32 [B] behind lengths int32 [B] cached tokens: pages
+        from the pool into page_table, starts, lengths, slots and positions of the new
+        tokens (qlin_kv_reserve). pool.count[1] tells what the pool lacked."""
+        dev = self.device
+        if dev.index != torch.cuda.current_device():
+            with torch.cuda.device(dev):
+                return self.reserve(lengths, new_tokens)
+        _enqueue(dev, _lib.qlin_kv_reserve, self.pool._ref, self._ref, self.max_tokens,
+                 self._lengths(lengths, "lengths"), self._lengths(new_tokens, "new_tokens"))
+        return self.batch
+
+    def release(self, lengths) -> None:
+        """Pages behind each request's first lengths int32 [B] tokens, up to its kv_len,
+        back to the pool (qlin_kv_release)."""
+        dev = self.device
+        if dev.index != torch.cuda.current_device():
+            with torch.cuda.device(dev):
+                return self.release(lengths)
+        _enqueue(dev, _lib.qlin_kv_release, self.pool._ref, self._ref, self._lengths(lengths, "lengths"))
 
 
 class Tree:
@@ -914,6 +1018,31 @@ def kv_append(cache: PagedKV, batch: PagedBatch, k, v, rope: Rope | None = None,
         _enqueue(dev, _lib.qlin_kv_append_norm, cache._ref, batch._ref, T, k.data_ptr(), ldk, v.data_ptr(), ldv,
                  norm._ref, *args)
     return q_out
+
+
+def kv_keep(layers: PagedLayers | PagedKV, batch: PagedBatch, path, kept, lengths=None):
+    """After a step of drafted tokens: each sequence's accepted ones, path int32 [B, W]
+    (numbers among its new tokens, ascending) of which the first kept int32 [B], become
+    its first new tokens in every layer's cache. Returns the cached tokens that are left,
+    int32 [B] (or writes them to `lengths`): what the next step starts from."""
+    if isinstance(layers, PagedKV):
+        layers = PagedLayers((layers,))
+    dev, B = layers.device, batch.batch
+    _on(batch.device, dev, "batch")
+    if dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return kv_keep(layers, batch, path, kept, lengths)
+    _check(path, "path", torch.int32, 2)
+    _check(kept, "kept", torch.int32, 1)
+    if lengths is None:
+        lengths = torch.empty_like(kept)
+    _check(lengths, "lengths", torch.int32, 1)
+    for name, t in (("path", path), ("kept", kept), ("lengths", lengths)):
+        if t.device != dev or t.shape[0] != B:
+            raise ValueError(f"{name} must have {B} rows on {dev}")
+    _enqueue(dev, _lib.qlin_kv_keep, layers._c, len(layers.caches), batch._ref, path.data_ptr(), path.shape[1],
+             kept.data_ptr(), lengths.data_ptr())
+    return lengths
 
 
 def attn_paged(cache: PagedKV, batch: PagedBatch, q, scale=None, causal=True, window=0, out=None,

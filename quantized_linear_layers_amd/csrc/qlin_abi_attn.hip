@@ -275,6 +275,69 @@ int qlin_tree_plan(const qlin_kv_batch* batch, int64_t T, const int32_t* parents
   return launch_tree_plan(*batch, T, parents, words, mask, positions, as_stream(stream));
 }
 
+static int tables_args(const qlin_kv_pool* p, const qlin_kv_tables* t) {
+  QLIN_CHECK(p && t, QLIN_ERR_ARG);
+  QLIN_CHECK(p->page_size >= 16 && p->page_size <= 256 && (p->page_size & (p->page_size - 1)) == 0 && p->pages >= 1 &&
+                 p->pages <= 0x7FFFFFFF / p->page_size && t->batch >= 0 && t->batch <= 0xFFFF && t->table_cols >= 1 &&
+                 t->table_cols <= (0x7FFFFFFF - 65536) / p->page_size,
+             QLIN_ERR_SHAPE);
+  if (t->batch == 0) return QLIN_OK;
+  QLIN_CHECK(p->free_pages && p->count && t->page_table && t->kv_len, QLIN_ERR_ARG);
+  QLIN_CHECK((((uintptr_t)p->free_pages | (uintptr_t)p->count | (uintptr_t)t->page_table | (uintptr_t)t->kv_len |
+               (uintptr_t)t->q_start | (uintptr_t)t->slots | (uintptr_t)t->positions) & 3) == 0,
+             QLIN_ERR_ALIGN);
+  return QLIN_OK;
+}
+
+int qlin_kv_reserve(const qlin_kv_pool* pool, const qlin_kv_tables* tables, int64_t T, const int32_t* lengths,
+                    const int32_t* new_tokens, qlin_stream_t stream) {
+  int rc = tables_args(pool, tables);
+  if (rc) return rc;
+  QLIN_CHECK(T >= 0 && T <= 0x7FFFFFFF, QLIN_ERR_SHAPE);
+  if (tables->batch == 0) return QLIN_OK;
+  QLIN_CHECK(tables->q_start && lengths && new_tokens, QLIN_ERR_ARG);
+  QLIN_CHECK((((uintptr_t)lengths | (uintptr_t)new_tokens) & 3) == 0, QLIN_ERR_ALIGN);
+  rc = device_ok();
+  if (rc) return rc;
+  return launch_reserve(*pool, *tables, lengths, new_tokens, T, as_stream(stream));
+}
+
+int qlin_kv_release(const qlin_kv_pool* pool, const qlin_kv_tables* tables, const int32_t* lengths,
+                    qlin_stream_t stream) {
+  int rc = tables_args(pool, tables);
+  if (rc) return rc;
+  if (tables->batch == 0) return QLIN_OK;
+  QLIN_CHECK(lengths, QLIN_ERR_ARG);
+  QLIN_CHECK(((uintptr_t)lengths & 3) == 0, QLIN_ERR_ALIGN);
+  rc = device_ok();
+  if (rc) return rc;
+  return launch_release(*pool, *tables, lengths, as_stream(stream));
+}
+
+int qlin_kv_keep(const qlin_kv_cache* caches, int64_t n_caches, const qlin_kv_batch* batch, const int32_t* path,
+                 int64_t path_cols, const int32_t* kept, int32_t* lengths, qlin_stream_t stream) {
+  QLIN_CHECK(caches && batch, QLIN_ERR_ARG);
+  QLIN_CHECK(n_caches >= 1 && n_caches <= 65535 && path_cols >= 0 && path_cols <= 0x7FFFFFFF, QLIN_ERR_SHAPE);
+  const bool empty = batch->batch == 0;
+  for (int64_t i = 0; i < n_caches; ++i) {
+    const qlin_kv_cache& c = caches[i];
+    // (the batch's max_q is not used; a sequence may have any number of new tokens)
+    qlin_kv_batch b = *batch;
+    b.max_q = 1;
+    const int rc = kv_args(&c, &b, 1);
+    if (rc) return rc;
+    QLIN_CHECK(c.pages == caches->pages && c.kv_heads == caches->kv_heads && c.page_size == caches->page_size &&
+                   c.head_dim == caches->head_dim && c.fmt == caches->fmt,
+               QLIN_ERR_SHAPE);
+  }
+  if (empty) return QLIN_OK;
+  QLIN_CHECK((path || path_cols == 0) && kept && lengths && lengths != batch->kv_len, QLIN_ERR_ARG);
+  QLIN_CHECK((((uintptr_t)path | (uintptr_t)kept | (uintptr_t)lengths) & 3) == 0, QLIN_ERR_ALIGN);
+  const int rc = device_ok();
+  if (rc) return rc;
+  return launch_keep(caches, n_caches, *batch, path, path_cols, kept, lengths, as_stream(stream));
+}
+
 int qlin_attn_plan(const qlin_kv_cache* cache, const qlin_kv_batch* batch, int64_t T, int64_t q_heads,
                    int64_t window, int64_t plan[3]) {
   QLIN_CHECK(cache && batch && plan && window >= 0, QLIN_ERR_ARG);

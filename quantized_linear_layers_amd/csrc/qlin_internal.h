@@ -122,5 +122,11 @@ void attn_plan(const qlin_kv_cache& cache, const qlin_kv_batch& batch, int64_t T
 // ---- a step's tables (qlin_tables.hip)
 int launch_tree_plan(const qlin_kv_batch& batch, int64_t T, const int32_t* parents, int64_t words,
                      uint64_t* mask, int32_t* positions, hipStream_t st);
+int launch_reserve(const qlin_kv_pool& pool, const qlin_kv_tables& t, const int32_t* lengths,
+                   const int32_t* new_tokens, int64_t T, hipStream_t st);
+// (accepted tokens: qlin_keep.hip)
+int launch_keep(const qlin_kv_cache* caches, int64_t n, const qlin_kv_batch& batch, const int32_t* path,
+                int64_t width, const int32_t* kept, int32_t* lengths, hipStream_t st);
+int launch_release(const qlin_kv_pool& pool, const qlin_kv_tables& t, const int32_t* lengths, hipStream_t st);
 
 }  // namespace qlin
