@@ -17,8 +17,7 @@ namespace qlin {
 namespace {
 
 constexpr int kKeepThreads = 256;
-constexpr int kKeepChunks = 8;    // 16-byte chunks of a thread, in flight together
-constexpr int kKeepScales = 2;    // and scales (a row has 4 chunks at least)
+constexpr int kKeepRows = 8;      // rows that a thread has a chunk of, in flight together
 constexpr int kKeepCaches = 32;   // caches of a launch (their addresses are kernel arguments)
 
 struct KeepArgs {
@@ -29,73 +28,64 @@ struct KeepArgs {
   int64_t cols, pages, heads;
   int width;        // of the path
   int page_shift, row_shift;  // tokens of a page; chunks of a row
-  int wg_heads, wg_tokens;    // heads of a workgroup, tokens of a pass
+  int wg_heads, step;         // heads of a workgroup; tokens that its threads cover at once
 };
 
 __global__ __launch_bounds__(kKeepThreads) void keep_kernel(const KeepArgs a) {
-  const int b = blockIdx.x;
+  __shared__ int64_t from[kKeepThreads], to[kKeepThreads];  // a token's row of head 0; from -1: it stays
+  const int b = blockIdx.x, tid = threadIdx.x;
+  // (the path's first numbers are on their way while it is not yet known how many count)
+  int32_t u = tid < a.width ? a.path[(int64_t)b * a.width + tid] : -1;
   const int64_t n = (int64_t)a.q_start[b + 1] - a.q_start[b], len = max(a.kv_len[b], 0);
   const int64_t first = len - max(n, (int64_t)0);
   const int count = (int)max(min(min((int64_t)a.kept[b], n), (int64_t)a.width), (int64_t)0);
-  if (blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x == 0) a.lengths[b] = (int32_t)max(first + count, (int64_t)0);
+  if (blockIdx.y == 0 && blockIdx.z == 0 && tid == 0) a.lengths[b] = (int32_t)max(first + count, (int64_t)0);
   const int64_t h0 = (int64_t)blockIdx.z * a.wg_heads;
-  const int heads = (int)min((int64_t)a.wg_heads, a.heads - h0);
   uint8_t* pool = a.pool[blockIdx.y];
   float* scale = a.scale[blockIdx.y];
-  // the row of a head and token in the pool, -1: none
-  auto row_of = [&](int64_t token, int h) -> int64_t {
-    const int64_t at = first + token, col = at >> a.page_shift;
+  // this thread's chunk of a head, and which of the tokens that are covered at once
+  const int c = tid & ((1 << a.row_shift) - 1), per = a.wg_heads << a.row_shift;
+  const int token = tid / per;
+  const int64_t h = (tid - token * per) >> a.row_shift;
+  const bool busy = token < a.step && h0 + h < a.heads;
+  auto row_of = [&](int64_t x) -> int64_t {
+    const int64_t at = first + x, col = at >> a.page_shift;
     if (at < 0 || col >= a.cols) return -1;
     const int64_t page = a.table[b * a.cols + col];
     if (page < 0 || page >= a.pages) return -1;
-    return ((page * a.heads + h0 + h) << a.page_shift) + (at & ((1 << a.page_shift) - 1));
+    return ((page * a.heads + h0) << a.page_shift) + (at & ((1 << a.page_shift) - 1));
   };
-  // item (i, h) of a pass: where its row comes from and goes (from -1: it stays)
-  auto move_of = [&](int i, int h, int64_t& from, int64_t& to) {
-    from = to = -1;
-    if (i >= count) return;
-    const int32_t u = a.path[(int64_t)b * a.width + i];
-    if (u < 0 || u >= n || u == i) return;
-    to = row_of(i, h);
-    if (to >= 0) from = row_of(u, h);
-  };
-  for (int i0 = 0; i0 < count; i0 += a.wg_tokens) {
-    const int items = min(a.wg_tokens, count - i0) * heads;  // (token, head), heads fastest
-    uint4 x[kKeepChunks];
-    int64_t dst[kKeepChunks];
-#pragma unroll
-    for (int k = 0; k < kKeepChunks; ++k) {
-      const int e = k * kKeepThreads + threadIdx.x, item = e >> a.row_shift;
-      const int c = e & ((1 << a.row_shift) - 1);
-      int64_t from = -1;
-      dst[k] = -1;
-      if (item < items) move_of(i0 + item / heads, item % heads, from, dst[k]);
-      if (from < 0)
-        dst[k] = -1;
-      else
-        x[k] = ldg16(pool + (((from << a.row_shift) + c) << 4));
-      if (dst[k] >= 0) dst[k] = (((dst[k] << a.row_shift) + c) << 4);
+  const int pass = kKeepRows * a.step;  // (at most 256 tokens: a chunk is a row's fourth at least)
+  for (int i0 = 0; i0 < count; i0 += pass) {
+    const int here = min(pass, count - i0);
+    if (i0) u = tid < here ? a.path[(int64_t)b * a.width + i0 + tid] : -1;
+    if (tid < here) {
+      const bool moves = u >= 0 && u < n && u != i0 + tid;
+      const int64_t x = moves ? row_of(u) : -1, y = moves ? row_of(i0 + tid) : -1;
+      from[tid] = y < 0 ? -1 : x;
+      to[tid] = y;
     }
-    float s[kKeepScales];
-    int64_t sdst[kKeepScales];
+    __syncthreads();
+    uint4 x[kKeepRows];
+    float s[kKeepRows];
+    int64_t dst[kKeepRows];
 #pragma unroll
-    for (int k = 0; k < kKeepScales; ++k) {
-      const int item = k * kKeepThreads + threadIdx.x;
-      int64_t from = -1;
-      sdst[k] = -1;
-      if (scale && item < items) move_of(i0 + item / heads, item % heads, from, sdst[k]);
-      if (from < 0)
-        sdst[k] = -1;
-      else
-        s[k] = scale[from];
+    for (int k = 0; k < kKeepRows; ++k) {
+      const int i = k * a.step + token;
+      dst[k] = -1;
+      if (!busy || i >= here || from[i] < 0) continue;
+      const int64_t src = from[i] + (h << a.page_shift);
+      dst[k] = to[i] + (h << a.page_shift);
+      x[k] = ldg16(pool + (((src << a.row_shift) + c) << 4));
+      if (scale && c == 0) s[k] = scale[src];
     }
     __syncthreads();  // every row of the pass has been read
 #pragma unroll
-    for (int k = 0; k < kKeepChunks; ++k)
-      if (dst[k] >= 0) *reinterpret_cast<uint4*>(pool + dst[k]) = x[k];
-#pragma unroll
-    for (int k = 0; k < kKeepScales; ++k)
-      if (sdst[k] >= 0) scale[sdst[k]] = s[k];
+    for (int k = 0; k < kKeepRows; ++k) {
+      if (dst[k] < 0) continue;
+      *reinterpret_cast<uint4*>(pool + (((dst[k] << a.row_shift) + c) << 4)) = x[k];
+      if (scale && c == 0) scale[dst[k]] = s[k];
+    }
     __syncthreads();  // and written, before the next pass reads
   }
 }
@@ -119,10 +109,11 @@ int launch_keep(const qlin_kv_cache* caches, int64_t n, const qlin_kv_batch& bat
   a.width = (int)width;
   a.page_shift = __builtin_ctzll((unsigned long long)c.page_size);
   a.row_shift = __builtin_ctzll((unsigned long long)c.head_dim) - (f8 ? 4 : 3);
-  // a pass holds 2048 chunks: of at most 512 / (a row's chunks) heads four tokens or more
+  // all heads if their chunks are no more than the threads, and as many tokens beside
   const int64_t chunks = (int64_t)1 << a.row_shift;
-  a.wg_heads = (int)(c.kv_heads < 512 / chunks ? c.kv_heads : 512 / chunks);
-  a.wg_tokens = (int)(kKeepChunks * kKeepThreads / (a.wg_heads * chunks));
+  a.wg_heads = (int)(c.kv_heads < kKeepThreads / chunks ? c.kv_heads : kKeepThreads / chunks);
+  a.step = (int)(kKeepThreads / (a.wg_heads * chunks));
+  a.step = a.step < kKeepThreads / kKeepRows ? a.step : kKeepThreads / kKeepRows;
   const unsigned z = (unsigned)((c.kv_heads + a.wg_heads - 1) / a.wg_heads);
   for (int64_t at = 0; at < n; at += kKeepCaches) {
     const int here = (int)(n - at < kKeepCaches ? n - at : kKeepCaches);
