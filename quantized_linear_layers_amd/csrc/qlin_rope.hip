@@ -51,7 +51,7 @@ struct RopeArgs {
   // head norms: weights of queries, keys and values (NULL: 1), parts that are
   // normalised (bit 0 queries, 1 keys, 2 values)
   const uint16_t* w[3];
-  float eps, offset;
+  float eps, offset, inv_d;
   int normed;
 };
 
@@ -87,7 +87,8 @@ __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
 // is not zero the remainders are multiples of 2^-57 sc, exact for every sc from 2^-92 on.
 // Scales outside 2^-80 .. 2^90, the range that was compared with division (equal
 // quotients and signs in 8e9 random pairs), are divided.
-__device__ __forceinline__ void divide(Piece& p, float sc) {
+// (true: by the reciprocal)
+__device__ __forceinline__ bool divide(Piece& p, float sc) {
   if (sc >= 0x1p-80f && sc <= 0x1p+90f) {
     const float y = 1.0f / sc;
 #pragma unroll
@@ -97,30 +98,80 @@ __device__ __forceinline__ void divide(Piece& p, float sc) {
       q = p.hi[i] * y;
       p.hi[i] = fmaf(-fmaf(q, sc, -p.hi[i]), y, q);
     }
-    return;
+    return true;
   }
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     p.lo[i] = p.lo[i] / sc;
     p.hi[i] = p.hi[i] / sc;
   }
+  return false;
 }
 
-// The sum of x over the n lanes (a power of two, aligned) that share a head, in each.
-// Lanes trade within a row of 16 by DPP: after each step the lanes that a mirror
-// trades between hold one value already.
-template <int CTRL>
-__device__ __forceinline__ float dpp_add(float x) {
-  return x + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), CTRL, 0xF, 0xF, false));
+// Eight E4M3 codes of values up to a row's largest over its scale: a quotient exceeds 448
+// by less than its rounding to a code forgives, so nothing is clamped. (Of scales below
+// fp32's normal range it may exceed it by more: those rows are clamped, by encode8.)
+__device__ __forceinline__ uint2 codes8(const float (&v)[8]) {
+  int w[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    w[h] = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * h], v[4 * h + 1], 0, false);
+    w[h] = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * h + 2], v[4 * h + 3], w[h], true);
+  }
+  return make_uint2((uint32_t)w[0], (uint32_t)w[1]);
 }
-__device__ __forceinline__ float head_sum(float x, int n) {
-  if (n >= 2) x = dpp_add<0xB1>(x);    // quad_perm 1 0 3 2
-  if (n >= 4) x = dpp_add<0x4E>(x);    // quad_perm 2 3 0 1
-  if (n >= 8) x = dpp_add<0x141>(x);   // the two quads of eight lanes
-  if (n >= 16) x = dpp_add<0x140>(x);  // the two eights of a row
-  if (n >= 32) x += __shfl_xor(x, 16, kWave);
-  if (n >= 64) x += __shfl_xor(x, 32, kWave);
+
+// The sum (MAX: the largest) of x over the n lanes (a power of two, aligned) that share a
+// head, in each. Lanes trade within a row of 16 by DPP: after each step the lanes that a
+// mirror trades between hold one value already.
+template <bool MAX, int CTRL>
+__device__ __forceinline__ float dpp_join(float x) {
+  const float y = __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), CTRL, 0xF, 0xF, false));
+  return MAX ? fmaxf(x, y) : x + y;
+}
+template <bool MAX>
+__device__ __forceinline__ float head_join(float x, int n) {
+  if (n >= 2) x = dpp_join<MAX, 0xB1>(x);    // quad_perm 1 0 3 2
+  if (n >= 4) x = dpp_join<MAX, 0x4E>(x);    // quad_perm 2 3 0 1
+  if (n >= 8) x = dpp_join<MAX, 0x141>(x);   // the two quads of eight lanes
+  if (n >= 16) x = dpp_join<MAX, 0x140>(x);  // the two eights of a row
+  if (n >= 32) {
+    const float y = __shfl_xor(x, 16, kWave);
+    x = MAX ? fmaxf(x, y) : x + y;
+  }
+  if (n >= 64) {
+    const float y = __shfl_xor(x, 32, kWave);
+    x = MAX ? fmaxf(x, y) : x + y;
+  }
   return x;
+}
+
+// The largest of m, |x| and |y| (numbers), in one instruction: fmaxf's would be told apart
+// from signalling NaNs first.
+__device__ __forceinline__ float max3_abs(float m, float x, float y) {
+  float r;
+  asm("v_max3_f32 %0, %1, |%2|, |%3|" : "=v"(r) : "v"(m), "v"(x), "v"(y));
+  return r;
+}
+
+// Sine and cosine of r turns, |r| <= 1/2: of the nearest quarter turn's remainder t, which
+// is exact, by their series in (2 pi t)^2 up to the powers 9 and 8 (at an eighth of a turn
+// the next terms are 2^-29 and 2^-25.3), then by the quarter.
+__device__ __forceinline__ void turn(float r, float& s, float& c) {
+  const float k = __builtin_rintf(4.0f * r), t = fmaf(-0.25f, k, r), u = t * t;
+  // (2 pi)^n / n!
+  float sine = fmaf(u, 42.0586939f, -76.7058597f);
+  sine = fmaf(u, sine, 81.6052493f);
+  sine = fmaf(u, sine, -41.3417022f);
+  sine = fmaf(u, sine, 6.28318531f) * t;
+  float cosine = fmaf(u, 60.2446413f, -85.4568172f);
+  cosine = fmaf(u, cosine, 64.9393940f);
+  cosine = fmaf(u, cosine, -19.7392088f);
+  cosine = fmaf(u, cosine, 1.0f);
+  const int q = (int)k;
+  const float x = q & 1 ? cosine : sine, y = q & 1 ? sine : cosine;
+  s = __uint_as_float(__float_as_uint(x) ^ ((uint32_t)q << 30 & 0x80000000u));
+  c = __uint_as_float(__float_as_uint(y) ^ ((uint32_t)(q + 1) << 30 & 0x80000000u));
 }
 
 // A head's piece over the head's root mean square: p / sqrt(sum of squares / D + eps),
@@ -131,7 +182,7 @@ __device__ __forceinline__ void normalise(Piece& p, int n, float inv_d, float ep
     float s = 0.0f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) s = fmaf(p.hi[i], p.hi[i], fmaf(p.lo[i], p.lo[i], s));
-    return head_sum(s, n);
+    return head_join<false>(s, n);
   };
   auto times = [&](float f) {
 #pragma unroll
@@ -150,21 +201,53 @@ __device__ __forceinline__ void normalise(Piece& p, int n, float inv_d, float ep
 }
 
 // APPEND: keys and values go to the cache; FP8: as E4M3 codes with a scale. NORM:
-// heads are normalised first.
-template <bool APPEND, bool FP8, bool NORM>
-__global__ __launch_bounds__(kRopeThreads) void rope_kernel(const RopeArgs a) {
-  const int per_head = a.D / 16;
+// heads are normalised first. PH: pieces of a head, for those sizes that every cache has,
+// 0: any number of them. With NORM five waves a SIMD, so that the calls which fill the
+// device once do it with room: 2250 tokens of 16 + 8 heads of 256 into E4M3, normalised,
+// are 4500 waves and take 15.9 us, 18.2 with four waves a SIMD (and no register spilled;
+// five spill five, outside the loop over heads).
+template <int PH, bool APPEND, bool FP8, bool NORM>
+__global__ __launch_bounds__(kRopeThreads, NORM ? 5 : 1) void rope_kernel(const RopeArgs a) {
+  const int D = PH ? 16 * PH : a.D, per_head = D / 16;
   const int c = threadIdx.x % per_head;       // this thread's piece of a head
   const int g = threadIdx.x / per_head;
   const int slot = g % a.slots;
   const int64_t t0 = (int64_t)blockIdx.x * a.toks;
   const int64_t t = t0 + g / a.slots;
+  const bool live = g / a.slots < a.toks && t < a.T;
+
+  // What needs no other load is on its way before the token's place is looked up: the
+  // first head and the position.
+  const bool turning = c < a.rot16;
+  // Offsets of the piece's two 16-byte runs in a head. Half layout: values
+  // 8c.. and rot/2 + 8c..; else 16 values in a row.
+  const bool halves = turning && !a.interleaved;
+  const int o0 = halves ? 8 * c : 16 * c;
+  const int o1 = halves ? 8 * c + 8 * a.rot16 : 16 * c + 8;
+  const int h_all = a.heads[0] + a.heads[1] + a.heads[2];
+  auto part_of = [&](int h) { return !APPEND || h < a.heads[0] ? 0 : h < a.heads[0] + a.heads[1] ? 1 : 2; };
+  auto head_of = [&](int h, int part) {
+    return h - (part > 0 ? a.heads[0] : 0) - (part > 1 ? a.heads[1] : 0);
+  };
+  uint4 n0 = make_uint4(0, 0, 0, 0), n1 = n0;
+  auto next = [&](int h) {  // the head after this one is read before this one is worked on
+    if (h >= h_all) return;
+    const int part = part_of(h);
+    const uint16_t* src = a.x[part] + t * a.ld[part] + head_of(h, part) * D;
+    n0 = ldg16(src + o0);
+    n1 = ldg16(src + o1);
+  };
+  const int step = gridDim.y * a.slots;
+  int h = blockIdx.y * a.slots + slot;
+  if (live) next(h);
+  int32_t given = 0;
+  if (live && turning && a.positions) given = a.positions[t];
   // every lane takes part in the sequence search before any leaves
   int64_t b = APPEND ? sequence_of(a.q_start, a.B, t0) : 0;
-  if (g / a.slots >= a.toks || t >= a.T) return;
+  if (!live) return;
 
   int64_t index = 0;      // the token's place in its sequence
-  int64_t page = -1;      // its page; -1: not stored
+  int32_t page = -1;      // its page; -1: not stored
   if (APPEND) {
     while (b < a.B && (int64_t)a.q_start[b + 1] <= t) ++b;
     if (b >= a.B || t < (int64_t)a.q_start[b]) return;  // padding: left as it is
@@ -179,54 +262,33 @@ __global__ __launch_bounds__(kRopeThreads) void rope_kernel(const RopeArgs a) {
 
   // Angles. pos * turns is exact to 2^-53 of its value in fp64, so its part of a
   // turn is right to 2^-22 up to the whole int32 range; sine and cosine are fp32.
-  const bool turning = c < a.rot16;
   float cs[8], sn[8];
   if (turning) {
-    const double pos = (double)(a.positions ? (int64_t)a.positions[t] : index);
+    const double pos = (double)(a.positions ? (int64_t)given : index);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const double w = pos * a.turns[8 * c + i];
       const float r = (float)(w - __builtin_rint(w));
       float s, co;
-      sincospif(2.0f * r, &s, &co);
+      if (NORM)
+        turn(r, s, co);
+      else
+        sincospif(2.0f * r, &s, &co);
       cs[i] = co * a.magnitude;
       sn[i] = s * a.magnitude * a.sign;
+      if (NORM && i % 2) __builtin_amdgcn_sched_barrier(0);  // (two at a time: registers)
     }
   }
-  // Offsets of the piece's two 16-byte runs in a head. Half layout: values
-  // 8c.. and rot/2 + 8c..; else 16 values in a row.
-  const bool halves = turning && !a.interleaved;
-  const int o0 = halves ? 8 * c : 16 * c;
-  const int o1 = halves ? 8 * c + 8 * a.rot16 : 16 * c + 8;
-
-  const int h_all = a.heads[0] + a.heads[1] + a.heads[2];
-  auto part_of = [&](int h) { return !APPEND || h < a.heads[0] ? 0 : h < a.heads[0] + a.heads[1] ? 1 : 2; };
-  auto head_of = [&](int h, int part) {
-    return h - (part > 0 ? a.heads[0] : 0) - (part > 1 ? a.heads[1] : 0);
-  };
-  uint4 n0 = make_uint4(0, 0, 0, 0), n1 = n0, w0 = n0, w1 = n0;
-  auto next = [&](int h) {  // the head after this one is read before this one is worked on
-    if (h >= h_all) return;
-    const int part = part_of(h);
-    const uint16_t* src = a.x[part] + t * a.ld[part] + (int64_t)head_of(h, part) * a.D;
-    n0 = ldg16(src + o0);
-    n1 = ldg16(src + o1);
-    if (NORM) {
-      const uint16_t* w = part == 0 ? a.w[0] : part == 1 ? a.w[1] : a.w[2];
-      w0 = w1 = make_uint4(0, 0, 0, 0);
-      if (w) {
-        w0 = ldg16(w + o0);
-        w1 = ldg16(w + o1);
-      }
-    }
-  };
-  const int step = gridDim.y * a.slots;
-  int h = blockIdx.y * a.slots + slot;
-  next(h);
   for (; h < h_all; h += step) {
     const int part = part_of(h), hh = head_of(h, part);
     uint4 r0 = n0, r1 = n1;
-    const uint4 g0 = w0, g1 = w1;
+    // (this head's weights, which all heads of a part share, arrive while it is summed)
+    uint4 w0 = make_uint4(0, 0, 0, 0), w1 = w0;
+    const uint16_t* weight = !NORM ? nullptr : part == 0 ? a.w[0] : part == 1 ? a.w[1] : a.w[2];
+    if (NORM && weight) {
+      w0 = ldg16(weight + o0);
+      w1 = ldg16(weight + o1);
+    }
     next(h + step);
     if (part > 0 && page < 0) continue;
     Piece p;
@@ -234,12 +296,12 @@ __global__ __launch_bounds__(kRopeThreads) void rope_kernel(const RopeArgs a) {
     unpack_bf16x8(r1, p.hi);
     const bool normed = NORM && ((a.normed >> part) & 1);
     if (normed) {
-      normalise(p, per_head, 1.0f / (float)a.D, a.eps);
-      // (fp32 from here to the one rounding at the end, the weights exact)
-      const float offset = (part == 0 ? a.w[0] : part == 1 ? a.w[1] : a.w[2]) ? a.offset : 1.0f;
+      normalise(p, per_head, a.inv_d, a.eps);
+      // times (offset + weight), in fp32 as all up to the one rounding at the end
+      const float offset = weight ? a.offset : 1.0f;
       Piece w;
-      unpack_bf16x8(g0, w.lo);
-      unpack_bf16x8(g1, w.hi);
+      unpack_bf16x8(w0, w.lo);
+      unpack_bf16x8(w1, w.hi);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         p.lo[i] *= w.lo[i] + offset;
@@ -272,16 +334,16 @@ __global__ __launch_bounds__(kRopeThreads) void rope_kernel(const RopeArgs a) {
       r1 = pack8(p.hi);
     }
     if (part == 0) {
-      uint16_t* dst = a.y + t * a.ldy + (int64_t)hh * a.D;
+      uint16_t* dst = a.y + t * a.ldy + hh * D;
       *reinterpret_cast<uint4*>(dst + o0) = r0;
       *reinterpret_cast<uint4*>(dst + o1) = r1;
       continue;
     }
     const int in_page = (int)(index & ((1 << a.page_shift) - 1));
-    const int64_t row = ((page * a.page_heads + hh) << a.page_shift) + in_page;
+    const int64_t row = (((int64_t)page * a.page_heads + hh) << a.page_shift) + in_page;
     uint8_t* pool = part == 1 ? a.kc : a.vc;
     if (!FP8) {
-      uint16_t* dst = reinterpret_cast<uint16_t*>(pool) + row * a.D;
+      uint16_t* dst = reinterpret_cast<uint16_t*>(pool) + row * D;
       *reinterpret_cast<uint4*>(dst + o0) = r0;
       *reinterpret_cast<uint4*>(dst + o1) = r1;
       continue;
@@ -289,16 +351,20 @@ __global__ __launch_bounds__(kRopeThreads) void rope_kernel(const RopeArgs a) {
     // the row's threads (4, 8 or 16 neighbours of one wave) share its absmax
     float m = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = fmaxf(m, fmaxf(fabsf(p.lo[i]), fabsf(p.hi[i])));
-    for (int o = per_head / 2; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor(m, o, kWave));
+    for (int i = 0; i < 8; ++i) m = max3_abs(m, p.lo[i], p.hi[i]);
+    m = head_join<true>(m, per_head);
     const float sc = m > 0.0f ? m / 448.0f : 0.0f;
     uint2 q0 = make_uint2(0, 0), q1 = make_uint2(0, 0);
     if (sc > 0.0f) {
-      divide(p, sc);
-      q0 = encode8<QLIN_E4M3>(p.lo);
-      q1 = encode8<QLIN_E4M3>(p.hi);
+      if (divide(p, sc)) {
+        q0 = codes8(p.lo);
+        q1 = codes8(p.hi);
+      } else {
+        q0 = encode8<QLIN_E4M3>(p.lo);
+        q1 = encode8<QLIN_E4M3>(p.hi);
+      }
     }
-    uint8_t* dst = pool + row * a.D;
+    uint8_t* dst = pool + row * D;
     *reinterpret_cast<uint2*>(dst + o0) = q0;
     *reinterpret_cast<uint2*>(dst + o1) = q1;
     if (c == 0) (part == 1 ? a.ks : a.vs)[row] = sc;
@@ -317,6 +383,9 @@ void rope_shape(RopeArgs& a, dim3& grid) {
   const int64_t blocks = a.T * h_all / groups;  // with one head a thread
   const int fold = blocks > 8192 ? 8 : blocks > 1024 ? 4 : 1;
   int slots = (h_all + fold - 1) / fold;
+  // (24 heads in groups of 6 would leave a fourth of the threads without a head)
+  if (groups / slots * slots < groups * 7 / 8)
+    while (slots & (slots - 1)) ++slots;
   slots = slots < groups ? slots : groups;
   a.slots = slots;
   a.toks = groups / slots;
@@ -338,12 +407,27 @@ bool rope_grid_ok(int64_t T, int64_t heads, int64_t D) {
   return (int64_t)grid.x * kRopeThreads <= 0xFFFFFFFF && grid.y <= 0xFFFF;
 }
 
+template <bool APPEND, bool FP8, bool NORM>
+static void launch_sizes(RopeArgs& a, hipStream_t st) {
+  dim3 grid;
+  rope_shape(a, grid);
+  if (a.D == 64)
+    rope_kernel<4, APPEND, FP8, NORM><<<grid, kRopeThreads, 0, st>>>(a);
+  else if (a.D == 128)
+    rope_kernel<8, APPEND, FP8, NORM><<<grid, kRopeThreads, 0, st>>>(a);
+  else if (a.D == 256)
+    rope_kernel<16, APPEND, FP8, NORM><<<grid, kRopeThreads, 0, st>>>(a);
+  else if constexpr (!APPEND)  // (caches have these three)
+    rope_kernel<0, APPEND, FP8, NORM><<<grid, kRopeThreads, 0, st>>>(a);
+}
+
 static void norm_args(RopeArgs& a, const qlin_head_norm& n) {
   a.w[0] = n.q_weight;
   a.w[1] = n.k_weight;
   a.w[2] = n.v_weight;
   a.eps = n.eps;
   a.offset = n.offset;
+  a.inv_d = 1.0f / (float)a.D;
   a.normed = n.values ? 7 : 3;
 }
 static void rope_args(RopeArgs& a, const qlin_rope_plan* rope) {
@@ -369,13 +453,11 @@ int launch_rope(const uint16_t* x, int64_t ldx, int64_t T, int64_t H, int64_t D,
   rope_args(a, rope);
   if (inverse) a.sign = -1.0f;
   a.positions = positions;
-  dim3 grid;
-  rope_shape(a, grid);
   if (norm) {
     norm_args(a, *norm);
-    rope_kernel<false, false, true><<<grid, kRopeThreads, 0, st>>>(a);
+    launch_sizes<false, false, true>(a, st);
   } else {
-    rope_kernel<false, false, false><<<grid, kRopeThreads, 0, st>>>(a);
+    launch_sizes<false, false, false>(a, st);
   }
   return launch_status();
 }
@@ -411,19 +493,12 @@ int launch_kv_append(const qlin_kv_cache& cache, const qlin_kv_batch& batch, int
   a.table = batch.page_table;
   a.B = batch.batch;
   a.cols = batch.table_cols;
-  dim3 grid;
-  rope_shape(a, grid);
   const bool f8 = cache.fmt == QLIN_KV_E4M3;
   if (norm) {
     norm_args(a, *norm);
-    if (f8)
-      rope_kernel<true, true, true><<<grid, kRopeThreads, 0, st>>>(a);
-    else
-      rope_kernel<true, false, true><<<grid, kRopeThreads, 0, st>>>(a);
-  } else if (f8) {
-    rope_kernel<true, true, false><<<grid, kRopeThreads, 0, st>>>(a);
+    f8 ? launch_sizes<true, true, true>(a, st) : launch_sizes<true, false, true>(a, st);
   } else {
-    rope_kernel<true, false, false><<<grid, kRopeThreads, 0, st>>>(a);
+    f8 ? launch_sizes<true, true, false>(a, st) : launch_sizes<true, false, false>(a, st);
   }
   return launch_status();
 }
