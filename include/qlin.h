@@ -603,13 +603,17 @@ int qlin_attn_paged(const qlin_kv_cache* cache, const qlin_kv_batch* batch, int6
  *             alone decides about new tokens.
  * Keys and values of the new tokens lie where qlin_kv_append puts them, in the order
  * of the rows (rotated at positions[t], which is the depth's, not the slot's). The
- * rest, workspace and plan included, as for qlin_attn_paged with causal != 0. */
+ * rest as for qlin_attn_paged with causal != 0; the workspace of
+ * qlin_attn_tree_workspace_bytes serves any window, and qlin_attn_tree_plan tells what a
+ * call chooses (below; workgroups of 16 rows too). */
 typedef struct {
   const uint64_t* mask;
   const int32_t* positions;
   int64_t words;
 } qlin_tree;
 
+size_t qlin_attn_tree_workspace_bytes(const qlin_kv_cache* cache, const qlin_kv_batch* batch, int64_t T,
+                                      int64_t q_heads);
 int qlin_attn_tree(const qlin_kv_cache* cache, const qlin_kv_batch* batch, int64_t T,
                    const qlin_bf16* q, int64_t ldq, int64_t q_heads, float scale, const qlin_tree* tree,
                    int64_t window, qlin_bf16* out, int64_t ldo, float* lse, void* ws,
@@ -648,6 +652,8 @@ int qlin_kv_keep(const qlin_kv_cache* caches, int64_t n_caches, const qlin_kv_ba
  * more than qlin_attn_workspace_bytes, which has to hold for every window. */
 int qlin_attn_plan(const qlin_kv_cache* cache, const qlin_kv_batch* batch, int64_t T, int64_t q_heads,
                    int64_t window, int64_t plan[3]);
+int qlin_attn_tree_plan(const qlin_kv_cache* cache, const qlin_kv_batch* batch, int64_t T, int64_t q_heads,
+                        int64_t window, int64_t plan[3]);
 
 #ifdef __cplusplus
 }

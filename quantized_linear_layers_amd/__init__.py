@@ -119,6 +119,8 @@ _SIGS = {
     "qlin_kv_reserve": (_INT, [C.POINTER(_KVPool), C.POINTER(_KVTables), _I64, _P, _P, _P]),
     "qlin_kv_release": (_INT, [C.POINTER(_KVPool), C.POINTER(_KVTables), _P, _P]),
     "qlin_kv_keep": (_INT, [C.POINTER(_KVCache), _I64, C.POINTER(_KVBatch), _P, _I64, _P, _P, _P]),
+    "qlin_attn_tree_workspace_bytes": (_SZ, [C.POINTER(_KVCache), C.POINTER(_KVBatch), _I64, _I64]),
+    "qlin_attn_tree_plan": (_INT, [C.POINTER(_KVCache), C.POINTER(_KVBatch), _I64, _I64, _I64, C.POINTER(_I64)]),
     "qlin_tree_plan": (_INT, [C.POINTER(_KVBatch), _I64, _P, _I64, _P, _P, _P]),
     "qlin_attn_plan": (_INT, [C.POINTER(_KVCache), C.POINTER(_KVBatch), _I64, _I64, _I64, C.POINTER(_I64)]),
 }
@@ -1074,10 +1076,11 @@ def attn_paged(cache: PagedKV, batch: PagedBatch, q, scale=None, causal=True, wi
         if not causal:
             raise ValueError("a tree's masks replace causal")
     lse = q.new_empty((T, heads), dtype=torch.float32) if return_lse else None
-    key = (T, heads, D, cache.kv_heads, cache.page_size, cache.fmt)  # what the size depends on beside the batch's own
+    key = (T, heads, D, cache.kv_heads, cache.page_size, cache.fmt, tree is None)  # what the size depends on beside the batch's own
     nb = batch._ws_bytes.get(key)
     if nb is None:
-        nb = batch._ws_bytes[key] = _lib.qlin_attn_workspace_bytes(cache._ref, batch._ref, T, heads)
+        size = _lib.qlin_attn_workspace_bytes if tree is None else _lib.qlin_attn_tree_workspace_bytes
+        nb = batch._ws_bytes[key] = size(cache._ref, batch._ref, T, heads)
     ws = _attn_workspace(nb, dev) if nb else None
     fn, mask = (_lib.qlin_attn_paged, 1 if causal else 0) if tree is None else (_lib.qlin_attn_tree, tree._ref)
     _enqueue(dev, fn, cache._ref, batch._ref, T, q.data_ptr(), ldq, heads,

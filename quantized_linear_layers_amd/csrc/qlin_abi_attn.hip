@@ -202,12 +202,19 @@ static bool attn_shape_ok(const qlin_kv_cache* c, const qlin_kv_batch* b, int64_
          b->max_q <= 0x7FFFFFFF && b->batch * c->kv_heads <= 0xFFFFFF && attn_grid_ok(*c, *b, T, q_heads);
 }
 
+static bool attn_has_work(const qlin_kv_cache* cache, const qlin_kv_batch* batch, int64_t T, int64_t q_heads) {
+  return cache && batch && kv_shape_ok(cache, batch, T) && T != 0 && batch->batch != 0 && batch->table_cols != 0 &&
+         batch->max_q != 0 && attn_shape_ok(cache, batch, T, q_heads);
+}
+
 size_t qlin_attn_workspace_bytes(const qlin_kv_cache* cache, const qlin_kv_batch* batch, int64_t T,
                                  int64_t q_heads) {
-  if (!cache || !batch || !kv_shape_ok(cache, batch, T) || T == 0 || batch->batch == 0 ||
-      batch->table_cols == 0 || batch->max_q == 0 || !attn_shape_ok(cache, batch, T, q_heads))
-    return 0;
-  return attn_workspace_bytes(*cache, *batch, T, q_heads);
+  return attn_has_work(cache, batch, T, q_heads) ? attn_workspace_bytes(*cache, *batch, T, q_heads) : 0;
+}
+
+size_t qlin_attn_tree_workspace_bytes(const qlin_kv_cache* cache, const qlin_kv_batch* batch, int64_t T,
+                                      int64_t q_heads) {
+  return attn_has_work(cache, batch, T, q_heads) ? attn_tree_workspace_bytes(*cache, *batch, T, q_heads) : 0;
 }
 
 static int attn_paged(const qlin_kv_cache* cache, const qlin_kv_batch* batch, int64_t T,
@@ -223,7 +230,8 @@ static int attn_paged(const qlin_kv_cache* cache, const qlin_kv_batch* batch, in
   if (T == 0 || batch->batch == 0) return QLIN_OK;
   QLIN_CHECK(q && out, QLIN_ERR_ARG);
   QLIN_CHECK(a16(q) && a16(out) && ldq % 8 == 0 && ldo % 8 == 0 && ((uintptr_t)lse & 3) == 0, QLIN_ERR_ALIGN);
-  const size_t need = attn_workspace_bytes(*cache, *batch, T, q_heads);
+  const size_t need = tree ? attn_tree_workspace_bytes(*cache, *batch, T, q_heads)
+                           : attn_workspace_bytes(*cache, *batch, T, q_heads);
   QLIN_CHECK(ws_bytes >= need && (need == 0 || ws), QLIN_ERR_WORKSPACE);
   QLIN_CHECK(need == 0 || ((uintptr_t)ws & 255) == 0, QLIN_ERR_ALIGN);
   rc = device_ok();
@@ -338,16 +346,27 @@ int qlin_kv_keep(const qlin_kv_cache* caches, int64_t n_caches, const qlin_kv_ba
   return launch_keep(caches, n_caches, *batch, path, path_cols, kept, lengths, as_stream(stream));
 }
 
-int qlin_attn_plan(const qlin_kv_cache* cache, const qlin_kv_batch* batch, int64_t T, int64_t q_heads,
-                   int64_t window, int64_t plan[3]) {
+static int plan_call(const qlin_kv_cache* cache, const qlin_kv_batch* batch, int64_t T, int64_t q_heads,
+                     int64_t window, bool tree, int64_t plan[3]) {
   QLIN_CHECK(cache && batch && plan && window >= 0, QLIN_ERR_ARG);
   QLIN_CHECK(cache->fmt == QLIN_KV_BF16 || cache->fmt == QLIN_KV_E4M3, QLIN_ERR_ARG);
   QLIN_CHECK(kv_shape_ok(cache, batch, T) && attn_shape_ok(cache, batch, T, q_heads), QLIN_ERR_SHAPE);
   plan[0] = plan[1] = plan[2] = 0;
   if (T == 0 || batch->batch == 0) return QLIN_OK;
   QLIN_CHECK(batch->table_cols >= 1 && batch->max_q >= 1, QLIN_ERR_SHAPE);
-  attn_plan(*cache, *batch, T, q_heads, window, plan);
+  attn_plan(*cache, *batch, T, q_heads, window, tree, plan);
   return QLIN_OK;
+}
+
+int qlin_attn_plan(const qlin_kv_cache* cache, const qlin_kv_batch* batch, int64_t T, int64_t q_heads,
+                   int64_t window, int64_t plan[3]) {
+  return plan_call(cache, batch, T, q_heads, window, false, plan);
+}
+
+int qlin_attn_tree_plan(const qlin_kv_cache* cache, const qlin_kv_batch* batch, int64_t T, int64_t q_heads,
+                        int64_t window, int64_t plan[3]) {
+  QLIN_CHECK(batch && batch->max_q <= 512, batch ? QLIN_ERR_SHAPE : QLIN_ERR_ARG);
+  return plan_call(cache, batch, T, q_heads, window, true, plan);
 }
 
 }  // extern "C"

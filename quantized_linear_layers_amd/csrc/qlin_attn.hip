@@ -21,20 +21,21 @@
 // needs no rescaling pass.
 //
 // K and V tiles arrive by buffer_load_dwordx4 ... lds (16 bytes a lane, 1 KB an
-// instruction, no registers). A resource covers 16 rows of one page at most, so
-// the memory system itself zeroes rows behind the last visible key and before
-// the first one, and pages that do not exist: stale values there, NaN too,
-// never reach a product. LDS rows are stored with their 16-byte chunks
+// instruction, no registers). A resource covers 16 rows of one page at most (a step's
+// whole tile of 32 where the pages have as many), so the memory system itself zeroes
+// rows behind the last visible key and before the first one, and pages that do not
+// exist: stale values there, NaN too, never reach a product. LDS rows are stored with their 16-byte chunks
 // exclusive-or-ed by row bits (k_swz, v_swz), so that both the row reads of K and
 // the transposing reads of V touch every bank once.
 //
-// Two kernels share this: attn_step_kernel (32 rows a workgroup: a decode step, a
-// small chunk), where each wave takes its own key tiles and the waves merge at the
+// Two kernels share this: attn_step_kernel (16 or 32 rows a workgroup: a decode step, a
+// small chunk, trees), where each wave takes its own key tiles and the waves merge at the
 // end, and attn_chunk_kernel (128 rows; E4M3 attn_chunk_e4m3_kernel, 256), where each
 // wave has its own rows and the workgroup shares the tiles. All split the key axis
 // over workgroups when the rows alone do not fill the device; the parts are joined by
 // the last workgroup to arrive (step) or by attn_join_kernel (chunk, whose parts are
-// many rows).
+// many rows). Both have a form (TREE) that takes a token's mask of the new keys in place
+// of their order: only tiles that reach into the new tokens read the bits.
 #include "qlin_internal.h"
 #include "qlin_device.h"
 
@@ -81,6 +82,7 @@ struct AttnArgs {
   const uint32_t* mask;
   const int32_t* positions;
   int words;
+  int ordered;  // step: sequences with the most keys first (at most 256 sequences)
 };
 
 __device__ __forceinline__ v16f mfma32(v8bf a, v8bf b, v16f c) {
@@ -133,19 +135,20 @@ struct Item {
   int rows;     // packed rows
 };
 
-// One 16-row group (first key `key`) of a page: its first row in the pool and
+// One group of MOST (16) rows (first key `key`) of a page: its first row in the pool and
 // how many of its rows lie before `hi` (0 if the page does not exist).
 struct Rows16 {
   uint64_t row;
   int rows;
 };
 __device__ __forceinline__ bool no_page(const AttnArgs& a, int page) { return (uint32_t)page >= (uint32_t)a.pages; }
+template <int MOST = 16>
 __device__ __forceinline__ Rows16 rows_of(const AttnArgs& a, const Item& it, int key, int page, int hi) {
   const bool none = no_page(a, page);
   const uint32_t block = (uint32_t)(none ? 0 : page) * (uint32_t)a.kv_heads + (uint32_t)it.h;
   Rows16 w;
   w.row = ((uint64_t)block << a.page_shift) + (uint32_t)(key & ((1 << a.page_shift) - 1));
-  w.rows = none ? 0 : max(min(hi - key, 16), 0);
+  w.rows = none ? 0 : max(min(hi - key, MOST), 0);
   return w;
 }
 template <int BYTES>
@@ -231,11 +234,33 @@ struct Stage {
     }
     dma16<kLoads>(lds + r0 * G::kRow, off, rs);
   }
+  // the same of 32 rows that lie together (a tile within a page), by one resource
+  template <bool V, bool EDGE>
+  static __device__ __forceinline__ void rows32(const v4i& rs, int skip, uint32_t lds) {
+    constexpr int kAll = 32 / G::kRowsPerLoad, kOnce = kAll < 8 ? kAll : 8;
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int j = 0; j < kAll; j += kOnce) {
+      uint32_t off[kOnce];
+#pragma unroll
+      for (int i = 0; i < kOnce; ++i) {
+        const int row = (j + i) * G::kRowsPerLoad + lane / G::kChunks;
+        off[i] = (uint32_t)(j * 1024 + lane / G::kChunks * G::kRow + 16 * (lane % G::kChunks ^ (V ? G::v_swz(row) : G::k_swz(row))));
+        if (EDGE && row < skip) off[i] = 0x80000000u;
+      }
+      dma16<kOnce>(lds + j * 1024, off, rs);
+    }
+  }
   template <bool EDGE>
   static __device__ __forceinline__ void scale_row(const v4i& rs, int skip, int r0, uint32_t lds) {
     const int lane = threadIdx.x & 63;
     const uint32_t at = lane >= 16 || (EDGE && lane < skip) ? 0x80000000u : (uint32_t)(lane * 4);
     dma4(lds + (r0 / 16) * 256, at, rs);
+  }
+  template <bool EDGE>
+  static __device__ __forceinline__ void scale_rows32(const v4i& rs, int skip, uint32_t lds) {
+    const int lane = threadIdx.x & 63;
+    dma4(lds, lane >= 32 || (EDGE && lane < skip) ? 0x80000000u : (uint32_t)(lane * 4), rs);
   }
 };
 
@@ -1021,6 +1046,12 @@ __global__ __launch_bounds__(512, D == 64 ? 4 : 2) void attn_chunk_e4m3_kernel(c
 // launch, three loads that each need the one before (lengths, page, keys and values) and
 // the join are all but 1.
 constexpr int kPieces = 512;
+// (one instruction; fmaxf's operands would be told apart from signalling NaNs first)
+__device__ __forceinline__ float max3(float x, float y, float z) {
+  float r;
+  asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(x), "v"(y), "v"(z));
+  return r;
+}
 __device__ __forceinline__ float groups_max(float x) {
   const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
   return halves_max(fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1])));
@@ -1030,19 +1061,81 @@ __device__ __forceinline__ float groups_sum(float x) {
   return x + __shfl_xor(x, 32, kWave);
 }
 
-// Waves a SIMD that the LDS places (4 waves a workgroup) leave room for.
-constexpr int step_waves(int D, bool fp8, int rb) {
-  return D == 64 ? 4 : D == 128 ? (fp8 && rb == 1 ? 4 : 2) : (fp8 && rb == 1 ? 2 : 1);
+// The place-th sequence in an order of sixteen classes of lengths, the longest first, and
+// its rows and keys: of a grid that does not fit the device at once the long sequences
+// must not come last (64 trees of 16 over up to 4096 E4M3 keys: 103 us for 112 in the batch's
+// order). At most 256 sequences, a lane has four.
+__device__ __forceinline__ bool item_by_length(const AttnArgs& a, int place, int h, Item& it) {
+  const int lane = threadIdx.x & 63;
+  int from[4], to[4], len[4], longest = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int b = 64 * i + lane;
+    from[i] = to[i] = len[i] = 0;
+    if (b < a.B) {
+      from[i] = a.q_start[b];
+      to[i] = a.q_start[b + 1];
+      len[i] = a.kv_len[b];
+    }
+    longest = max(longest, len[i]);
+  }
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) longest = max(longest, __shfl_xor(longest, o, kWave));
+  const float per = 16.0f / ((float)longest + 1.0f);
+  int key[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) key[i] = 64 * i + lane < a.B ? min((int)((float)max(len[i], 0) * per), 15) : -1;
+  for (int c = 15; c >= 0; --c) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const unsigned long long these = __ballot(key[i] == c);
+      const int n = __popcll(these);
+      if (place < n) {
+        const bool mine = key[i] == c && __popcll(these & ((1ull << lane) - 1)) == place;
+        const int j = __ffsll(__ballot(mine)) - 1;
+        return item_from(a, 64 * i + j, h, __builtin_amdgcn_readlane(from[i], j), __builtin_amdgcn_readlane(to[i], j),
+                         __builtin_amdgcn_readlane(len[i], j), it);
+      }
+      place -= n;
+    }
+  }
+  return false;
 }
 
+// Waves a SIMD that the LDS places (4 waves a workgroup) leave room for.
+constexpr int step_waves(int D, bool fp8, int rb, int nw) {
+  if (nw == 8) return D == 64 ? 4 : 2;
+  return D == 64 ? 4 : D == 128 ? (fp8 ? (rb == 1 ? 4 : 2) : 2) : (fp8 && rb == 1 ? 2 : 1);
+}
+
+// Columns of the merge at a time: all, or as few (32 at least) as fit the places' room.
+constexpr int merge_turns(int D, int rows, int ring) {
+  int turns = 1;
+  while (D / turns >= 64 && rows * (D / turns + 4) * 4 > ring) turns *= 2;
+  return turns;
+}
+
+// Places for K and for V a wave. With one, a load is issued as soon as its place is free and
+// only if there is such a tile; with two always (of tiles behind the part nothing is
+// read), so that as many are on their way at every wait. Two where LDS has room for
+// them beside as many workgroups: E4M3 tiles of 32 rows (with the one resource a tile
+// below, 64 trees of 16 over up to 4096 keys: 97 us for 103).
+constexpr int step_places(int D, bool fp8, int rb) { return fp8 && rb == 2 && D >= 128 ? 2 : 1; }
+
 template <int D, bool FP8, int RB, int NW, bool TREE>
-__global__ __launch_bounds__(NW * 64, step_waves(D, FP8, RB)) void attn_step_kernel(const AttnArgs a) {
+__global__ __launch_bounds__(NW * 64, step_waves(D, FP8, RB, NW)) void attn_step_kernel(const AttnArgs a) {
   using St = Stage<D, FP8, 32, 16, true>;
   using G = Geo<D, FP8, true>;
   constexpr int kStage = 2 * St::kTile + 2 * St::kScale;     // K, V, their scales
-  constexpr int kOps = 2 * (St::kLoads + (FP8 ? 1 : 0));     // loads of a K or V tile
-  constexpr int kRows = 16 * RB, kOut = D + 4;               // floats of a row in the merge
-  constexpr int kMerge = NW * kRows * kOut * 4, kRing = NW * kStage;
+  constexpr int kOps = 2 * St::kLoads + (FP8 ? 1 : 0);       // loads of a K or V tile, at least
+  constexpr int R = step_places(D, FP8, RB);
+  // the merge, of all columns or of half of them at a time, where that keeps it in the
+  // room of the places (E4M3, heads of 128, 32 rows: 37 KB for 68, three workgroups a CU
+  // for two)
+  constexpr int kRows = 16 * RB, kRing = NW * kStage * R;
+  constexpr int kTurns = D >= 128 ? merge_turns(D, NW * kRows, kRing) : 1;
+  constexpr int kCols = D / kTurns, kOut = kCols + 4;  // columns at a time, floats of a row
+  constexpr int kMerge = NW * kRows * kOut * 4;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[kRing > kMerge ? kRing : kMerge];
   __shared__ float wm[NW][kRows], wl[NW][kRows];
   __shared__ int last_flag;
@@ -1053,7 +1146,8 @@ __global__ __launch_bounds__(NW * 64, step_waves(D, FP8, RB)) void attn_step_ker
   Item it;
   // (heads fastest: with eight or sixteen the row tiles of one share an XCD's L2)
   const int h = blockIdx.x % a.kv_heads, row0 = blockIdx.x / a.kv_heads * a.part_rows;
-  if (!item_of(a, blockIdx.y, h, it) || row0 >= it.rows) return;
+  if (!(TREE && a.ordered ? item_by_length(a, blockIdx.y, h, it) : item_of(a, blockIdx.y, h, it)) || row0 >= it.rows)
+    return;
   const int rows = min(it.rows - row0, a.part_rows);  // this workgroup's
   const Range rg = range_of<TREE>(a, it, row0, row0 + rows);
   int t0 = rg.lo / 32, t1 = (rg.hi + 31) / 32;
@@ -1082,38 +1176,76 @@ __global__ __launch_bounds__(NW * 64, step_waves(D, FP8, RB)) void attn_step_ker
     t0 = t0 + split * n;
     t1 = min(t0 + n, t1);
   }
-  uint8_t* mine = lds + wave * kStage;
-  const uint32_t lk = lds_addr(mine), lv = lk + St::kTile, ls = lv + St::kTile;
-  // K (or V) rows of tile t and their scales
-  auto load = [&](int t, const int (&page)[2], auto is_v, auto edge) {
-#pragma unroll
-    for (int n = 0; n < 2; ++n) {
-      const Rows16 w = rows_of(a, it, t * 32 + 16 * n, page[n], rg.hi);
-      const int skip = rg.lo - t * 32 - 16 * n;
-      v4i rs = resource<G::kRow>(is_v ? a.v : a.k, w);
+  uint8_t* mine = lds + wave * kStage * R;
+  const uint32_t lk0 = lds_addr(mine);
+  uint32_t place = 0;  // of the tile that is worked on, in bytes
+  auto next_place = [&] { place = R == 1 || place == (R - 1) * kStage ? 0 : place + kStage; };
+  const int hi = R > 1 ? min(rg.hi, 32 * t1) : rg.hi;
+  const bool whole = a.page_shift >= 5;  // a tile lies in one page
+  const int scale_step = whole ? 64 : 256;  // from the scales of a tile's first 16 keys to the others'
+  // The rows of tile t (x, or x and y), and K (or V) rows of them with their scales. (By
+  // value: an array of these would lie in memory.)
+  struct Tile {
+    Rows16 x, y;
+  };
+  auto rows_at = [&](int t, int page0, int page1) {
+    Tile w;
+    w.x = whole ? rows_of<32>(a, it, t * 32, page0, hi) : rows_of(a, it, t * 32, page0, hi);
+    w.y = rows_of(a, it, t * 32 + 16, page1, hi);
+    return w;
+  };
+  auto load = [&](int t, const Tile w, auto is_v, auto edge) {
+    const uint32_t to = lk0 + place + (is_v ? St::kTile : 0), scales = lk0 + place + 2 * St::kTile + (is_v ? St::kScale : 0);
+    const int skip = rg.lo - t * 32;
+    if (whole) {
+      v4i rs = resource<G::kRow>(is_v ? a.v : a.k, w.x);
       settled(rs);
-      St::template rows<is_v, edge>(rs, skip, 16 * n, is_v ? lv : lk);
+      St::template rows32<is_v, edge>(rs, skip, to);
       if constexpr (FP8) {
-        v4i sc = resource<4>(is_v ? a.vs : a.ks, w);
+        v4i sc = resource<4>(is_v ? a.vs : a.ks, w.x);
         settled(sc);
-        St::template scale_row<edge>(sc, skip, 16 * n, is_v ? ls + St::kScale : ls);
+        St::template scale_rows32<edge>(sc, skip, scales);
       }
+      return;
     }
+    auto half = [&](const Rows16 x, int n) {
+      v4i rs = resource<G::kRow>(is_v ? a.v : a.k, x);
+      settled(rs);
+      St::template rows<is_v, edge>(rs, skip - 16 * n, 16 * n, to);
+      if constexpr (FP8) {
+        v4i sc = resource<4>(is_v ? a.vs : a.ks, x);
+        settled(sc);
+        St::template scale_row<edge>(sc, skip - 16 * n, 16 * n, scales);
+      }
+    };
+    half(w.x, 0);
+    half(w.y, 1);
   };
   constexpr std::integral_constant<bool, true> kYes;
   constexpr std::integral_constant<bool, false> kNo;
   auto pages = [&](int t, int (&page)[2]) {
     page[0] = page_of(a, it, t * 32);
-    page[1] = page_of(a, it, t * 32 + 16);
+    page[1] = whole ? page[0] : page_of(a, it, t * 32 + 16);
   };
   int t = t0 + wave;
-  int page[2], next[2];
-  pages(t, page);
+  int page[R][2], next[2];  // of the tiles in the places; of the next one to be loaded
+  Tile w = {};  // the rows of the tile that is loaded next
+#pragma unroll
+  for (int i = 0; i < R; ++i) pages(t + i * NW, page[i]);
   if (t < t1) {
-    load(t, page, kNo, kYes);
-    load(t, page, kYes, kYes);
+    w = rows_at(t, page[0][0], page[0][1]);
+    load(t, w, kNo, kYes);
+    load(t, w, kYes, kYes);
+#pragma unroll
+    for (int i = 1; i < R; ++i) {
+      next_place();
+      w = rows_at(t + i * NW, page[i][0], page[i][1]);
+      load(t + i * NW, w, kNo, kNo);
+      load(t + i * NW, w, kYes, kNo);
+    }
+    next_place();
   }
-  pages(t + NW, next);
+  pages(t + R * NW, next);
   v8bf q[RB][D / 32];
   int vlo[RB], vhi[RB];
   float m[RB], l[RB];
@@ -1133,14 +1265,15 @@ __global__ __launch_bounds__(NW * 64, step_waves(D, FP8, RB)) void attn_step_ker
       q[rb][u] = load_q8(a, src + (FP8 ? 64 * (u / 2) + 16 * g + 8 * (u % 2) : 32 * u + 8 * g));
   }
   for (; t < t1; t += NW) {
-    const bool more = t + NW < t1;
-    const uint32_t bad = (no_page(a, page[0]) ? 1u : 0u) | (no_page(a, page[1]) ? 2u : 0u);
+    const bool more = R > 1 || t + NW < t1;
+    const uint32_t bad = (no_page(a, page[0][0]) ? 1u : 0u) | (no_page(a, page[0][1]) ? 2u : 0u);
     const int key = t * 32;
-    dma_wait<kOps>();  // K has arrived, V may be under way
+    const uint8_t* at = mine + place;
+    dma_wait<(2 * R - 1) * kOps>();  // K has arrived, V and the other place may be under way
     v4f s[RB][2];
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
-      const uint8_t* base = mine + (16 * b + r) * G::kRow;
+      const uint8_t* base = at + (16 * b + r) * G::kRow;
       const int sw = G::k_swz(16 * b + r);
 #pragma unroll
       for (int rb = 0; rb < RB; ++rb) s[rb][b] = v4f{};
@@ -1161,7 +1294,7 @@ __global__ __launch_bounds__(NW * 64, step_waves(D, FP8, RB)) void attn_step_ker
     if (FP8) {
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
-        const v4f k = *reinterpret_cast<const v4f*>(mine + 2 * St::kTile + 256 * b + 16 * g);
+        const v4f k = *reinterpret_cast<const v4f*>(at + 2 * St::kTile + scale_step * b + 16 * g);
 #pragma unroll
         for (int rb = 0; rb < RB; ++rb)
 #pragma unroll
@@ -1169,7 +1302,10 @@ __global__ __launch_bounds__(NW * 64, step_waves(D, FP8, RB)) void attn_step_ker
       }
     }
     lds_reads_done();
-    if (more) load(t + NW, next, kNo, kNo);
+    if (more) {
+      w = rows_at(t + R * NW, next[0], next[1]);
+      load(t + R * NW, w, kNo, kNo);
+    }
     if (bad != 0 || key + 32 > rg.all_hi || key < rg.all_lo) {
 #pragma unroll
       for (int rb = 0; rb < RB; ++rb) {
@@ -1185,12 +1321,12 @@ __global__ __launch_bounds__(NW * 64, step_waves(D, FP8, RB)) void attn_step_ker
     }
 #pragma unroll
     for (int rb = 0; rb < RB; ++rb) {
-      float mx = s[rb][0][0];
+      // (each lane's own keys first: the row's maximum is needed only where it is raised)
+      float mx = fmaxf(s[rb][0][0], s[rb][0][1]);
 #pragma unroll
-      for (int i = 1; i < 8; ++i) mx = fmaxf(mx, s[rb][i / 4][i % 4]);
-      mx = groups_max(mx) * a.c;
-      if (__any(mx > m[rb] + 8.0f)) {
-        const float top = fmaxf(m[rb], mx);
+      for (int i = 2; i < 8; i += 2) mx = max3(mx, s[rb][i / 4][i % 4], s[rb][i / 4][i % 4 + 1]);
+      if (__any(mx * a.c > m[rb] + 8.0f)) {
+        const float top = fmaxf(m[rb], groups_max(mx) * a.c);
         const float f = top == -kInf ? 0.0f : exp2_hw(m[rb] - top);
         m[rb] = top;
         l[rb] *= f;
@@ -1208,7 +1344,7 @@ __global__ __launch_bounds__(NW * 64, step_waves(D, FP8, RB)) void attn_step_ker
       }
     }
     if (more)
-      dma_wait<kOps>();  // V has arrived, the next K may be under way
+      dma_wait<(2 * R - 1) * kOps>();  // V has arrived, the next K may be under way
     else
       dma_wait<0>();
     v8bf p[RB];
@@ -1216,7 +1352,7 @@ __global__ __launch_bounds__(NW * 64, step_waves(D, FP8, RB)) void attn_step_ker
     if (FP8) {
 #pragma unroll
       for (int b = 0; b < 2; ++b)
-        sv[b] = *reinterpret_cast<const v4f*>(mine + 2 * St::kTile + St::kScale + 256 * b + 16 * g);
+        sv[b] = *reinterpret_cast<const v4f*>(at + 2 * St::kTile + St::kScale + scale_step * b + 16 * g);
     }
 #pragma unroll
     for (int rb = 0; rb < RB; ++rb) {
@@ -1232,7 +1368,7 @@ __global__ __launch_bounds__(NW * 64, step_waves(D, FP8, RB)) void attn_step_ker
       }
       p[rb] = as_bf16(w);
     }
-    const uint8_t* vt = mine + St::kTile;
+    const uint8_t* vt = at + St::kTile;
 #pragma unroll
     for (int d = 0; d < D / 16; ++d) {
       v8bf v;
@@ -1255,11 +1391,16 @@ __global__ __launch_bounds__(NW * 64, step_waves(D, FP8, RB)) void attn_step_ker
       for (int rb = 0; rb < RB; ++rb) o[rb][d] = mfma_bf16(v, p[rb], o[rb][d]);
     }
     lds_reads_done();
-    if (more) load(t + NW, next, kYes, kNo);
-    page[0] = next[0];
-    page[1] = next[1];
-    pages(t + 2 * NW, next);
+    if (more) load(t + R * NW, w, kYes, kNo);
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      page[i][0] = i + 1 < R ? page[(i + 1) % R][0] : next[0];
+      page[i][1] = i + 1 < R ? page[(i + 1) % R][1] : next[1];
+    }
+    pages(t + (R + 1) * NW, next);
+    next_place();
   }
+  if (R > 1) dma_wait<0>();  // the merge takes the places
   // merge: every wave's rows on the common maximum, then summed over the waves
 #pragma unroll
   for (int rb = 0; rb < RB; ++rb) {
@@ -1268,22 +1409,31 @@ __global__ __launch_bounds__(NW * 64, step_waves(D, FP8, RB)) void attn_step_ker
   }
   __syncthreads();
   float* all = reinterpret_cast<float*>(lds);
+  float factor[RB];
 #pragma unroll
   for (int rb = 0; rb < RB; ++rb) {
     const int row = 16 * rb + r;
     float top = -kInf;
 #pragma unroll
     for (int w = 0; w < NW; ++w) top = fmaxf(top, wm[w][row]);
-    const float f = m[rb] == -kInf ? (l[rb] == 0.0f ? 0.0f : 1.0f) : exp2_hw(m[rb] - top);
-    if (row < rows) {
-      float* dst = all + (wave * kRows + row) * kOut + 4 * g;
-#pragma unroll
-      for (int d = 0; d < D / 16; ++d)
-        *reinterpret_cast<v4f*>(dst + 16 * d) = v4f{o[rb][d][0] * f, o[rb][d][1] * f, o[rb][d][2] * f, o[rb][d][3] * f};
-      if (g == 0) wl[wave][row] = l[rb] * f;
-    }
+    factor[rb] = m[rb] == -kInf ? (l[rb] == 0.0f ? 0.0f : 1.0f) : exp2_hw(m[rb] - top);
+    if (row < rows && g == 0) wl[wave][row] = l[rb] * factor[rb];
   }
-  __syncthreads();
+  auto put = [&](int turn) {  // this wave's rows, the turn's columns
+#pragma unroll
+    for (int rb = 0; rb < RB; ++rb) {
+      const int row = 16 * rb + r;
+      const float f = factor[rb];
+      if (row < rows) {
+        float* dst = all + (wave * kRows + row) * kOut + 4 * g;
+#pragma unroll
+        for (int d = 0; d < D / 16; ++d)
+          if (d / (kCols / 16) == turn)
+            *reinterpret_cast<v4f*>(dst + 16 * d - kCols * turn) =
+                v4f{o[rb][d][0] * f, o[rb][d][1] * f, o[rb][d][2] * f, o[rb][d][3] * f};
+      }
+    }
+  };
   const int64_t heads = (int64_t)a.kv_heads * a.group;
   auto finish = [&](int row, int c4, const v4f& x, float mm, float ll) {
     const int64_t tok = it.q0 + (row0 + row) / a.group;
@@ -1302,27 +1452,33 @@ __global__ __launch_bounds__(NW * 64, step_waves(D, FP8, RB)) void attn_step_ker
       a.po + (int64_t)wg * a.splits * a.part_rows * D, (short)0, a.splits * a.part_rows * D * 4, 0x00020000);
   const __amdgpu_buffer_rsrc_t rm = __builtin_amdgcn_make_buffer_rsrc(
       a.pml + (int64_t)wg * a.splits * a.part_rows * 2, (short)0, a.splits * a.part_rows * 8, 0x00020000);
-  for (int i = threadIdx.x; i < rows * (D / 4); i += NW * 64) {
-    const int row = i / (D / 4), c4 = i % (D / 4) * 4;
-    float mm = -kInf, ll = 0.0f;
-    v4f x = {};
 #pragma unroll
-    for (int w = 0; w < NW; ++w) {
-      mm = fmaxf(mm, wm[w][row]);
-      ll += wl[w][row];
-      const v4f y = *reinterpret_cast<const v4f*>(all + (w * kRows + row) * kOut + c4);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) x[j] += y[j];
-    }
-    if (parts == 1) {
-      finish(row, c4, x, mm, ll);
-    } else {
-      const int at = split * a.part_rows + row;
-      if (c4 == 0) {
-        const v2i y = {(int)__float_as_uint(mm), (int)__float_as_uint(ll)};
-        __builtin_amdgcn_raw_buffer_store_b64(y, rm, at * 8, 0, kSc1);
+  for (int turn = 0; turn < kTurns; ++turn) {
+    if (turn) __syncthreads();  // the last turn's columns have been read
+    put(turn);
+    __syncthreads();
+    for (int i = threadIdx.x; i < rows * (kCols / 4); i += NW * 64) {
+      const int row = i / (kCols / 4), c = i % (kCols / 4) * 4, c4 = c + kCols * turn;
+      float mm = -kInf, ll = 0.0f;
+      v4f x = {};
+  #pragma unroll
+      for (int w = 0; w < NW; ++w) {
+        mm = fmaxf(mm, wm[w][row]);
+        ll += wl[w][row];
+        const v4f y = *reinterpret_cast<const v4f*>(all + (w * kRows + row) * kOut + c);
+  #pragma unroll
+        for (int j = 0; j < 4; ++j) x[j] += y[j];
       }
-      __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4i, x), ro, (at * D + c4) * 4, 0, kSc1);
+      if (parts == 1) {
+        finish(row, c4, x, mm, ll);
+      } else {
+        const int at = split * a.part_rows + row;
+        if (c4 == 0) {
+          const v2i y = {(int)__float_as_uint(mm), (int)__float_as_uint(ll)};
+          __builtin_amdgcn_raw_buffer_store_b64(y, rm, at * 8, 0, kSc1);
+        }
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4i, x), ro, (at * D + c4) * 4, 0, kSc1);
+      }
     }
   }
   if (parts == 1) return;
@@ -1429,6 +1585,7 @@ struct Plan {
   int splits;
   int64_t tiles;             // chunk: workgroups for the rows, at most
   int part_rows, row_tiles;  // step
+  bool wide;                 // step: eight waves
   size_t parts;              // rows of parts in the workspace
 };
 
@@ -1463,6 +1620,53 @@ Plan step_plan(const qlin_kv_cache& cache, const qlin_kv_batch& batch, int64_t r
   const int even = (int)std::sqrt(32.0 * (double)keys / (double)(p.part_rows * cache.head_dim));
   p.splits = std::max(1, std::min(p.splits, even));
   if (wgs >= most) p.splits = 1;
+  p.parts = p.splits <= 1 ? 0 : (size_t)p.splits * wgs * p.part_rows;
+  return p;
+}
+
+// Parts of a tree's key axis: of 256 keys or more, as many as fill the device; of long
+// tables, whose sequences differ most, more. (More keys never mean fewer parts.)
+int tree_splits(bool e4m3, int64_t keys, int64_t wgs) {
+  if (keys < 2048) return 1;
+  int64_t n = (keys >= 8192 && e4m3 ? 512 : 256) / wgs;
+  if (keys >= 8192 && wgs <= 512) n = std::max<int64_t>(n, e4m3 ? keys / 4096 : 2);
+  return (int)std::max<int64_t>(1, std::min({(int64_t)16, keys / 256, n}));
+}
+
+// The same for trees, whose calls have some 16 to 256 rows a sequence and head: workgroups
+// of 16 or 32 rows, of four waves or (the tiles of a part taken by twice as many at once)
+// eight. A workgroup of eight costs less than a second part, whose join takes as long as a
+// thousand keys. us, 32 + 8 heads of 128:
+//   16 rows and eight waves while all run at once, few bytes are read twice, and always where
+//     codes are converted (E4M3): a tree of 8, 1024 keys: 11.9, of 32 rows 18.7; 4096 keys in
+//     16 parts 14.6 (four waves 17.4, 32 rows 18.0); E4M3, eight trees of 32, 4096 keys:
+//     30.7 and 34.1;
+//   32 rows beyond: a tree of 32, 16384 keys in 8 parts 29.0 (16 rows 33.0), eight trees of
+//     32, 4096 keys 31.6 (four waves 36.3); 64 trees of 16 four waves: 142 (eight 152);
+//   short tables: 16 rows, four waves: eight trees of 32, 256 keys: 8.7 and 9.9; E4M3, 64 of
+//     them, 1024 keys: 62 and 67.
+Plan tree_step_plan(const qlin_kv_cache& cache, const qlin_kv_batch& batch, int64_t rows, int64_t keys) {
+  Plan p = {};
+  p.step = true;
+  const bool e4m3 = cache.fmt == QLIN_KV_E4M3;
+  const int64_t D = cache.head_dim, heads = batch.batch * cache.kv_heads;
+  const int64_t few = heads * ((rows + 15) / 16), many = heads * ((rows + 31) / 32);  // workgroups of 16, 32 rows
+  const int64_t at_once = e4m3 && D < 256 ? 512 : 256;                                // of eight waves
+  const double reread = (double)few * keys * D * (e4m3 ? 2 : 4);                      // bytes, by 16 rows each
+  bool narrow = rows <= 16 || (e4m3 && D == 256);
+  if (few <= at_once && (e4m3 ? reread < 0x1p30 || many > 128 : reread < 0x1p29)) {
+    narrow = p.wide = true;
+  } else if (keys <= 1024 && (e4m3 ? D > 64 : D == 128 && few <= 512)) {
+    narrow = true;
+  } else {
+    const int64_t wgs = narrow ? few : many;
+    p.wide = wgs <= (keys >= 4096 ? 512 : 256);
+  }
+  if (D == 256 && !(e4m3 && narrow)) p.wide = false;  // (their places would not fit LDS)
+  const int64_t tile = narrow ? 16 : 32, wgs = narrow ? few : many;
+  p.part_rows = (int)std::min(tile, rows);
+  p.row_tiles = (int)((rows + tile - 1) / tile);
+  p.splits = tree_splits(e4m3, keys, wgs);
   p.parts = p.splits <= 1 ? 0 : (size_t)p.splits * wgs * p.part_rows;
   return p;
 }
@@ -1506,10 +1710,30 @@ int64_t few_rows_keys(const qlin_kv_cache& cache, const qlin_kv_batch& batch, in
   return ((room << (e4m3 ? 21 : 20)) - 1) / wgs;
 }
 
-Plan plan_of(const qlin_kv_cache& cache, const qlin_kv_batch& batch, int64_t T, int64_t q_heads, int64_t window) {
+// Whether a tree's call takes these workgroups: where the others do, and up to 256 rows
+// also, in E4M3, over long tables (64 trees of 64, 4096 keys: 263 us, in workgroups of 256
+// rows 301; eight, 16384 keys: 113 and 154), in bf16 with few of them (a tree of 32, 65536
+// keys: 69 and 97; of 64, 16384 keys: 38 and 44). bf16 heads of 256 leave them sooner (64
+// trees of 32, 1024 keys: 95 and 66; 16, 4096 keys: 201 and 180).
+bool tree_steps(const qlin_kv_cache& cache, const qlin_kv_batch& batch, int64_t T, int64_t rows, int64_t group,
+                int64_t keys) {
+  const int64_t many = batch.batch * cache.kv_heads * ((rows + 31) / 32);
+  const bool e4m3 = cache.fmt == QLIN_KV_E4M3;
+  if (!e4m3 && cache.head_dim == 256 && rows > 32 && (many > 256 || many * keys > 1 << 18)) return false;
+  if (keys <= few_rows_keys(cache, batch, T, rows, group)) return true;
+  if (rows > 256) return false;
+  if (e4m3) return keys > 1024 && (batch.batch > 1 || keys <= 32768 || cache.head_dim == 64);
+  return many <= 32 || (many <= 64 && keys <= 16384);
+}
+
+Plan plan_of(const qlin_kv_cache& cache, const qlin_kv_batch& batch, int64_t T, int64_t q_heads, int64_t window,
+             bool tree) {
   const int64_t group = q_heads / cache.kv_heads, rows = std::min(batch.max_q, T) * group;
   int64_t keys = batch.table_cols * cache.page_size;
   if (window > 0) keys = std::min(keys, std::min(window, keys) + batch.max_q);
+  if (tree)
+    return tree_steps(cache, batch, T, rows, group, keys) ? tree_step_plan(cache, batch, rows, keys)
+                                                          : chunk_plan(cache, batch, T, rows, group, keys);
   return keys <= few_rows_keys(cache, batch, T, rows, group) ? step_plan(cache, batch, rows, keys)
                                                              : chunk_plan(cache, batch, T, rows, group, keys);
 }
@@ -1518,10 +1742,25 @@ template <int D, bool FP8, bool TREE>
 void launch_parts(const AttnArgs& a, const Plan& p, hipStream_t st) {
   if (p.step) {
     const dim3 grid(a.kv_heads * p.row_tiles, a.B, p.splits);
-    if (p.part_rows <= 16)
-      attn_step_kernel<D, FP8, 1, 4, TREE><<<grid, 256, 0, st>>>(a);
-    else
-      attn_step_kernel<D, FP8, 2, 4, TREE><<<grid, 256, 0, st>>>(a);
+    if constexpr (TREE && (D < 256 || FP8)) {
+      if (p.part_rows <= 16 && p.wide) {
+        attn_step_kernel<D, FP8, 1, 8, TREE><<<grid, 512, 0, st>>>(a);
+        return;
+      }
+    }
+    if constexpr (TREE && D < 256) {
+      if (p.part_rows > 16 && p.wide) {
+        attn_step_kernel<D, FP8, 2, 8, TREE><<<grid, 512, 0, st>>>(a);
+        return;
+      }
+    }
+    if constexpr (!(TREE && FP8 && D == 256)) {  // (its trees have 16 rows a workgroup)
+      if (p.part_rows > 16) {
+        attn_step_kernel<D, FP8, 2, 4, TREE><<<grid, 256, 0, st>>>(a);
+        return;
+      }
+    }
+    attn_step_kernel<D, FP8, 1, 4, TREE><<<grid, 256, 0, st>>>(a);
   } else {
     const int64_t items = p.tiles * a.kv_heads * p.splits;
     const unsigned grid = (unsigned)((items + 7) / 8 * 8);
@@ -1530,10 +1769,10 @@ void launch_parts(const AttnArgs& a, const Plan& p, hipStream_t st) {
       attn_chunk_e4m3_kernel<D, TK, TREE><<<grid, 512, 0, st>>>(a);
     else
       attn_chunk_kernel<D, TK, TREE><<<grid, 256, 0, st>>>(a);
-  }
-  if (p.splits > 1 && !p.step) {
-    const int64_t rows = a.T * a.kv_heads * a.group, wg = 1024 / D;  // rows of a workgroup
-    attn_join_kernel<D><<<(unsigned)((rows + wg - 1) / wg), 256, 0, st>>>(a);
+    if (p.splits > 1) {
+      const int64_t rows = a.T * a.kv_heads * a.group, wg = 1024 / D;  // rows of a workgroup
+      attn_join_kernel<D><<<(unsigned)((rows + wg - 1) / wg), 256, 0, st>>>(a);
+    }
   }
 }
 
@@ -1558,7 +1797,7 @@ static size_t parts_bytes(size_t parts, int64_t head_dim) {
 size_t attn_workspace_bytes(const qlin_kv_cache& cache, const qlin_kv_batch& batch, int64_t T, int64_t q_heads) {
   // Enough for a call with any window: a window lowers the keys, which may also turn
   // a chunk into workgroups of 32 rows (either plan's parts only fall with the keys).
-  Plan p = plan_of(cache, batch, T, q_heads, 0);
+  Plan p = plan_of(cache, batch, T, q_heads, 0, false);
   if (!p.step) {
     const int64_t group = q_heads / cache.kv_heads, rows = std::min(batch.max_q, T) * group;
     p.parts = std::max(p.parts, step_plan(cache, batch, rows, few_rows_keys(cache, batch, T, rows, group)).parts);
@@ -1566,10 +1805,24 @@ size_t attn_workspace_bytes(const qlin_kv_cache& cache, const qlin_kv_batch& bat
   return parts_bytes(p.parts, cache.head_dim);
 }
 
+size_t attn_tree_workspace_bytes(const qlin_kv_cache& cache, const qlin_kv_batch& batch, int64_t T, int64_t q_heads) {
+  // For any window, as above: of fewer keys each kind of workgroup has as many parts or
+  // fewer, but another kind may be taken, so the largest of all.
+  const int64_t group = q_heads / cache.kv_heads, rows = std::min(batch.max_q, T) * group;
+  const int64_t keys = batch.table_cols * cache.page_size, heads = batch.batch * cache.kv_heads;
+  size_t parts = chunk_plan(cache, batch, T, rows, group, keys).parts;
+  for (const int64_t tile : {16, 32}) {
+    const int64_t wgs = heads * ((rows + tile - 1) / tile);
+    const int64_t splits = tree_splits(cache.fmt == QLIN_KV_E4M3, keys, wgs);
+    if (splits > 1) parts = std::max(parts, (size_t)(splits * wgs * std::min(tile, rows)));
+  }
+  return parts_bytes(parts, cache.head_dim);
+}
+
 void attn_plan(const qlin_kv_cache& cache, const qlin_kv_batch& batch, int64_t T, int64_t q_heads, int64_t window,
-               int64_t out[3]) {
-  const Plan p = plan_of(cache, batch, T, q_heads, window);
-  out[0] = p.step ? 32 : chunk_rows(cache);
+               bool tree, int64_t out[3]) {
+  const Plan p = plan_of(cache, batch, T, q_heads, window, tree);
+  out[0] = p.step ? (tree && p.part_rows <= 16 ? 16 : 32) : chunk_rows(cache);
   out[1] = p.splits;
   out[2] = (int64_t)parts_bytes(p.parts, cache.head_dim);
 }
@@ -1577,7 +1830,7 @@ void attn_plan(const qlin_kv_cache& cache, const qlin_kv_batch& batch, int64_t T
 int launch_attn(const qlin_kv_cache& cache, const qlin_kv_batch& batch, int64_t T, const uint16_t* q, int64_t ldq,
                 int64_t q_heads, float scale, int causal, int64_t window, const qlin_tree* tree, uint16_t* out,
                 int64_t ldo, float* lse, void* ws, size_t ws_bytes, hipStream_t st) {
-  const Plan p = plan_of(cache, batch, T, q_heads, window);
+  const Plan p = plan_of(cache, batch, T, q_heads, window, tree != nullptr);
   const size_t used = parts_bytes(p.parts, cache.head_dim);
   if (used > ws_bytes || (used && !ws)) return QLIN_ERR_WORKSPACE;
   AttnArgs a = {};
@@ -1606,6 +1859,7 @@ int launch_attn(const qlin_kv_cache& cache, const qlin_kv_batch& batch, int64_t 
   a.part_rows = p.part_rows;
   a.row_tiles = p.row_tiles;
   a.tiles = (int)p.tiles;
+  a.ordered = p.step && a.B <= 256 && (int64_t)a.kv_heads * p.row_tiles * a.B > 512;
   a.negate = scale < 0.0f;
   // a scale of 0 must keep masked scores at -inf (0 * -inf is NaN): the smallest factor,
   // 2^-149, gives every finite score a weight within 2^-21 of 1. (Factors below fp32's

@@ -109,6 +109,8 @@ int launch_kv_append(const qlin_kv_cache& cache, const qlin_kv_batch& batch, int
 inline float attn_factor(float scale) { return (scale < 0.0f ? -scale : scale) * 1.44269504088896340736f; }
 size_t attn_workspace_bytes(const qlin_kv_cache& cache, const qlin_kv_batch& batch, int64_t T,
                             int64_t q_heads);
+size_t attn_tree_workspace_bytes(const qlin_kv_cache& cache, const qlin_kv_batch& batch, int64_t T,
+                                 int64_t q_heads);
 // (tree: NULL for the order of the tokens)
 int launch_attn(const qlin_kv_cache& cache, const qlin_kv_batch& batch, int64_t T, const uint16_t* q,
                 int64_t ldq, int64_t q_heads, float scale, int causal, int64_t window, const qlin_tree* tree,
@@ -117,7 +119,7 @@ int launch_attn(const qlin_kv_cache& cache, const qlin_kv_batch& batch, int64_t 
 bool attn_grid_ok(const qlin_kv_cache& cache, const qlin_kv_batch& batch, int64_t T, int64_t q_heads);
 // Rows of a workgroup, parts of the key axis, bytes of the workspace that a call uses.
 void attn_plan(const qlin_kv_cache& cache, const qlin_kv_batch& batch, int64_t T, int64_t q_heads,
-               int64_t window, int64_t out[3]);
+               int64_t window, bool tree, int64_t out[3]);
 
 // ---- a step's tables (qlin_tables.hip)
 int launch_tree_plan(const qlin_kv_batch& batch, int64_t T, const int32_t* parents, int64_t words,

@@ -1,10 +1,11 @@
 """Refusals of the trees' entry points, on the host (no GPU needed)."""
 
+import ctypes as C
 import math
 
 import pytest
 
-from test_abi_attn_host import BAD_BATCH, BAD_CACHE, A, batch, cache, p
+from test_abi_attn_host import BAD_BATCH, BAD_CACHE, LONG, A, any_cache, batch, cache, p
 
 
 @pytest.fixture(scope="module")
@@ -49,12 +50,79 @@ def test_attn_tree_refusals(q):
 
 def test_attn_tree_workspace(q):
     c, b = cache(q), batch(q, batch=1, table_cols=4096, max_q=8)
-    need = q.lib().qlin_attn_workspace_bytes(c, b, 8, 4)
-    assert need > 0
+    need = q.lib().qlin_attn_tree_workspace_bytes(c, b, 8, 4)
+    assert need > 0 and need % 256 == 0
     kw = dict(c=c, b=b, T=8)
     assert attn_call(q, nb=need - 1, **kw) == q.ERR_WORKSPACE
     assert attn_call(q, ws=None, nb=need, **kw) == q.ERR_WORKSPACE
     assert attn_call(q, ws=(1 << 20) + 16, nb=need, **kw) == q.ERR_ALIGN
+
+
+def attn_plan(q, c, b, T, heads, window=0):
+    out = (C.c_int64 * 3)(-1, -1, -1)
+    assert q.lib().qlin_attn_tree_plan(c, b, T, heads, window, out) == q.OK
+    return tuple(out)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_no_window_needs_more_workspace_than_reported(q, fmt, D):
+    """A call plans with its window, and its parts have to fit the workspace that is sized
+    without one, whatever kind of workgroups the window turns it to."""
+    page, calls, kinds = 64, 0, set()
+    for Hkv in (1, 2, 8, 40):
+        for G in (1, 4, 8):
+            c = any_cache(q, fmt, D, Hkv, page)
+            for B in (1, 2, 5, 64, 700):
+                for mq in (1, 3, 16, 17, 40, 129, 512):
+                    for cols in (1, 9, 31, 32, 64, 65, 128, 513, 4096):
+                        b = batch(q, batch=B, max_q=mq, table_cols=cols)
+                        for T in {mq, B * mq, B * (mq // 2 + 1)}:
+                            have = q.lib().qlin_attn_tree_workspace_bytes(c, b, T, Hkv * G)
+                            for w in (0, mq, 512, 1000, 2047, 2048, 4000, 8192, 16384, 70000, 2 ** 62):
+                                rows, parts, used = attn_plan(q, c, b, T, Hkv * G, w)
+                                assert used <= have, (Hkv, G, B, mq, cols, T, w)
+                                assert (parts > 1) == (used > 0) and (rows > 32 or parts <= 16)
+                                kinds.add((rows, parts > 1))
+                                calls += 1
+    step = (16,) if fmt == "e4m3" and D == 256 else (16, 32)
+    assert calls > 100000 and kinds == {(r, s) for r in step + (128 if fmt == "bf16" else 256,) for s in (False, True)}
+
+
+# The kernels' variants, for the GPU tests: new tokens, words of the mask, key/value heads,
+# query heads of one, keys of the table for (bf16, E4M3) and heads of 64, 128 and 256, rows of a
+# workgroup and whether the key axis may be in parts.
+KERNELS = {
+    "16 rows, eight waves": ([8, 3], 1, 2, 2, [(400, 400)] * 3, [(16, 16)] * 3),
+    "16 rows, eight waves, parts": ([16, 0, 9], 1, 1, 4, [(2048, 2048)] * 3, [(16, 16)] * 3),
+    "16 rows, four waves": ([8, 1, 0, 5, 7] * 14, 1, 8, 2, [(320, 320)] * 3, [(16, 16)] * 3),
+    "32 rows, eight waves": ([16, 9, 0, 13], 1, 8, 2, [(2 ** 15, 2 ** 17), (2 ** 14, 2 ** 16), (2 ** 13, 2 ** 16)],
+                             [(32, 32), (32, 32), (32, 16)]),
+    "32 rows, four waves": ([16, 9, 0, 13] * 10, 1, 8, 2, [(1536, 1536), (1536, 1536), (800, 1536)],
+                            [(32, 32), (32, 32), (32, 16)]),
+    "chunk": ([200, 0, 65], 4, 64, 4, [(720, 720)] * 3, [(128, 256)] * 3),
+    "chunk, parts": ([200, 0, 65, 128], 4, 1, 5, [(2 ** 18, 2 ** 18)] * 3, [(128, 256)] * 3),
+}
+
+
+@pytest.mark.parametrize("name", KERNELS)
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+def test_kernels_that_the_gpu_tests_are_for(q, fmt, D, name):
+    new, words, Hkv, G, keys, rows = KERNELS[name]
+    i, f = (64, 128, 256).index(D), fmt == "e4m3"
+    b = batch(q, batch=len(new), max_q=max(new), table_cols=keys[i][f] // 16)
+    got = attn_plan(q, any_cache(q, fmt, D, Hkv, 16), b, sum(new), Hkv * G)
+    assert got[0] == rows[i][f] and (got[1] > 1) == ("parts" in name or keys[i][f] >= 8192)
+
+
+def test_attn_tree_plan_refusals(q):
+    out = (C.c_int64 * 3)()
+    c, b, f = cache(q), batch(q), q.lib().qlin_attn_tree_plan
+    assert f(None, b, 1, 4, 0, out) == q.ERR_ARG and f(c, None, 1, 4, 0, out) == q.ERR_ARG
+    assert f(c, b, 1, 4, -1, out) == q.ERR_ARG and f(c, b, 1, 4, 0, None) == q.ERR_ARG
+    assert f(c, batch(q, max_q=513), 1, 4, 0, out) == q.ERR_SHAPE and f(c, b, 1, 3, 0, out) == q.ERR_SHAPE
+    assert attn_plan(q, c, b, 0, 4) == (0, 0, 0)
 
 
 def plan_call(q, b="", T=4, parents=A, words=1, mask=A, positions=A):

@@ -6,6 +6,7 @@ import pytest
 import torch
 
 from helpers import dev, host
+from test_abi_tree_host import KERNELS
 from test_gpu_attn import attn_check, bits, fill_cache, long_table, make_batch, projections, stale_pool
 
 pytestmark = pytest.mark.gpu
@@ -131,6 +132,21 @@ def test_tree_long_table(q, oracle, D, Hkv, fmt):
     """The chunks' kernels, whole and in parts."""
     run_tree(q, oracle, D, [64, 33, 0, 50, 1], [64, 133, 9, 1050, 90], Hkv, 4, D, 16, fmt, pad=2,
              extra_cols=long_table(16))
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("name", KERNELS)
+def test_tree_kernels(q, oracle, name, D, fmt):
+    """Every variant of the kernels; which one a case runs is pinned beside the plans."""
+    new, words, Hkv, G, keys, _ = KERNELS[name]
+    keys = keys[(64, 128, 256).index(D)][fmt == "e4m3"]
+    rng = np.random.default_rng(D)
+    kv = [n + int(rng.integers(0, min(keys, 500) - 16 * words)) for n in new]
+    if keys > 1024:
+        kv[0] = new[0] + 1000
+    cols = max(-(-k // 16) for k in kv)
+    run_tree(q, oracle, D, new, kv, Hkv, G, D, 16, fmt, words=words, extra_cols=keys // 16 - cols, pad=1)
 
 
 @pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
