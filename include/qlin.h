@@ -455,9 +455,11 @@ int qlin_kv_reserve(const qlin_kv_pool* pool, const qlin_kv_tables* tables, int6
  * of the list, the last request's last page first, so that giving back what was
  * reserved last restores the list. Entries that are no page of the pool are passed
  * over, and so is what would not fit the list. Tables are left as they are (kv_len
- * too: the next reservation is told the lengths). A page that several requests share must
- * lie within the lengths that all but one of them keep: it is given back as often as
- * it is released. */
+ * too: the next reservation is told the lengths), so a reservation is followed by one
+ * release at most: a second would give the same pages back again. A request ends in its
+ * last step's release, with lengths[b] = 0, or in one behind a reservation of no new
+ * tokens. A page that several requests share must lie within the lengths that all but one
+ * of them keep: it is given back as often as it is released. */
 int qlin_kv_release(const qlin_kv_pool* pool, const qlin_kv_tables* tables, const int32_t* lengths,
                     qlin_stream_t stream);
 

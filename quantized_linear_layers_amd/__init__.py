@@ -876,7 +876,8 @@ class PageTables:
 
     def release(self, lengths) -> None:
         """Pages behind each request's first lengths int32 [B] tokens, up to its kv_len,
-        back to the pool (qlin_kv_release)."""
+        back to the pool (qlin_kv_release). Once after a `reserve` (of no new tokens, if
+        requests end between steps): a second time would give back the same pages."""
         dev = self.device
         if dev.index != torch.cuda.current_device():
             with torch.cuda.device(dev):
