@@ -445,7 +445,9 @@ typedef struct {
  * Other entries of the page table, and rows of slots and positions from q_start[batch] on,
  * are left as they are; rows from T on are not written. The sum of new_tokens has to be
  * below 2^31. Everything else in the pool and the tables is device data of any value:
- * nothing outside the arrays is read or written for it.
+ * nothing outside the arrays is read or written for it. No two arrays may overlap
+ * (QLIN_ERR_ARG), but lengths may be kv_len or new_tokens and, when pages are released,
+ * what is only read may be anything.
  * Calls that share a pool must be ordered on one stream. */
 int qlin_kv_reserve(const qlin_kv_pool* pool, const qlin_kv_tables* tables, int64_t T, const int32_t* lengths,
                     const int32_t* new_tokens, qlin_stream_t stream);
@@ -627,7 +629,8 @@ int qlin_attn_tree(const qlin_kv_cache* cache, const qlin_kv_batch* batch, int64
  * gets the token's ancestors and itself, positions [T] (or NULL) the sequence's
  * length before the new tokens plus the number of ancestors. Of the batch q_start,
  * kv_len, batch and max_q are used; rows of no sequence are left as they are. mask
- * 8-byte aligned. */
+ * 8-byte aligned; mask and positions overlap nothing (QLIN_ERR_ARG), but positions may
+ * be parents. */
 int qlin_tree_plan(const qlin_kv_batch* batch, int64_t T, const int32_t* parents, int64_t words, uint64_t* mask,
                    int32_t* positions, qlin_stream_t stream);
 
@@ -638,12 +641,13 @@ int qlin_tree_plan(const qlin_kv_batch* batch, int64_t T, const int32_t* parents
  * place of token i, as if all had been read before any is written. path [batch]
  * [path_cols] and kept [batch] int32; kept beyond path_cols or the new tokens counts as
  * those. lengths [batch] gets the cached tokens then: kv_len less the new tokens plus
- * the kept ones; it must not overlap the batch's arrays (QLIN_ERR_ARG for kv_len
- * itself). Rows of other tokens, the dropped ones among them, are left as they are. A
+ * the kept ones; it must not overlap path, kept or the batch's arrays (QLIN_ERR_ARG).
+ * Rows of other tokens, the dropped ones among them, are left as they are. A
  * number outside the new tokens, or a place that the table does not reach or whose page
  * is none of the pool's, moves nothing; of a path that does not ascend the moved rows
- * are not defined. No two sequences may share a page of new tokens. n_caches is 1 to
- * 65535; of the batch max_q is not used. */
+ * are not defined. No two sequences may share a page of new tokens, and no two caches
+ * (nor a cache's keys and values) memory. n_caches is 1 to 65535; of the batch max_q is
+ * not used. */
 int qlin_kv_keep(const qlin_kv_cache* caches, int64_t n_caches, const qlin_kv_batch* batch, const int32_t* path,
                  int64_t path_cols, const int32_t* kept, int32_t* lengths, qlin_stream_t stream);
 

@@ -559,10 +559,11 @@ def moe_w4a16(x, topk_ids, topk_w, codes13, steps13, codes2, steps2, return_stag
 
 
 # ---------------------------------------------------------------- attention
-# torch's own raw-stream query, where it has one: a Stream object costs more
-# host time than a small launch
+# torch's own raw queries, where it has them: a Stream object costs more host time than a
+# small launch, and the device's number a quarter of a microsecond
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _rows_arg(t, name, dev, head_dim, heads=None):
@@ -780,6 +781,10 @@ class PagedLayers:
             _on(c.device, one.device, "cache")
             if c.k.shape != one.k.shape or c.fmt != one.fmt:
                 raise ValueError("the caches must have one size and format")
+        size = one.k.numel() * one.k.element_size()
+        at = sorted(t.data_ptr() for c in self.caches for t in (c.k, c.v))
+        if size and any(b - a < size for a, b in zip(at, at[1:])):  # (rows would be moved twice)
+            raise ValueError("the caches must not share memory")
         self.device = one.device
         self._c = (_KVCache * len(self.caches))(*(c._c for c in self.caches))
 
@@ -867,7 +872,7 @@ class PageTables:
         from the pool into page_table, starts, lengths, slots and positions of the new
         tokens (qlin_kv_reserve). pool.count[1] tells what the pool lacked."""
         dev = self.device
-        if dev.index != torch.cuda.current_device():
+        if dev.index != _current_device():
             with torch.cuda.device(dev):
                 return self.reserve(lengths, new_tokens)
         _enqueue(dev, _lib.qlin_kv_reserve, self.pool._ref, self._ref, self.max_tokens,
@@ -879,7 +884,7 @@ class PageTables:
         back to the pool (qlin_kv_release). Once after a `reserve` (of no new tokens, if
         requests end between steps): a second time would give back the same pages."""
         dev = self.device
-        if dev.index != torch.cuda.current_device():
+        if dev.index != _current_device():
             with torch.cuda.device(dev):
                 return self.release(lengths)
         _enqueue(dev, _lib.qlin_kv_release, self.pool._ref, self._ref, self._lengths(lengths, "lengths"))
@@ -918,7 +923,7 @@ def tree_plan(batch: PagedBatch, parents, tree: Tree | None = None):
     _check(parents, "parents", torch.int32, 1)
     _on(parents.device, dev, "parents")
     T = parents.numel()
-    if dev.index != torch.cuda.current_device():
+    if dev.index != _current_device():
         with torch.cuda.device(dev):
             return tree_plan(batch, parents, tree)
     if tree is None:
@@ -937,7 +942,7 @@ def rope(x, positions, plan: Rope, out=None, inverse=False):
     rotation)."""
     D, dev = plan.head_dim, plan.device
     T, H, ldx = _rows_arg(x, "x", dev, D)
-    if dev.index != torch.cuda.current_device():
+    if dev.index != _current_device():
         with torch.cuda.device(dev):
             return rope(x, positions, plan, out, inverse)
     pos = _positions_arg(positions, dev, T)
@@ -957,7 +962,7 @@ def norm_rope(x, norm: HeadNorm, positions=None, plan: Rope | None = None, out=N
     no keys. `out` may be x."""
     D, dev = norm.head_dim, norm.device
     T, H, ldx = _rows_arg(x, "x", dev, D)
-    if dev.index != torch.cuda.current_device():
+    if dev.index != _current_device():
         with torch.cuda.device(dev):
             return norm_rope(x, norm, positions, plan, out)
     if plan is not None:
@@ -988,7 +993,7 @@ def kv_append(cache: PagedKV, batch: PagedBatch, k, v, rope: Rope | None = None,
     D, dev = cache.head_dim, cache.device
     _on(batch.device, dev, "batch")
     T, _, ldk = _rows_arg(k, "k", dev, D, cache.kv_heads)
-    if dev.index != torch.cuda.current_device():
+    if dev.index != _current_device():
         with torch.cuda.device(dev):
             return kv_append(cache, batch, k, v, rope, q, q_out, positions, norm)
     T2, _, ldv = _rows_arg(v, "v", dev, D, cache.kv_heads)
@@ -1032,7 +1037,7 @@ def kv_keep(layers: PagedLayers | PagedKV, batch: PagedBatch, path, kept, length
         layers = PagedLayers((layers,))
     dev, B = layers.device, batch.batch
     _on(batch.device, dev, "batch")
-    if dev.index != torch.cuda.current_device():
+    if dev.index != _current_device():
         with torch.cuda.device(dev):
             return kv_keep(layers, batch, path, kept, lengths)
     _check(path, "path", torch.int32, 2)
@@ -1061,7 +1066,7 @@ def attn_paged(cache: PagedKV, batch: PagedBatch, q, scale=None, causal=True, wi
     D, dev = cache.head_dim, cache.device
     _on(batch.device, dev, "batch")
     T, heads, ldq = _rows_arg(q, "q", dev, D)
-    if dev.index != torch.cuda.current_device():
+    if dev.index != _current_device():
         with torch.cuda.device(dev):
             return attn_paged(cache, batch, q, scale, causal, window, out, return_lse, tree)
     if out is None:

@@ -33,6 +33,21 @@ int device_ok() {
 
 bool a16(const void* p) { return aligned16(p); }
 
+// An array of n int32; no two of some share memory (NULL is none).
+struct Ints {
+  const int32_t* p;
+  int64_t n;
+};
+template <int N>
+bool apart(const Ints (&x)[N]) {
+  for (int i = 0; i < N; ++i)
+    for (int j = 0; j < i; ++j) {
+      const uintptr_t a = (uintptr_t)x[i].p, b = (uintptr_t)x[j].p;
+      if (a && b && a < b + 4 * (uintptr_t)x[j].n && b < a + 4 * (uintptr_t)x[i].n) return false;
+    }
+  return true;
+}
+
 }  // namespace
 
 }  // namespace qlin
@@ -278,6 +293,10 @@ int qlin_tree_plan(const qlin_kv_batch* batch, int64_t T, const int32_t* parents
   QLIN_CHECK(((uintptr_t)mask & 7) == 0 && (((uintptr_t)batch->q_start | (uintptr_t)batch->kv_len |
                                              (uintptr_t)parents | (uintptr_t)positions) & 3) == 0,
              QLIN_ERR_ALIGN);
+  const Ints bits = {(const int32_t*)mask, 2 * T * words}, at = {positions, T}, start = {batch->q_start, batch->batch + 1};
+  QLIN_CHECK(apart<3>({bits, at, start}) && apart<3>({bits, at, {batch->kv_len, batch->batch}}) &&
+                 apart<3>({bits, positions == parents ? Ints{} : at, {parents, T}}),
+             QLIN_ERR_ARG);
   const int rc = device_ok();
   if (rc) return rc;
   return launch_tree_plan(*batch, T, parents, words, mask, positions, as_stream(stream));
@@ -305,6 +324,12 @@ int qlin_kv_reserve(const qlin_kv_pool* pool, const qlin_kv_tables* tables, int6
   if (tables->batch == 0) return QLIN_OK;
   QLIN_CHECK(tables->q_start && lengths && new_tokens, QLIN_ERR_ARG);
   QLIN_CHECK((((uintptr_t)lengths | (uintptr_t)new_tokens) & 3) == 0, QLIN_ERR_ALIGN);
+  const qlin_kv_tables& t = *tables;
+  QLIN_CHECK(apart<9>({{t.page_table, t.batch * t.table_cols}, {t.q_start, t.batch + 1}, {t.kv_len, t.batch},
+                       {t.slots, T}, {t.positions, T}, {pool->free_pages, pool->pages}, {pool->count, 2},
+                       {lengths == t.kv_len || lengths == new_tokens ? nullptr : lengths, t.batch},
+                       {new_tokens, t.batch}}),
+             QLIN_ERR_ARG);
   rc = device_ok();
   if (rc) return rc;
   return launch_reserve(*pool, *tables, lengths, new_tokens, T, as_stream(stream));
@@ -317,6 +342,11 @@ int qlin_kv_release(const qlin_kv_pool* pool, const qlin_kv_tables* tables, cons
   if (tables->batch == 0) return QLIN_OK;
   QLIN_CHECK(lengths, QLIN_ERR_ARG);
   QLIN_CHECK(((uintptr_t)lengths & 3) == 0, QLIN_ERR_ALIGN);
+  const qlin_kv_tables& t = *tables;
+  const Ints list = {pool->free_pages, pool->pages}, count = {pool->count, 2};
+  QLIN_CHECK(apart<3>({list, count, {t.page_table, t.batch * t.table_cols}}) &&
+                 apart<3>({list, count, {t.kv_len, t.batch}}) && apart<3>({list, count, {lengths, t.batch}}),
+             QLIN_ERR_ARG);
   rc = device_ok();
   if (rc) return rc;
   return launch_release(*pool, *tables, lengths, as_stream(stream));
@@ -339,8 +369,14 @@ int qlin_kv_keep(const qlin_kv_cache* caches, int64_t n_caches, const qlin_kv_ba
                QLIN_ERR_SHAPE);
   }
   if (empty) return QLIN_OK;
-  QLIN_CHECK((path || path_cols == 0) && kept && lengths && lengths != batch->kv_len, QLIN_ERR_ARG);
+  QLIN_CHECK((path || path_cols == 0) && kept && lengths, QLIN_ERR_ARG);
   QLIN_CHECK((((uintptr_t)path | (uintptr_t)kept | (uintptr_t)lengths) & 3) == 0, QLIN_ERR_ALIGN);
+  const int64_t B = batch->batch;
+  const Ints out = {lengths, B};
+  QLIN_CHECK(apart<2>({out, {batch->kv_len, B}}) && apart<2>({out, {batch->q_start, B + 1}}) &&
+                 apart<2>({out, {batch->page_table, B * batch->table_cols}}) && apart<2>({out, {kept, B}}) &&
+                 apart<2>({out, {path, B * path_cols}}),
+             QLIN_ERR_ARG);
   const int rc = device_ok();
   if (rc) return rc;
   return launch_keep(caches, n_caches, *batch, path, path_cols, kept, lengths, as_stream(stream));

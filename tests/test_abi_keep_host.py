@@ -38,6 +38,17 @@ def test_refusals(q):
         assert keep(q, **bad) == q.ERR_ALIGN, bad
 
 
+def test_lengths_that_overlap(q):
+    """Every workgroup reads the batch, the path and its counts; one of them writes lengths."""
+    B, F = 8 * A, q.OK
+    far = dict(path=2 * B, kept=3 * B, lengths=4 * B, width=5)
+    b = batch(q, batch=6, q_start=5 * B, kv_len=6 * B, page_table=7 * B, table_cols=3)
+    for lengths in (2 * B, 2 * B + 4 * 29, 2 * B - 4 * 5, 3 * B, 3 * B + 20, 5 * B + 24, 6 * B - 4, 6 * B, 7 * B + 4 * 17):
+        assert keep(q, b=b, **{**far, "lengths": lengths}) == q.ERR_ARG, lengths
+    for lengths in (2 * B + 4 * 30, 2 * B - 4 * 6, 3 * B + 24, 5 * B + 28, 6 * B - 24, 7 * B + 4 * 18):
+        assert keep(q, b=b, **{**far, "lengths": lengths}) not in (q.ERR_ARG, F), lengths  # (no GPU here)
+
+
 def test_oracle_keep(oracle):
     pool = np.arange(3 * 16, dtype=np.int32).reshape(3, 1, 16, 1)  # three pages of one head
     table = np.array([[2, 0], [1, 1]], np.int32)

@@ -58,6 +58,31 @@ def test_refusals(q):
     assert release(q, lengths=A + 2) == q.ERR_ALIGN
 
 
+def test_arrays_that_overlap(q):
+    """What a call writes must not be what it reads or writes elsewhere, but for lengths in
+    place; what a release only reads may be one array."""
+    B = 8 * A
+    pl = dict(free_pages=2 * B, count=3 * B, pages=40)
+    t = dict(page_table=4 * B, q_start=5 * B, kv_len=6 * B, slots=7 * B, positions=8 * B, batch=6, table_cols=3)
+
+    def calls(pl, t, lengths=9 * B, new=10 * B):
+        return (reserve(q, pool(q, **pl), tables(q, **t), 11, lengths, new), release(q, pool(q, **pl), tables(q, **t), lengths))
+
+    apart = calls(pl, t)
+    assert q.ERR_ARG not in apart and calls(pl, t, lengths=6 * B) == apart and calls(pl, t, lengths=10 * B) == apart
+    assert calls(pl, {**t, "slots": None, "positions": None}) == apart
+    for pl2, t2, kw in (({"count": 2 * B + 4 * 39}, {}, {}), ({}, {"page_table": 2 * B - 4 * 17}, {}),
+                        ({}, {"kv_len": 3 * B + 4}, {}), ({}, {}, {"lengths": 2 * B + 4 * 39}), ({"count": 4 * B + 4 * 17}, {}, {})):
+        assert calls({**pl, **pl2}, {**t, **t2}, **kw) == (q.ERR_ARG, q.ERR_ARG), (pl2, t2, kw)
+    for t2, kw in (({"kv_len": 5 * B + 24}, {}), ({"q_start": 6 * B - 24}, {}), ({"slots": 8 * B - 40}, {}),
+                   ({"positions": 5 * B}, {}), ({}, {"lengths": 6 * B + 4}), ({}, {"new": 6 * B}), ({}, {"new": 5 * B + 24}),
+                   ({}, {"lengths": 4 * B + 4 * 17}), ({}, {"lengths": 10 * B + 4})):
+        got = calls(pl, {**t, **t2}, **kw)
+        assert got == (q.ERR_ARG, apart[1]), (t2, kw)
+    near = {**t, "q_start": 6 * B - 28, "slots": 8 * B - 44}
+    assert calls({**pl, "count": 2 * B + 160}, near) == apart
+
+
 def test_oracle_tables(oracle):
     table = np.full((3, 3), -5, np.int32)
     table[0, 0] = 4

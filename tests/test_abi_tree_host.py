@@ -141,3 +141,16 @@ def test_tree_plan_refusals(q):
                          (dict(b=batch(q, kv_len=None)), "ERR_ARG"), (dict(mask=A + 4), "ERR_ALIGN"),
                          (dict(parents=A + 2), "ERR_ALIGN"), (dict(positions=A + 1), "ERR_ALIGN")]:
         assert plan_call(q, **over) == getattr(q, status), over
+
+
+def test_tree_plan_arrays_that_overlap(q):
+    B = 8 * A
+    far = dict(b=batch(q, q_start=B, kv_len=2 * B, batch=6), parents=3 * B, mask=4 * B, positions=5 * B, T=11, words=2)
+    apart = plan_call(q, **far)
+    assert apart not in (q.OK, q.ERR_ARG)  # (no GPU here)
+    assert plan_call(q, **{**far, "positions": 3 * B}) == apart and plan_call(q, **{**far, "positions": None}) == apart
+    for at in (dict(mask=5 * B - 8 * 22 + 8), dict(mask=3 * B + 40), dict(mask=B + 24), dict(positions=2 * B + 20),
+               dict(positions=3 * B + 4), dict(positions=B - 40), dict(positions=4 * B + 8 * 22 - 4)):
+        assert plan_call(q, **{**far, **at}) == q.ERR_ARG, at
+    for at in (dict(mask=5 * B - 8 * 22), dict(mask=3 * B + 48), dict(positions=2 * B + 24), dict(positions=3 * B - 44)):
+        assert plan_call(q, **{**far, **at}) == apart, at

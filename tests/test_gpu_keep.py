@@ -162,3 +162,14 @@ def test_keep_binding_refusals(q):
         q.kv_keep(one, b, path.long(), kept)
     with pytest.raises(q.QlinError):
         q.kv_keep(one, b, path, kept, b.kv_len)
+
+
+def test_caches_that_share_memory(q):
+    c = q.PagedKV.empty(8, 2, 64, 16)
+    for caches in ([c, c], [c, q.PagedKV(c.v, torch.empty_like(c.v))], [q.PagedKV(c.k, c.k)]):
+        with pytest.raises(ValueError):
+            q.PagedLayers(caches)
+    whole = torch.empty(17, 2, 16, 64, dtype=torch.bfloat16, device="cuda")  # neighbours in one allocation
+    q.PagedLayers([q.PagedKV(whole[:8], c.v), q.PagedKV(whole[8:16], c.k)])
+    with pytest.raises(ValueError):
+        q.PagedLayers([q.PagedKV(whole[:8], c.v), q.PagedKV(whole[7:15], c.k)])

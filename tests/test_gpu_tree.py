@@ -97,6 +97,9 @@ def test_plan(q, oracle, new, words):
         bare = q.Tree(torch.full_like(tree.mask, 77))
         q.tree_plan(batch, dev(np.concatenate([parents, np.zeros(pad, np.int32)])), bare)
         assert torch.equal(bare.mask, tree.mask)
+        same = dev(np.concatenate([parents, np.full(pad, 77, np.int32)]))  # positions in the parents' place
+        q.tree_plan(batch, same, q.Tree(bare.mask, same))
+        assert torch.equal(same, tree.positions) and torch.equal(bare.mask, tree.mask)
         own = q.tree_plan(batch, dev(parents))
         wide = own.mask.shape[1]
         assert wide == -(-max(new) // 64) and torch.equal(own.mask, tree.mask[:T, :wide])
