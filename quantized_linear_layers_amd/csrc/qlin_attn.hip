@@ -1321,10 +1321,13 @@ __global__ __launch_bounds__(NW * 64, step_waves(D, FP8, RB, NW)) void attn_step
     }
 #pragma unroll
     for (int rb = 0; rb < RB; ++rb) {
-      // (each lane's own keys first: the row's maximum is needed only where it is raised)
-      float mx = fmaxf(s[rb][0][0], s[rb][0][1]);
+      // (each lane's own keys first: the row's maximum is needed only where it is raised.
+      // The first maximum, of both score blocks, is the compiler's, which waits for their
+      // products; max3's, which it would not wait for, all follow from it.)
+      float mx = fmaxf(s[rb][0][0], s[rb][1][0]);
 #pragma unroll
-      for (int i = 2; i < 8; i += 2) mx = max3(mx, s[rb][i / 4][i % 4], s[rb][i / 4][i % 4 + 1]);
+      for (int b = 0; b < 2; ++b) mx = max3(mx, s[rb][b][1], s[rb][b][2]);
+      mx = max3(mx, s[rb][0][3], s[rb][1][3]);
       if (__any(mx * a.c > m[rb] + 8.0f)) {
         const float top = fmaxf(m[rb], groups_max(mx) * a.c);
         const float f = top == -kInf ? 0.0f : exp2_hw(m[rb] - top);
