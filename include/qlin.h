@@ -548,7 +548,9 @@ typedef struct {
 
 /* qlin_kv_append of heads that are normalised first (in the same pass): by norm,
  * never NULL, which the queries' and keys' rotation follows if there is one. An E4M3
- * row is quantised from the normalised (and rotated) fp32 values. */
+ * row is quantised from the normalised (and rotated) fp32 values x, its codes those of
+ * x / (absmax / 448), rounded to fp32 once (values that are not normalised: as without
+ * norm). */
 int qlin_kv_append_norm(const qlin_kv_cache* cache, const qlin_kv_batch* batch, int64_t T,
                         const qlin_bf16* k, int64_t ldk, const qlin_bf16* v, int64_t ldv,
                         const qlin_head_norm* norm, const qlin_rope_plan* rope, const int32_t* positions,

@@ -8,11 +8,15 @@
 // Bound by memory from about 1000 tokens on: 8192 tokens of 32 heads of 128 26.5 us
 // (5.07 TB/s read and written); queries, keys and values of eight prompts of up to 1024
 // tokens into a bf16 cache 30.2 us (4.81 TB/s). E4M3 rows are short of that (2249 tokens,
-// heads of 256: 14.0 us, 3.61 TB/s): absmax, quotients that equal the per-token
+// heads of 256: 13.5 us, 3.74 TB/s): absmax, quotients that equal the per-token
 // quantiser's, and encoding take the vector unit as long. A decode step takes 3.7 us (8
 // tokens) to 5.2 (64 with the append): the launch and its loads, which are waited for one
 // after the other (positions or lengths and page, frequencies, heads) although of these
 // only the page needs the one before.
+//
+// Head norms (NORM) cost nothing where memory bounds the call: 8192 tokens of 32 heads of 128
+// 28.4 us (4.73 TB/s, 97% of a large copy's rate). E4M3 rows, bound by the vector unit, take
+// 15.3 us for 13.5 (2250 tokens of 16 + 8 heads of 256). A decode step takes 4.7.
 #include "qlin_internal.h"
 #include "qlin_device.h"
 #include "qlin_quant_row.h"
@@ -87,16 +91,23 @@ __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
 // is not zero the remainders are multiples of 2^-57 sc, exact for every sc from 2^-92 on.
 // Scales outside 2^-80 .. 2^90, the range that was compared with division (equal
 // quotients and signs in 8e9 random pairs), are divided.
+// REST: by sc + rest, what a scale was before it was rounded (rest is below 2^-24 sc):
+// the remainder is that much larger.
 // (true: by the reciprocal)
-__device__ __forceinline__ bool divide(Piece& p, float sc) {
+template <bool REST>
+__device__ __forceinline__ bool divide(Piece& p, float sc, float rest) {
   if (sc >= 0x1p-80f && sc <= 0x1p+90f) {
     const float y = 1.0f / sc;
+    auto one = [&](float& x) {
+      const float q = x * y;
+      float r = fmaf(q, sc, -x);
+      if (REST) r = fmaf(q, rest, r);
+      x = fmaf(-r, y, q);
+    };
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      float q = p.lo[i] * y;
-      p.lo[i] = fmaf(-fmaf(q, sc, -p.lo[i]), y, q);
-      q = p.hi[i] * y;
-      p.hi[i] = fmaf(-fmaf(q, sc, -p.hi[i]), y, q);
+      one(p.lo[i]);
+      one(p.hi[i]);
     }
     return true;
   }
@@ -154,19 +165,22 @@ __device__ __forceinline__ float max3_abs(float m, float x, float y) {
   return r;
 }
 
-// Sine and cosine of r turns, |r| <= 1/2: of the nearest quarter turn's remainder t, which
-// is exact, by their series in (2 pi t)^2 up to the powers 9 and 8 (at an eighth of a turn
-// the next terms are 2^-29 and 2^-25.3), then by the quarter.
-__device__ __forceinline__ void turn(float r, float& s, float& c) {
-  const float k = __builtin_rintf(4.0f * r), t = fmaf(-0.25f, k, r), u = t * t;
-  // (2 pi)^n / n!
-  float sine = fmaf(u, 42.0586939f, -76.7058597f);
-  sine = fmaf(u, sine, 81.6052493f);
-  sine = fmaf(u, sine, -41.3417022f);
-  sine = fmaf(u, sine, 6.28318531f) * t;
-  float cosine = fmaf(u, 60.2446413f, -85.4568172f);
-  cosine = fmaf(u, cosine, 64.9393940f);
-  cosine = fmaf(u, cosine, -19.7392088f);
+// Sine and cosine of r turns, |r| <= 1/2: of the nearest quarter turn's remainder t (in
+// quarters, taken in fp64: its fp32 value is within 2^-28 of a turn), by their series in
+// (pi t / 2)^2 up to the powers 9 and 10 (at an eighth of a turn the next terms are 2^-29
+// and 2^-33), then by the quarter.
+__device__ __forceinline__ void turn(double r, float& s, float& c) {
+  const double k = __builtin_rint(4.0 * r);
+  const float t = (float)__builtin_fma(4.0, r, -k), u = t * t;
+  // (pi / 2)^n / n!
+  float sine = fmaf(u, 1.60441185e-4f, -4.68175414e-3f);
+  sine = fmaf(u, sine, 7.96926262e-2f);
+  sine = fmaf(u, sine, -6.45964098e-1f);
+  sine = fmaf(u, sine, 1.57079633f) * t;
+  float cosine = fmaf(u, -2.52020424e-5f, 9.19260274e-4f);
+  cosine = fmaf(u, cosine, -2.08634808e-2f);
+  cosine = fmaf(u, cosine, 2.53669508e-1f);
+  cosine = fmaf(u, cosine, -1.23370055f);
   cosine = fmaf(u, cosine, 1.0f);
   const int q = (int)k;
   const float x = q & 1 ? cosine : sine, y = q & 1 ? sine : cosine;
@@ -176,8 +190,10 @@ __device__ __forceinline__ void turn(float r, float& s, float& c) {
 
 // A head's piece over the head's root mean square: p / sqrt(sum of squares / D + eps),
 // the sum over the head's n lanes in fp32. Squares that pass fp32's range (a value
-// above 1.8e19) are summed again of values times 2^-72.
-__device__ __forceinline__ void normalise(Piece& p, int n, float inv_d, float eps) {
+// above 1.8e19) are summed again of values times 2^-72. With CODES only the power of two
+// of 1 / sqrt is multiplied in, which rounds nothing; the rest, of [1, 2), is returned.
+template <bool CODES>
+__device__ __forceinline__ float normalise(Piece& p, int n, float inv_d, float eps, bool codes) {
   auto squares = [&] {
     float s = 0.0f;
 #pragma unroll
@@ -197,15 +213,19 @@ __device__ __forceinline__ void normalise(Piece& p, int n, float inv_d, float ep
     s = squares();
     eps = eps * 0x1p-72f * 0x1p-72f;
   }
-  times(__builtin_amdgcn_rsqf(fmaf(s, inv_d, eps)));
+  const float f = __builtin_amdgcn_rsqf(fmaf(s, inv_d, eps));
+  const uint32_t bits = __float_as_uint(f);
+  const bool both = !CODES || !codes;
+  times(both ? f : __uint_as_float(bits & 0x7F800000u));
+  return both ? 1.0f : __uint_as_float((bits & 0x007FFFFFu) | 0x3F800000u);
 }
 
 // APPEND: keys and values go to the cache; FP8: as E4M3 codes with a scale. NORM:
 // heads are normalised first. PH: pieces of a head, for those sizes that every cache has,
 // 0: any number of them. With NORM five waves a SIMD, so that the calls which fill the
 // device once do it with room: 2250 tokens of 16 + 8 heads of 256 into E4M3, normalised,
-// are 4500 waves and take 15.9 us, 18.2 with four waves a SIMD (and no register spilled;
-// five spill five, outside the loop over heads).
+// are 4500 waves and take 16.5 us, 18.2 with four waves a SIMD (and no register spilled;
+// five spill seven, outside the loop over heads).
 template <int PH, bool APPEND, bool FP8, bool NORM>
 __global__ __launch_bounds__(kRopeThreads, NORM ? 5 : 1) void rope_kernel(const RopeArgs a) {
   const int D = PH ? 16 * PH : a.D, per_head = D / 16;
@@ -268,12 +288,12 @@ __global__ __launch_bounds__(kRopeThreads, NORM ? 5 : 1) void rope_kernel(const 
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const double w = pos * a.turns[8 * c + i];
-      const float r = (float)(w - __builtin_rint(w));
+      const double r = w - __builtin_rint(w);
       float s, co;
       if (NORM)
         turn(r, s, co);
       else
-        sincospif(2.0f * r, &s, &co);
+        sincospif(2.0f * (float)r, &s, &co);
       cs[i] = co * a.magnitude;
       sn[i] = s * a.magnitude * a.sign;
       if (NORM && i % 2) __builtin_amdgcn_sched_barrier(0);  // (two at a time: registers)
@@ -295,8 +315,9 @@ __global__ __launch_bounds__(kRopeThreads, NORM ? 5 : 1) void rope_kernel(const 
     unpack_bf16x8(r0, p.lo);
     unpack_bf16x8(r1, p.hi);
     const bool normed = NORM && ((a.normed >> part) & 1);
+    float factor = 1.0f;  // of the whole row, not multiplied in: a row's scale takes it
     if (normed) {
-      normalise(p, per_head, a.inv_d, a.eps);
+      factor = normalise<FP8>(p, per_head, a.inv_d, a.eps, part > 0);
       // times (offset + weight), in fp32 as all up to the one rounding at the end
       const float offset = weight ? a.offset : 1.0f;
       Piece w;
@@ -354,9 +375,13 @@ __global__ __launch_bounds__(kRopeThreads, NORM ? 5 : 1) void rope_kernel(const 
     for (int i = 0; i < 8; ++i) m = max3_abs(m, p.lo[i], p.hi[i]);
     m = head_join<true>(m, per_head);
     const float sc = m > 0.0f ? m / 448.0f : 0.0f;
+    // Rows that are stored as they came have the per-token quantiser's codes, of the
+    // quotient by the rounded scale; of normalised ones nothing is rounded but the
+    // weight's and rotation's products and the quotient by the largest / 448.
+    const float rest = normed ? fmaf(-sc, 448.0f, m) * (1.0f / 448.0f) : 0.0f;
     uint2 q0 = make_uint2(0, 0), q1 = make_uint2(0, 0);
     if (sc > 0.0f) {
-      if (divide(p, sc)) {
+      if (divide<NORM>(p, sc, rest)) {
         q0 = codes8(p.lo);
         q1 = codes8(p.hi);
       } else {
@@ -367,7 +392,7 @@ __global__ __launch_bounds__(kRopeThreads, NORM ? 5 : 1) void rope_kernel(const 
     uint8_t* dst = pool + row * D;
     *reinterpret_cast<uint2*>(dst + o0) = q0;
     *reinterpret_cast<uint2*>(dst + o1) = q1;
-    if (c == 0) (part == 1 ? a.ks : a.vs)[row] = sc;
+    if (c == 0) (part == 1 ? a.ks : a.vs)[row] = sc * factor;
   }
 }
 
