@@ -20,7 +20,7 @@
 // Bound by latency: the launch (1.8 us) and loads that each need the one before. A tree of 8
 // 2.0 us, 256 of up to 256 tokens 5.9 (ten barriers and masks of 1.7 MB); the tables of 64
 // requests with up to 16 new tokens 3.5 and, back, 3.0; 64 prompts of up to 8192 tokens, 17000
-// pages of 16, 1.9 + 4.7 and 8.7.
+// pages of 16, 1.9 + 4.7 and 8.3.
 #include "qlin_internal.h"
 #include "qlin_device.h"
 
@@ -320,42 +320,57 @@ __global__ __launch_bounds__(NT) void release_kernel(const TablesArgs a) {
     const int share = 31 - __clz(NT / here), lanes = 1 << share, g = i & (lanes - 1), r = i >> share;
     // a thread's entries, e counted from its request's last: whole fours (four of them on
     // their way together), and what is left singly
-    auto each = [&](auto four, auto one) {
-      if (r >= here) return;
-      const int entries = count[r], whole = entries & ~3;
-      if (entries == 0) return;
-      const int32_t* row = a.table + (b1 - 1 - r) * a.cols + end[r];
-      const int64_t at = to[r];
-      for (int64_t e0 = 4 * g; e0 < whole; e0 += 16 * lanes) {
-        Four p[4];
+    const int entries = r < here ? count[r] : 0, whole = entries & ~3;
+    const int32_t* row = a.table + (entries ? (b1 - 1 - r) * a.cols + end[r] : 0);
+    const int64_t at0 = entries ? to[r] : 0;
+    auto load = [&](int64_t e0, Four (&p)[4]) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if (e0 + 4 * k * lanes < whole) p[k] = *reinterpret_cast<const Four*>(row - (e0 + 4 * k * lanes) - 3);
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if (e0 + 4 * k * lanes < whole) four(at + e0 + 4 * k * lanes, p[k]);
-      }
-      for (int e = whole + g; e < entries; e += lanes) one(at + e, row[-e]);
+      for (int k = 0; k < 4; ++k)
+        if (e0 + 4 * k * lanes < whole) p[k] = *reinterpret_cast<const Four*>(row - (e0 + 4 * k * lanes) - 3);
     };
     bool bad = false;
     const uint32_t pages = (uint32_t)a.pages;
-    each([&](int64_t, const Four& p) {
-      bad |= (uint32_t)p.x[0] >= pages || (uint32_t)p.x[1] >= pages || (uint32_t)p.x[2] >= pages || (uint32_t)p.x[3] >= pages;
-    }, [&](int64_t, int32_t p) { bad |= (uint32_t)p >= pages; });
-    if (!__syncthreads_or(bad)) {
-      each([&](int64_t slot, const Four& p) {
+    auto look = [&](int64_t e0, const Four (&p)[4]) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (e0 + 4 * k * lanes < whole)
+          bad |= (uint32_t)p[k].x[0] >= pages || (uint32_t)p[k].x[1] >= pages || (uint32_t)p[k].x[2] >= pages ||
+                 (uint32_t)p[k].x[3] >= pages;
+    };
+    auto write = [&](int64_t e0, const Four (&p)[4]) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int64_t e = e0 + 4 * k * lanes, slot = at0 + e;
+        if (e >= whole) break;
         if (slot + 3 < a.pages) {
-          *reinterpret_cast<Four*>(a.free_pages + slot) = Four{{p.x[3], p.x[2], p.x[1], p.x[0]}};
+          *reinterpret_cast<Four*>(a.free_pages + slot) = Four{{p[k].x[3], p[k].x[2], p[k].x[1], p[k].x[0]}};
         } else {
-          for (int k = 0; k < 4; ++k)
-            if (slot + k < a.pages) a.free_pages[slot + k] = p.x[3 - k];
+          for (int j = 0; j < 4; ++j)
+            if (slot + j < a.pages) a.free_pages[slot + j] = p[k].x[3 - j];
         }
-      }, [&](int64_t slot, int32_t p) {
-        if (slot < a.pages) a.free_pages[slot] = p;
-      });
+      }
+    };
+    Four kept[4], p[4];  // (the first sixteen stay in registers between the two passes)
+    const int left = whole + g < entries ? row[-(whole + g)] : 0;
+    load(4 * g, kept);
+    look(4 * g, kept);
+    for (int64_t e0 = 4 * g + 16 * lanes; e0 < whole; e0 += 16 * lanes) {
+      load(e0, p);
+      look(e0, p);
+    }
+    // (less than four are left: a lane has one, or all with one or two lanes)
+    for (int e = whole + g; e < entries; e += lanes) bad |= (uint32_t)row[-e] >= pages;
+    if (!__syncthreads_or(bad)) {
+      write(4 * g, kept);
+      for (int64_t e0 = 4 * g + 16 * lanes; e0 < whole; e0 += 16 * lanes) {
+        load(e0, p);
+        write(e0, p);
+      }
+      for (int e = whole + g; e < entries; e += lanes)
+        if (at0 + e < a.pages) a.free_pages[at0 + e] = e == whole + g ? left : row[-e];
       have += all.a;
     } else {  // (entries that are no page are passed over: a thread a request counts first)
-      const int32_t* row = a.table + (b1 - 1 - i) * a.cols + (n ? end[i] : 0);
+      row = a.table + (b1 - 1 - i) * a.cols + (n ? end[i] : 0);
       int64_t good = 0;
       for (int e = 0; e < n; ++e) good += (uint32_t)row[-e] < pages;
       Sums pushed;

@@ -194,3 +194,59 @@ def test_requests_that_end_and_start(q, oracle):
                                      host(s.tables.page_table), D ** -0.5, True, 0, host(s.tree.mask).view(np.uint64),
                                      host(s.tree.positions))
             attn_check(want, host(got), host(lse), D, f"{lengths} {new} layer {i}")
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+def test_queries_in_place(q, fmt):
+    """A fused projection's queries normalised and turned where they lie."""
+    rng = np.random.default_rng(5)
+    start, table = torch.tensor([0, 7, 40], dtype=torch.int32, device="cuda"), torch.arange(8, dtype=torch.int32, device="cuda")
+    b = q.PagedBatch(start, torch.tensor([20, 33], dtype=torch.int32, device="cuda"), table.view(2, 4), 33)
+    norm, rope = q.HeadNorm(dev(projections(rng, (64,))), head_dim=64), q.Rope(64)
+    for T in (40, 43):
+        qkv = dev(projections(rng, (T, 8, 64)))
+        other = qkv.clone()
+        one, two = stale_pool(q, 8, 2, 16, 64, fmt), stale_pool(q, 8, 2, 16, 64, fmt)
+        want = q.kv_append(one, b, qkv[:, 4:6], qkv[:, 6:], rope, qkv[:, :4], norm=norm)
+        got = q.kv_append(two, b, other[:, 4:6], other[:, 6:], rope, other[:, :4], other[:, :4], norm=norm)
+        assert torch.equal(got[:40].view(torch.int16), want[:40].view(torch.int16)) and torch.equal(
+            other[:, 4:].view(torch.int16), qkv[:, 4:].view(torch.int16))
+        assert torch.equal(other[40:].view(torch.int16), qkv[40:].view(torch.int16))
+        assert torch.equal(one.k.view(torch.uint8), two.k.view(torch.uint8)) and torch.equal(one.v.view(torch.uint8), two.v.view(torch.uint8))
+        x = qkv[:, :4].contiguous()
+        want = q.norm_rope(x, norm, table[:1].expand(T).contiguous(), rope)
+        assert q.norm_rope(x, norm, table[:1].expand(T).contiguous(), rope, out=x) is x
+        assert torch.equal(x.view(torch.int16), want.view(torch.int16))
+
+
+def test_empty_calls(q):
+    """No tokens, no requests, requests without tokens: nothing is written and nothing fails."""
+    i32 = dict(dtype=torch.int32, device="cuda")
+    cache, rope, norm = stale_pool(q, 4, 2, 16, 64, "bf16"), q.Rope(64), q.HeadNorm(head_dim=64)
+    before = cache.k.clone()
+    none = torch.empty((0, 4, 64), dtype=torch.bfloat16, device="cuda")
+    for B in (0, 3):
+        pool = q.PagePool.full(4, 16)
+        tables = q.PageTables(pool, torch.full((B, 2), -1, **i32), 0, 1)
+        zeros = torch.zeros(B, **i32)
+        b = tables.reserve(zeros, zeros)
+        tree = q.tree_plan(b, torch.empty(0, **i32))
+        assert tree.mask.shape == (0, 1)
+        out = q.kv_append(cache, b, none[:, :2], none[:, :2], rope, none, positions=tree.positions, norm=norm)
+        assert out.shape == none.shape and q.norm_rope(none, norm, tree.positions, rope).shape == none.shape
+        out, lse = q.attn_paged(cache, b, none, tree=tree, return_lse=True)
+        assert out.shape == none.shape and lse.shape == (0, 4)
+        assert q.kv_keep(cache, b, torch.zeros((B, 5), **i32), zeros).tolist() == [0] * B
+        assert q.kv_keep(cache, b, torch.zeros((B, 0), **i32), zeros).tolist() == [0] * B
+        tables.release(zeros)
+        assert host(pool.count).tolist() == [4, 0] and host(b.q_start).tolist() == [0] * (B + 1)
+    # rows that belong to no request
+    x = torch.full((5, 8, 64), 2.0, dtype=torch.bfloat16, device="cuda")
+    b = q.PagedBatch(torch.zeros(4, **i32), torch.zeros(3, **i32), torch.zeros((3, 2), **i32), 1)
+    tree = q.Tree(torch.full((5, 1), 7, dtype=torch.int64, device="cuda"), torch.full((5,), 7, **i32))
+    q.tree_plan(b, torch.zeros(5, **i32), tree)
+    assert (tree.mask == 7).all() and (tree.positions == 7).all()
+    out = torch.full((5, 4, 64), 3.0, dtype=torch.bfloat16, device="cuda")
+    q.kv_append(cache, b, x[:, 4:6], x[:, 6:], rope, x[:, :4], out, norm=norm)
+    q.attn_paged(cache, b, x[:, :4], out=out, tree=tree)
+    assert (out == 3.0).all() and torch.equal(cache.k.view(torch.int16), before.view(torch.int16))
