@@ -1120,15 +1120,17 @@ constexpr int merge_turns(int D, int rows, int ring) {
 // read), so that as many are on their way at every wait. Two where LDS has room for
 // them beside as many workgroups: E4M3 tiles of 32 rows (with the one resource a tile
 // below, 64 trees of 16 over up to 4096 keys: 97 us for 103).
-constexpr int step_places(int D, bool fp8, int rb) { return fp8 && rb == 2 && D >= 128 ? 2 : 1; }
+constexpr int step_places(int D, bool fp8, int rb, bool tree) { return tree && fp8 && rb == 2 && D >= 128 ? 2 : 1; }
 
-template <int D, bool FP8, int RB, int NW, bool TREE>
+// WHOLE (E4M3): a page holds a tile, which then takes one resource: 64 times 8 tokens of 4096,
+// 8 heads of 64 and 32: 51 us for 58. (In bf16, of twice the loads, it makes no difference.)
+template <int D, bool FP8, int RB, int NW, bool TREE, bool WHOLE>
 __global__ __launch_bounds__(NW * 64, step_waves(D, FP8, RB, NW)) void attn_step_kernel(const AttnArgs a) {
   using St = Stage<D, FP8, 32, 16, true>;
   using G = Geo<D, FP8, true>;
   constexpr int kStage = 2 * St::kTile + 2 * St::kScale;     // K, V, their scales
-  constexpr int kOps = 2 * St::kLoads + (FP8 ? 1 : 0);       // loads of a K or V tile, at least
-  constexpr int R = step_places(D, FP8, RB);
+  constexpr int kOps = 2 * St::kLoads + (FP8 ? WHOLE ? 1 : 2 : 0);  // loads of a K or V tile
+  constexpr int R = step_places(D, FP8, RB, TREE);
   // the merge, of all columns or of half of them at a time, where that keeps it in the
   // room of the places (E4M3, heads of 128, 32 rows: 37 KB for 68, three workgroups a CU
   // for two)
@@ -1181,51 +1183,51 @@ __global__ __launch_bounds__(NW * 64, step_waves(D, FP8, RB, NW)) void attn_step
   uint32_t place = 0;  // of the tile that is worked on, in bytes
   auto next_place = [&] { place = R == 1 || place == (R - 1) * kStage ? 0 : place + kStage; };
   const int hi = R > 1 ? min(rg.hi, 32 * t1) : rg.hi;
-  const bool whole = a.page_shift >= 5;  // a tile lies in one page
-  const int scale_step = whole ? 64 : 256;  // from the scales of a tile's first 16 keys to the others'
-  // The rows of tile t (x, or x and y), and K (or V) rows of them with their scales. (By
-  // value: an array of these would lie in memory.)
+  constexpr int kScaleStep = WHOLE ? 64 : 256;  // from the scales of a tile's first 16 keys to the others'
+  // Where tile t lies, and K (or V) rows of it with their scales. (By value: an array of
+  // these would lie in memory. The rows of two pages are found for K and for V: kept, they
+  // cost scalar registers, E4M3, heads of 128, pages of 16, four times 16 tokens of 512: 11.9
+  // us for 11.4.)
   struct Tile {
-    Rows16 x, y;
+    Rows16 rows;      // WHOLE
+    int page0, page1;
   };
   auto rows_at = [&](int t, int page0, int page1) {
     Tile w;
-    w.x = whole ? rows_of<32>(a, it, t * 32, page0, hi) : rows_of(a, it, t * 32, page0, hi);
-    w.y = rows_of(a, it, t * 32 + 16, page1, hi);
+    if (WHOLE) w.rows = rows_of<32>(a, it, t * 32, page0, hi);
+    w.page0 = page0;
+    w.page1 = page1;
     return w;
   };
   auto load = [&](int t, const Tile w, auto is_v, auto edge) {
     const uint32_t to = lk0 + place + (is_v ? St::kTile : 0), scales = lk0 + place + 2 * St::kTile + (is_v ? St::kScale : 0);
     const int skip = rg.lo - t * 32;
-    if (whole) {
-      v4i rs = resource<G::kRow>(is_v ? a.v : a.k, w.x);
-      settled(rs);
+    if constexpr (WHOLE) {
+      v4i rs = resource<G::kRow>(is_v ? a.v : a.k, w.rows), sc = resource<4>(is_v ? a.vs : a.ks, w.rows);
+      settled(rs, sc);
       St::template rows32<is_v, edge>(rs, skip, to);
-      if constexpr (FP8) {
-        v4i sc = resource<4>(is_v ? a.vs : a.ks, w.x);
-        settled(sc);
-        St::template scale_rows32<edge>(sc, skip, scales);
-      }
-      return;
+      St::template scale_rows32<edge>(sc, skip, scales);
+    } else {
+      auto half = [&](int page, int n) {
+        const Rows16 x = rows_of(a, it, t * 32 + 16 * n, page, hi);
+        v4i rs = resource<G::kRow>(is_v ? a.v : a.k, x);
+        settled(rs);
+        St::template rows<is_v, edge>(rs, skip - 16 * n, 16 * n, to);
+        if constexpr (FP8) {
+          v4i sc = resource<4>(is_v ? a.vs : a.ks, x);
+          settled(sc);
+          St::template scale_row<edge>(sc, skip - 16 * n, 16 * n, scales);
+        }
+      };
+      half(w.page0, 0);
+      half(w.page1, 1);
     }
-    auto half = [&](const Rows16 x, int n) {
-      v4i rs = resource<G::kRow>(is_v ? a.v : a.k, x);
-      settled(rs);
-      St::template rows<is_v, edge>(rs, skip - 16 * n, 16 * n, to);
-      if constexpr (FP8) {
-        v4i sc = resource<4>(is_v ? a.vs : a.ks, x);
-        settled(sc);
-        St::template scale_row<edge>(sc, skip - 16 * n, 16 * n, scales);
-      }
-    };
-    half(w.x, 0);
-    half(w.y, 1);
   };
   constexpr std::integral_constant<bool, true> kYes;
   constexpr std::integral_constant<bool, false> kNo;
   auto pages = [&](int t, int (&page)[2]) {
     page[0] = page_of(a, it, t * 32);
-    page[1] = whole ? page[0] : page_of(a, it, t * 32 + 16);
+    page[1] = WHOLE ? page[0] : page_of(a, it, t * 32 + 16);
   };
   int t = t0 + wave;
   int page[R][2], next[2];  // of the tiles in the places; of the next one to be loaded
@@ -1294,7 +1296,7 @@ __global__ __launch_bounds__(NW * 64, step_waves(D, FP8, RB, NW)) void attn_step
     if (FP8) {
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
-        const v4f k = *reinterpret_cast<const v4f*>(at + 2 * St::kTile + scale_step * b + 16 * g);
+        const v4f k = *reinterpret_cast<const v4f*>(at + 2 * St::kTile + kScaleStep * b + 16 * g);
 #pragma unroll
         for (int rb = 0; rb < RB; ++rb)
 #pragma unroll
@@ -1355,7 +1357,7 @@ __global__ __launch_bounds__(NW * 64, step_waves(D, FP8, RB, NW)) void attn_step
     if (FP8) {
 #pragma unroll
       for (int b = 0; b < 2; ++b)
-        sv[b] = *reinterpret_cast<const v4f*>(at + 2 * St::kTile + St::kScale + scale_step * b + 16 * g);
+        sv[b] = *reinterpret_cast<const v4f*>(at + 2 * St::kTile + St::kScale + kScaleStep * b + 16 * g);
     }
 #pragma unroll
     for (int rb = 0; rb < RB; ++rb) {
@@ -1741,29 +1743,34 @@ Plan plan_of(const qlin_kv_cache& cache, const qlin_kv_batch& batch, int64_t T, 
                                                              : chunk_plan(cache, batch, T, rows, group, keys);
 }
 
+template <int D, bool FP8, bool TREE, bool WHOLE>
+void launch_step(const AttnArgs& a, const Plan& p, hipStream_t st) {
+  const dim3 grid(a.kv_heads * p.row_tiles, a.B, p.splits);
+  if constexpr (TREE && (D < 256 || FP8)) {
+    if (p.part_rows <= 16 && p.wide) {
+      attn_step_kernel<D, FP8, 1, 8, TREE, WHOLE><<<grid, 512, 0, st>>>(a);
+      return;
+    }
+  }
+  if constexpr (TREE && D < 256) {
+    if (p.part_rows > 16 && p.wide) {
+      attn_step_kernel<D, FP8, 2, 8, TREE, WHOLE><<<grid, 512, 0, st>>>(a);
+      return;
+    }
+  }
+  if constexpr (!(TREE && FP8 && D == 256)) {  // (its trees have 16 rows a workgroup)
+    if (p.part_rows > 16) {
+      attn_step_kernel<D, FP8, 2, 4, TREE, WHOLE><<<grid, 256, 0, st>>>(a);
+      return;
+    }
+  }
+  attn_step_kernel<D, FP8, 1, 4, TREE, WHOLE><<<grid, 256, 0, st>>>(a);
+}
+
 template <int D, bool FP8, bool TREE>
 void launch_parts(const AttnArgs& a, const Plan& p, hipStream_t st) {
   if (p.step) {
-    const dim3 grid(a.kv_heads * p.row_tiles, a.B, p.splits);
-    if constexpr (TREE && (D < 256 || FP8)) {
-      if (p.part_rows <= 16 && p.wide) {
-        attn_step_kernel<D, FP8, 1, 8, TREE><<<grid, 512, 0, st>>>(a);
-        return;
-      }
-    }
-    if constexpr (TREE && D < 256) {
-      if (p.part_rows > 16 && p.wide) {
-        attn_step_kernel<D, FP8, 2, 8, TREE><<<grid, 512, 0, st>>>(a);
-        return;
-      }
-    }
-    if constexpr (!(TREE && FP8 && D == 256)) {  // (its trees have 16 rows a workgroup)
-      if (p.part_rows > 16) {
-        attn_step_kernel<D, FP8, 2, 4, TREE><<<grid, 256, 0, st>>>(a);
-        return;
-      }
-    }
-    attn_step_kernel<D, FP8, 1, 4, TREE><<<grid, 256, 0, st>>>(a);
+    FP8 && a.page_shift >= 5 ? launch_step<D, FP8, TREE, FP8>(a, p, st) : launch_step<D, FP8, TREE, false>(a, p, st);
   } else {
     const int64_t items = p.tiles * a.kv_heads * p.splits;
     const unsigned grid = (unsigned)((items + 7) / 8 * 8);
