@@ -590,7 +590,7 @@ def _rows_arg(t, name, dev, head_dim, heads=None):
 
 def _like(t):
     """A new contiguous tensor of t's shape."""
-    return torch.empty_like(t) if t.is_contiguous() else t.new_empty(t.shape)
+    return torch.empty_like(t, memory_format=torch.contiguous_format)
 
 
 def _int64(x, name):
