@@ -657,7 +657,9 @@ int qlin_kv_keep(const qlin_kv_cache* caches, int64_t n_caches, const qlin_kv_ba
  * at and may be NULL): plan[0] rows of a workgroup (32: the kernel of decode steps
  * and small chunks; 128 or, E4M3, 256: chunks; 0: an empty call), plan[1] parts of
  * the key axis, at most, plan[2] bytes of the workspace that the call uses, never
- * more than qlin_attn_workspace_bytes, which has to hold for every window. */
+ * more than qlin_attn_workspace_bytes, which has to hold for every window.
+ * qlin_attn_tree_plan: the same of qlin_attn_tree (plan[0] may be 16, max_q is at most
+ * 512, plan[2] never more than qlin_attn_tree_workspace_bytes). */
 int qlin_attn_plan(const qlin_kv_cache* cache, const qlin_kv_batch* batch, int64_t T, int64_t q_heads,
                    int64_t window, int64_t plan[3]);
 int qlin_attn_tree_plan(const qlin_kv_cache* cache, const qlin_kv_batch* batch, int64_t T, int64_t q_heads,

@@ -1082,7 +1082,8 @@ def attn_paged(cache: PagedKV, batch: PagedBatch, q, scale=None, causal=True, wi
         if not causal:
             raise ValueError("a tree's masks replace causal")
     lse = q.new_empty((T, heads), dtype=torch.float32) if return_lse else None
-    key = (T, heads, D, cache.kv_heads, cache.page_size, cache.fmt, tree is None)  # what the size depends on beside the batch's own
+    # what the size depends on beside the batch's own
+    key = (T, heads, D, cache.kv_heads, cache.page_size, cache.fmt, tree is None)
     nb = batch._ws_bytes.get(key)
     if nb is None:
         size = _lib.qlin_attn_workspace_bytes if tree is None else _lib.qlin_attn_tree_workspace_bytes

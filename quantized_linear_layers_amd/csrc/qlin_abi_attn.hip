@@ -293,7 +293,8 @@ int qlin_tree_plan(const qlin_kv_batch* batch, int64_t T, const int32_t* parents
   QLIN_CHECK(((uintptr_t)mask & 7) == 0 && (((uintptr_t)batch->q_start | (uintptr_t)batch->kv_len |
                                              (uintptr_t)parents | (uintptr_t)positions) & 3) == 0,
              QLIN_ERR_ALIGN);
-  const Ints bits = {(const int32_t*)mask, 2 * T * words}, at = {positions, T}, start = {batch->q_start, batch->batch + 1};
+  const Ints bits = {(const int32_t*)mask, 2 * T * words}, at = {positions, T};
+  const Ints start = {batch->q_start, batch->batch + 1};
   QLIN_CHECK(apart<3>({bits, at, start}) && apart<3>({bits, at, {batch->kv_len, batch->batch}}) &&
                  apart<3>({bits, positions == parents ? Ints{} : at, {parents, T}}),
              QLIN_ERR_ARG);

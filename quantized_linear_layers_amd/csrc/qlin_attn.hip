@@ -245,7 +245,8 @@ struct Stage {
 #pragma unroll
       for (int i = 0; i < kOnce; ++i) {
         const int row = (j + i) * G::kRowsPerLoad + lane / G::kChunks;
-        off[i] = (uint32_t)(j * 1024 + lane / G::kChunks * G::kRow + 16 * (lane % G::kChunks ^ (V ? G::v_swz(row) : G::k_swz(row))));
+        off[i] = (uint32_t)(j * 1024 + lane / G::kChunks * G::kRow +
+                            16 * (lane % G::kChunks ^ (V ? G::v_swz(row) : G::k_swz(row))));
         if (EDGE && row < skip) off[i] = 0x80000000u;
       }
       dma16<kOnce>(lds + j * 1024, off, rs);
@@ -1171,7 +1172,8 @@ __global__ __launch_bounds__(NW * 64, step_waves(D, FP8, RB, NW)) void attn_step
       sum += __shfl_xor(sum, o, kWave);
     }
     // (at least 1: a batch without any key has rows to write too)
-    const int share = max(max((longest + a.splits - 1) / a.splits, 1), (int)(sum * (float)a.kv_heads * (1.0f / kPieces)));
+    const int share =
+        max(max((longest + a.splits - 1) / a.splits, 1), (int)(sum * (float)a.kv_heads * (1.0f / kPieces)));
     const int n = __builtin_amdgcn_readfirstlane((share + NW - 1) / NW * NW);
     parts = max((t1 - t0 + n - 1) / n, 1);
     if (split >= parts) return;
@@ -1200,7 +1202,8 @@ __global__ __launch_bounds__(NW * 64, step_waves(D, FP8, RB, NW)) void attn_step
     return w;
   };
   auto load = [&](int t, const Tile w, auto is_v, auto edge) {
-    const uint32_t to = lk0 + place + (is_v ? St::kTile : 0), scales = lk0 + place + 2 * St::kTile + (is_v ? St::kScale : 0);
+    const uint32_t to = lk0 + place + (is_v ? St::kTile : 0);
+    const uint32_t scales = lk0 + place + 2 * St::kTile + (is_v ? St::kScale : 0);
     const int skip = rg.lo - t * 32;
     if constexpr (WHOLE) {
       v4i rs = resource<G::kRow>(is_v ? a.v : a.k, w.rows), sc = resource<4>(is_v ? a.vs : a.ks, w.rows);
@@ -1466,12 +1469,12 @@ __global__ __launch_bounds__(NW * 64, step_waves(D, FP8, RB, NW)) void attn_step
       const int row = i / (kCols / 4), c = i % (kCols / 4) * 4, c4 = c + kCols * turn;
       float mm = -kInf, ll = 0.0f;
       v4f x = {};
-  #pragma unroll
+#pragma unroll
       for (int w = 0; w < NW; ++w) {
         mm = fmaxf(mm, wm[w][row]);
         ll += wl[w][row];
         const v4f y = *reinterpret_cast<const v4f*>(all + (w * kRows + row) * kOut + c);
-  #pragma unroll
+#pragma unroll
         for (int j = 0; j < 4; ++j) x[j] += y[j];
       }
       if (parts == 1) {
@@ -1509,7 +1512,8 @@ __global__ __launch_bounds__(NW * 64, step_waves(D, FP8, RB, NW)) void attn_step
       v4i y[8];
 #pragma unroll
       for (int b = 0; b < 8; ++b)
-        y[b] = __builtin_amdgcn_raw_buffer_load_b128(ro, ((min(s0 + b, parts - 1) * a.part_rows + row) * D + c4) * 4, 0, kSc1);
+        y[b] = __builtin_amdgcn_raw_buffer_load_b128(
+            ro, ((min(s0 + b, parts - 1) * a.part_rows + row) * D + c4) * 4, 0, kSc1);
 #pragma unroll
       for (int b = 0; b < 8; ++b) {
         if (s0 + b < parts) {

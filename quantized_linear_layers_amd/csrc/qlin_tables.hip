@@ -207,7 +207,9 @@ __device__ __forceinline__ void fill(const TablesArgs& a, int64_t b, const Known
       const int32_t at = s.r.len + (int)i;
       if (i >= n) break;
       if (a.slots)
-        slots[i] = (uint32_t)page[k] < (uint32_t)a.pages ? (page[k] << a.page_shift) + (at & ((1 << a.page_shift) - 1)) : -1;
+        slots[i] = (uint32_t)page[k] < (uint32_t)a.pages
+                       ? (page[k] << a.page_shift) + (at & ((1 << a.page_shift) - 1))
+                       : -1;
       if (a.positions) positions[i] = at;
     }
   }
