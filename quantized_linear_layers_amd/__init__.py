@@ -781,9 +781,9 @@ class PagedLayers:
             _on(c.device, one.device, "cache")
             if c.k.shape != one.k.shape or c.fmt != one.fmt:
                 raise ValueError("the caches must have one size and format")
-        size = one.k.numel() * one.k.element_size()
-        at = sorted(t.data_ptr() for c in self.caches for t in (c.k, c.v))
-        if size and any(b - a < size for a, b in zip(at, at[1:])):  # (rows would be moved twice)
+        at = sorted((t.data_ptr(), t.numel() * t.element_size()) for c in self.caches
+                    for t in (c.k, c.v, c.k_scale, c.v_scale) if t is not None and t.numel())
+        if any(a + size > b for (a, size), (b, _) in zip(at, at[1:])):  # (rows would be moved twice)
             raise ValueError("the caches must not share memory")
         self.device = one.device
         self._c = (_KVCache * len(self.caches))(*(c._c for c in self.caches))

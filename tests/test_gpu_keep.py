@@ -173,3 +173,7 @@ def test_caches_that_share_memory(q):
     q.PagedLayers([q.PagedKV(whole[:8], c.v), q.PagedKV(whole[8:16], c.k)])
     with pytest.raises(ValueError):
         q.PagedLayers([q.PagedKV(whole[:8], c.v), q.PagedKV(whole[7:15], c.k)])
+    e = [q.PagedKV.empty(4, 2, 64, 16, "e4m3") for _ in range(2)]
+    q.PagedLayers(e)
+    with pytest.raises(ValueError):
+        q.PagedLayers([e[0], q.PagedKV(e[1].k, e[1].v, e[0].v_scale, e[1].v_scale)])
