@@ -19,6 +19,12 @@ def table_cols(keys, page):
     return -(-keys // page)
 
 
+def ordered(new, Hkv, G, tile):
+    """Whether the longest sequences come first: a grid that does not fit the device at once,
+    of at most 256 sequences."""
+    return len(new) <= 256 and len(new) * Hkv * -(-max(new) * G // tile) > 512
+
+
 @pytest.mark.parametrize("page", [32, 64, 256])
 @pytest.mark.parametrize("name", KERNELS)
 @pytest.mark.parametrize("D", [64, 128, 256])
@@ -51,3 +57,22 @@ def test_windows_in_larger_pages(q, name, page):
         b = batch(q, batch=len(WINDOW_NEW), max_q=8, table_cols=table_cols(keys, page))
         got = attn_plan(q, any_cache(q, "e4m3", D, WINDOW_HKV, page), b, sum(WINDOW_NEW), WINDOW_HKV * WINDOW_G, window)
         assert got[0] == 32
+
+
+# Several workgroups of 32 rows for a sequence and head, in the order of the lengths (at most
+# 256 sequences) and in the batch's.
+ROW_TILES = {
+    "longest first": ([16, 9, 0, 13, 16, 12, 11, 10] * 8, 8, 4, 1536),
+    "batch order, few at once": ([16, 9, 0, 13, 16, 12, 11, 10], 8, 4, 2 ** 16),
+    "batch order, many sequences": ([16, 9, 0, 13, 16] * 60, 2, 4, 1536),
+}
+
+
+@pytest.mark.parametrize("fmt,D", [("bf16", 64), ("bf16", 128), ("e4m3", 64), ("e4m3", 128)])
+@pytest.mark.parametrize("name", ROW_TILES)
+def test_row_tiles(q, name, fmt, D):
+    new, Hkv, G, keys = ROW_TILES[name]
+    assert max(new) * G == 64 and ordered(new, Hkv, G, 32) == ("longest" in name)
+    for page in (16, 64):
+        b = batch(q, batch=len(new), max_q=16, table_cols=table_cols(keys, page))
+        assert attn_plan(q, any_cache(q, fmt, D, Hkv, page), b, sum(new), Hkv * G)[0] == 32, page

@@ -7,7 +7,7 @@ import pytest
 import torch
 
 from test_abi_tree_host import KERNELS
-from test_abi_tree_pages_host import WINDOW_G, WINDOW_HKV, WINDOW_NEW, WINDOWS, table_cols
+from test_abi_tree_pages_host import ROW_TILES, WINDOW_G, WINDOW_HKV, WINDOW_NEW, WINDOWS, table_cols
 from test_gpu_tree import run_tree
 
 pytestmark = pytest.mark.gpu
@@ -79,3 +79,16 @@ def test_missing_pages_and_short_sequences_in_larger_pages(q, oracle, name, D, p
     r = run_tree(q, oracle, D + page, new, kv, Hkv, G, D, page, "e4m3", words=words,
                  extra_cols=to_width(keys, page, kv), table_edit=pages, edit=masks, pad=2)
     assert (r["seen"][25:38] == 0).all() and (r["seen"][20] == 0).all()
+
+
+@pytest.mark.parametrize("page", [16, 64])
+@pytest.mark.parametrize("fmt,D", [("bf16", 64), ("bf16", 128), ("e4m3", 64), ("e4m3", 128)])
+@pytest.mark.parametrize("name", ROW_TILES)
+def test_row_tiles(q, oracle, name, fmt, D, page):
+    """Ragged sequences of up to two workgroups' rows, some without new tokens, some as long
+    as others, in the order of their lengths and in the batch's."""
+    new, Hkv, G, keys = ROW_TILES[name]
+    rng = np.random.default_rng(D + page)
+    kv = [n + int(rng.choice([0, 7, 100, 100, 350])) for n in new]
+    kv[len(kv) // 2] = new[len(kv) // 2] + 1200
+    run_tree(q, oracle, D + page, new, kv, Hkv, G, D, page, fmt, extra_cols=to_width(keys, page, kv), pad=1)
