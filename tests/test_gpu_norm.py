@@ -242,3 +242,48 @@ def test_norm_binding_refusals(q):
     with pytest.raises(ValueError):
         q.kv_append(cache, b, k, k, norm=norm)
     assert q.norm_rope(x[:0], norm).shape == (0, 2, 64)
+
+
+@pytest.mark.parametrize("page", [16, 64])
+@pytest.mark.parametrize("rot,inter", [(0, False), (128, False), (64, True)])
+def test_append_norm_e4m3_of_many_tokens(q, oracle, rot, inter, page):
+    """Enough tokens that a thread handles several heads: every stored row's codes and scale
+    against the oracle (bounds as in test_append_norm), values that are not normalised bit
+    for bit, and queries against norm_rope."""
+    rng = np.random.default_rng(rot + page)
+    new, kv = [20, 0, 700], [60, 9, 900]
+    start, table, pages = make_batch(rng, new, kv, page)
+    T, Hq, Hkv, D = 720, 16, 4, 128
+    qkv = projections(rng, (T, Hq + 2 * Hkv, D))
+    qkv[5, Hq:] = 0
+    d = dev(qkv)
+    b = q.PagedBatch(dev(start), dev(np.array(kv, np.int32)), dev(table), 700)
+    plan = q.Rope(D, rot_dim=rot, interleaved=inter) if rot else None
+    turns = host(plan.turns) if rot else np.zeros(1)
+    w = [weight(rng, D, 0.0) for _ in range(3)]
+    slot, place = oracle.kv_slots(start, kv, table, page, pages, T)
+    assert (slot >= 0).all()
+    page_of, row = slot // page, slot % page
+    decode = oracle.fp8_decode_table(oracle.OCP)
+    for values in (False, True):
+        cache = stale_pool(q, pages, Hkv, page, D, "e4m3")
+        norm = q.HeadNorm(dev(w[0]), dev(w[1]), dev(w[2]) if values else None, eps=1e-5)
+        qn = q.kv_append(cache, b, d[:, Hq:Hq + Hkv], d[:, Hq + Hkv:], rope=plan, q=d[:, :Hq], norm=norm)
+        alone = q.norm_rope(d[:, :Hq], norm, dev(place.astype(np.int32)) if rot else None, plan)
+        assert torch.equal(qn.view(torch.int16), alone.view(torch.int16))
+        for name, at in (("k", Hq), ("v", Hq + Hkv)):
+            x = np.ascontiguousarray(qkv[:, at:at + Hkv])
+            got, sc = (host(getattr(cache, name + s))[page_of, :, row] for s in ("", "_scale"))
+            if name == "v" and not values:
+                want, ws = oracle.quant_act(x.reshape(-1, D), oracle.OCP)
+                assert np.array_equal(got.reshape(-1, D), want) and np.array_equal(sc.ravel(), ws)
+                continue
+            turned = (place.astype(np.int32), turns, rot, inter) if name == "k" else (place.astype(np.int32), turns, 0)
+            y, mag = oracle.norm_rope(x, w[1 if name == "k" else 2], norm._c.eps, 0.0, *turned)
+            top = np.abs(y).max(-1)
+            off = 3 * 2.0 ** -20 * mag.max(-1)
+            assert (np.abs(sc - top / 448) <= (off + top * 2.0 ** -23) / 448).all()
+            val = decode[got] * sc[..., None].astype(np.float64)
+            tol = np.maximum(2.0 ** -4 * np.abs(y), 2.0 ** -10 * (top / 448)[..., None]) + 3 * off[..., None]
+            assert (np.abs(val - y) <= tol).all()
+            assert (sc[5] == 0).all() and (got[5] == 0).all()
