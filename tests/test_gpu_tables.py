@@ -209,3 +209,33 @@ def test_tables_binding_refusals(q):
     empty.reserve(torch.zeros(0, **i32), torch.zeros(0, **i32))
     empty.release(torch.zeros(0, **i32))
     assert host(pool.count).tolist() == [8, 0]
+
+
+@pytest.mark.parametrize("T", [0, 300, 5000])
+@pytest.mark.parametrize("B", [1, 40, 400])
+def test_tables_without_slots_or_positions(q, oracle, B, T):
+    """The C interface's tables may have no slots, no positions or neither, in one launch and
+    in two: all other arrays are as with them."""
+    import ctypes as C
+
+    rng = np.random.default_rng(B + T)
+    lib, stream = q.lib(), torch.cuda.current_stream().cuda_stream
+    for absent in (("slots",), ("positions",), ("slots", "positions")):
+        both = Both(q, rng, B, 30, 16, B * 30, B * 20, T)
+        t = q._KVTables.from_buffer_copy(both.tables._c)
+        for name in absent:
+            setattr(t, name, None)
+            setattr(both, name, np.full(T, -9, np.int32))
+        lengths = rng.integers(0, 200, B).astype(np.int32)
+        new = rng.integers(0, max(2 * T // B, 60), B).astype(np.int32)
+        ld, nd = dev(lengths), dev(new)
+        assert lib.qlin_kv_reserve(both.pool._ref, C.byref(t), T, ld.data_ptr(), nd.data_ptr(), stream) == q.OK
+        slots, positions = both.slots.copy(), both.positions.copy()
+        both.q_start, both.kv_len = oracle.kv_reserve(lengths, new, both.table, both.free, both.count, 16, slots, positions)
+        for name, full in (("slots", slots), ("positions", positions)):
+            if name not in absent:
+                setattr(both, name, full)
+        both.same()
+        assert lib.qlin_kv_release(both.pool._ref, C.byref(t), ld.data_ptr(), stream) == q.OK
+        oracle.kv_release(lengths, both.kv_len, both.table, both.free, both.count, 16)
+        both.same()
