@@ -448,7 +448,14 @@ typedef struct {
  * nothing outside the arrays is read or written for it. No two arrays may overlap
  * (QLIN_ERR_ARG), but lengths may be kv_len or new_tokens and, when pages are released,
  * what is only read may be anything.
- * Calls that share a pool must be ordered on one stream. */
+ * Calls that share a pool must be ordered on one stream.
+ *
+ * A step whose reservation lacked pages (count[1] > 0) is dropped by a release with the
+ * same lengths, and made again once requests have ended or been put off: tokens without a
+ * page are neither cached nor seen, but later reservations take the page of a request's
+ * last cached tokens as there, whatever its entry says. A program that looks at count[1]
+ * only after qlin_kv_keep (of one graph, say) reserves no new tokens behind the lengths
+ * that it left, then releases to those from before the step. */
 int qlin_kv_reserve(const qlin_kv_pool* pool, const qlin_kv_tables* tables, int64_t T, const int32_t* lengths,
                     const int32_t* new_tokens, qlin_stream_t stream);
 
@@ -643,7 +650,8 @@ int qlin_tree_plan(const qlin_kv_batch* batch, int64_t T, const int32_t* parents
  * place of token i, as if all had been read before any is written. path [batch]
  * [path_cols] and kept [batch] int32; kept beyond path_cols or the new tokens counts as
  * those. lengths [batch] gets the cached tokens then: kv_len less the new tokens plus
- * the kept ones; it must not overlap path, kept or the batch's arrays (QLIN_ERR_ARG).
+ * the kept ones (those that had no page among them: a step whose reservation lacked
+ * pages is dropped before, see qlin_kv_reserve); it must not overlap path, kept or the batch's arrays (QLIN_ERR_ARG).
  * Rows of other tokens, the dropped ones among them, are left as they are. A
  * number outside the new tokens, or a place that the table does not reach or whose page
  * is none of the pool's, moves nothing; of a path that does not ascend the moved rows

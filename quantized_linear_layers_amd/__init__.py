@@ -870,7 +870,8 @@ class PageTables:
     def reserve(self, lengths, new_tokens) -> PagedBatch:
         """Room for new_tokens int32 [B] behind lengths int32 [B] cached tokens: pages
         from the pool into page_table, starts, lengths, slots and positions of the new
-        tokens (qlin_kv_reserve). pool.count[1] tells what the pool lacked."""
+        tokens (qlin_kv_reserve). pool.count[1] tells what the pool lacked: if not 0, drop
+        the step with release(lengths) before anything is kept."""
         dev = self.device
         if dev.index != _current_device():
             with torch.cuda.device(dev):
@@ -1032,7 +1033,8 @@ def kv_keep(layers: PagedLayers | PagedKV, batch: PagedBatch, path, kept, length
     """After a step of drafted tokens: each sequence's accepted ones, path int32 [B, W]
     (numbers among its new tokens, ascending) of which the first kept int32 [B], become
     its first new tokens in every layer's cache. Returns the cached tokens that are left,
-    int32 [B] (or writes them to `lengths`): what the next step starts from."""
+    int32 [B] (or writes them to `lengths`): what the next step starts from. Kept tokens
+    count whether or not they had a page (PageTables.reserve)."""
     if isinstance(layers, PagedKV):
         layers = PagedLayers((layers,))
     dev, B = layers.device, batch.batch

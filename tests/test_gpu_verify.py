@@ -250,3 +250,92 @@ def test_empty_calls(q):
     q.kv_append(cache, b, x[:, 4:6], x[:, 6:], rope, x[:, :4], out, norm=norm)
     q.attn_paged(cache, b, x[:, :4], out=out, tree=tree)
     assert (out == 3.0).all() and torch.equal(cache.k.view(torch.int16), before.view(torch.int16))
+
+
+def drafted_step(rng, s, new):
+    """Rows, trees and an accepted chain of each request for a step of `new` tokens."""
+    start, T = np.concatenate([[0], np.cumsum(new)]), int(sum(new))
+    parents = trees(rng, new, "random")
+    path, kept = np.zeros(s.path.shape, np.int32), np.zeros(len(new), np.int32)
+    for b, n in enumerate(new):
+        at, chain = n - 1, []
+        while at >= 0:
+            chain.append(at)
+            at = int(parents[start[b] + at])
+        kept[b] = len(chain)
+        path[b, :kept[b]] = chain[::-1]
+    return projections(rng, (LAYERS, T, (GROUP + 2) * HKV, s.qkv.shape[-1])), parents, path, kept
+
+
+def load_step(s, new, x, parents, path, kept):
+    s.qkv[:, :x.shape[1]].copy_(dev(x))
+    s.parents[:len(parents)].copy_(dev(parents))
+    for t, a in ((s.new, np.array(new, np.int32)), (s.path, path), (s.kept, kept)):
+        t.copy_(dev(a))
+
+
+@pytest.mark.parametrize("graph", [False, True])
+def test_steps_that_lack_pages_are_dropped_and_tried_again(q, graph):
+    """A pool that runs short tells so in count[1]. The step is dropped, before anything is
+    kept (a release with the old lengths) or, where one graph holds it whole, after (a
+    reservation of no tokens behind the new lengths, released to the old ones): the pool has
+    its pages again, and once another request has ended the step gives what it gives with a
+    pool that never runs short."""
+    rng = np.random.default_rng(21)
+    D, page, B, cols = 64, 16, 3, 12
+    args = (q, B, D, page, "e4m3", cols, 200, 64, q.Rope(D), [q.HeadNorm(head_dim=D)] * LAYERS, 0)
+    short, ample = Server(*args), Server(*args)
+    short.pool.count.copy_(dev(np.array([10, 0], np.int32)))  # ten pages
+    none = torch.zeros_like(short.lengths)
+    if graph:
+        side, recorded = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(recorded, stream=side):
+            short.step()
+
+    def held(lengths):
+        return sum(-(-n // page) for n in lengths.tolist())
+
+    drops = 0
+    for new in ([20, 20, 20], [50, 50, 50], [30, 40, 30]):  # (the second needs twelve pages at least)
+        while True:
+            what = drafted_step(rng, short, new)
+            for s in (short, ample):
+                load_step(s, new, *what)
+            before = short.lengths.clone()
+            torch.cuda.synchronize()
+            if graph:
+                recorded.replay()
+                torch.cuda.synchronize()
+                lacking = int(short.pool.count[1])
+                if lacking:
+                    short.tables.reserve(short.lengths, none)
+                    short.tables.release(before)
+                    short.lengths.copy_(before)
+            else:
+                short.tables.reserve(short.lengths, short.new)
+                lacking = int(short.pool.count[1])
+                short.tables.release(short.lengths)  # (whole steps reserve for themselves)
+                if not lacking:
+                    short.step()
+            if not lacking:
+                break
+            drops += 1
+            assert host(short.pool.count)[0] == 10 - held(before)
+            ends = int(np.argmax(new))
+            new = [0 if b == ends else n for b, n in enumerate(new)]
+            for s in (short, ample):
+                s.tables.reserve(s.lengths, none)
+                s.lengths[ends] = 0
+                s.tables.release(s.lengths)
+        ample.step()
+        lengths = short.lengths
+        assert torch.equal(lengths, ample.lengths)
+        assert host(short.pool.count).tolist() == [10 - held(lengths), 0]
+        for i in range(LAYERS):
+            for b in range(B):
+                for g, w in zip(rows_of(short, i, b, int(lengths[b])), rows_of(ample, i, b, int(lengths[b]))):
+                    assert np.array_equal(g, w)
+            assert torch.equal(short.out[i, :sum(new)].view(torch.int16), ample.out[i, :sum(new)].view(torch.int16))
+    assert drops
+    assert np.unique(host(short.pool.free)[:int(short.pool.count[0])]).size == int(short.pool.count[0])
