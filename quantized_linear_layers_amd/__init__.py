@@ -844,7 +844,12 @@ class PageTables:
     """The tables of a batch of requests over `pool`: page_table int32 [B, cols] (the
     requests' pages), and q_start, kv_len, slots and positions of at most max_tokens new
     tokens, max_q of one request, which `reserve` writes. `batch` is the PagedBatch of
-    them. All of them stay in place, so a captured graph may hold the calls."""
+    them. All of them stay in place, so a captured graph may hold the calls.
+
+    max_q chooses kernels and bounds a tree (512 tokens, and a window): where one set of
+    tables serves prompts and trees, the trees' steps take a batch of their own over the
+    same tensors, PagedBatch(tables.q_start, tables.kv_len, tables.page_table, max_q). Tables
+    of more than 4096 tokens are reserved in two launches, whatever the step's tokens."""
 
     def __init__(self, pool: PagePool, page_table, max_tokens: int, max_q: int):
         _check(page_table, "page_table", torch.int32, 2)

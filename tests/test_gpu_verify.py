@@ -339,3 +339,44 @@ def test_steps_that_lack_pages_are_dropped_and_tried_again(q, graph):
             assert torch.equal(short.out[i, :sum(new)].view(torch.int16), ample.out[i, :sum(new)].view(torch.int16))
     assert drops
     assert np.unique(host(short.pool.free)[:int(short.pool.count[0])]).size == int(short.pool.count[0])
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+def test_tables_of_prompts_serve_trees(q, oracle, fmt):
+    """Tables with room for prompts, whose own batch is too long for trees, and a second batch
+    over the same tensors for the steps of drafted tokens."""
+    rng = np.random.default_rng(31)
+    D, page, B, cols = 128, 32, 3, 70
+    s = Server(q, B, D, page, fmt, cols, 4500, 2000, q.Rope(D), [q.HeadNorm(head_dim=D)] * LAYERS, 0)
+    prompts = [2000, 7, 600]
+    T = sum(prompts)
+    s.qkv[:, :T].copy_(dev(projections(rng, (LAYERS, T, (GROUP + 2) * HKV, D))))
+    s.new.copy_(dev(np.array(prompts, np.int32)))
+    s.step(drafted=False)
+    with pytest.raises(q.QlinError):
+        q.tree_plan(s.tables.batch, s.parents, s.tree)
+    steps = q.PagedBatch(s.tables.q_start, s.tables.kv_len, s.tables.page_table, 64)
+    lengths = prompts
+    for new in ([64, 1, 33], [5, 64, 0]):
+        x, parents, path, kept = drafted_step(rng, s, new)
+        load_step(s, new, x, parents, path, kept)
+        T = sum(new)
+        assert s.tables.reserve(s.lengths, s.new) is s.tables.batch
+        parents, rows = s.parents[:T], [s.qkv[i, :T] for i in range(LAYERS)]
+        tree = q.tree_plan(steps, parents)
+        start, kv, table = host(steps.q_start), host(steps.kv_len), host(steps.page_table)
+        assert kv.tolist() == [n + m for n, m in zip(lengths, new)]
+        for i, c in enumerate(s.caches):
+            n = GROUP * HKV
+            turned = q.kv_append(c, steps, rows[i][:, n:n + HKV], rows[i][:, n + HKV:], s.rope, rows[i][:, :n],
+                                 positions=tree.positions, norm=s.norms[i])
+            got, lse = q.attn_paged(c, steps, turned, tree=tree, return_lse=True)
+            e4 = (host(c.k_scale), host(c.v_scale)) if fmt == "e4m3" else (None, None)
+            want = oracle.attn_paged(host(turned), host(c.k), host(c.v), *e4, start, kv, table, D ** -0.5, True, 0,
+                                     host(tree.mask).view(np.uint64), host(tree.positions))
+            attn_check(want, host(got), host(lse), D, f"{new} layer {i}")
+        q.kv_keep(s.layers, steps, s.path, s.kept, s.lengths)
+        s.tables.release(s.lengths)
+        lengths = [n + int(k) for n, k in zip(lengths, kept)]
+        assert s.lengths.tolist() == lengths
+        assert host(s.pool.count).tolist() == [B * cols - sum(-(-n // page) for n in lengths), 0]
