@@ -589,6 +589,11 @@ int qlin_norm_rope(const qlin_bf16* x, int64_t ldx, int64_t T, int64_t H, int64_
  *   q, out [T][ldq], [T][ldo] bf16 (ld >= q_heads * head_dim, multiples of 8);
  *   lse [T][q_heads] fp32 or NULL; scale * log2(e) finite in fp32 (|scale| below
  *   2.35e38; else QLIN_ERR_ARG).
+ * Scores, maxima, sums, joins and lse are fp32. Two roundings to fewer bits: each weight to
+ * bf16 before it multiplies its value (with the value's E4M3 scale in it; 2^-8 of the
+ * mean of |v| under the weights at most), and out to bf16 (2^-8 of itself). Against out in
+ * fp64 the error is 1.3 to 1.4 times that of the rounding of out alone. The same of
+ * qlin_attn_tree.
  * Workspace: qlin_attn_workspace_bytes bytes, 256-byte aligned (0 when the key
  * axis is not split). As the GEMMs', it starts with 64 KiB of arrival counters
  * that must be zero before the first call that uses it (qlin_workspace_init);

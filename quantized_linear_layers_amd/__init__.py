@@ -1067,7 +1067,8 @@ def attn_paged(cache: PagedKV, batch: PagedBatch, q, scale=None, causal=True, wi
     return_lse the rows' ln of the sum of exponentials, f32 [T, q_heads]. scale
     defaults to D ** -0.5; window > 0 limits each token to its last `window` keys.
     With `tree`, each new token sees the earlier ones of its sequence and those new
-    ones that its mask names (qlin_attn_tree; a window is then at least max_q). Rows
+    ones that its mask names (qlin_attn_tree; a window is then at least max_q). Weights are
+    rounded to bf16 before they multiply the values, sums and lse are f32. Rows
     of q outside every sequence are left as they are in `out` (undefined in a new
     one)."""
     D, dev = cache.head_dim, cache.device
