@@ -1645,15 +1645,17 @@ int tree_splits(bool e4m3, int64_t keys, int64_t wgs) {
 // The same for trees, whose calls have some 16 to 256 rows a sequence and head: workgroups
 // of 16 or 32 rows, of four waves or (the tiles of a part taken by twice as many at once)
 // eight. A workgroup of eight costs less than a second part, whose join takes as long as a
-// thousand keys. us, 32 + 8 heads of 128:
-//   16 rows and eight waves while all run at once, few bytes are read twice, and always where
-//     codes are converted (E4M3): a tree of 8, 1024 keys: 11.9, of 32 rows 18.7; 4096 keys in
-//     16 parts 14.6 (four waves 17.4, 32 rows 18.0); E4M3, eight trees of 32, 4096 keys:
-//     30.7 and 34.1;
-//   32 rows beyond: a tree of 32, 16384 keys in 8 parts 29.0 (16 rows 33.0), eight trees of
-//     32, 4096 keys 31.6 (four waves 36.3); 64 trees of 16 four waves: 142 (eight 152);
-//   short tables: 16 rows, four waves: eight trees of 32, 256 keys: 8.7 and 9.9; E4M3, 64 of
-//     them, 1024 keys: 62 and 67.
+// thousand keys. us, 32 + 8 heads of 128, all in one run, calls behind each other in a graph:
+//   16 rows and eight waves while all run at once and few bytes are read twice: a tree of 8,
+//     1024 keys: 10.0 (four waves 11.6, 32 rows 13.6); 4096 keys in 16 parts 14.4 (17.6,
+//     17.9). E4M3, eight trees of 32, 4096 keys: 32.5 (34.6; 32 rows 32.3);
+//   32 rows beyond: a tree of 32, 16384 keys 29.5 (16 rows 33.8); eight trees of 32, 4096
+//     keys 32.9 (16 rows 36.2, four waves 42.1); 64 trees of 16, four waves: 139 (eight 152,
+//     16 rows 189). E4M3 beyond 2^30 bytes: three trees of 64, 65536 keys 187 (16 rows 227),
+//     16 of 16, 16384 keys 106 (124), but eight of 32, 16384 keys 89 (75): such shapes
+//     are the few that the limit on bytes decides wrong;
+//   short tables: 16 rows, four waves: eight trees of 32, 256 keys: 9.0 (32 rows 9.9); E4M3,
+//     64 of them, 1024 keys: 59.5 (64.3).
 Plan tree_step_plan(const qlin_kv_cache& cache, const qlin_kv_batch& batch, int64_t rows, int64_t keys) {
   Plan p = {};
   p.step = true;
@@ -1663,7 +1665,7 @@ Plan tree_step_plan(const qlin_kv_cache& cache, const qlin_kv_batch& batch, int6
   const int64_t at_once = e4m3 && D < 256 ? 512 : 256;                                // of eight waves
   const double reread = (double)few * keys * D * (e4m3 ? 2 : 4);                      // bytes, by 16 rows each
   bool narrow = rows <= 16 || (e4m3 && D == 256);
-  if (few <= at_once && (e4m3 ? reread < 0x1p30 || many > 128 : reread < 0x1p29)) {
+  if (few <= at_once && reread < (e4m3 ? 0x1p30 : 0x1p29)) {
     narrow = p.wide = true;
   } else if (keys <= 1024 && (e4m3 ? D > 64 : D == 128 && few <= 512)) {
     narrow = true;
