@@ -86,8 +86,8 @@ __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
 // reciprocal and q = x y, the remainder q sc - x is exact and q - (q sc - x) y rounds to
 // the quotient (Markstein). The remainder is taken in this order because a zero then keeps
 // its sign, and with it its code (x - q sc is +0 for either; copysignf costs 0.4 us).
-// Three instructions in place of a division's ten: 14.1 us for the 15.3 of the E4M3 call
-// above. Unlike in divide8 the rows are not bf16 but use all of fp32's bits: where a code
+// Three instructions in place of a division's ten: the E4M3 call above takes 13.5 us, 14.5
+// with divisions. Unlike in divide8 the rows are not bf16 but use all of fp32's bits: where a code
 // is not zero the remainders are multiples of 2^-57 sc, exact for every sc from 2^-92 on.
 // Scales outside 2^-80 .. 2^90, the range that was compared with division (equal
 // quotients and signs in 8e9 random pairs), are divided.
@@ -223,9 +223,10 @@ __device__ __forceinline__ float normalise(Piece& p, int n, float inv_d, float e
 // APPEND: keys and values go to the cache; FP8: as E4M3 codes with a scale. NORM:
 // heads are normalised first. PH: pieces of a head, for those sizes that every cache has,
 // 0: any number of them. With NORM five waves a SIMD, so that the calls which fill the
-// device once do it with room: 2250 tokens of 16 + 8 heads of 256 into E4M3, normalised,
-// are 4500 waves and take 16.5 us, 18.2 with four waves a SIMD (and no register spilled;
-// five spill seven, outside the loop over heads).
+// device once do it with room: 2250 tokens of 16 + 8 heads of 256 into E4M3, normalised, are
+// 4500 waves. Repeated in a graph they take 16.4 us (15.3 among calls on other inputs), with
+// four waves a SIMD 18.3 (and no register spilled; five spill seven, outside the loop over
+// heads).
 template <int PH, bool APPEND, bool FP8, bool NORM>
 __global__ __launch_bounds__(kRopeThreads, NORM ? 5 : 1) void rope_kernel(const RopeArgs a) {
   const int D = PH ? 16 * PH : a.D, per_head = D / 16;

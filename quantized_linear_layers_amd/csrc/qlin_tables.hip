@@ -18,7 +18,8 @@
 // first one left.
 //
 // Bound by latency: the launch (1.8 us) and loads that each need the one before. A tree of 8
-// 2.0 us, 256 of up to 256 tokens 5.9 (ten barriers and masks of 1.7 MB); the tables of 64
+// 2.0 us, 256 of up to 256 tokens 5.6 (two barriers a round, eight rounds for a chain of
+// 256, and masks of 1.7 MB); the tables of 64
 // requests with up to 16 new tokens 3.5 and, back, 3.0; 64 prompts of up to 8192 tokens, 17000
 // pages of 16, 1.9 + 4.7 and 8.3.
 #include "qlin_internal.h"
