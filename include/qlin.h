@@ -453,7 +453,9 @@ typedef struct {
  * A step whose reservation lacked pages (count[1] > 0) is dropped by a release with the
  * same lengths, and made again once requests have ended or been put off: tokens without a
  * page are neither cached nor seen, but later reservations take the page of a request's
- * last cached tokens as there, whatever its entry says. A program that looks at count[1]
+ * last cached tokens as there, whatever its entry says. (Tokens behind the table's reach
+ * are not counted in count[1]: a request's lengths + new_tokens are to stay within
+ * table_cols * page_size.) A program that looks at count[1]
  * only after qlin_kv_keep (of one graph, say) reserves no new tokens behind the lengths
  * that it left, then releases to those from before the step. */
 int qlin_kv_reserve(const qlin_kv_pool* pool, const qlin_kv_tables* tables, int64_t T, const int32_t* lengths,

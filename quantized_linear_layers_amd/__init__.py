@@ -876,7 +876,8 @@ class PageTables:
         """Room for new_tokens int32 [B] behind lengths int32 [B] cached tokens: pages
         from the pool into page_table, starts, lengths, slots and positions of the new
         tokens (qlin_kv_reserve). pool.count[1] tells what the pool lacked: if not 0, drop
-        the step with release(lengths) before anything is kept."""
+        the step with release(lengths) before anything is kept. (Tokens behind the table's
+        columns have no page either and are not counted there.)"""
         dev = self.device
         if dev.index != _current_device():
             with torch.cuda.device(dev):

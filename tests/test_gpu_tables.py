@@ -239,3 +239,11 @@ def test_tables_without_slots_or_positions(q, oracle, B, T):
         assert lib.qlin_kv_release(both.pool._ref, C.byref(t), ld.data_ptr(), stream) == q.OK
         oracle.kv_release(lengths, both.kv_len, both.table, both.free, both.count, 16)
         both.same()
+
+
+def test_tokens_behind_the_table_are_not_lacking(q, oracle):
+    """A request that outgrows its table: no page is taken or counted for those tokens."""
+    both = Both(q, np.random.default_rng(8), 2, 3, 16, 6, 6, 60)
+    both.reserve(oracle, [40, 0], [30, 20])
+    assert both.count.tolist() == [4, 0]
+    assert (both.slots[8:30] == -1).all() and (both.slots[:8] >= 0).all() and (both.slots[30:50] >= 0).all()
